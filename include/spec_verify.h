@@ -473,6 +473,185 @@ int spec_shard_phase_launch(const spec_shard_args* args, hipStream_t stream);
 int spec_shard_decide_launch(const spec_shard_args* args, hipStream_t stream);
 int spec_shard_draw_launch(const spec_shard_args* args, hipStream_t stream);
 
+/* --------------------------------------------------- token log probabilities
+ *
+ * What a serving API returns beside the tokens a verification emitted: the
+ * log probability of each, the entropy of the distribution it came from and
+ * that distribution's most likely tokens ("P-EAGLE" page, section "Triton
+ * Kernel": the target's rows of the verified batch).  Row r of request b with
+ * token t = tokens[b, r] and p = softmax(logits[b, r, :] / T_b):
+ *   logprobs[b, r] = ln p(t),  entropy[b, r] = -sum_v p(v) ln p(v),
+ *   top_ids[b, r, :] the `top` largest logits in descending order (equal
+ *   logits: the lower index first), top_logprobs their ln p.
+ * T_b = 0 (greedy) and temperature == NULL take the unscaled logits.  With
+ * tokens = the output_tokens of a verification and logits = its
+ * target_logits, row r is the row that token r was checked against or drawn
+ * from.  A prompt is one request whose rows are its positions.
+ *
+ * A row whose token is -1 holds no token: it is not read, and gets logprob
+ * and entropy 0, ids -1 and log probabilities 0.  A row with any other token
+ * outside [0, V), with a temperature that is negative, NaN, infinite or
+ * positive below FLT_MIN, without a finite logit, or with a NaN or +inf
+ * logit, is a data error: logprob, entropy and top_logprobs NaN, ids -1.  A
+ * token whose logit is -inf has log probability -inf; logits of -inf are
+ * never alternatives: places of top_ids without a finite logit hold -1, with
+ * log probability -inf.
+ */
+#define SPEC_MAX_TOP 32 /* most alternatives per row */
+typedef struct {
+  int32_t B;                /* requests, >= 0 */
+  int32_t R;                /* rows per request, >= 0 */
+  int32_t V;                /* vocabulary size, 1..SPEC_MAX_V */
+  int32_t dtype;            /* spec_dtype of the logits */
+  const void* logits;       /* device [B, R, V] */
+  int64_t req_stride;       /* elements between requests, 0 (shared rows) or >= R * row_stride */
+  int64_t row_stride;       /* elements between rows, >= V */
+  const int32_t* tokens;    /* device [B, R]; -1 = no token */
+  const float* temperature; /* device [B] or NULL */
+  int32_t top;              /* alternatives per row, 0..SPEC_MAX_TOP */
+  float* logprobs;          /* device out [B, R] */
+  float* entropy;           /* device out [B, R], or NULL */
+  int32_t* top_ids;         /* device out [B, R, top] (top > 0) */
+  float* top_logprobs;      /* device out [B, R, top] (top > 0) */
+  void* workspace;          /* device, >= spec_logprobs_workspace_bytes(B, R, V, top), 16-byte aligned */
+  size_t workspace_bytes;
+} spec_logprobs_args;
+
+/* Bytes of device workspace (0 for an invalid shape); stateless, no
+ * initialisation; calls that overlap on one workspace race. */
+size_t spec_logprobs_workspace_bytes(int32_t B, int32_t R, int32_t V, int32_t top);
+int spec_logprobs_launch(const spec_logprobs_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------ 8-bit paged KV cache
+ *
+ * The cache behind the slot mapping of spec_expand_launch, held in 8 bits
+ * (the pages serve with an fp8 KV cache, "P-EAGLE" page, section
+ * "Hidden State 管理" for the slots): slot s is token s % block_size of
+ * physical block s / block_size.  Keys and values are OCP e4m3 codes; the
+ * tokens of a block fall into groups of scale_tokens, and each group has one
+ * power-of-two scale per head, held as an exponent byte: the value of a code
+ * c is c * 2^(byte - 127).  (e4m3 is a floating-point format: a scale that is
+ * no power of two would gain it no precision, and with powers of two a value
+ * is exact in bf16 and a growing scale moves codes without rounding them,
+ * but for the smallest.)
+ * Layout: code of head h, element d at
+ *   codes + block * block_stride + token * token_stride + h * head_stride + d,
+ * scale byte of group g of a block at
+ *   scales + block * scale_block_stride + h * scale_head_stride + g.
+ */
+typedef struct {
+  int32_t num_blocks;          /* physical blocks, >= 1 */
+  int32_t block_size;          /* tokens per block: a power of two, 16..1024 */
+  int32_t scale_tokens;        /* tokens per scale: a power of two, 1..64, <= block_size */
+  int32_t heads;               /* KV heads, 1..1024 */
+  int32_t head_dim;            /* multiple of 16, 16..256 */
+  uint8_t* k_codes;            /* device, 16-byte aligned */
+  uint8_t* v_codes;            /* device, 16-byte aligned, the strides of k_codes */
+  int64_t block_stride;        /* bytes, multiples of 16; tokens and heads of a block in either */
+  int64_t token_stride;        /* order, without overlap */
+  int64_t head_stride;
+  uint8_t* k_scales;           /* device */
+  uint8_t* v_scales;           /* device, the strides of k_scales */
+  int64_t scale_block_stride;  /* bytes, >= heads * scale_head_stride */
+  int64_t scale_head_stride;   /* bytes, >= block_size / scale_tokens */
+} spec_kv_cache;
+
+/* Write: token i's keys and values go to slot slots[i]; entries outside
+ * [0, num_blocks * block_size) (the -1 of a slot mapping) are skipped.  The
+ * scale of a group that a call writes to: let e be the smallest exponent
+ * with |x| <= 448 * 2^e for every finite x written to it, at least -117.  If
+ * the group's first token is among the written ones the group begins anew
+ * with scale 2^e; otherwise the scale becomes the larger of 2^e and what it
+ * was, and where it grew, the tokens in front of the first written one are
+ * requantised (tokens behind it that this call does not write are stale in a
+ * cache written in order: drafts that were rejected; their codes stay).
+ * Values are rounded to nearest, ties to even; a NaN or infinite element is
+ * stored as NaN.
+ * Precondition: the entries of one group stand together in the list (skipped
+ * entries between them do not matter), as a slot mapping has them; of equal
+ * slots the last entry counts.  A list that breaks this leaves unspecified
+ * values in the groups concerned (all accesses stay in bounds).
+ */
+typedef struct {
+  spec_kv_cache cache;
+  int32_t N;                   /* entries, >= 0 */
+  int32_t dtype;               /* spec_dtype of key and value */
+  const void* key;             /* device [N, heads, head_dim], unit stride in head_dim */
+  const void* value;           /* device [N, heads, head_dim] */
+  int64_t k_token_stride, k_head_stride;  /* elements, >= 0 */
+  int64_t v_token_stride, v_head_stride;
+  const int64_t* slots;        /* device [N] */
+} spec_kv_write_args;
+
+int spec_kv_write_launch(const spec_kv_write_args* args, hipStream_t stream);
+
+/* Read: key[i], value[i] = the values at slot slots[i] in the given type
+ * (exact in both), zeros for entries outside the cache. */
+typedef struct {
+  spec_kv_cache cache;
+  int32_t N;                   /* entries, >= 0 */
+  int32_t dtype;               /* spec_dtype of key and value */
+  void* key;                   /* device out [N, heads, head_dim], contiguous */
+  void* value;                 /* device out [N, heads, head_dim], contiguous */
+  const int64_t* slots;        /* device [N] */
+} spec_kv_read_args;
+
+int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
+
+/* Attention of each request's new tokens over its cached context ("P-EAGLE"
+ * page, section "核心方法": the target scores the K + 1 positions of a round
+ * in one pass; explainer page, section "核心思想").  Request b has the new
+ * tokens [q_start[b], q_start[b+1]) of the batch, n_b of them, and ctx_len[b]
+ * tokens in the cache, the new ones included and last; token i of it stands
+ * at position p = ctx_len[b] - n_b + i and sees the positions j with
+ * 0 <= j <= p and, with window > 0, j > p - window.  Position j lies in block
+ * block_table[b, j / block_size]; positions whose entry is outside
+ * [0, num_blocks) hold nothing and are not seen.  Query head h reads KV head
+ * h / (q_heads / heads):
+ *   s_j = scale * q . k_j,  z = ln(sum_j exp(s_j) + exp(sinks[h])),
+ *   out = sum_j exp(s_j - z) v_j,  lse = z
+ * (without sinks that term is absent).  A token that sees nothing gets out 0
+ * and lse = sinks[h], or -inf without sinks.
+ * Codes of positions that a token does not see never reach its output, NaN
+ * among them.  A request whose ctx_len is negative or above max_ctx or
+ * max_blocks * block_size, or whose n_b is above max_q, is a data error: NaN
+ * in its rows of out and lse.  A request whose range is empty or not inside
+ * [0, N] writes nothing; rows outside every range stay as they were.  A
+ * decreasing q_start is outside the contract (results unspecified, all
+ * accesses stay in bounds).
+ */
+typedef struct {
+  spec_kv_cache cache;
+  int32_t B;                   /* requests, >= 0 */
+  int32_t N;                   /* new tokens of the batch (rows of q), >= 0 */
+  int32_t q_heads;             /* a multiple of cache.heads, at most 64 times it */
+  int32_t max_q;               /* upper bound of n_b, 1..2^24 */
+  int32_t max_ctx;             /* upper bound of ctx_len, 0..2^30 */
+  int32_t window;              /* 0 = none */
+  int32_t dtype;               /* SPEC_BF16: q and out */
+  float scale;                 /* finite */
+  const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
+  int64_t q_token_stride, q_head_stride;  /* elements, >= 0 */
+  const int32_t* q_start;      /* device [B + 1] */
+  const int32_t* ctx_len;      /* device [B] */
+  const int32_t* block_table;  /* device [B, >= max_blocks] */
+  int64_t bt_row_stride;       /* elements, >= max_blocks */
+  int32_t max_blocks;          /* >= 0 */
+  const float* sinks;          /* device [q_heads] or NULL */
+  void* out;                   /* device out [N, q_heads, head_dim], contiguous */
+  float* lse;                  /* device out [N, q_heads] or NULL */
+  void* workspace;             /* device, >= spec_attn_workspace_bytes(args), 16-byte aligned (may be NULL
+                                  where that is 0) */
+  size_t workspace_bytes;
+} spec_attn_args;
+
+/* Bytes of device workspace for these sizes (the sizes alone are read: B, N,
+ * q_heads, max_q, max_ctx, window and cache.heads, head_dim, block_size; 0
+ * also where they are invalid); stateless, no initialisation; calls that
+ * overlap on one workspace race. */
+size_t spec_attn_workspace_bytes(const spec_attn_args* args);
+int spec_attn_launch(const spec_attn_args* args, hipStream_t stream);
+
 /* Human-readable name of a spec_status value (static storage). */
 const char* spec_status_string(int status);
 

@@ -21,6 +21,7 @@ SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_MAX_K = 63
 SPEC_MAX_V = 2147418112  # 2^31 - 2^16
 SPEC_NOALLOC_SCRATCH_BYTES = 16 << 20
+SPEC_MAX_TOP = 32  # most alternatives per row of token_logprobs
 SPEC_PHASES_DYNAMIC = 1  # phase_starts value: decisions inside the row pass (dynamic early exit)
 
 EXPORTED = ("spec_verify_workspace_bytes", "spec_verify_plan_phases", "spec_verify_phase_cost",
@@ -29,6 +30,8 @@ EXPORTED = ("spec_verify_workspace_bytes", "spec_verify_plan_phases", "spec_veri
             "spec_draft_workspace_bytes",
             "spec_draft_sample_launch", "spec_shard_workspace_bytes", "spec_shard_stats_launch",
             "spec_shard_phase_launch", "spec_shard_decide_launch", "spec_shard_draw_launch",
+            "spec_logprobs_workspace_bytes", "spec_logprobs_launch", "spec_kv_write_launch",
+            "spec_kv_read_launch", "spec_attn_workspace_bytes", "spec_attn_launch",
             "spec_workspace_error", "spec_status_string")
 
 
@@ -95,6 +98,57 @@ class SpecShardArgs(ctypes.Structure):
     ]
 
 
+class SpecLogprobsArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("R", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("req_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p), ("temperature", ctypes.c_void_p), ("top", ctypes.c_int32),
+        ("logprobs", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+        ("top_logprobs", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SpecKVCache(ctypes.Structure):
+    _fields_ = [
+        ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("scale_tokens", ctypes.c_int32),
+        ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+    ]
+
+
+class SpecKVWriteArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SpecKVCache), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("key", ctypes.c_void_p), ("value", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+    ]
+
+
+class SpecKVReadArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SpecKVCache), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("key", ctypes.c_void_p), ("value", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+    ]
+
+
+class SpecAttnArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SpecKVCache), ("B", ctypes.c_int32), ("N", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+        ("max_q", ctypes.c_int32), ("max_ctx", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("q_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("bt_row_stride", ctypes.c_int64), ("max_blocks", ctypes.c_int32),
+        ("sinks", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _load():
     # torch ships its own HIP runtime under the same SONAME as the system one;
     # loading torch first makes this library bind to that single runtime
@@ -134,6 +188,14 @@ def _load():
     for name in ("spec_shard_stats_launch", "spec_shard_phase_launch", "spec_shard_decide_launch",
                  "spec_shard_draw_launch"):
         getattr(L, name).argtypes = [ctypes.POINTER(SpecShardArgs), ctypes.c_void_p]
+        getattr(L, name).restype = ctypes.c_int
+    L.spec_logprobs_workspace_bytes.argtypes = [ctypes.c_int32] * 4
+    L.spec_logprobs_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_attn_workspace_bytes.argtypes = [ctypes.POINTER(SpecAttnArgs)]
+    L.spec_attn_workspace_bytes.restype = ctypes.c_size_t
+    for name, struct in (("spec_logprobs_launch", SpecLogprobsArgs), ("spec_kv_write_launch", SpecKVWriteArgs),
+                         ("spec_kv_read_launch", SpecKVReadArgs), ("spec_attn_launch", SpecAttnArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(struct), ctypes.c_void_p]
         getattr(L, name).restype = ctypes.c_int
     L.spec_status_string.argtypes = [ctypes.c_int]
     L.spec_status_string.restype = ctypes.c_char_p
@@ -238,6 +300,31 @@ def spec_shard_decide_launch(args, stream_ptr):
 
 def spec_shard_draw_launch(args, stream_ptr):
     return int(lib.spec_shard_draw_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_logprobs_workspace_bytes(B, R, V, top):
+    return int(lib.spec_logprobs_workspace_bytes(int(B), int(R), int(V), int(top)))
+
+
+def spec_logprobs_launch(args, stream_ptr):
+    return int(lib.spec_logprobs_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_kv_write_launch(args, stream_ptr):
+    return int(lib.spec_kv_write_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_kv_read_launch(args, stream_ptr):
+    return int(lib.spec_kv_read_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_attn_workspace_bytes(args):
+    """Workspace of an attention from the sizes in its argument block."""
+    return int(lib.spec_attn_workspace_bytes(ctypes.byref(args)))
+
+
+def spec_attn_launch(args, stream_ptr):
+    return int(lib.spec_attn_launch(ctypes.byref(args), stream_ptr))
 
 
 def spec_status_string(status):
@@ -625,3 +712,315 @@ def verify_sharded(target, draft, draft_tokens, temperature, G, seed=0, step=0, 
                      draft_row_index=draft_row_index)
     st.run()
     return st.acc[0].clone(), st.tok.max(dim=0).values, st.acc
+
+
+# ------------------------------------------------- token log probabilities
+class _on:
+    """The device of `tensor` current, and `stream` (or that device's current
+    stream) its current stream: what is allocated here belongs to the stream
+    that the work is enqueued on."""
+
+    def __init__(self, tensor, stream=None):
+        torch = _torch()
+        self.stream = stream if stream is not None else torch.cuda.current_stream(tensor.device)
+        if self.stream.device != tensor.device:
+            raise ValueError("the stream is on another device than the tensors")
+        # already current: nothing to set
+        self.ctx = None
+        if stream is not None or torch.cuda.current_device() != tensor.device.index:
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _same_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on the same GPU")
+
+
+def _want(t, dtype, shape, name):
+    """A contiguous tensor of this type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s" % (name, dtype, list(shape)))
+
+
+def _bytes_of(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+class TokenLogprobs:
+    """logprobs [B, R] and entropy [B, R] float32 (entropy None if not asked
+    for), top_ids [B, R, top] int32, top_logprobs [B, R, top] float32."""
+    __slots__ = ("logprobs", "entropy", "top_ids", "top_logprobs")
+
+    def __init__(self, logprobs, entropy, top_ids, top_logprobs):
+        self.logprobs, self.entropy, self.top_ids, self.top_logprobs = logprobs, entropy, top_ids, top_logprobs
+
+
+def token_logprobs_outputs(B, R, top, device, entropy=True):
+    torch = _torch()
+    return TokenLogprobs(torch.empty(B, R, dtype=torch.float32, device=device),
+                         torch.empty(B, R, dtype=torch.float32, device=device) if entropy else None,
+                         torch.empty(B, R, top, dtype=torch.int32, device=device),
+                         torch.empty(B, R, top, dtype=torch.float32, device=device))
+
+
+def token_logprobs_args(logits, tokens, temperature, out, workspace):
+    """Fill a SpecLogprobsArgs (no copies): logits [B, R, V] with unit column
+    stride (an expanded request dimension shares rows), tokens [B, R] int32,
+    temperature [B] float32 or None, out a TokenLogprobs."""
+    torch = _torch()
+    if logits.dim() != 3 or (logits.stride(2) != 1 and logits.shape[2] > 1):
+        raise ValueError("logits must be [B, R, V] with contiguous rows")
+    B, R, V = logits.shape
+    _same_device(logits, tokens, temperature, out.logprobs, out.entropy, out.top_ids, out.top_logprobs, workspace)
+    _want(tokens, torch.int32, (B, R), "tokens")
+    if temperature is not None:
+        _want(temperature, torch.float32, (B,), "temperature")
+    top = out.top_ids.shape[-1]
+    _want(out.logprobs, torch.float32, (B, R), "logprobs")
+    if out.entropy is not None:
+        _want(out.entropy, torch.float32, (B, R), "entropy")
+    _want(out.top_ids, torch.int32, (B, R, top), "top_ids")
+    _want(out.top_logprobs, torch.float32, (B, R, top), "top_logprobs")
+    a = SpecLogprobsArgs()
+    a.B, a.R, a.V, a.dtype, a.top = B, R, V, _logit_dtype(logits), top
+    a.logits = logits.data_ptr()
+    a.req_stride = logits.stride(0) if B > 1 else 0
+    a.row_stride = logits.stride(1) if R > 1 else V
+    a.tokens = tokens.data_ptr()
+    a.temperature = None if temperature is None else temperature.data_ptr()
+    a.logprobs = out.logprobs.data_ptr()
+    a.entropy = None if out.entropy is None else out.entropy.data_ptr()
+    a.top_ids, a.top_logprobs = out.top_ids.data_ptr(), out.top_logprobs.data_ptr()
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), _bytes_of(workspace)
+    return a
+
+
+def token_logprobs(logits, tokens, temperature=None, top=0, entropy=True, workspace=None, stream=None, out=None):
+    """Log probabilities of tokens [B, R] (int32; -1: no token, its row is not
+    read) under softmax(logits / T), logits [B, R, V]; the entropy of each row
+    and its `top` most likely tokens.  tokens may be the output_tokens of a
+    verification with logits its target.  Enqueued on `stream` or the tensors'
+    device's current stream; returns a TokenLogprobs."""
+    torch = _torch()
+    if logits.dim() != 3 or not logits.is_cuda:
+        raise ValueError("logits must be [B, R, V] on the GPU")
+    B, R, V = logits.shape
+    if not 0 <= top <= SPEC_MAX_TOP:
+        raise ValueError("top must be in 0..%d" % SPEC_MAX_TOP)
+    with _on(logits, stream) as s:
+        if out is None:
+            out = token_logprobs_outputs(B, R, top, logits.device, entropy)
+        if workspace is None:
+            n = spec_logprobs_workspace_bytes(B, R, V, top)
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=logits.device)
+        rc = spec_logprobs_launch(token_logprobs_args(logits, tokens, temperature, out, workspace), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return out
+
+
+# ----------------------------------------------------- 8-bit paged KV cache
+class KVCache:
+    """A paged cache of keys and values in 8 bits: codes k, v (uint8, or
+    float8_e4m3fn) [num_blocks, block_size, heads, head_dim] and scale
+    exponents k_scale, v_scale (uint8, or float8_e8m0fnu) [num_blocks, heads,
+    block_size / scale_tokens]; the value of a code is code * 2^(byte - 127).
+    Blocks may hold their heads outside their tokens (a transposed view); k
+    and v share strides, and so do their scales.  block_size is a power of two
+    from 16 to 1024, scale_tokens one from 1 to 64, head_dim a multiple of 16
+    up to 256."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "block_size", "heads", "head_dim", "scale_tokens",
+                 "device", "args")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or k_scale.dim() != 3:
+            raise ValueError("codes must be [num_blocks, block_size, heads, head_dim], scales [num_blocks, heads, "
+                             "groups]")
+        _same_device(k, v, k_scale, v_scale)
+        if k.element_size() != 1 or v.dtype != k.dtype or k_scale.element_size() != 1 or v_scale.dtype != k_scale.dtype:
+            raise TypeError("codes and scales must be 8-bit tensors, alike for k and v")
+        nb, bs, heads, dim = k.shape
+        groups = k_scale.shape[2]
+        if v.shape != k.shape or v.stride() != k.stride() or v_scale.shape != k_scale.shape or \
+                v_scale.stride() != k_scale.stride() or k_scale.shape[0] != nb or k_scale.shape[1] != heads:
+            raise ValueError("k and v (and their scales) must agree in shape and strides")
+        if k.stride(3) != 1 or (groups > 1 and k_scale.stride(2) != 1) or groups < 1 or bs % groups:
+            raise ValueError("codes must be contiguous along head_dim, scales along their groups, which divide a block")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_blocks, self.block_size, self.heads, self.head_dim = nb, bs, heads, dim
+        self.scale_tokens, self.device = bs // groups, k.device
+        a = SpecKVCache()
+        a.num_blocks, a.block_size, a.scale_tokens, a.heads, a.head_dim = nb, bs, bs // groups, heads, dim
+        a.k_codes, a.v_codes = k.data_ptr(), v.data_ptr()
+        a.block_stride, a.token_stride, a.head_stride = k.stride(0), k.stride(1), k.stride(2)
+        if heads == 1:
+            a.head_stride = max(a.head_stride, dim)
+        a.k_scales, a.v_scales = k_scale.data_ptr(), v_scale.data_ptr()
+        a.scale_block_stride, a.scale_head_stride = k_scale.stride(0), k_scale.stride(1)
+        self.args = a
+
+
+def make_kv_cache(num_blocks, block_size, heads, head_dim, scale_tokens=None, device="cuda"):
+    """A KVCache of zeros; scale_tokens tokens share a scale (default: a whole
+    block, at most 64)."""
+    torch = _torch()
+    st = min(block_size, 64) if scale_tokens is None else scale_tokens
+    if st < 1 or block_size % st:
+        raise ValueError("scale_tokens must divide block_size")
+    codes = [torch.zeros(num_blocks, block_size, heads, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros(num_blocks, heads, block_size // st, dtype=torch.uint8, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def kv_write_args(cache, key, value, slots):
+    """Fill a SpecKVWriteArgs (no copies): key and value [N, heads, head_dim]
+    with unit stride along head_dim, slots [N] int64 (-1: not written)."""
+    torch = _torch()
+    _same_device(cache.k, key, value, slots)
+    N = slots.shape[0]
+    _want(slots, torch.int64, (N,), "slots")
+    for t in (key, value):
+        if t.shape != (N, cache.heads, cache.head_dim) or t.stride(2) != 1:
+            raise ValueError("key and value must be [N, heads, head_dim], contiguous along head_dim")
+    if key.dtype != value.dtype:
+        raise TypeError("key and value must share a dtype")
+    a = SpecKVWriteArgs()
+    a.cache, a.N, a.dtype = cache.args, N, _kv_dtype(key.dtype)
+    a.key, a.value, a.slots = key.data_ptr(), value.data_ptr(), slots.data_ptr()
+    a.k_token_stride, a.k_head_stride = key.stride(0), key.stride(1)
+    a.v_token_stride, a.v_head_stride = value.stride(0), value.stride(1)
+    return a
+
+
+def _kv_dtype(dtype):
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return SPEC_BF16
+    if dtype == torch.float32:
+        return SPEC_F32
+    raise TypeError("keys and values must be bfloat16 or float32, got %s" % dtype)
+
+
+def kv_write(cache, key, value, slots, stream=None):
+    """Quantise keys and values [N, heads, head_dim] into the cache at slots
+    [N] int64 (the slot_mapping of an expansion; -1 is skipped); returns the
+    cache."""
+    with _on(cache.k, stream) as s:
+        rc = spec_kv_write_launch(kv_write_args(cache, key, value, slots), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return cache
+
+
+def kv_read(cache, slots, dtype=None, stream=None, out=None):
+    """Keys and values [N, heads, head_dim] at slots [N] int64, bfloat16 (the
+    default) or float32, zeros where a slot is -1."""
+    torch = _torch()
+    _same_device(cache.k, slots)
+    N = slots.shape[0]
+    _want(slots, torch.int64, (N,), "slots")
+    shape = (N, cache.heads, cache.head_dim)
+    with _on(cache.k, stream) as s:
+        if out is None:
+            dt = torch.bfloat16 if dtype is None else dtype
+            key = torch.empty(shape, dtype=dt, device=cache.device)
+            value = torch.empty(shape, dtype=dt, device=cache.device)
+        else:
+            key, value = out
+            _same_device(cache.k, key, value)
+            dt = key.dtype if dtype is None else dtype
+            _want(key, dt, shape, "key")
+            _want(value, dt, shape, "value")
+        a = SpecKVReadArgs()
+        a.cache, a.N, a.dtype = cache.args, N, _kv_dtype(dt)
+        a.key, a.value, a.slots = key.data_ptr(), value.data_ptr(), slots.data_ptr()
+        rc = spec_kv_read_launch(a, s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return key, value
+
+
+def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse=None, window=0,
+                      sinks=None, workspace=None):
+    """Fill a SpecAttnArgs (no copies): q [N, q_heads, head_dim] bfloat16 with
+    unit stride along head_dim, block_table [B, max_blocks] int32 (row stride
+    free), q_start [B + 1] and ctx_len [B] int32, sinks [q_heads] float32,
+    out [N, q_heads, head_dim] bfloat16, lse [N, q_heads] float32."""
+    torch = _torch()
+    _same_device(cache.k, q, block_table, q_start, ctx_len, sinks, out, lse, workspace)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.stride(2) != 1:
+        raise ValueError("q must be [N, q_heads, head_dim], contiguous along head_dim")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    N, Hq = q.shape[0], q.shape[1]
+    B = ctx_len.shape[0]
+    _want(ctx_len, torch.int32, (B,), "ctx_len")
+    _want(q_start, torch.int32, (B + 1,), "q_start")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be int32 [B, max_blocks] with unit column stride")
+    if sinks is not None:
+        _want(sinks, torch.float32, (Hq,), "sinks")
+    _want(out, torch.bfloat16, (N, Hq, cache.head_dim), "out")
+    if lse is not None:
+        _want(lse, torch.float32, (N, Hq), "lse")
+    a = SpecAttnArgs()
+    a.cache, a.B, a.N, a.q_heads = cache.args, B, N, Hq
+    a.max_q, a.max_ctx, a.window, a.dtype, a.scale = int(max_q), int(max_ctx), int(window), SPEC_BF16, float(scale)
+    a.q, a.q_token_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+    a.q_start, a.ctx_len = q_start.data_ptr(), ctx_len.data_ptr()
+    a.max_blocks = block_table.shape[1]
+    a.block_table = block_table.data_ptr()
+    a.bt_row_stride = block_table.stride(0) if B > 1 else a.max_blocks
+    a.sinks = None if sinks is None else sinks.data_ptr()
+    a.out = out.data_ptr()
+    a.lse = None if lse is None else lse.data_ptr()
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), _bytes_of(workspace)
+    return a
+
+
+def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, scale=None, window=0, sinks=None,
+                 return_lse=False, workspace=None, stream=None, out=None):
+    """Attention of the new tokens q [N, q_heads, head_dim] of B requests
+    (request b: rows q_start[b]..q_start[b+1] - 1) over their cached contexts
+    of ctx_len[b] tokens, the new ones included and last.  max_q and max_ctx
+    bound the new tokens and the context of a request (max_ctx defaults to
+    what the block table holds); scale defaults to head_dim ** -0.5; window >
+    0 sees only the last `window` positions; sinks [q_heads] float32 take part
+    in the softmax without a value.  Returns (out, lse or None)."""
+    torch = _torch()
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [N, q_heads, head_dim] and block_table [B, max_blocks]")
+    if max_ctx is None:
+        max_ctx = min(block_table.shape[1] * cache.block_size, 1 << 30)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    with _on(cache.k, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device) if return_lse else None
+        a = kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse, window, sinks,
+                              workspace)
+        if workspace is None:
+            n = spec_attn_workspace_bytes(a)
+            if n:
+                workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+                a.workspace, a.workspace_bytes = workspace.data_ptr(), n
+        rc = spec_attn_launch(a, s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return out, lse

@@ -2,11 +2,13 @@
 // kernel launches.  Every check here runs before anything is enqueued, and no
 // launch entry point synchronises the stream or allocates memory (the host
 // query spec_workspace_error waits for the stream it is given).
+#include <float.h>
 #include <stdint.h>
 
 #include <mutex>
 
 #include "spec_verify.h"
+#include "ops_kernels.hpp"
 #include "verify_kernels.hpp"
 #include "verify_layout.hpp"
 
@@ -21,6 +23,7 @@ static __device__ __align__(256) unsigned char scratch[SPEC_NOALLOC_SCRATCH_BYTE
 namespace {
 
 constexpr int64_t kExpandRowsPerWG = 4;
+constexpr int64_t kThreads = 256;  // per workgroup of the statistics, cache and attention kernels
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -228,6 +231,156 @@ bool shard_vec(const spec_shard_args* a) {
   return aligned16(a->target_logits) && aligned16(a->draft_logits) && (a->t_row_stride * es) % 16 == 0 &&
          (a->t_req_stride * es) % 16 == 0 && (a->d_row_stride * es) % 16 == 0 &&
          (a->draft_row_index || (a->d_req_stride * es) % 16 == 0);
+}
+
+// ------------------------------------------- log probabilities, paged cache
+size_t logprobs_ws_bytes(int32_t B, int32_t R, int32_t V, int32_t top) {
+  const size_t segs = (size_t)B * R * (((size_t)V + kSeg - 1) / kSeg);
+  return align256(segs * sizeof(LpRecord)) + (top > 0 ? align256(segs * kLpCells * sizeof(float)) : 0);
+}
+
+bool logprobs_shape_ok(int32_t B, int32_t R, int32_t V, int32_t top) {
+  if (B < 0 || R < 0 || V < 1 || V > SPEC_MAX_V || top < 0 || top > SPEC_MAX_TOP) return false;
+  const int64_t rows = (int64_t)B * R, nseg = ((int64_t)V + kSeg - 1) / kSeg;
+  const int64_t C = (nseg + kLpChunkSegs - 1) / kLpChunkSegs;
+  return rows <= INT32_MAX && rows * C <= INT32_MAX && fits_dispatch(rows * C, kThreads) && fits_dispatch(rows, 64);
+}
+
+int logprobs_check(const spec_logprobs_args* a) {
+  if (!a) return SPEC_EINVAL;
+  if (!logprobs_shape_ok(a->B, a->R, a->V, a->top)) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (a->B == 0 || a->R == 0) return SPEC_OK;
+  if (!a->logits || !a->tokens || !a->logprobs || !a->workspace) return SPEC_EINVAL;
+  if (a->top > 0 && (!a->top_ids || !a->top_logprobs)) return SPEC_EINVAL;
+  if (a->row_stride < a->V) return SPEC_EINVAL;
+  if (a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;
+  if (!aligned16(a->workspace)) return SPEC_EALIGN;
+  if (a->workspace_bytes < logprobs_ws_bytes(a->B, a->R, a->V, a->top)) return SPEC_EWORKSPACE;
+  return SPEC_OK;
+}
+
+bool power_of_two(int32_t x, int32_t lo, int32_t hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
+
+int log2_of(int32_t x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+bool cache_shape_ok(const spec_kv_cache& c) {
+  return c.num_blocks >= 1 && power_of_two(c.block_size, 16, 1024) && power_of_two(c.scale_tokens, 1, 64) &&
+         c.scale_tokens <= c.block_size && c.heads >= 1 && c.heads <= 1024 && c.head_dim >= 16 && c.head_dim <= 256 &&
+         c.head_dim % 16 == 0;
+}
+
+int cache_check(const spec_kv_cache& c) {
+  if (!cache_shape_ok(c)) return SPEC_EINVAL;
+  if (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales) return SPEC_EINVAL;
+  if (!aligned16(c.k_codes) || !aligned16(c.v_codes)) return SPEC_EALIGN;
+  if (c.block_stride % 16 || c.token_stride % 16 || c.head_stride % 16) return SPEC_EALIGN;
+  if (c.token_stride < c.head_dim || c.head_stride < c.head_dim) return SPEC_EINVAL;
+  // (2^42 bytes between tokens or heads is beyond any card's memory, and the
+  // sums below stay far from 2^63)
+  constexpr int64_t kMost = (int64_t)1 << 42;
+  if (c.token_stride > kMost || c.head_stride > kMost) return SPEC_EINVAL;
+  const int64_t tokens = (int64_t)(c.block_size - 1) * c.token_stride, heads = (int64_t)(c.heads - 1) * c.head_stride;
+  // heads inside a token or tokens inside a head, and a block's extent apart
+  const bool heads_in = c.token_stride >= heads + c.head_dim, tokens_in = c.head_stride >= tokens + c.head_dim;
+  if (!(heads_in || tokens_in || c.heads == 1)) return SPEC_EINVAL;
+  if (c.num_blocks > 1 && c.block_stride < tokens + heads + c.head_dim) return SPEC_EINVAL;
+  if (c.scale_head_stride < c.block_size / c.scale_tokens || c.scale_head_stride > kMost) return SPEC_EINVAL;
+  if (c.scale_block_stride < c.heads * c.scale_head_stride && c.num_blocks > 1) return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
+CacheView cache_view(const spec_kv_cache& c) {
+  CacheView v;
+  v.num_blocks = c.num_blocks;
+  v.heads = c.heads;
+  v.dim = c.head_dim;
+  v.bs_shift = log2_of(c.block_size);
+  v.st_shift = log2_of(c.scale_tokens);
+  v.codes[0] = c.k_codes;
+  v.codes[1] = c.v_codes;
+  v.scales[0] = c.k_scales;
+  v.scales[1] = c.v_scales;
+  v.block = c.block_stride;
+  v.token = c.token_stride;
+  v.head = c.head_stride;
+  v.sblock = c.scale_block_stride;
+  v.shead = c.scale_head_stride;
+  return v;
+}
+
+int kv_write_check(const spec_kv_write_args* a) {
+  if (!a || a->N < 0) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  const int rc = cache_check(a->cache);
+  if (rc != SPEC_OK) return rc;
+  if (a->N == 0) return SPEC_OK;
+  if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
+  if (a->k_token_stride < 0 || a->k_head_stride < 0 || a->v_token_stride < 0 || a->v_head_stride < 0)
+    return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
+int kv_read_check(const spec_kv_read_args* a) {
+  if (!a || a->N < 0) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  const int rc = cache_check(a->cache);
+  if (rc != SPEC_OK) return rc;
+  if (a->N == 0) return SPEC_OK;
+  if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
+bool attn_sizes_ok(const spec_attn_args* a) {
+  if (a->B < 0 || a->N < 0 || a->max_q < 1 || a->max_q > (1 << 24) || a->max_ctx < 0 || a->max_ctx > (1 << 30) ||
+      a->window < 0)
+    return false;
+  const spec_kv_cache& c = a->cache;
+  if (c.heads < 1 || c.heads > 1024 || c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16) return false;
+  if (a->q_heads < c.heads || a->q_heads % c.heads || a->q_heads / c.heads > 64) return false;
+  return true;
+}
+
+AttnPlan attn_plan(const spec_attn_args* a) {
+  return plan_attn(a->B, a->q_heads / a->cache.heads, a->cache.heads, a->cache.head_dim, a->max_q, a->max_ctx,
+                   a->window);
+}
+
+size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
+  if (p.nsplit <= 1 || a->B == 0) return 0;
+  const size_t parts = (size_t)a->N * a->q_heads * p.nsplit;
+  return align256(parts * a->cache.head_dim * sizeof(float)) + align256(parts * sizeof(float2));
+}
+
+int attn_check(const spec_attn_args* a, AttnPlan& plan) {
+  if (!a || !attn_sizes_ok(a)) return SPEC_EINVAL;
+  if (a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  const int rc = cache_check(a->cache);
+  if (rc != SPEC_OK) return rc;
+  if (!(a->scale >= -FLT_MAX && a->scale <= FLT_MAX)) return SPEC_EINVAL;
+  if (a->max_blocks < 0 || a->bt_row_stride < a->max_blocks) return SPEC_EINVAL;
+  if (a->B == 0 || a->N == 0) return SPEC_OK;
+  if (!a->q || !a->q_start || !a->ctx_len || !a->out) return SPEC_EINVAL;
+  if (a->max_blocks > 0 && !a->block_table) return SPEC_EINVAL;
+  if (a->q_token_stride < 0 || a->q_head_stride < 0) return SPEC_EINVAL;
+  if (!aligned16(a->out)) return SPEC_EALIGN;
+  plan = attn_plan(a);
+  const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;  // <= 2^31 * 2^10 * 2^26 checked in steps
+  if ((int64_t)a->B * a->cache.heads > INT32_MAX || grid / plan.nrb != (int64_t)a->B * a->cache.heads ||
+      grid > INT32_MAX || grid * plan.nsplit > INT32_MAX || !fits_dispatch(grid * plan.nsplit, kThreads))
+    return SPEC_EINVAL;
+  if (!fits_dispatch(((int64_t)a->N * a->q_heads + 3) / 4, kThreads)) return SPEC_EINVAL;
+  const size_t need = attn_ws_bytes(a, plan);
+  if (need > 0) {
+    if (!a->workspace) return SPEC_EINVAL;
+    if (!aligned16(a->workspace)) return SPEC_EALIGN;
+    if (a->workspace_bytes < need) return SPEC_EWORKSPACE;
+  }
+  return SPEC_OK;
 }
 
 }  // namespace
@@ -520,6 +673,113 @@ int spec_verify_expand_launch(const spec_verify_args* v, const spec_expand_args*
   if (!verify_grids_fit(P.B, P.K, P.C1, P.nseg, P.dyn != 0, P.dstats != nullptr, (int64_t)P.B * P.ex_G))
     return SPEC_EINVAL;
   return verify_enqueue(P, v, vec, stream);
+}
+
+size_t spec_logprobs_workspace_bytes(int32_t B, int32_t R, int32_t V, int32_t top) {
+  return logprobs_shape_ok(B, R, V, top) ? logprobs_ws_bytes(B, R, V, top) : 0;
+}
+
+int spec_logprobs_launch(const spec_logprobs_args* a, hipStream_t stream) {
+  const int rc = logprobs_check(a);
+  if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
+  const int es = a->dtype == SPEC_BF16 ? 2 : 4;
+  LogprobsParams P;
+  P.B = a->B;
+  P.R = a->R;
+  P.V = a->V;
+  P.nseg = (int32_t)(((int64_t)a->V + kSeg - 1) / kSeg);
+  P.C = (P.nseg + kLpChunkSegs - 1) / kLpChunkSegs;
+  P.top = a->top;
+  P.logits = static_cast<const char*>(a->logits);
+  P.req = a->req_stride;
+  P.row = a->row_stride;
+  P.tokens = a->tokens;
+  P.temperature = a->temperature;
+  P.logprobs = a->logprobs;
+  P.entropy = a->entropy;
+  P.top_ids = a->top_ids;
+  P.top_lp = a->top_logprobs;
+  char* ws = static_cast<char*>(a->workspace);
+  P.rec = reinterpret_cast<LpRecord*>(ws);
+  P.cells = reinterpret_cast<float*>(ws + align256((size_t)a->B * a->R * P.nseg * sizeof(LpRecord)));
+  const bool vec = aligned16(a->logits) && (a->row_stride * es) % 16 == 0 && (a->req_stride * es) % 16 == 0;
+  return launch_logprobs(P, a->dtype, vec, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+int spec_kv_write_launch(const spec_kv_write_args* a, hipStream_t stream) {
+  const int rc = kv_write_check(a);
+  if (rc != SPEC_OK || a->N == 0) return rc;
+  const int es = a->dtype == SPEC_BF16 ? 2 : 4;
+  KvWriteParams P;
+  P.c = cache_view(a->cache);
+  P.N = a->N;
+  // few entries: few to a workgroup, so that they spread over the card
+  P.chunk = a->N >= 8192 ? 64 : a->N >= 1024 ? 16 : 4;
+  P.src[0] = static_cast<const char*>(a->key);
+  P.src[1] = static_cast<const char*>(a->value);
+  P.tok[0] = a->k_token_stride;
+  P.hd[0] = a->k_head_stride;
+  P.tok[1] = a->v_token_stride;
+  P.hd[1] = a->v_head_stride;
+  P.slots = a->slots;
+  const bool vec = aligned16(a->key) && aligned16(a->value) && (a->k_token_stride * es) % 16 == 0 &&
+                   (a->k_head_stride * es) % 16 == 0 && (a->v_token_stride * es) % 16 == 0 &&
+                   (a->v_head_stride * es) % 16 == 0;
+  return launch_kv_write(P, a->dtype, vec, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+int spec_kv_read_launch(const spec_kv_read_args* a, hipStream_t stream) {
+  const int rc = kv_read_check(a);
+  if (rc != SPEC_OK || a->N == 0) return rc;
+  KvReadParams P;
+  P.c = cache_view(a->cache);
+  P.N = a->N;
+  P.dst[0] = static_cast<char*>(a->key);
+  P.dst[1] = static_cast<char*>(a->value);
+  P.slots = a->slots;
+  return launch_kv_read(P, a->dtype, aligned16(a->key) && aligned16(a->value), stream) == hipSuccess ? SPEC_OK
+                                                                                                     : SPEC_ELAUNCH;
+}
+
+size_t spec_attn_workspace_bytes(const spec_attn_args* a) {
+  if (!a || !attn_sizes_ok(a)) return 0;
+  return attn_ws_bytes(a, attn_plan(a));
+}
+
+int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
+  AttnPlan plan;
+  const int rc = attn_check(a, plan);
+  if (rc != SPEC_OK || a->B == 0 || a->N == 0) return rc;
+  AttnParams P;
+  P.c = cache_view(a->cache);
+  P.B = a->B;
+  P.N = a->N;
+  P.Hq = a->q_heads;
+  P.G = a->q_heads / a->cache.heads;
+  P.max_q = a->max_q;
+  P.max_ctx = a->max_ctx;
+  P.window = a->window;
+  P.max_blocks = a->max_blocks;
+  P.nrb = plan.nrb;
+  P.nsplit = plan.nsplit;
+  P.split_keys = plan.split_keys;
+  P.scale2 = a->scale * 1.44269504088896341f;
+  P.q = static_cast<const char*>(a->q);
+  P.q_tok = a->q_token_stride;
+  P.q_head = a->q_head_stride;
+  P.q_start = a->q_start;
+  P.ctx_len = a->ctx_len;
+  P.bt = a->block_table;
+  P.bt_stride = a->bt_row_stride;
+  P.sinks = a->sinks;
+  P.out = static_cast<uint16_t*>(a->out);
+  P.lse = a->lse;
+  P.po = static_cast<float*>(a->workspace);
+  P.pm = reinterpret_cast<float2*>(
+      static_cast<char*>(a->workspace) +
+      align256((size_t)a->N * a->q_heads * plan.nsplit * a->cache.head_dim * sizeof(float)));
+  P.qvec = aligned16(a->q) && a->q_token_stride % 8 == 0 && a->q_head_stride % 8 == 0;
+  return launch_attn(P, plan, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }
 
 int spec_workspace_error(const void* workspace, hipStream_t stream) {

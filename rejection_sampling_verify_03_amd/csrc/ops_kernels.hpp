@@ -1,0 +1,98 @@
+// ops_kernels.hpp -- parameter blocks and launchers of the operators around
+// a verification step: token log probabilities, the 8-bit paged cache and
+// the attention over it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+#include "verify_layout.hpp"
+
+namespace specv {
+
+// ------------------------------------------------------ log probabilities --
+struct LpRecord {  // one 4096-logit segment of a row
+  double s;        // sum of 2^((x - m) * log2(e) / T)
+  double w;        // sum of the same times its exponent
+  float m;         // largest logit
+  int32_t pad;
+};
+static_assert(sizeof(LpRecord) == 24, "LpRecord layout");
+
+constexpr int kLpCells = 64;     // cells of 64 consecutive logits in a segment
+constexpr int kLpChunkSegs = 8;  // segments per workgroup of the statistics pass
+
+struct LogprobsParams {
+  int32_t B, R, V, nseg, C, top;  // C: chunks of kLpChunkSegs segments per row
+  const char* logits;
+  int64_t req, row;
+  const int32_t* tokens;
+  const float* temperature;  // or null
+  float* logprobs;
+  float* entropy;  // or null
+  int32_t* top_ids;
+  float* top_lp;
+  LpRecord* rec;   // [B * R, nseg]
+  float* cells;    // [B * R, nseg, kLpCells] largest logit of each cell (top > 0)
+};
+
+hipError_t launch_logprobs(const LogprobsParams& P, int dtype, bool vec, hipStream_t stream);
+
+// ------------------------------------------------------------ paged cache --
+struct CacheView {
+  int32_t num_blocks, heads, dim;
+  int32_t bs_shift, st_shift;  // log2 of block_size and scale_tokens
+  uint8_t* codes[2];           // keys, values
+  uint8_t* scales[2];
+  int64_t block, token, head;  // strides of the codes, bytes
+  int64_t sblock, shead;       // strides of the scales, bytes
+};
+
+struct KvWriteParams {
+  CacheView c;
+  int32_t N, chunk;  // entries per workgroup
+  const char* src[2];
+  int64_t tok[2], hd[2];  // strides in elements
+  const int64_t* slots;
+};
+
+struct KvReadParams {
+  CacheView c;
+  int32_t N;
+  char* dst[2];
+  const int64_t* slots;
+};
+
+hipError_t launch_kv_write(const KvWriteParams& P, int dtype, bool vec, hipStream_t stream);
+hipError_t launch_kv_read(const KvReadParams& P, int dtype, bool vec, hipStream_t stream);
+
+// -------------------------------------------------------------- attention --
+struct AttnParams {
+  CacheView c;
+  int32_t B, N, Hq, G;  // G: query heads per KV head
+  int32_t max_q, max_ctx, window, max_blocks;
+  int32_t nrb, nsplit, split_keys;  // row blocks per (request, KV head), key splits, keys per split
+  float scale2;                     // scale * log2(e)
+  const char* q;
+  int64_t q_tok, q_head;  // elements
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* bt;
+  int64_t bt_stride;
+  const float* sinks;
+  uint16_t* out;
+  float* lse;
+  float* po;   // [N, Hq, nsplit, dim] partial sums (nsplit > 1)
+  float2* pm;  // [N, Hq, nsplit] their reference exponents and sums of weights
+  int32_t qvec;
+};
+
+struct AttnPlan {
+  int32_t rt, nrb, nsplit, split_keys;
+};
+// How the rows of a (request, KV head) and its keys are cut into workgroups.
+AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window);
+hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream);
+
+}  // namespace specv

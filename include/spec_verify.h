@@ -548,7 +548,7 @@ typedef struct {
   uint8_t* k_codes;            /* device, 16-byte aligned */
   uint8_t* v_codes;            /* device, 16-byte aligned, the strides of k_codes */
   int64_t block_stride;        /* bytes, multiples of 16; tokens and heads of a block in either */
-  int64_t token_stride;        /* order, without overlap */
+  int64_t token_stride;        /* order, without overlap; token_stride at most 2^26 */
   int64_t head_stride;
   uint8_t* k_scales;           /* device */
   uint8_t* v_scales;           /* device, the strides of k_scales */

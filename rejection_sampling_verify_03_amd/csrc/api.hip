@@ -280,10 +280,10 @@ int cache_check(const spec_kv_cache& c) {
   if (!aligned16(c.k_codes) || !aligned16(c.v_codes)) return SPEC_EALIGN;
   if (c.block_stride % 16 || c.token_stride % 16 || c.head_stride % 16) return SPEC_EALIGN;
   if (c.token_stride < c.head_dim || c.head_stride < c.head_dim) return SPEC_EINVAL;
-  // (2^42 bytes between tokens or heads is beyond any card's memory, and the
-  // sums below stay far from 2^63)
+  // 16 tokens within 32 bits for the kernels' offsets; heads within what keeps
+  // the sums below far from 2^63
   constexpr int64_t kMost = (int64_t)1 << 42;
-  if (c.token_stride > kMost || c.head_stride > kMost) return SPEC_EINVAL;
+  if (c.token_stride > ((int64_t)1 << 26) || c.head_stride > kMost) return SPEC_EINVAL;
   const int64_t tokens = (int64_t)(c.block_size - 1) * c.token_stride, heads = (int64_t)(c.heads - 1) * c.head_stride;
   // heads inside a token or tokens inside a head, and a block's extent apart
   const bool heads_in = c.token_stride >= heads + c.head_dim, tokens_in = c.head_stride >= tokens + c.head_dim;
@@ -351,8 +351,8 @@ AttnPlan attn_plan(const spec_attn_args* a) {
 }
 
 size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
-  if (p.nsplit <= 1 || a->B == 0) return 0;
-  const size_t parts = (size_t)a->N * a->q_heads * p.nsplit;
+  if (p.chunks == 0 || a->B == 0) return 0;
+  const size_t parts = (size_t)p.chunks * 2 * a->cache.heads * 16 * p.rt;
   return align256(parts * a->cache.head_dim * sizeof(float)) + align256(parts * sizeof(float2));
 }
 
@@ -371,9 +371,9 @@ int attn_check(const spec_attn_args* a, AttnPlan& plan) {
   plan = attn_plan(a);
   const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;  // <= 2^31 * 2^10 * 2^26 checked in steps
   if ((int64_t)a->B * a->cache.heads > INT32_MAX || grid / plan.nrb != (int64_t)a->B * a->cache.heads ||
-      grid > INT32_MAX || grid * plan.nsplit > INT32_MAX || !fits_dispatch(grid * plan.nsplit, kThreads))
+      grid > INT32_MAX || !fits_dispatch((plan.groups + 7) / 8 * 8 * plan.items, kThreads) ||
+      (plan.chunks > 0 && !fits_dispatch(grid, kThreads)))
     return SPEC_EINVAL;
-  if (!fits_dispatch(((int64_t)a->N * a->q_heads + 3) / 4, kThreads)) return SPEC_EINVAL;
   const size_t need = attn_ws_bytes(a, plan);
   if (need > 0) {
     if (!a->workspace) return SPEC_EINVAL;
@@ -756,14 +756,19 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.N = a->N;
   P.Hq = a->q_heads;
   P.G = a->q_heads / a->cache.heads;
+  P.g_inv = 65535u / (uint32_t)P.G + 1u;
   P.max_q = a->max_q;
   P.max_ctx = a->max_ctx;
   P.window = a->window;
   P.max_blocks = a->max_blocks;
   P.nrb = plan.nrb;
-  P.nsplit = plan.nsplit;
-  P.split_keys = plan.split_keys;
-  P.scale2 = a->scale * 1.44269504088896341f;
+  P.chunks = plan.chunks;
+  P.items = (int32_t)plan.items;
+  P.groups = (int32_t)plan.groups;
+  P.q_flip = a->scale < 0.f ? 0x80008000u : 0u;
+  P.scale2 = (a->scale < 0.f ? -a->scale : a->scale) * 1.44269504088896341f;
+  P.q_keep = P.scale2 > 0.f ? ~0u : 0u;
+  if (!(P.scale2 > 0.f)) P.scale2 = 1.f;
   P.q = static_cast<const char*>(a->q);
   P.q_tok = a->q_token_stride;
   P.q_head = a->q_head_stride;
@@ -775,9 +780,11 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.out = static_cast<uint16_t*>(a->out);
   P.lse = a->lse;
   P.po = static_cast<float*>(a->workspace);
-  P.pm = reinterpret_cast<float2*>(
-      static_cast<char*>(a->workspace) +
-      align256((size_t)a->N * a->q_heads * plan.nsplit * a->cache.head_dim * sizeof(float)));
+  P.pm = nullptr;
+  if (plan.chunks > 0)
+    P.pm = reinterpret_cast<float2*>(
+        static_cast<char*>(a->workspace) +
+        align256((size_t)plan.chunks * 2 * a->cache.heads * 16 * plan.rt * a->cache.head_dim * sizeof(float)));
   P.qvec = aligned16(a->q) && a->q_token_stride % 8 == 0 && a->q_head_stride % 8 == 0;
   return launch_attn(P, plan, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }

@@ -11,7 +11,10 @@
 // range of keys, each of its four waves every fourth tile of 32 keys, on its
 // own: keys and values go from memory to the matrix units through registers
 // alone, no barrier stands in the loop, and the waves' sums are joined once
-// at the end.  Splits of the key range are joined by a second kernel.
+// at the end.  Where there are few blocks with long contexts, the tiles of
+// all blocks, end to end, are cut into equal runs, one to each workgroup that
+// the card holds at once, whatever the lengths of the contexts; a second
+// kernel joins the blocks that several runs hold.
 //
 // Both products run on v_mfma_f32_16x16x32_bf16 in the transposed order:
 //   S^T (keys x rows) = K Q^T,   O^T (dims x rows) += V^T P^T,
@@ -55,85 +58,82 @@ __device__ __forceinline__ float lane_xor32(float x) {
   return __int_as_float(i);
 }
 
-// The keys that a block of rows sees, [kbeg, kend) with kbeg brought down to
-// a whole tile, and the positions of its first and last token.
-struct KeyRange {
-  int lo, hi;      // tile-aligned first key, end
-  int p_lo, p_hi;  // positions of the block's first and last token
-  bool bad;        // the request's data cannot be used
-};
-__device__ __forceinline__ KeyRange key_range(const AttnParams& P, int n, int ctx, int tok_lo, int tok_hi) {
-  KeyRange r;
-  const int64_t cap = min((int64_t)P.max_ctx, (int64_t)P.max_blocks << P.c.bs_shift);
-  r.bad = ctx < 0 || ctx > cap || n > P.max_q;
-  r.p_lo = ctx - n + tok_lo;
-  r.p_hi = ctx - n + tok_hi;
-  const int beg = P.window > 0 ? max(0, r.p_lo - P.window + 1) : 0;
-  r.lo = beg & ~(kTileKeys - 1);
-  r.hi = max(r.p_hi + 1, r.lo);
-  return r;
+// The kernels' parameters where the launch put them.  Values that only the
+// start and the end of a unit need are read from there again (scalar loads of
+// a cached line): kept in scalar registers through the loop over the keys they
+// would not fit, and spill into vector registers.
+typedef const AttnParams __attribute__((address_space(4)))* Params;
+__device__ __forceinline__ Params params_again() {
+  Params p = (Params)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
 }
 
-template <int DP>
-struct TileRegs {
-  u32x4 k[2][DP / 64];      // subtile u: key l % 16, dims [g DP/4, (g+1) DP/4)
-  uint32_t v[8][DP / 64];   // slot j's key, dims [c DP/16, (c+1) DP/16), c = l % 16
-  uint32_t ks[2];           // scale bytes of the keys' groups
-  uint32_t vs[8];           // scale bytes of the values' groups (two used if !FINE)
-  uint32_t ok;              // bit u: subtile u's block exists
+// A unit of work: a block of 16 * RT rows of one request, for one KV head.
+// Unit v is block v % nrb of request v / nrb; row k of it is token
+// t0 + (h0 + k) / G of the request, head (h0 + k) % G of the group.
+struct Unit {
+  int b, q0, n, ctx;
+  int t0, h0, rows;
+  int lo, hi;      // the keys that its rows see lie in [lo, hi), lo a whole tile
+  int p_lo, p_hi;  // positions of its first and last token
+  int tiles;       // key tiles; 1 for a unit that only writes (nothing seen, or bad), 0 for no rows
+  bool bad;        // the request's data cannot be used: its first unit writes NaN to all its rows
 };
 
-// FINE: scale_tokens < 4, so that the four keys of a lane differ in scale.
-template <int DP, bool FINE>
-__device__ __forceinline__ void load_tile(const AttnParams& P, const int32_t* bt, int key0, int head, int lane,
-                                          TileRegs<DP>& t) {
-  const CacheView& c = P.c;
-  const int r = lane & 15, g = lane >> 4;
-  const int in_mask = (1 << c.bs_shift) - 1;
-  t.ok = 0;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int k0 = key0 + 16 * u;
-    const int lb = k0 >> c.bs_shift;
-    int phys = lb < P.max_blocks ? bt[lb] : -1;
-    if (phys >= 0 && phys < c.num_blocks)
-      t.ok |= 1u << u;
-    else
-      phys = 0;
-    const int in = k0 & in_mask;
-    const uint8_t* kb = c.codes[0] + (int64_t)phys * c.block + (int64_t)head * c.head + (int64_t)in * c.token;
-    const uint8_t* vb = c.codes[1] + (int64_t)phys * c.block + (int64_t)head * c.head + (int64_t)in * c.token;
-    const int64_t so = (int64_t)phys * c.sblock + (int64_t)head * c.shead;
-    const uint8_t* ksb = c.scales[0] + so;
-    const uint8_t* vsb = c.scales[1] + so;
-    t.ks[u] = ksb[(in + r) >> c.st_shift];
-#pragma unroll
-    for (int w = 0; w < DP / 64; ++w) {
-      const int d = g * (DP / 4) + w * 16;
-      t.k[u][w] = d < c.dim ? *reinterpret_cast<const u32x4*>(kb + (int64_t)r * c.token + d) : u32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int key = 4 * g + j;
-      const uint8_t* p = vb + (int64_t)key * c.token;
-      const int d = r * (DP / 16);
-      if constexpr (DP == 64) {
-        t.v[4 * u + j][0] = d < c.dim ? *reinterpret_cast<const uint32_t*>(p + d) : 0u;
-      } else if constexpr (DP == 128) {
-        const u32x2 w = d < c.dim ? *reinterpret_cast<const u32x2*>(p + d) : u32x2{0, 0};
-        t.v[4 * u + j][0] = w.x;
-        t.v[4 * u + j][1] = w.y;
-      } else {
-        const u32x4 w = d < c.dim ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{0, 0, 0, 0};
-        t.v[4 * u + j][0] = w.x;
-        t.v[4 * u + j][1] = w.y;
-        t.v[4 * u + j][2] = w.z;
-        t.v[4 * u + j][3] = w.w;
-      }
-      if constexpr (FINE) t.vs[4 * u + j] = vsb[(in + key) >> c.st_shift];
-    }
-    if constexpr (!FINE) t.vs[u] = vsb[(in + 4 * g) >> c.st_shift];
+// x / G for the few rows of a block: a product and a shift, exact while
+// x < 2^16 / G (x < 16 * RT + G here).
+__device__ __forceinline__ int div_group(Params P, int x) { return (int)(((uint32_t)x * P->g_inv) >> 16); }
+
+__device__ __forceinline__ Unit unit_of(Params P, int v, int block_rows) {
+  Unit u;
+  u.b = v / P->nrb;
+  const int rb = v - u.b * P->nrb;
+  u.q0 = P->q_start[u.b];
+  const int q1 = P->q_start[u.b + 1];
+  u.ctx = P->ctx_len[u.b];
+  u.n = q1 - u.q0;
+  u.tiles = 0;
+  u.t0 = u.h0 = u.rows = u.lo = u.hi = u.p_lo = u.p_hi = 0;
+  u.bad = false;
+  if (u.q0 < 0 || q1 > P->N || q1 <= u.q0) return u;
+  const int64_t cap = min((int64_t)P->max_ctx, (int64_t)P->max_blocks << P->c.bs_shift);
+  u.bad = u.ctx < 0 || u.ctx > cap || u.n > P->max_q;
+  if (u.bad) {
+    u.tiles = rb == 0;
+    return u;
   }
+  const int rows = u.n * P->G, m0 = rb * block_rows;  // at most 2^30 (max_q <= 2^24, G <= 64)
+  if (m0 >= rows) return u;
+  u.rows = min(rows - m0, block_rows);
+  u.t0 = m0 / P->G;
+  u.h0 = m0 - u.t0 * P->G;
+  u.p_lo = u.ctx - u.n + u.t0;
+  u.p_hi = u.p_lo + div_group(P, u.h0 + u.rows - 1);
+  u.lo = (P->window > 0 ? max(0, u.p_lo - P->window + 1) : 0) & ~(kTileKeys - 1);
+  u.hi = max(u.p_hi + 1, u.lo);
+  u.tiles = max(1, (u.hi - u.lo + kTileKeys - 1) / kTileKeys);
+  return u;
+}
+
+// A value that is the same in every lane, held in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  return ((int64_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x);
+}
+
+// The tiles of all units in front of unit v0 (or of all, v0 = their number).
+__device__ __forceinline__ int64_t tiles_before(Params P, int v0, int block_rows, int lane) {
+  double t = 0.0;
+  for (int v = lane; v < v0; v += 64) t += (double)unit_of(P, v, block_rows).tiles;
+  return uniform64((int64_t)wave_total_d(t));
+}
+
+// Tiles to a chunk: all units' tiles, end to end, are cut into P->chunks equal
+// runs, none shorter than kMinChunk.
+constexpr int kMinChunk = 16;
+__device__ __forceinline__ int64_t chunk_tiles(Params P, int64_t total) {
+  return max((total + P->chunks - 1) / P->chunks, (int64_t)kMinChunk);
 }
 
 __device__ __forceinline__ bf16x8 pack8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -159,81 +159,145 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Where a block's rows stop being computed here and go to memory.
+// The largest of a lane's eight scores, three to an instruction.
+__device__ __forceinline__ float max_of(const f32x4 (&s)[2]) {
+  const float a = fmaxf(fmaxf(s[0][0], s[0][1]), s[0][2]), b = fmaxf(fmaxf(s[0][3], s[1][0]), s[1][1]);
+  return fmaxf(fmaxf(fmaxf(s[1][2], s[1][3]), a), b);
+}
+
+// The lowest n bits, n clamped to 0..32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// The keys of a tile that a row sees, a bit each: p is the row's position
+// behind the tile's first key, ok the subtiles whose blocks exist.
+__device__ __forceinline__ uint32_t seen_keys(int p, int window, uint32_t ok) {
+  const uint32_t gone = window == 0 ? 0u : low_bits(p - window + 1);
+  return low_bits(p + 1) & ~gone & ((ok & 1u) * 0xffffu | (ok >> 1) * 0xffff0000u);
+}
+
+// The place of row k of a run's partial sums: run j has two, for the unit that
+// it begins with and for a later one (its last).
+__device__ __forceinline__ int64_t part_row(Params P, int j, bool later, int head, int block_rows, int k) {
+  return (((int64_t)j * 2 + later) * P->c.heads + head) * block_rows + k;
+}
+
+// FINE: scale_tokens < 16, a scale for each key; otherwise one for each 16.
 template <int DP, int RT, bool FINE>
-__global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
+__global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   constexpr int C = DP / 32;   // steps of the sum over dims
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
+  constexpr int W = DP / 64;   // 16-byte loads of a lane's share of a key
+  // tiles in flight: two where the registers hold them
+  constexpr int NB = 1;
+  constexpr int kWindow = 32;  // tiles whose pages a wave holds at a time, a subtile to a lane
   __shared__ __align__(16) char s_mem[(RT * C * 64 * 16 > kWaves * 16 * DP * 4) ? RT * C * 64 * 16
                                                                                 : kWaves * 16 * DP * 4];
   __shared__ float s_ref[kWaves][RT * 16], s_sum[kWaves][RT * 16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  int x = blockIdx.x;
-  const int rb = x % P.nrb;
-  x /= P.nrb;
-  const int sp = x % P.nsplit;
-  x /= P.nsplit;
-  const int head = x % P.c.heads, b = x / P.c.heads;
+  __shared__ uint32_t s_nan[kWaves][DP];
+  Params P = params_again();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // consecutive workgroups go to the 8 XCDs in turn; those that share lines
+  // of the cache (P->items of them) stay on one
+  int x = blockIdx.x >> 3;
+  const int grp = (x / P->items) * 8 + (blockIdx.x & 7);
+  if (grp >= P->groups) return;
+  x = grp * P->items + x % P->items;
+  const int units = P->B * P->nrb;
 
-  const int q0 = P.q_start[b], q1 = P.q_start[b + 1];
-  if (q0 < 0 || q1 > P.N || q1 <= q0) return;
-  const int n = q1 - q0, G = P.G;
-  const int ctx = P.ctx_len[b];
-  const int64_t rows = (int64_t)n * G;
-  const int64_t m0 = (int64_t)rb * (RT * 16);
-  // a request that cannot be used: NaN in all its rows (those of a request
-  // with more than max_q tokens among them)
-  {
-    const KeyRange all = key_range(P, n, ctx, 0, n - 1);
-    if (all.bad) {
-      if (sp != 0) return;
-      for (int64_t m = (int64_t)rb * kWG + tid; m < rows; m += (int64_t)P.nrb * kWG) {
-        const int64_t row = (int64_t)(q0 + m / G) * P.Hq + head * G + m % G;
-        for (int d = 0; d < P.c.dim; ++d) P.out[row * P.c.dim + d] = 0x7fc0;
-        if (P.lse) P.lse[row] = __builtin_nanf("");
+  // the run of tiles [at, at + left) of unit v, v + 1, ... that this workgroup
+  // takes for its head: a whole unit, or (P->chunks > 0) one of the equal runs
+  int v, at = 0, head;
+  int left = INT_MAX;
+  if (P->chunks == 0) {
+    const int rb = x % P->nrb;
+    x /= P->nrb;
+    head = x % P->c.heads;
+    v = (x / P->c.heads) * P->nrb + rb;
+  } else {
+    const int lane = threadIdx.x & 63;
+    head = x % P->c.heads;
+    const int64_t total = tiles_before(P, units, RT * 16, lane);
+    left = (int)chunk_tiles(P, total);  // (units * 2^25 tiles over at least 8 runs, units <= 4096: below 2^31 for
+                                        // any cache that fits the card)
+    const int64_t first = (int64_t)(x / P->c.heads) * left;
+    if (first >= total) return;
+    // the unit that holds tile `first`
+    double base = 0.0;
+    int v0 = 0;
+    for (;; v0 += 64) {
+      const double t = v0 + lane < units ? (double)unit_of(P, v0 + lane, RT * 16).tiles : 0.0;
+      const double end = wave_scan_d(t);
+      const uint64_t past = __ballot(base + end > (double)first);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        v = v0 + l;
+        at = uniform((int)((double)first - (base + lane_d(end - t, l))));
+        break;
       }
-      return;
+      base += lane_d(end, 63);
     }
   }
-  if (m0 >= rows) return;
-  const int64_t m1 = min(rows, m0 + RT * 16);
-  const KeyRange kr = key_range(P, n, ctx, (int)(m0 / G), (int)((m1 - 1) / G));
-  const int64_t kb64 = (int64_t)kr.lo + (int64_t)sp * P.split_keys;
-  if (sp > 0 && kb64 >= kr.hi) return;  // (the first split of an empty range still writes its zeros)
-  const int k_beg = (int)kb64, k_end = (int)min((int64_t)kr.hi, kb64 + P.split_keys);
 
-  // Q to LDS as the fragments of the first product: fragment (rt, c), lane l:
-  // row 16 rt + l % 16, dims (l / 16) DP/4 + 8 c ..+ 8
-  {
-    u32x4* qf = reinterpret_cast<u32x4*>(s_mem);
-    for (int f = tid; f < RT * C * 64; f += kWG) {
-      const int l = f & 63, c = (f >> 6) % C, rt = (f >> 6) / C;
-      const int64_t m = m0 + rt * 16 + (l & 15);
-      const int d = (l >> 4) * (DP / 4) + 8 * c;
-      u32x4 v{0, 0, 0, 0};
-      if (m < m1 && d < P.c.dim) {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(P.q) + (int64_t)(q0 + m / G) * P.q_tok +
-                              (int64_t)(head * G + m % G) * P.q_head + d;
-        if (P.qvec) {
-          v = *reinterpret_cast<const u32x4*>(src);
-        } else {
-          uint32_t w[4];
+  for (bool run_begin = true;; run_begin = false) {
+  // the lane's number anew for each unit: what derives from it would
+  // otherwise be kept in registers over the whole loop
+  P = params_again();
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int G = P->G, dim = P->c.dim;
+  const int tok_stride = (int)P->c.token;
+  // a lane whose dims are past the head's takes the key's first ones instead:
+  // Q is 0 there, and those dims of the output are not stored
+  uint32_t koff[W];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = (uint32_t)src[2 * i] | ((uint32_t)src[2 * i + 1] << 16);
-          v = u32x4{w[0], w[1], w[2], w[3]};
-        }
+  for (int w = 0; w < W; ++w)
+    koff[w] = (uint32_t)(r * tok_stride + (g * (DP / 4) + w * 16 < dim ? g * (DP / 4) + w * 16 : 0));
+  const uint32_t voff = (uint32_t)(4 * g * tok_stride + (r * (DP / 16) < dim ? r * (DP / 16) : 0));
+  const Unit un = unit_of(P, v, RT * 16);
+  const int len = min(left, un.tiles - at);  // of this unit
+  if (un.bad && un.tiles > 0) {
+    for (int64_t m = tid; m < (int64_t)un.n * G; m += kWG) {
+      const int64_t row = (int64_t)(un.q0 + m / G) * P->Hq + head * G + m % G;
+      for (int d = 0; d < P->c.dim; ++d) P->out[row * P->c.dim + d] = 0x7fc0;
+      if (P->lse) P->lse[row] = __builtin_nanf("");
+    }
+  } else if (un.tiles > 0) {
+  const int k_beg = un.lo + at * kTileKeys, k_end = min(un.hi, k_beg + len * kTileKeys);
+  const bool joined = len < un.tiles;  // other runs hold more of this unit's keys
+  const int nt = (len - wave + kWaves - 1) / kWaves;
+
+  // Q, to become the fragments of the first product in LDS: fragment (rt, c),
+  // lane l: row 16 rt + l % 16, dims (l / 16) DP/4 + 8 c ..+ 8
+  constexpr int QF = (RT * C * 64 + kWG - 1) / kWG;
+  u32x4 qreg[QF];
+#pragma unroll
+  for (int i = 0; i < QF; ++i) {
+    const int f = tid + i * kWG;
+    const int l = f & 63, cc = (f >> 6) % C, rt = (f >> 6) / C;
+    const int k = rt * 16 + (l & 15);
+    const int d = (l >> 4) * (DP / 4) + 8 * cc;
+    qreg[i] = u32x4{0, 0, 0, 0};
+    if (k < un.rows && d < P->c.dim) {
+      const int t = div_group(P, un.h0 + k);
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(P->q) + (int64_t)(un.q0 + un.t0 + t) * P->q_tok +
+                            (int64_t)(head * G + un.h0 + k - t * G) * P->q_head + d;
+      if (P->qvec) {
+        qreg[i] = *reinterpret_cast<const u32x4*>(src);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+        qreg[i] = u32x4{w[0], w[1], w[2], w[3]};
       }
-      qf[f] = v;
     }
   }
-  __syncthreads();
 
   int pos[RT];  // the position of this lane's row, -1 for rows past the block
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    const int64_t m = m0 + rt * 16 + r;
-    pos[rt] = m < m1 ? ctx - n + (int)(m / G) : -1;
+    const int k = rt * 16 + r;
+    pos[rt] = k < un.rows ? un.p_lo + div_group(P, un.h0 + k) : -1;
   }
   f32x4 acc[RT][DT];
   float ref[RT], sum[RT];
@@ -245,94 +309,185 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
     for (int dt = 0; dt < DT; ++dt) acc[rt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int32_t* bt = P.bt + (int64_t)b * P.bt_stride;
-  const u32x4* qf = reinterpret_cast<const u32x4*>(s_mem);
-  TileRegs<DP> nx;
-  int key0 = k_beg + wave * kTileKeys;
-  if (key0 < k_end) load_tile<DP, FINE>(P, bt, key0, head, lane, nx);
-  for (; key0 < k_end; key0 += kWaves * kTileKeys) {
-    TileRegs<DP> t = nx;
-    if (key0 + kWaves * kTileKeys < k_end) load_tile<DP, FINE>(P, bt, key0 + kWaves * kTileKeys, head, lane, nx);
+  const float scale2 = P->scale2;
+  const int window = P->window;
+  const uint8_t *k_codes = P->c.codes[0], *v_codes = P->c.codes[1];
+  const u32x4* qf = reinterpret_cast<const u32x4*>(s_mem) + lane;
+
+  // Lane l knows subtile l % 2 of tile i0 + l / 2 of this wave: where its keys
+  // begin, whether their block exists, and (!FINE) their scales.
+  int pg_lo = 0, pg_hi = 0, sc_lo = 0, sc_hi = 0, ksv = 0, vsv = 0;
+  uint64_t okv = 0;
+  auto look_up = [&](int i0) {
+    const Params P = params_again();
+    const int32_t* bt = P->bt + (int64_t)un.b * P->bt_stride;
+    const int key = k_beg + ((i0 + (lane >> 1)) * kWaves + wave) * kTileKeys + (lane & 1) * 16;
+    const int lb = key >> P->c.bs_shift, in = key & ((1 << P->c.bs_shift) - 1);
+    int page = -1;
+    if (key < k_end && lb < P->max_blocks) page = bt[lb];
+    const bool ok = page >= 0 && page < P->c.num_blocks;
+    page = ok ? page : 0;
+    okv = __ballot(ok);
+    const int64_t po = (int64_t)page * P->c.block + (int64_t)head * P->c.head + (int64_t)in * P->c.token;
+    const int64_t so = (int64_t)page * P->c.sblock + (int64_t)head * P->c.shead + (in >> P->c.st_shift);
+    pg_lo = (int)po;
+    pg_hi = (int)(po >> 32);
+    if constexpr (FINE) {
+      sc_lo = (int)so;
+      sc_hi = (int)(so >> 32);
+    } else {
+      ksv = P->c.scales[0][so];
+      vsv = P->c.scales[1][so];
+    }
+  };
+  auto lane64 = [&](int lo, int hi, int l) { return ((int64_t)lane_i(hi, l) << 32) | (uint32_t)lane_i(lo, l); };
+
+  // subtile u: key l % 16, dims [g DP/4, (g+1) DP/4); slot j's key, dims
+  // [r DP/16, (r+1) DP/16)
+  struct Buffer {
+    u32x4 k[2][W];
+    uint32_t v[8][W];
+    uint32_t kfine[2], vfine[2];  // (FINE) scale bytes of key r, and of keys 4 g ..+ 4
+    float ksc[2], vsc[2];
+    uint32_t ok;
+  } buf[NB];
+  auto load_k = [&](Buffer& t, int i) {
+    if ((i & (kWindow - 1)) == 0) look_up(i);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int l = ((i & (kWindow - 1)) << 1) + u;
+      const uint8_t* kb = k_codes + lane64(pg_lo, pg_hi, l);
+#pragma unroll
+      for (int w = 0; w < W; ++w) t.k[u][w] = *reinterpret_cast<const u32x4*>(kb + koff[w]);
+      if constexpr (FINE) {
+        const int64_t so = lane64(sc_lo, sc_hi, l);
+        t.kfine[u] = P->c.scales[0][so + (uint32_t)(r >> P->c.st_shift)];
+      } else {
+        t.ksc[u] = scale_of((uint32_t)lane_i(ksv, l));
+      }
+    }
+    t.ok = (uint32_t)(okv >> ((i & (kWindow - 1)) << 1)) & 3u;
+  };
+  auto load_v = [&](Buffer& t, int i) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int l = ((i & (kWindow - 1)) << 1) + u;
+      const uint8_t* vb = v_codes + lane64(pg_lo, pg_hi, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* p = vb + (int64_t)j * tok_stride;
+        if constexpr (W == 1) {
+          t.v[4 * u + j][0] = *reinterpret_cast<const uint32_t*>(p + voff);
+        } else if constexpr (W == 2) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(p + voff);
+          t.v[4 * u + j][0] = w.x;
+          t.v[4 * u + j][1] = w.y;
+        } else {
+          const u32x4 w = *reinterpret_cast<const u32x4*>(p + voff);
+          t.v[4 * u + j][0] = w.x;
+          t.v[4 * u + j][1] = w.y;
+          t.v[4 * u + j][2] = w.z;
+          t.v[4 * u + j][3] = w.w;
+        }
+      }
+      if constexpr (FINE) {
+        const uint8_t* sb = P->c.scales[1] + lane64(sc_lo, sc_hi, l) + (uint32_t)((4 * g) >> P->c.st_shift);
+        if (P->c.st_shift == 0) {
+          uint32_t w;
+          __builtin_memcpy(&w, sb, 4);
+          t.vfine[u] = w;
+        } else if (P->c.st_shift == 1) {
+          t.vfine[u] = (uint32_t)sb[0] * 0x0101u | (uint32_t)sb[1] * 0x01010000u;
+        } else {
+          t.vfine[u] = (uint32_t)sb[0] * 0x01010101u;
+        }
+      } else {
+        t.vsc[u] = scale_of((uint32_t)lane_i(vsv, l));
+      }
+    }
+  };
+
+  auto tile = [&](Buffer& t, int i) {
+    // more than a few fragments of Q are read from LDS for every tile rather
+    // than kept in registers (the compiler would move the reads out of the loop)
+    if constexpr (RT * C > 4) asm volatile("" ::: "memory");
+    const int key0 = k_beg + (i * kWaves + wave) * kTileKeys;
+    const uint32_t okt = t.ok;
     // every row of the block sees every key of the tile
-    const bool whole = t.ok == 3u && key0 + kTileKeys - 1 <= kr.p_lo && (P.window == 0 || key0 > kr.p_hi - P.window);
+    const bool whole = okt == 3u && key0 + kTileKeys - 1 <= un.p_lo && (window == 0 || key0 > un.p_hi - window);
 
     // S^T
     f32x4 s[RT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float ksc = scale_of(t.ks[u]);
+      const float sc = FINE ? scale_of(t.kfine[u]) : t.ksc[u];
       bf16x8 ka[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const u32x4 w4 = t.k[u][c / 2];
-        const uint32_t w0 = (c & 1) ? w4.z : w4.x, w1 = (c & 1) ? w4.w : w4.y;
-        ka[c] = pack8(widen2<false>(w0, ksc), widen2<true>(w0, ksc), widen2<false>(w1, ksc), widen2<true>(w1, ksc));
+      for (int cc = 0; cc < C; ++cc) {
+        const u32x4 w4 = t.k[u][cc / 2];
+        const uint32_t w0 = (cc & 1) ? w4.z : w4.x, w1 = (cc & 1) ? w4.w : w4.y;
+        ka[cc] = pack8(widen2<false>(w0, sc), widen2<true>(w0, sc), widen2<false>(w1, sc), widen2<true>(w1, sc));
       }
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        f32x4 a{0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka[c], __builtin_bit_cast(bf16x8, qf[(rt * C + c) * 64 + lane]), a,
-                                                      0, 0, 0);
-        s[rt][u] = a;
-      }
+      for (int cc = 0; cc < C; ++cc)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka[cc], __builtin_bit_cast(bf16x8, qf[(rt * C + cc) * 64]),
+                                                             s[rt][u], 0, 0, 0);
     }
+    load_k(t, min(i + NB, nt - 1));
 
-    // a tile that some row sees only in part: nothing of the keys that no row
-    // sees may enter (0 * NaN, 0 * inf), and a NaN among the others is kept
-    // apart
+    // a tile that some row sees only in part: scores not seen become -inf;
+    // nothing of the keys that no row sees may enter (0 * NaN, 0 * inf), and a
+    // NaN among the others is kept apart
     bool nans = false;
     if (!whole) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         bool some = false;
+        uint32_t fine = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int key = key0 + 16 * u + 4 * g + j;
-          const bool any = ((t.ok >> u) & 1u) && key <= kr.p_hi && (P.window == 0 || key > kr.p_lo - P.window);
+          const bool there = (okt >> u) & 1u;
+          const bool any = there && key <= un.p_hi && (window == 0 || key > un.p_lo - window);
           some |= any;
 #pragma unroll
-          for (int w = 0; w < DP / 64; ++w) {
+          for (int w = 0; w < W; ++w) {
             t.v[4 * u + j][w] = any ? t.v[4 * u + j][w] : 0u;
             nans |= nan_bytes(t.v[4 * u + j][w]) != 0;
           }
-          if constexpr (FINE) t.vs[4 * u + j] = any ? t.vs[4 * u + j] : (uint32_t)kScaleBias;
+          if constexpr (FINE) fine |= any ? t.vfine[u] & (0xffu << (8 * j)) : (uint32_t)kScaleBias << (8 * j);
         }
-        if constexpr (!FINE) t.vs[u] = some ? t.vs[u] : (uint32_t)kScaleBias;
+        if constexpr (FINE) t.vfine[u] = fine;
+        if constexpr (!FINE) t.vsc[u] = __ballot(some) ? t.vsc[u] : 1.0f;
+        __builtin_amdgcn_sched_barrier(0);  // (few conditions at a time: each is a pair of scalar registers)
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        // bit 16 u + 4 g + j of `see`: the row sees that key
+        const uint32_t see = seen_keys(pos[rt] - key0, window, okt) >> (4 * g);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[rt][u][j] = (see >> (16 * u + j)) & 1u ? s[rt][u][j] : -INFINITY;
+        __builtin_amdgcn_sched_barrier(0);
       }
       nans = __ballot(nans) != 0;
     }
 
-    // scores in units of log2, those not seen at -inf; the reference follows
-    bf16x8 pb[RT];
+    // the weights, against a reference that follows the scores
     bool move = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v = s[rt][u][j] * P.scale2;
-          if (!whole) {
-            const int key = key0 + 16 * u + 4 * g + j;
-            const bool see = ((t.ok >> u) & 1u) && key <= pos[rt] && (P.window == 0 || key > pos[rt] - P.window);
-            v = see ? v : -INFINITY;
-          }
-          s[rt][u][j] = v;
-          mx = fmaxf(mx, v);
-        }
-      move |= mx > ref[rt] + kRefSlack;
+      move |= max_of(s[rt]) * scale2 > ref[rt] + kRefSlack;
     }
     if (__ballot(move)) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float mx = ref[rt];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx = fmaxf(mx, s[rt][u][j]);
+        float mx = fmaxf(ref[rt], max_of(s[rt]) * scale2);
         mx = fmaxf(mx, lane_xor16(mx));
         mx = fmaxf(mx, lane_xor32(mx));
         const float f = exp2_fast(ref[rt] - mx);
@@ -342,17 +497,18 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
         for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= f;
       }
     }
+    bf16x8 pb[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float p[8];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[4 * u + j] = exp2_fast(s[rt][u][j] - ref[rt]);
+        for (int j = 0; j < 4; ++j) p[4 * u + j] = exp2_fast(__builtin_fmaf(s[rt][u][j], scale2, -ref[rt]));
       sum[rt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       if constexpr (FINE) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] *= scale_of(t.vs[j]);
+        for (int j = 0; j < 8; ++j) p[j] *= scale_of((t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu);
       }
       uint32_t w[4];
 #pragma unroll
@@ -361,69 +517,78 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
       pb[rt] = pack8(w[0], w[1], w[2], w[3]);
     }
 
-    const float vsc0 = FINE ? 1.0f : scale_of(t.vs[0]), vsc1 = FINE ? 1.0f : scale_of(t.vs[1]);
     if (nans) {
-      // rows that see a NaN value get NaN in that dim: visibility times
-      // NaN-ness, then the NaNs leave the codes
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ka = key0 + 16 * (j >> 1) + 4 * g + 2 * (j & 1);
-          const bool ok = (t.ok >> (j >> 1)) & 1u;
-          const bool a = ok && ka <= pos[rt] && (P.window == 0 || ka > pos[rt] - P.window);
-          const bool c = ok && ka + 1 <= pos[rt] && (P.window == 0 || ka + 1 > pos[rt] - P.window);
-          w[j] = (a ? 0x3f80u : 0u) | (c ? 0x3f800000u : 0u);
-        }
-        const bf16x8 see = pack8(w[0], w[1], w[2], w[3]);
-#pragma unroll
-        for (int dw = 0; dw < DP / 64; ++dw) {
-          uint32_t lo[4], hi[4];
-          transpose4(nan_bytes(t.v[0][dw]), nan_bytes(t.v[1][dw]), nan_bytes(t.v[2][dw]), nan_bytes(t.v[3][dw]), lo);
-          transpose4(nan_bytes(t.v[4][dw]), nan_bytes(t.v[5][dw]), nan_bytes(t.v[6][dw]), nan_bytes(t.v[7][dw]), hi);
-#pragma unroll
-          for (int dd = 0; dd < 4; ++dd) {
-            uint32_t a[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t y = (q < 2 ? lo[dd] : hi[dd]) >> (16 * (q & 1));
-              a[q] = ((y & 0x80u) ? 0x3f80u : 0u) | ((y & 0x8000u) ? 0x3f800000u : 0u);
-            }
-            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pack8(a[0], a[1], a[2], a[3]), see,
-                                                                      f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (hit[q] > 0.f) acc[rt][4 * dw + dd][q] = __builtin_nanf("");
-          }
-        }
-      }
+      // a row that sees a NaN value gets NaN in that dim: the keys with a NaN
+      // in each dim as a mask in LDS, against the keys that a row sees; then
+      // the NaNs leave the codes
+      uint32_t* mask = s_nan[wave];
+      for (int d = lane; d < DP; d += 64) mask[d] = 0;
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int w = 0; w < DP / 64; ++w) {
+        for (int w = 0; w < W; ++w) {
           const uint32_t nb = nan_bytes(t.v[j][w]);
+          for (uint32_t m = nb; m; m &= m - 1)
+            atomicOr(&mask[r * DT + 4 * w + (__builtin_ctz(m) >> 3)], 1u << (16 * (j >> 2) + 4 * g + (j & 3)));
           t.v[j][w] &= ~((nb >> 7) * 0xffu);
+        }
+      __builtin_amdgcn_wave_barrier();
+      uint32_t see[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) see[rt] = seen_keys(pos[rt] - key0, window, okt);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t m = mask[(4 * g + q) * DT + dt];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) acc[rt][dt][q] = m & see[rt] ? __builtin_nanf("") : acc[rt][dt][q];
+          __builtin_amdgcn_sched_barrier(0);  // (one at a time: the path is rare and must not cost registers)
         }
     }
 
     // O^T
+    const float v0 = FINE ? 1.0f : t.vsc[0], v1 = FINE ? 1.0f : t.vsc[1];
 #pragma unroll
-    for (int dw = 0; dw < DP / 64; ++dw) {
+    for (int dw = 0; dw < W; ++dw) {
       uint32_t lo[4], hi[4];
       transpose4(t.v[0][dw], t.v[1][dw], t.v[2][dw], t.v[3][dw], lo);
       transpose4(t.v[4][dw], t.v[5][dw], t.v[6][dw], t.v[7][dw], hi);
 #pragma unroll
       for (int dd = 0; dd < 4; ++dd) {
-        const bf16x8 va = pack8(widen2<false>(lo[dd], vsc0), widen2<true>(lo[dd], vsc0), widen2<false>(hi[dd], vsc1),
-                                widen2<true>(hi[dd], vsc1));
+        const bf16x8 va = pack8(widen2<false>(lo[dd], v0), widen2<true>(lo[dd], v0), widen2<false>(hi[dd], v1),
+                                widen2<true>(hi[dd], v1));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           acc[rt][4 * dw + dd] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pb[rt], acc[rt][4 * dw + dd], 0, 0, 0);
       }
     }
+    load_v(t, min(i + NB, nt - 1));
+  };
+  // (in this order the first tiles are on their way before Q is waited for)
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+    if (i < nt) {
+      load_k(buf[i], i);
+      load_v(buf[i], i);
+    }
+#pragma unroll
+  for (int i = 0; i < QF; ++i)
+    if (tid + i * kWG < RT * C * 64)
+      reinterpret_cast<u32x4*>(s_mem)[tid + i * kWG] = (qreg[i] & P->q_keep) ^ P->q_flip;
+  __syncthreads();
+  // every tile's loads are unconditional (the last ones' read a tile again):
+  // behind a condition the compiler could not count the loads in flight, and
+  // would wait for the values just asked for before it uses the keys
+  for (int i = 0; i < nt; i += NB) {
+    tile(buf[0], i);
+    if constexpr (NB > 1) {
+      if (i + 1 < nt) tile(buf[NB - 1], i + 1);
+    }
   }
 
+  P = params_again();
   // the four waves' sums joined: lane l holds of row l % 16 the dims
   // (4 g + q) DP/16 + dt
 #pragma unroll
@@ -454,8 +619,8 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
     // 4 dims a thread
     for (int cell = tid; cell < 16 * (DP / 4); cell += kWG) {
       const int rr = cell / (DP / 4), d = (cell % (DP / 4)) * 4;
-      const int64_t m = m0 + rt * 16 + rr;
-      if (m >= m1 || d >= P.c.dim) continue;
+      const int k = rt * 16 + rr;
+      if (k >= un.rows || d >= P->c.dim) continue;
       f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) o += *reinterpret_cast<const f32x4*>(part + (w * 16 + rr) * DP + d);
@@ -465,14 +630,16 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
       float l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) l += s_sum[w][rt * 16 + rr] * exp2_fast(s_ref[w][rt * 16 + rr] - mx);
-      const int hq = head * G + (int)(m % G);
-      const int64_t row = (int64_t)(q0 + m / G) * P.Hq + hq;
-      if (P.nsplit > 1) {
-        *reinterpret_cast<f32x4*>(P.po + (row * P.nsplit + sp) * P.c.dim + d) = o;
-        if (d == 0) P.pm[row * P.nsplit + sp] = float2{mx, l};
+      const int t = div_group(P, un.h0 + k);
+      const int hq = head * G + un.h0 + k - t * G;
+      const int64_t row = (int64_t)(un.q0 + un.t0 + t) * P->Hq + hq;
+      if (joined) {
+        const int64_t part = part_row(P, grp, !run_begin, head, RT * 16, k);
+        *reinterpret_cast<f32x4*>(P->po + part * P->c.dim + d) = o;
+        if (d == 0) P->pm[part] = float2{mx, l};
       } else {
-        if (P.sinks) {
-          const float sk = P.sinks[hq] * 1.44269504088896341f;
+        if (P->sinks) {
+          const float sk = P->sinks[hq] * 1.44269504088896341f;
           const float top2 = fmaxf(mx, sk);
           const float fa = exp2_fast(mx - top2);
           l = l * fa + exp2_fast(sk - top2);
@@ -485,105 +652,112 @@ __global__ __launch_bounds__(kWG) void attn_kernel(AttnParams P) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{o[2 * q] * inv, o[2 * q + 1] * inv}, bf16x2));
-        *reinterpret_cast<u32x2*>(P.out + row * P.c.dim + d) = u32x2{w[0], w[1]};
-        if (d == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+        *reinterpret_cast<u32x2*>(P->out + row * P->c.dim + d) = u32x2{w[0], w[1]};
+        if (d == 0 && P->lse) P->lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
       }
     }
   }
+  }
+  // the next unit of the run
+  left -= len;
+  at = 0;
+  if (P->chunks == 0 || left <= 0 || ++v >= units) break;
+  __syncthreads();
+  }
 }
 
-// Joins the splits of a row: one wave per (token, query head).
-__global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams P, int row_tiles) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (row >= (int64_t)P.N * P.Hq) return;
-  const int tok = (int)(row / P.Hq), hq = (int)(row - (int64_t)tok * P.Hq);
-  // the request that holds the token: the last b with q_start[b] <= tok
-  int lo = 0, hi = P.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (P.q_start[mid] <= tok)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int q0 = P.q_start[lo], q1 = P.q_start[lo + 1];
-  if (q0 < 0 || q1 > P.N || tok < q0 || tok >= q1) return;
-  const int n = q1 - q0, ctx = P.ctx_len[lo];
-  if (key_range(P, n, ctx, 0, n - 1).bad) return;  // its rows hold NaN already
-  // the block of rows that held this one, and the splits that it has
-  const int m = (tok - q0) * P.G + hq % P.G;
-  const int rb = m / (16 * row_tiles);
-  const int m1 = min(n * P.G, (rb + 1) * 16 * row_tiles);
-  const KeyRange kr = key_range(P, n, ctx, rb * 16 * row_tiles / P.G, (m1 - 1) / P.G);
-  const int ns = max(1, (int)(((int64_t)kr.hi - kr.lo + P.split_keys - 1) / P.split_keys));
-  const float2* pm = P.pm + row * P.nsplit;
-  float mx = P.sinks ? P.sinks[hq] * 1.44269504088896341f : kNoRef;
-  for (int s = lane; s < ns; s += 64) mx = fmaxf(mx, pm[s].x);
-  mx = wave_max_f(mx);
-  float l = 0.f;
-  for (int s = lane; s < ns; s += 64) l += pm[s].y * exp2_fast(pm[s].x - mx);
-  l = (float)wave_total_d((double)l);
-  if (P.sinks) l += exp2_fast(P.sinks[hq] * 1.44269504088896341f - mx);
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const float* po = P.po + row * P.nsplit * P.c.dim;
-  for (int d = lane * 4; d < P.c.dim; d += 256) {
+// Joins the runs of a unit that several hold: one workgroup per (unit, KV
+// head), 4 dims a thread.
+__global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams, int block_rows) {
+  const Params P = params_again();
+  const int v = blockIdx.x / P->c.heads, head = blockIdx.x % P->c.heads, lane = threadIdx.x & 63;
+  const Unit u = unit_of(P, v, block_rows);
+  if (u.tiles <= 1) return;
+  const int64_t base = tiles_before(P, v, block_rows, lane);
+  const int64_t per = chunk_tiles(P, tiles_before(P, P->B * P->nrb, block_rows, lane));
+  const int j0 = (int)(base / per), j1 = (int)((base + u.tiles - 1) / per);
+  if (j0 == j1) return;  // written whole
+  const bool late = base > j0 * per;  // its first run began with another unit
+  const int cols = P->c.dim >> 2;
+  for (int cell = threadIdx.x; cell < u.rows * cols; cell += kWG) {
+    const int k = cell / cols, d = (cell - k * cols) * 4;
+    const int t = div_group(P, u.h0 + k);
+    const int hq = head * P->G + u.h0 + k - t * P->G;
+    const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
+    const float sk = P->sinks ? P->sinks[hq] * 1.44269504088896341f : kNoRef;
+    float mx = sk;
+#pragma unroll 8
+    for (int j = j0; j <= j1; ++j) mx = fmaxf(mx, P->pm[part_row(P, j, late && j == j0, head, block_rows, k)].x);
+    float l = P->sinks ? exp2_fast(sk - mx) : 0.f;
     f32x4 o{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < ns; ++s) o += *reinterpret_cast<const f32x4*>(po + (int64_t)s * P.c.dim + d) * exp2_fast(pm[s].x - mx);
+#pragma unroll 8
+    for (int j = j0; j <= j1; ++j) {
+      const int64_t part = part_row(P, j, late && j == j0, head, block_rows, k);
+      const float2 p = P->pm[part];
+      const float f = exp2_fast(p.x - mx);
+      l += p.y * f;
+      o += *reinterpret_cast<const f32x4*>(P->po + part * P->c.dim + d) * f;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
     uint32_t w[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{o[2 * q] * inv, o[2 * q + 1] * inv}, bf16x2));
-    *reinterpret_cast<u32x2*>(P.out + row * P.c.dim + d) = u32x2{w[0], w[1]};
+    *reinterpret_cast<u32x2*>(P->out + row * P->c.dim + d) = u32x2{w[0], w[1]};
+    if (d == 0 && P->lse) P->lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
   }
-  if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
 AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * G;
   const int64_t tiles = (rows + 15) / 16;
-  const int rt_max = dim > 128 ? 2 : 4;
-  p.rt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : rt_max;
+  const int rt_max = dim > 128 ? 1 : dim > 64 ? 3 : 5;
+  p.nrb = (int32_t)((tiles + rt_max - 1) / rt_max);
+  p.rt = (int32_t)((tiles + p.nrb - 1) / p.nrb);
   p.nrb = (int32_t)((tiles + p.rt - 1) / p.rt);
-  // keys that one block of rows can see, from a whole tile on
+  // keys that one block of rows can see
   int64_t keys = max_ctx;
-  if (window > 0) {
-    const int64_t toks = (p.rt * 16 + G - 1) / G + 1;
-    const int64_t w = (int64_t)window + toks + kTileKeys;
-    if (w < keys) keys = w;
+  if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
+  const int64_t units = (int64_t)B * p.nrb;
+  const int slots = 256 * (dim <= 64 && p.rt == 1 ? 4 : dim <= 64 && p.rt == 2 ? 3 : 2);  // resident workgroups
+  if (keys <= 1024 || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
+    // short contexts, very many units, or many blocks of long prompts: a unit
+    // to a workgroup; the blocks of one head on one XCD, for its keys
+    p.chunks = 0;
+    p.items = p.nrb;
+    p.groups = (int64_t)B * heads;
+  } else {
+    // equal runs, as many as are resident at once; a run's heads on one XCD
+    p.chunks = slots / heads > 8 ? slots / heads / 8 * 8 : 8;
+    p.items = heads;
+    p.groups = p.chunks;
   }
-  const int64_t wgs = (int64_t)B * heads * p.nrb;
-  int64_t ns = wgs > 0 ? 1024 / wgs : 1;
-  const int64_t most = (keys + 511) / 512;  // at least 512 keys to a split
-  if (ns > most) ns = most;
-  if (ns < 1) ns = 1;
-  const int64_t per = kWaves * kTileKeys;
-  p.split_keys = (int32_t)(((keys + ns - 1) / ns + per - 1) / per * per);
-  if (p.split_keys < per) p.split_keys = (int32_t)per;
-  p.nsplit = (int32_t)((keys + p.split_keys - 1) / p.split_keys);
-  if (p.nsplit < 1) p.nsplit = 1;
   return p;
 }
 
 template <int DP, int RT>
 static hipError_t launch_attn_typed(const AttnParams& P, hipStream_t stream) {
-  const int64_t grid = (int64_t)P.B * P.c.heads * P.nrb * P.nsplit;
-  if (P.c.st_shift < 2)
-    hipLaunchKernelGGL((attn_kernel<DP, RT, true>), dim3((unsigned)grid), dim3(kWG), 0, stream, P);
+  const dim3 grid((unsigned)(((int64_t)P.groups + 7) / 8 * 8 * P.items));
+  if (P.c.st_shift < 4)
+    hipLaunchKernelGGL((attn_kernel<DP, RT, true>), grid, dim3(kWG), 0, stream, P);
   else
-    hipLaunchKernelGGL((attn_kernel<DP, RT, false>), dim3((unsigned)grid), dim3(kWG), 0, stream, P);
+    hipLaunchKernelGGL((attn_kernel<DP, RT, false>), grid, dim3(kWG), 0, stream, P);
   return hipGetLastError();
 }
 
 template <int DP>
 static hipError_t launch_attn_rows(const AttnParams& P, int rt, hipStream_t stream) {
   if (rt == 1) return launch_attn_typed<DP, 1>(P, stream);
-  if (rt == 2) return launch_attn_typed<DP, 2>(P, stream);
-  if constexpr (DP <= 128)
-    return launch_attn_typed<DP, 4>(P, stream);
-  else
-    return hipErrorInvalidValue;
+  if constexpr (DP <= 128) {
+    if (rt == 2) return launch_attn_typed<DP, 2>(P, stream);
+    if (rt == 3) return launch_attn_typed<DP, 3>(P, stream);
+  }
+  if constexpr (DP <= 64) {
+    if (rt == 4) return launch_attn_typed<DP, 4>(P, stream);
+    if (rt == 5) return launch_attn_typed<DP, 5>(P, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream) {
@@ -594,10 +768,8 @@ hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t st
     e = launch_attn_rows<128>(P, plan.rt, stream);
   else
     e = launch_attn_rows<256>(P, plan.rt, stream);
-  if (e != hipSuccess || plan.nsplit <= 1) return e;
-  const int64_t rows = (int64_t)P.N * P.Hq;
-  hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kWG), 0, stream, P,
-                     plan.rt);
+  if (e != hipSuccess || plan.chunks == 0) return e;
+  hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(P.B * P.nrb * P.c.heads)), dim3(kWG), 0, stream, P, plan.rt * 16);
   return hipGetLastError();
 }
 

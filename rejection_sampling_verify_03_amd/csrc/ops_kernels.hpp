@@ -71,9 +71,15 @@ hipError_t launch_kv_read(const KvReadParams& P, int dtype, bool vec, hipStream_
 struct AttnParams {
   CacheView c;
   int32_t B, N, Hq, G;  // G: query heads per KV head
+  uint32_t g_inv;       // 65535 / G + 1
   int32_t max_q, max_ctx, window, max_blocks;
-  int32_t nrb, nsplit, split_keys;  // row blocks per (request, KV head), key splits, keys per split
-  float scale2;                     // scale * log2(e)
+  int32_t nrb, chunks;              // row blocks per (request, KV head); equal runs of tiles (0: a unit each)
+  int32_t items, groups;            // workgroups kept on one XCD, and how many such sets
+  // the scores are scale2 * q . k with scale2 = |scale| * log2(e) > 0: a
+  // negative scale is the sign of q (q_flip: the sign bits of two bf16), a
+  // scale of 0 a q of 0 (q_keep = 0, else all bits)
+  uint32_t q_flip, q_keep;
+  float scale2;
   const char* q;
   int64_t q_tok, q_head;  // elements
   const int32_t* q_start;
@@ -83,13 +89,14 @@ struct AttnParams {
   const float* sinks;
   uint16_t* out;
   float* lse;
-  float* po;   // [N, Hq, nsplit, dim] partial sums (nsplit > 1)
-  float2* pm;  // [N, Hq, nsplit] their reference exponents and sums of weights
+  float* po;   // [chunks, 2, heads, 16 * rt, dim] partial sums (chunks > 0)
+  float2* pm;  // [chunks, 2, heads, 16 * rt] their reference exponents and sums of weights
   int32_t qvec;
 };
 
 struct AttnPlan {
-  int32_t rt, nrb, nsplit, split_keys;
+  int32_t rt, nrb, chunks;
+  int64_t items, groups;
 };
 // How the rows of a (request, KV head) and its keys are cut into workgroups.
 AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window);

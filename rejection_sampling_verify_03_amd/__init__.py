@@ -714,50 +714,63 @@ def verify_sharded(target, draft, draft_tokens, temperature, G, seed=0, step=0, 
     return st.acc[0].clone(), st.tok.max(dim=0).values, st.acc
 
 
-# ------------------------------------------------- token log probabilities
+# --------------------------------- operators around a verification step
+# (kept short on the host: at the sizes of one decode step these calls cost
+# about what their kernels do)
 class _on:
-    """The device of `tensor` current, and `stream` (or that device's current
+    """Device `dev` current, and `stream` (or that device's current
     stream) its current stream: what is allocated here belongs to the stream
     that the work is enqueued on."""
+    __slots__ = ("ptr", "ctx")
 
-    def __init__(self, tensor, stream=None):
+    def __init__(self, dev, stream=None):
         torch = _torch()
-        self.stream = stream if stream is not None else torch.cuda.current_stream(tensor.device)
-        if self.stream.device != tensor.device:
-            raise ValueError("the stream is on another device than the tensors")
-        # already current: nothing to set
         self.ctx = None
-        if stream is not None or torch.cuda.current_device() != tensor.device.index:
-            self.ctx = torch.cuda.stream(self.stream)
+        if stream is None:
+            # (the address alone: a torch.cuda.Stream object costs a quarter of a small call)
+            self.ptr = torch._C._cuda_getCurrentRawStream(dev.index)
+            if torch._C._cuda_getDevice() != dev.index:
+                self.ctx = torch.cuda.device(dev)
+        else:
+            if stream.device != dev:
+                raise ValueError("the stream is on another device than the tensors")
+            self.ctx = torch.cuda.stream(stream)
+            self.ptr = stream.cuda_stream
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self.ptr
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _same_device(first, *others):
-    if not first.is_cuda:
+def _gpu_device(t):
+    if not t.is_cuda:
         raise ValueError("all tensors must be on the GPU")
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on the same GPU")
+    return t.device
 
 
-def _want(t, dtype, shape, name):
-    """A contiguous tensor of this type and shape."""
+def _want(t, dtype, shape, dev, name):
+    """The address of a contiguous tensor of this type, shape and device."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s %s" % (name, dtype, list(shape)))
+    if t.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    return t.data_ptr()
 
 
-def _bytes_of(workspace):
-    return workspace.numel() * workspace.element_size()
+def _want_workspace(t, dev):
+    if t is None:
+        return None, 0
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous on the tensors' GPU")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
+# ------------------------------------------------- token log probabilities
 class TokenLogprobs:
     """logprobs [B, R] and entropy [B, R] float32 (entropy None if not asked
     for), top_ids [B, R, top] int32, top_logprobs [B, R, top] float32."""
@@ -769,10 +782,11 @@ class TokenLogprobs:
 
 def token_logprobs_outputs(B, R, top, device, entropy=True):
     torch = _torch()
-    return TokenLogprobs(torch.empty(B, R, dtype=torch.float32, device=device),
-                         torch.empty(B, R, dtype=torch.float32, device=device) if entropy else None,
-                         torch.empty(B, R, top, dtype=torch.int32, device=device),
-                         torch.empty(B, R, top, dtype=torch.float32, device=device))
+    f32, empty = torch.float32, torch.empty
+    return TokenLogprobs(empty((B, R), dtype=f32, device=device),
+                         empty((B, R), dtype=f32, device=device) if entropy else None,
+                         empty((B, R, top), dtype=torch.int32, device=device),
+                         empty((B, R, top), dtype=f32, device=device))
 
 
 def token_logprobs_args(logits, tokens, temperature, out, workspace):
@@ -780,32 +794,32 @@ def token_logprobs_args(logits, tokens, temperature, out, workspace):
     stride (an expanded request dimension shares rows), tokens [B, R] int32,
     temperature [B] float32 or None, out a TokenLogprobs."""
     torch = _torch()
-    if logits.dim() != 3 or (logits.stride(2) != 1 and logits.shape[2] > 1):
-        raise ValueError("logits must be [B, R, V] with contiguous rows")
-    B, R, V = logits.shape
-    _same_device(logits, tokens, temperature, out.logprobs, out.entropy, out.top_ids, out.top_logprobs, workspace)
-    _want(tokens, torch.int32, (B, R), "tokens")
-    if temperature is not None:
-        _want(temperature, torch.float32, (B,), "temperature")
-    top = out.top_ids.shape[-1]
-    _want(out.logprobs, torch.float32, (B, R), "logprobs")
+    dev = _gpu_device(logits)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    B, R, _ = logits.shape
     if out.entropy is not None:
-        _want(out.entropy, torch.float32, (B, R), "entropy")
-    _want(out.top_ids, torch.int32, (B, R, top), "top_ids")
-    _want(out.top_logprobs, torch.float32, (B, R, top), "top_logprobs")
-    a = SpecLogprobsArgs()
-    a.B, a.R, a.V, a.dtype, a.top = B, R, V, _logit_dtype(logits), top
-    a.logits = logits.data_ptr()
-    a.req_stride = logits.stride(0) if B > 1 else 0
-    a.row_stride = logits.stride(1) if R > 1 else V
-    a.tokens = tokens.data_ptr()
-    a.temperature = None if temperature is None else temperature.data_ptr()
-    a.logprobs = out.logprobs.data_ptr()
-    a.entropy = None if out.entropy is None else out.entropy.data_ptr()
-    a.top_ids, a.top_logprobs = out.top_ids.data_ptr(), out.top_logprobs.data_ptr()
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), _bytes_of(workspace)
-    return a
+        _want(out.entropy, torch.float32, (B, R), dev, "entropy")
+    top = out.top_ids.shape[-1]
+    _want(out.logprobs, torch.float32, (B, R), dev, "logprobs")
+    _want(out.top_ids, torch.int32, (B, R, top), dev, "top_ids")
+    _want(out.top_logprobs, torch.float32, (B, R, top), dev, "top_logprobs")
+    return _logprobs_args(logits, tokens, temperature, top, out, _want_workspace(workspace, dev))
+
+
+def _logprobs_args(logits, tokens, temperature, top, out, ws):
+    torch = _torch()
+    dev = logits.device
+    B, R, V = logits.shape
+    s0, s1, s2 = logits.stride()
+    if s2 != 1 and V > 1:
+        raise ValueError("logits must be [B, R, V] with contiguous rows")
+    return SpecLogprobsArgs(
+        B, R, V, _logit_dtype(logits), logits.data_ptr(), s0 if B > 1 else 0, s1 if R > 1 else V,
+        _want(tokens, torch.int32, (B, R), dev, "tokens"),
+        None if temperature is None else _want(temperature, torch.float32, (B,), dev, "temperature"), top,
+        out.logprobs.data_ptr(), None if out.entropy is None else out.entropy.data_ptr(), out.top_ids.data_ptr(),
+        out.top_logprobs.data_ptr(), ws[0], ws[1])
 
 
 def token_logprobs(logits, tokens, temperature=None, top=0, entropy=True, workspace=None, stream=None, out=None):
@@ -813,20 +827,27 @@ def token_logprobs(logits, tokens, temperature=None, top=0, entropy=True, worksp
     read) under softmax(logits / T), logits [B, R, V]; the entropy of each row
     and its `top` most likely tokens.  tokens may be the output_tokens of a
     verification with logits its target.  Enqueued on `stream` or the tensors'
-    device's current stream; returns a TokenLogprobs."""
-    torch = _torch()
-    if logits.dim() != 3 or not logits.is_cuda:
-        raise ValueError("logits must be [B, R, V] on the GPU")
-    B, R, V = logits.shape
+    device's current stream; returns a TokenLogprobs (`out`, where given, says
+    with its shapes what is computed)."""
+    dev = _gpu_device(logits)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
     if not 0 <= top <= SPEC_MAX_TOP:
         raise ValueError("top must be in 0..%d" % SPEC_MAX_TOP)
-    with _on(logits, stream) as s:
-        if out is None:
-            out = token_logprobs_outputs(B, R, top, logits.device, entropy)
+    with _on(dev, stream) as s:
+        B, R, V = logits.shape
+        if out is not None:
+            top = out.top_ids.shape[-1]
         if workspace is None:
-            n = spec_logprobs_workspace_bytes(B, R, V, top)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=logits.device)
-        rc = spec_logprobs_launch(token_logprobs_args(logits, tokens, temperature, out, workspace), s)
+            torch = _torch()
+            workspace = torch.empty(max(lib.spec_logprobs_workspace_bytes(B, R, V, top), 16), dtype=torch.uint8,
+                                    device=dev)
+        if out is not None:
+            a = token_logprobs_args(logits, tokens, temperature, out, workspace)
+        else:
+            out = token_logprobs_outputs(B, R, top, dev, entropy)
+            a = _logprobs_args(logits, tokens, temperature, top, out, _want_workspace(workspace, dev))
+        rc = lib.spec_logprobs_launch(a, s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return out
@@ -849,28 +870,25 @@ class KVCache:
         if k.dim() != 4 or k_scale.dim() != 3:
             raise ValueError("codes must be [num_blocks, block_size, heads, head_dim], scales [num_blocks, heads, "
                              "groups]")
-        _same_device(k, v, k_scale, v_scale)
-        if k.element_size() != 1 or v.dtype != k.dtype or k_scale.element_size() != 1 or v_scale.dtype != k_scale.dtype:
+        dev = _gpu_device(k)
+        if v.device != dev or k_scale.device != dev or v_scale.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        if k.itemsize != 1 or v.dtype != k.dtype or k_scale.itemsize != 1 or v_scale.dtype != k_scale.dtype:
             raise TypeError("codes and scales must be 8-bit tensors, alike for k and v")
         nb, bs, heads, dim = k.shape
-        groups = k_scale.shape[2]
-        if v.shape != k.shape or v.stride() != k.stride() or v_scale.shape != k_scale.shape or \
-                v_scale.stride() != k_scale.stride() or k_scale.shape[0] != nb or k_scale.shape[1] != heads:
+        snb, sheads, groups = k_scale.shape
+        st, sst = k.stride(), k_scale.stride()
+        if v.shape != k.shape or v.stride() != st or v_scale.shape != k_scale.shape or v_scale.stride() != sst or \
+                snb != nb or sheads != heads:
             raise ValueError("k and v (and their scales) must agree in shape and strides")
-        if k.stride(3) != 1 or (groups > 1 and k_scale.stride(2) != 1) or groups < 1 or bs % groups:
+        if st[3] != 1 or (groups > 1 and sst[2] != 1) or groups < 1 or bs % groups:
             raise ValueError("codes must be contiguous along head_dim, scales along their groups, which divide a block")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_blocks, self.block_size, self.heads, self.head_dim = nb, bs, heads, dim
-        self.scale_tokens, self.device = bs // groups, k.device
-        a = SpecKVCache()
-        a.num_blocks, a.block_size, a.scale_tokens, a.heads, a.head_dim = nb, bs, bs // groups, heads, dim
-        a.k_codes, a.v_codes = k.data_ptr(), v.data_ptr()
-        a.block_stride, a.token_stride, a.head_stride = k.stride(0), k.stride(1), k.stride(2)
-        if heads == 1:
-            a.head_stride = max(a.head_stride, dim)
-        a.k_scales, a.v_scales = k_scale.data_ptr(), v_scale.data_ptr()
-        a.scale_block_stride, a.scale_head_stride = k_scale.stride(0), k_scale.stride(1)
-        self.args = a
+        self.scale_tokens, self.device = bs // groups, dev
+        self.args = SpecKVCache(nb, bs, bs // groups, heads, dim, k.data_ptr(), v.data_ptr(), st[0], st[1],
+                                st[2] if heads > 1 else dim, k_scale.data_ptr(), v_scale.data_ptr(), sst[0],
+                                sst[1] if heads > 1 else groups)
 
 
 def make_kv_cache(num_blocks, block_size, heads, head_dim, scale_tokens=None, device="cuda"):
@@ -885,26 +903,6 @@ def make_kv_cache(num_blocks, block_size, heads, head_dim, scale_tokens=None, de
     return KVCache(*codes, *scales)
 
 
-def kv_write_args(cache, key, value, slots):
-    """Fill a SpecKVWriteArgs (no copies): key and value [N, heads, head_dim]
-    with unit stride along head_dim, slots [N] int64 (-1: not written)."""
-    torch = _torch()
-    _same_device(cache.k, key, value, slots)
-    N = slots.shape[0]
-    _want(slots, torch.int64, (N,), "slots")
-    for t in (key, value):
-        if t.shape != (N, cache.heads, cache.head_dim) or t.stride(2) != 1:
-            raise ValueError("key and value must be [N, heads, head_dim], contiguous along head_dim")
-    if key.dtype != value.dtype:
-        raise TypeError("key and value must share a dtype")
-    a = SpecKVWriteArgs()
-    a.cache, a.N, a.dtype = cache.args, N, _kv_dtype(key.dtype)
-    a.key, a.value, a.slots = key.data_ptr(), value.data_ptr(), slots.data_ptr()
-    a.k_token_stride, a.k_head_stride = key.stride(0), key.stride(1)
-    a.v_token_stride, a.v_head_stride = value.stride(0), value.stride(1)
-    return a
-
-
 def _kv_dtype(dtype):
     torch = _torch()
     if dtype == torch.bfloat16:
@@ -914,12 +912,29 @@ def _kv_dtype(dtype):
     raise TypeError("keys and values must be bfloat16 or float32, got %s" % dtype)
 
 
+def kv_write_args(cache, key, value, slots):
+    """Fill a SpecKVWriteArgs (no copies): key and value [N, heads, head_dim]
+    with unit stride along head_dim, slots [N] int64 (-1: not written)."""
+    N, dev = slots.shape[0], cache.device
+    shape = (N, cache.heads, cache.head_dim)
+    k0, k1, k2 = key.stride() if key.dim() == 3 else (0, 0, 0)
+    v0, v1, v2 = value.stride() if value.dim() == 3 else (0, 0, 0)
+    if key.shape != shape or value.shape != shape or k2 != 1 or v2 != 1:
+        raise ValueError("key and value must be [N, heads, head_dim], contiguous along head_dim")
+    if key.dtype != value.dtype:
+        raise TypeError("key and value must share a dtype")
+    if key.device != dev or value.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    return SpecKVWriteArgs(cache.args, N, _kv_dtype(key.dtype), key.data_ptr(), value.data_ptr(), k0, k1, v0, v1,
+                           _want(slots, _torch().int64, (N,), dev, "slots"))
+
+
 def kv_write(cache, key, value, slots, stream=None):
     """Quantise keys and values [N, heads, head_dim] into the cache at slots
     [N] int64 (the slot_mapping of an expansion; -1 is skipped); returns the
     cache."""
-    with _on(cache.k, stream) as s:
-        rc = spec_kv_write_launch(kv_write_args(cache, key, value, slots), s)
+    with _on(cache.device, stream) as s:
+        rc = lib.spec_kv_write_launch(kv_write_args(cache, key, value, slots), s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return cache
@@ -929,25 +944,20 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
     """Keys and values [N, heads, head_dim] at slots [N] int64, bfloat16 (the
     default) or float32, zeros where a slot is -1."""
     torch = _torch()
-    _same_device(cache.k, slots)
-    N = slots.shape[0]
-    _want(slots, torch.int64, (N,), "slots")
+    N, dev = slots.shape[0], cache.device
     shape = (N, cache.heads, cache.head_dim)
-    with _on(cache.k, stream) as s:
+    with _on(cache.device, stream) as s:
         if out is None:
             dt = torch.bfloat16 if dtype is None else dtype
-            key = torch.empty(shape, dtype=dt, device=cache.device)
-            value = torch.empty(shape, dtype=dt, device=cache.device)
+            key, value = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
         else:
             key, value = out
-            _same_device(cache.k, key, value)
             dt = key.dtype if dtype is None else dtype
-            _want(key, dt, shape, "key")
-            _want(value, dt, shape, "value")
-        a = SpecKVReadArgs()
-        a.cache, a.N, a.dtype = cache.args, N, _kv_dtype(dt)
-        a.key, a.value, a.slots = key.data_ptr(), value.data_ptr(), slots.data_ptr()
-        rc = spec_kv_read_launch(a, s)
+            _want(key, dt, shape, dev, "key")
+            _want(value, dt, shape, dev, "value")
+        a = SpecKVReadArgs(cache.args, N, _kv_dtype(dt), key.data_ptr(), value.data_ptr(),
+                           _want(slots, torch.int64, (N,), dev, "slots"))
+        rc = lib.spec_kv_read_launch(a, s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return key, value
@@ -960,37 +970,27 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
     free), q_start [B + 1] and ctx_len [B] int32, sinks [q_heads] float32,
     out [N, q_heads, head_dim] bfloat16, lse [N, q_heads] float32."""
     torch = _torch()
-    _same_device(cache.k, q, block_table, q_start, ctx_len, sinks, out, lse, workspace)
+    dev = cache.device
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.stride(2) != 1:
         raise ValueError("q must be [N, q_heads, head_dim], contiguous along head_dim")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16, got %s" % q.dtype)
-    N, Hq = q.shape[0], q.shape[1]
+    N, Hq, D = q.shape
     B = ctx_len.shape[0]
-    _want(ctx_len, torch.int32, (B,), "ctx_len")
-    _want(q_start, torch.int32, (B + 1,), "q_start")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
             (block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError("block_table must be int32 [B, max_blocks] with unit column stride")
-    if sinks is not None:
-        _want(sinks, torch.float32, (Hq,), "sinks")
-    _want(out, torch.bfloat16, (N, Hq, cache.head_dim), "out")
-    if lse is not None:
-        _want(lse, torch.float32, (N, Hq), "lse")
-    a = SpecAttnArgs()
-    a.cache, a.B, a.N, a.q_heads = cache.args, B, N, Hq
-    a.max_q, a.max_ctx, a.window, a.dtype, a.scale = int(max_q), int(max_ctx), int(window), SPEC_BF16, float(scale)
-    a.q, a.q_token_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
-    a.q_start, a.ctx_len = q_start.data_ptr(), ctx_len.data_ptr()
-    a.max_blocks = block_table.shape[1]
-    a.block_table = block_table.data_ptr()
-    a.bt_row_stride = block_table.stride(0) if B > 1 else a.max_blocks
-    a.sinks = None if sinks is None else sinks.data_ptr()
-    a.out = out.data_ptr()
-    a.lse = None if lse is None else lse.data_ptr()
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), _bytes_of(workspace)
-    return a
+    if q.device != dev or block_table.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    max_blocks = block_table.shape[1]
+    ws = _want_workspace(workspace, dev)
+    return SpecAttnArgs(
+        cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q.stride(0), q.stride(1),
+        _want(q_start, torch.int32, (B + 1,), dev, "q_start"), _want(ctx_len, torch.int32, (B,), dev, "ctx_len"),
+        block_table.data_ptr(), block_table.stride(0) if B > 1 else max_blocks, max_blocks,
+        None if sinks is None else _want(sinks, torch.float32, (Hq,), dev, "sinks"),
+        _want(out, torch.bfloat16, (N, Hq, D), dev, "out"),
+        None if lse is None else _want(lse, torch.float32, (N, Hq), dev, "lse"), ws[0], ws[1])
 
 
 def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, scale=None, window=0, sinks=None,
@@ -1001,26 +1001,26 @@ def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, s
     bound the new tokens and the context of a request (max_ctx defaults to
     what the block table holds); scale defaults to head_dim ** -0.5; window >
     0 sees only the last `window` positions; sinks [q_heads] float32 take part
-    in the softmax without a value.  Returns (out, lse or None)."""
+    in the softmax without a value.  Returns (out, lse or None); rows of `out`
+    and lse outside every request's range are not written."""
     torch = _torch()
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [N, q_heads, head_dim] and block_table [B, max_blocks]")
+    dev = cache.device
     if max_ctx is None:
-        max_ctx = min(block_table.shape[1] * cache.block_size, 1 << 30)
+        max_ctx = min(block_table.shape[-1] * cache.block_size, 1 << 30)
     if scale is None:
         scale = cache.head_dim ** -0.5
-    with _on(cache.k, stream) as s:
+    with _on(cache.device, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device) if return_lse else None
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
         a = kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse, window, sinks,
                               workspace)
         if workspace is None:
-            n = spec_attn_workspace_bytes(a)
+            n = lib.spec_attn_workspace_bytes(a)
             if n:
-                workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
                 a.workspace, a.workspace_bytes = workspace.data_ptr(), n
-        rc = spec_attn_launch(a, s)
+        rc = lib.spec_attn_launch(a, s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return out, lse

@@ -682,7 +682,6 @@ size_t spec_logprobs_workspace_bytes(int32_t B, int32_t R, int32_t V, int32_t to
 int spec_logprobs_launch(const spec_logprobs_args* a, hipStream_t stream) {
   const int rc = logprobs_check(a);
   if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
-  const int es = a->dtype == SPEC_BF16 ? 2 : 4;
   LogprobsParams P;
   P.B = a->B;
   P.R = a->R;
@@ -702,8 +701,7 @@ int spec_logprobs_launch(const spec_logprobs_args* a, hipStream_t stream) {
   char* ws = static_cast<char*>(a->workspace);
   P.rec = reinterpret_cast<LpRecord*>(ws);
   P.cells = reinterpret_cast<float*>(ws + align256((size_t)a->B * a->R * P.nseg * sizeof(LpRecord)));
-  const bool vec = aligned16(a->logits) && (a->row_stride * es) % 16 == 0 && (a->req_stride * es) % 16 == 0;
-  return launch_logprobs(P, a->dtype, vec, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+  return launch_logprobs(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }
 
 int spec_kv_write_launch(const spec_kv_write_args* a, hipStream_t stream) {

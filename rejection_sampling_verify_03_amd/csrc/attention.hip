@@ -23,8 +23,8 @@
 //   slot 8 g + j  =  key 4 g + j (j < 4),  key 16 + 4 g + j - 4 (j >= 4)
 // that is where the second product wants P^T: the weights never leave their
 // lanes.  The order of the sum over dims is free too: lane group g takes
-// dims [g DP/4, (g+1) DP/4) of the keys, so a key is read in whole 16-byte
-// loads.  The codes widen to bf16 exactly, scale included (one instruction
+// dims 64 w + 16 g ..+ 16 of the keys, so that keys are read in 16-byte loads
+// of which four lanes' stand together.  The codes widen to bf16 exactly, scale included (one instruction
 // for two); the values' bytes, which lie along dims, are first transposed
 // four by four in registers.
 //
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   uint32_t koff[W];
 #pragma unroll
   for (int w = 0; w < W; ++w)
-    koff[w] = (uint32_t)(r * tok_stride + (g * (DP / 4) + w * 16 < dim ? g * (DP / 4) + w * 16 : 0));
+    koff[w] = (uint32_t)(r * tok_stride + (w * 64 + g * 16 < dim ? w * 64 + g * 16 : 0));
   const uint32_t voff = (uint32_t)(4 * g * tok_stride + (r * (DP / 16) < dim ? r * (DP / 16) : 0));
   const Unit un = unit_of(P, v, RT * 16);
   const int len = min(left, un.tiles - at);  // of this unit
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   const int nt = (len - wave + kWaves - 1) / kWaves;
 
   // Q, to become the fragments of the first product in LDS: fragment (rt, c),
-  // lane l: row 16 rt + l % 16, dims (l / 16) DP/4 + 8 c ..+ 8
+  // lane l: row 16 rt + l % 16, dims 64 (c / 2) + 16 (l / 16) + 8 (c % 2) ..+ 8
   constexpr int QF = (RT * C * 64 + kWG - 1) / kWG;
   u32x4 qreg[QF];
 #pragma unroll
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     const int f = tid + i * kWG;
     const int l = f & 63, cc = (f >> 6) % C, rt = (f >> 6) / C;
     const int k = rt * 16 + (l & 15);
-    const int d = (l >> 4) * (DP / 4) + 8 * cc;
+    const int d = (cc >> 1) * 64 + (l >> 4) * 16 + (cc & 1) * 8;
     qreg[i] = u32x4{0, 0, 0, 0};
     if (k < un.rows && d < P->c.dim) {
       const int t = div_group(P, un.h0 + k);
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   };
   auto lane64 = [&](int lo, int hi, int l) { return ((int64_t)lane_i(hi, l) << 32) | (uint32_t)lane_i(lo, l); };
 
-  // subtile u: key l % 16, dims [g DP/4, (g+1) DP/4); slot j's key, dims
+  // subtile u: key l % 16, dims 64 w + 16 g ..+ 16; slot j's key, dims
   // [r DP/16, (r+1) DP/16)
   struct Buffer {
     u32x4 k[2][W];

@@ -5,9 +5,7 @@
 // t_v = (x_v - m) * s:  S = sum 2^t_v,  W = sum 2^t_v t_v,
 //   ln p(v) = (x_v - m) / T - ln S,   entropy = ln S - ln 2 * W / S,
 // so one pass that keeps (m, S, W) gives both.  A lane sums its 64 terms in
-// fp32 (the largest logit's are exactly 1 and 0), all further sums are in
-// double.  The differences x - m are formed before they are scaled, so no
-// range of logits or temperatures is lost.
+// fp32, and so do the lanes of a segment; segments are joined in double.
 //
 // Two kernels, one read of each row:
 //
@@ -28,18 +26,42 @@
 
 #include "device_common.hpp"
 #include "ops_kernels.hpp"
-#include "sampling.hpp"
 
 namespace specv {
 
-// Maximum over each run of 8 lanes, the same in all of them (DPP: mirrored
-// half rows, then quads).
-__device__ __forceinline__ float max8_lanes(float x) {
-  const int ninf = __float_as_int(-INFINITY);
-  x = fmaxf(x, __int_as_float(dpp_i<0x141, 0xf>(__float_as_int(x), ninf)));  // lane i with 7 - i
-  x = fmaxf(x, __int_as_float(dpp_i<0xb1, 0xf>(__float_as_int(x), ninf)));   // quad [1, 0, 3, 2]
-  x = fmaxf(x, __int_as_float(dpp_i<0x4e, 0xf>(__float_as_int(x), ninf)));   // quad [2, 3, 0, 1]
-  return x;
+// x of another lane of the same 8 (every lane has a source: no fill).
+template <int CTRL>
+__device__ __forceinline__ float dpp_all(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+// Lane i of each 8 gets the maximum of v[i] over the 8: the lanes exchange
+// the half of the values that they do not keep, three times.
+__device__ __forceinline__ float max8_scatter(const float (&v)[8], int lane) {
+  float a[4], b[2];
+  const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // lane i with 7 - i
+    a[i] = fmaxf(h4 ? v[i + 4] : v[i], dpp_all<0x141>(h4 ? v[i] : v[i + 4]));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)  // quad [2, 3, 0, 1]
+    b[i] = fmaxf(h2 ? a[i + 2] : a[i], dpp_all<0x4e>(h2 ? a[i] : a[i + 2]));
+  return fmaxf(h1 ? b[1] : b[0], dpp_all<0xb1>(h1 ? b[0] : b[1]));  // quad [1, 0, 3, 2]
+}
+
+// Sum over the 64 lanes in a fixed order, the same in every lane.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + __int_as_float(dpp_i<CTRL, ROW_MASK>(__float_as_int(x), 0));
+}
+__device__ __forceinline__ float wave_total_f(float x) {
+  x = add_dpp<0x111, 0xf>(x);
+  x = add_dpp<0x112, 0xf>(x);
+  x = add_dpp<0x114, 0xf>(x);
+  x = add_dpp<0x118, 0xf>(x);
+  x = add_dpp<0x142, 0xa>(x);
+  x = add_dpp<0x143, 0xc>(x);
+  return lane_f(x, 63);
 }
 
 __device__ __forceinline__ float row_temperature(const LogprobsParams& P, int b) {
@@ -47,39 +69,88 @@ __device__ __forceinline__ float row_temperature(const LogprobsParams& P, int b)
   return T == 0.0f ? 1.0f : T;
 }
 
-// Sums a segment held in registers against its maximum m.  CLAMP: exponents
-// no lower than -16384, so that a logit of -inf (or one so far below m that
-// its exponent overflows) adds 0 * -16384 and not 0 * -inf to W.
-template <int ES, bool VEC, bool CLAMP>
-__device__ __forceinline__ void segment_sums(RawGroup<ES, VEC> (&rg)[kSegGroups], float m, float s, float& S,
-                                             float& W) {
-  float Sg[kSegGroups], Wg[kSegGroups];
-#pragma unroll
-  for (int g = 0; g < kSegGroups; ++g) {
-    opaque_group<ES, VEC>(rg[g]);
-    float x[8], e[8], w[8];
-    unpack_group<ES, VEC>(rg[g], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float t = (x[i] - m) * s;
-      e[i] = __builtin_amdgcn_exp2f(t);
-      if (CLAMP) t = fmaxf(t, -16384.f);
-      w[i] = t;
-    }
-    Sg[g] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-    float a = e[0] * w[0], b = e[4] * w[4];
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      a = __builtin_fmaf(e[i], w[i], a);
-      b = __builtin_fmaf(e[4 + i], w[4 + i], b);
-    }
-    Wg[g] = a + b;
+// 8 logits as stored, from any element on: the hardware's 16-byte loads need
+// no alignment, so rows of any length and stride take the same path.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+template <int ES>
+__device__ __forceinline__ RawGroup<ES, true> load_any(const char* row, int64_t e0) {
+  RawGroup<ES, true> r;
+  if constexpr (ES == 2) {
+    r.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + e0 * 2));
+  } else {
+    r.a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4));
+    r.b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4 + 16));
   }
-  S = ((Sg[0] + Sg[1]) + (Sg[2] + Sg[3])) + ((Sg[4] + Sg[5]) + (Sg[6] + Sg[7]));
-  W = ((Wg[0] + Wg[1]) + (Wg[2] + Wg[3])) + ((Wg[4] + Wg[5]) + (Wg[6] + Wg[7]));
+  return r;
 }
 
-template <int ES, bool VEC, bool TOP>
+// The same, with -inf for those past the end of the row.
+template <int ES>
+__device__ __forceinline__ RawGroup<ES, true> load_any_bounded(const char* row, int e0, int V) {
+  if (e0 < V && e0 + 8 <= V) return load_any<ES>(row, e0);
+  RawGroup<ES, true> r = neg_inf_group<ES, true>();
+  if (e0 < V) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = e0 + i < V ? load_one<ES>(row, e0 + i) : -INFINITY;
+    if constexpr (ES == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xffff0000u);
+      r.v = u32x4{w[0], w[1], w[2], w[3]};
+    } else {
+      r.a = f32x4{x[0], x[1], x[2], x[3]};
+      r.b = f32x4{x[4], x[5], x[6], x[7]};
+    }
+  }
+  return r;
+}
+
+// The places n and up of a group as `pad` (bf16: its upper half).
+template <int ES>
+__device__ __forceinline__ void pad_group(RawGroup<ES, true>& r, int n, float pad) {
+  if constexpr (ES == 2) {
+    const uint32_t p = __float_as_uint(pad) >> 16;
+    uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = 2 * i + 1 < n ? w[i] : (w[i] & 0xffffu) | (p << 16);
+      w[i] = 2 * i < n ? w[i] : (w[i] & 0xffff0000u) | p;
+    }
+    r.v = u32x4{w[0], w[1], w[2], w[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = i < n ? r.a[i] : pad;
+      r.b[i] = i + 4 < n ? r.b[i] : pad;
+    }
+  }
+}
+
+// The largest of 8 logits, three to an instruction (a NaN shows in S).
+template <int ES>
+__device__ __forceinline__ float group_max(const RawGroup<ES, true>& r) {
+  float x[8];
+  unpack_group<ES, true>(r, x);
+  const float a = fmaxf(fmaxf(x[0], x[1]), x[2]), b = fmaxf(fmaxf(x[3], x[4]), x[5]);
+  return fmaxf(fmaxf(fmaxf(x[6], x[7]), a), b);
+}
+
+// What 8 exponents t add to S and W.
+__device__ __forceinline__ void add_group(const float (&e)[8], const float (&t)[8], float& S, float& W) {
+  S += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+  float a = e[0] * t[0], b = e[4] * t[4];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    a = __builtin_fmaf(e[i], t[i], a);
+    b = __builtin_fmaf(e[4 + i], t[4 + i], b);
+  }
+  W += a + b;
+}
+
+template <int ES, bool TOP>
 __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
   const int c = blockIdx.x % P.C;
   const int i = blockIdx.x / P.C;  // row b * R + r
@@ -93,56 +164,87 @@ __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
   const int j1 = min(P.nseg, (c + 1) * kLpChunkSegs);
   for (int j = c * kLpChunkSegs + wave; j < j1; j += kWaves) {
     const int s0 = j * kSeg;
-    RawGroup<ES, VEC> rg[kSegGroups];
+    RawGroup<ES, true> rg[kSegGroups];
     if (s0 + kSeg <= P.V) {
 #pragma unroll
-      for (int g = 0; g < kSegGroups; ++g) rg[g] = load_raw<ES, VEC>(row, s0 + (g * 64 + lane) * 8);
+      for (int g = 0; g < kSegGroups; ++g) rg[g] = load_any<ES>(row, s0 + (g * 64 + lane) * 8);
     } else {
 #pragma unroll
       for (int g = 0; g < kSegGroups; ++g) {
         const int e = s0 + (g * 64 + lane) * 8;
-        rg[g] = e < P.V ? load_raw_bounded<ES, VEC>(row, e, P.V) : neg_inf_group<ES, VEC>();
+        rg[g] = load_any_bounded<ES>(row, e, P.V);
       }
     }
     float gm[kSegGroups], m = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kSegGroups; ++g) {
-      float x[8];
-      unpack_group<ES, VEC>(rg[g], x);
-      gm[g] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      gm[g] = group_max<ES>(rg[g]);
       m = fmaxf(m, gm[g]);
     }
     m = wave_max_f(m);
     const int64_t rec = (int64_t)i * P.nseg + j;
     if constexpr (TOP) {
-      // lane 8j + q ends with the maximum of cell 8q + j
-      float v = 0.f;
+      // lane 8j + q holds the maximum of cell 8q + j
+      P.cells[rec * kLpCells + (lane & 7) * 8 + (lane >> 3)] = max8_scatter(gm, lane);
+    }
+    float S = 0.f, W = 0.f;
+    // the exponents (x - m) s as x s - c, c = m s rounded: what c is off by
+    // (eps) is the same in all of them and taken out of the sums at the end
+    const float c = m * s, eps = __builtin_fmaf(m, s, -c);
+    if (s0 + kSeg > P.V) {
+      // the places past the row's end: so far below the maximum that 2^t is 0,
+      // but finite
+      const float pad = m - 16384.f / s;
+#pragma unroll
+      for (int g = 0; g < kSegGroups; ++g) pad_group<ES>(rg[g], P.V - (s0 + (g * 64 + lane) * 8), pad);
+    }
+    bool again = !(fabsf(c) <= 0x1p24f);
+    if (!again) {
 #pragma unroll
       for (int g = 0; g < kSegGroups; ++g) {
-        const float cm = max8_lanes(gm[g]);
-        v = (lane & 7) == g ? cm : v;
-      }
-      P.cells[rec * kLpCells + (lane & 7) * 8 + (lane >> 3)] = v;
-    }
-    float S, W;
-    if (m > -INFINITY) {
-      segment_sums<ES, VEC, false>(rg, m, s, S, W);
-      if (__ballot(W != W)) segment_sums<ES, VEC, true>(rg, m, s, S, W);
-    } else {
-      // no logit above -inf: nothing to add, unless a NaN hides among them
-      bool nan = false;
+        opaque_group<ES, true>(rg[g]);
+        float x[8], e[8];
+        unpack_group<ES, true>(rg[g], x);
 #pragma unroll
-      for (int g = 0; g < kSegGroups; ++g) {
-        float x[8];
-        unpack_group<ES, VEC>(rg[g], x);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) nan |= x[q] != x[q];
+        for (int i = 0; i < 8; ++i) {
+          x[i] = __builtin_fmaf(x[i], s, -c);
+          e[i] = __builtin_amdgcn_exp2f(x[i]);
+        }
+        add_group(e, x, S, W);
       }
-      S = nan ? __builtin_nanf("") : 0.f;
-      W = 0.f;
+      const float f = __builtin_amdgcn_exp2f(-eps);
+      W = __builtin_fmaf(-eps, S, W) * f;
+      S *= f;
+      again = __ballot(W != W) != 0;
     }
-    const double Sd = wave_total_d((double)S), Wd = wave_total_d((double)W);
-    if (lane == 0) P.rec[rec] = LpRecord{Sd, Wd, m, 0};
+    if (again) {
+      // logits of -inf (0 * -inf in W: exponents no lower than -16384 here), a
+      // range that c does not hold, a NaN or +inf, or nothing above -inf: the
+      // logits once more, one group after another (a second copy of the sums
+      // from registers would double their number)
+      S = W = 0.f;
+#pragma unroll 1
+      for (int g = 0; g < kSegGroups && s0 + g * 512 < P.V; ++g) {
+        float x[8], e[8];
+        unpack_group<ES, true>(load_any_bounded<ES>(row, s0 + (g * 64 + lane) * 8, P.V), x);
+        if (m > -INFINITY) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float t = (x[i] - m) * s;
+            e[i] = __builtin_amdgcn_exp2f(t);
+            x[i] = fmaxf(t, -16384.f);
+          }
+          add_group(e, x, S, W);
+        } else {
+          // only -inf adds nothing, but a NaN or +inf may hide among it
+#pragma unroll
+          for (int i = 0; i < 8; ++i) S = x[i] == -INFINITY ? S : __builtin_nanf("");
+        }
+      }
+    }
+    S = wave_total_f(S);
+    W = wave_total_f(W);
+    if (lane == 0) P.rec[rec] = LpRecord{m, S, W, 0.f};
   }
 }
 
@@ -175,26 +277,53 @@ __device__ __forceinline__ int nth_largest(const int (&k)[K], int n) {
 
 constexpr int kLpList = 256;  // candidates a wave can hold, 4 per lane
 
-// Appends the lanes' items (those of ascending lanes first) whose key
-// reaches thr to a list in LDS: all above it, and of those equal to it the
-// first n.  Counts what it would have appended past the list's end too.
-struct LpCollect {
+// Candidates in LDS, in ascending order of their ids: all whose key is above
+// the threshold, and of those equal to it the first n.  What the list cannot
+// hold is counted all the same.
+struct LpList {
+  int* keys;
+  int* ids;
   int count, equal;  // appended (or past the end), of them equal to the threshold
 };
-__device__ __forceinline__ void collect(LpCollect& st, int* keys, int* ids, int lane, bool in, int key, int id, int thr,
-                                        int n) {
-  const uint64_t eq = __ballot(in && key == thr);
-  const uint64_t below = lane ? (~0ull >> (64 - lane)) : 0ull;
-  const bool take = in && (key > thr || (key == thr && st.equal + __builtin_popcountll(eq & below) < n));
-  const uint64_t tk = __ballot(take);
-  if (tk == 0) return;
-  const int at = st.count + __builtin_popcountll(tk & below);
-  if (take && at < kLpList) {
-    keys[at] = key;
-    ids[at] = id;
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Appends from each lane Q items with consecutive ids from `id` on; lanes in
+// ascending order hold ascending ids.
+template <int Q>
+__device__ __forceinline__ void collect(LpList& st, const int (&key)[Q], int id, int thr, int n) {
+  int most = key[0];
+#pragma unroll
+  for (int q = 1; q < Q; ++q) most = max(most, key[q]);
+  if (!__ballot(most >= thr)) return;
+  int rank = st.equal, equal = 0;  // of this lane's first item among those equal to the threshold
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const uint64_t b = __ballot(key[q] == thr);
+    rank += lanes_below(b);
+    equal += __builtin_popcountll(b);
   }
-  st.count += __builtin_popcountll(tk);
-  st.equal += __builtin_popcountll(eq);
+  st.equal += equal;
+  bool take[Q];
+  int at = st.count;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    take[q] = key[q] > thr || (key[q] == thr && rank < n);
+    rank += key[q] == thr;
+    const uint64_t b = __ballot(take[q]);
+    at += lanes_below(b);
+    st.count += __builtin_popcountll(b);
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (take[q] && at < kLpList) {
+      st.keys[at] = key[q];
+      st.ids[at] = id + q;
+    }
+    at += take[q];
+  }
 }
 
 // The n-th largest key of a full list: a threshold above the one it was
@@ -206,98 +335,115 @@ __device__ __forceinline__ int raise_threshold(const int* keys, int lane, int n)
   return nth_largest<kLpList / 64>(k, n);
 }
 
-// The alternatives of one row: ids and keys of the n largest logits above
-// -inf in out_ids / out_keys (lane p the p-th), -1 where there are fewer.
-template <int ES, bool VEC>
+// The alternatives of one row: ids and values of the n largest logits above
+// -inf (lane p the p-th), -1 where there are fewer.  Every read of a step is
+// on its way before the first is used: a row is one wave's chain of steps.
+constexpr int kLpWindow = 16;  // loads of 256 cells held at a time: 4096 cells, a row of up to 262144 logits
+template <int ES>
 __device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* row, const float* cells, int n,
-                                           int lane, int* ck, int* ci, int* ek, int* ei, int& out_id, float& out_x) {
-  const int ncell = P.nseg * kLpCells;  // at most 2^25
+                                           int lane, int* lists, int& out_id, float& out_x) {
+  const int ncell = P.nseg * kLpCells;  // at most 2^25, a multiple of 64
   const int kNone = order_key(-INFINITY);
+  const int windows = (ncell + kLpWindow * 256 - 1) / (kLpWindow * 256);
+  f32x4 c[kLpWindow];
+  auto load_window = [&](int w) {
+#pragma unroll
+    for (int j = 0; j < kLpWindow; ++j) {
+      const int at = (w * kLpWindow + j) * 256 + lane * 4;
+      c[j] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (at < ncell) c[j] = *reinterpret_cast<const f32x4*>(cells + at);
+    }
+  };
   // a threshold that at least n cells reach (or -inf: every cell above it)
   float lm = -INFINITY;
-  for (int j = lane; j < ncell; j += 64) lm = fmaxf(lm, cells[j]);
-  const int mk[1] = {order_key(lm)};
-  int thr = max(nth_largest<1>(mk, n), kNone + 1);
-  LpCollect st;
+  for (int w = 0; w < windows; ++w) {
+    load_window(w);
+#pragma unroll
+    for (int j = 0; j < kLpWindow; ++j) lm = fmaxf(fmaxf(fmaxf(c[j].x, c[j].y), fmaxf(c[j].z, c[j].w)), lm);
+  }
+  int thr;
+  if (ncell <= 256) {
+    const int mk[4] = {order_key(c[0].x), order_key(c[0].y), order_key(c[0].z), order_key(c[0].w)};
+    thr = nth_largest<4>(mk, n);
+  } else {
+    const int mk[1] = {order_key(lm)};
+    thr = nth_largest<1>(mk, n);
+  }
+  thr = max(thr, kNone + 1);
+  LpList lc{lists, lists + kLpList, 0, 0};
   for (;;) {
-    st = LpCollect{0, 0};
-    for (int j0 = 0; j0 < ncell; j0 += 64) {
-      const int key = order_key(cells[j0 + lane]);
-      if (__ballot(key >= thr)) collect(st, ck, ci, lane, true, key, j0 + lane, thr, n);
+    lc.count = lc.equal = 0;
+    for (int w = 0; w < windows; ++w) {
+      if (windows > 1) load_window(w);
+#pragma unroll
+      for (int j = 0; j < kLpWindow; ++j) {
+        const int key[4] = {order_key(c[j].x), order_key(c[j].y), order_key(c[j].z), order_key(c[j].w)};
+        collect<4>(lc, key, (w * kLpWindow + j) * 256 + lane * 4, thr, n);
+      }
     }
     __builtin_amdgcn_wave_barrier();
-    if (st.count <= kLpList) break;
-    thr = raise_threshold(ck, lane, n);
+    if (lc.count <= kLpList) break;
+    thr = raise_threshold(lc.keys, lane, n);
   }
-  // the cells' logits that reach the threshold: 8 cells at a time, 8 lanes
-  // to a cell; the cells stand in ascending order, and so do the logits
-  const int nc = st.count;
+  // the cells' logits that reach the threshold: 8 lanes to a cell, 8 cells a
+  // load, 4 loads at a time; the cells stand in ascending order
+  LpList le{lists + 2 * kLpList, lists + 3 * kLpList, 0, 0};
   for (;;) {
-    st = LpCollect{0, 0};
-    for (int c0 = 0; c0 < nc; c0 += 8) {
-      const int c = c0 + (lane >> 3);
-      int key[8];
-      const int e0 = c < nc ? ci[c] * 64 + (lane & 7) * 8 : 0;
-      float x[8];
-      if (c < nc && e0 < P.V) {
-        if (e0 + 8 <= P.V) {
-          load_group<ES, VEC>(row, e0, x);
-        } else {
+    le.count = le.equal = 0;
+    for (int c0 = 0; c0 < lc.count; c0 += 32) {
+      RawGroup<ES, true> rg[4];
+      int e0[4];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = e0 + q < P.V ? load_one<ES>(row, e0 + q) : -INFINITY;
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = -INFINITY;
+      for (int j = 0; j < 4; ++j) {
+        const int at = c0 + j * 8 + (lane >> 3);
+        e0[j] = at < lc.count ? lc.ids[at] * 64 + (lane & 7) * 8 : P.V;
+        rg[j] = load_any_bounded<ES>(row, e0[j], P.V);
       }
-      int most = kNone;
+      int key[4][8];
+      int most = INT_MIN;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        key[q] = order_key(x[q]);
-        most = max(most, key[q]);
-      }
-      // lanes in ascending order hold ascending indexes; a lane's eight come
-      // one after another
-      uint64_t lanes = __ballot(most >= thr);
-      while (lanes) {
-        const int L = __builtin_ctzll(lanes);
-        lanes &= lanes - 1;
-        int kq = 0;
+      for (int j = 0; j < 4; ++j) {
+        float x[8];
+        unpack_group<ES, true>(rg[j], x);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const int v = lane_i(key[q], L);
-          kq = lane == q ? v : kq;
+          key[j][q] = order_key(x[q]);
+          most = max(most, key[j][q]);
         }
-        collect(st, ek, ei, lane, lane < 8, kq, lane_i(e0, L) + lane, thr, n);
       }
+      // before anything is collected the threshold may rise to what n lanes reach
+      if (c0 == 0) {
+        const int mk[1] = {most};
+        thr = max(thr, nth_largest<1>(mk, n));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) collect<8>(le, key[j], e0[j], thr, n);
     }
     __builtin_amdgcn_wave_barrier();
-    if (st.count <= kLpList) break;
-    thr = raise_threshold(ek, lane, n);
+    if (le.count <= kLpList) break;
+    thr = raise_threshold(le.keys, lane, n);
   }
   // sorted by rank: the place of an item is the number of items in front
-  const int ne = st.count;
-  out_id = -1;
-  out_x = -INFINITY;
-  for (int q = 0; q * 64 < ne; ++q) {
-    const int at = q * 64 + lane;
-    const int key = at < ne ? ek[at] : INT_MIN;
-    const int id = at < ne ? ei[at] : INT_MAX;
+  const int ne = le.count;
+  lc.keys[lane] = kNone;
+  lc.ids[lane] = -1;
+  __builtin_amdgcn_wave_barrier();
+  for (int at = lane; at < ne; at += 64) {
+    const int key = le.keys[at];
     int rank = 0;
-    for (int o = 0; o < ne; ++o) rank += ek[o] > key || (ek[o] == key && o < at);
-    // the lane whose number is an item's place takes it
-    for (uint64_t w = __ballot(at < ne && rank < n); w; w &= w - 1) {
-      const int L = __builtin_ctzll(w);
-      const int p = lane_i(rank, L), k = lane_i(key, L), d = lane_i(id, L);
-      if (lane == p) {
-        out_id = d;
-        out_x = order_value(k);
-      }
+#pragma unroll 8
+    for (int o = 0; o < ne; ++o) rank += le.keys[o] > key || (le.keys[o] == key && o < at);
+    if (rank < n) {
+      lc.keys[rank] = key;
+      lc.ids[rank] = le.ids[at];
     }
   }
+  __builtin_amdgcn_wave_barrier();
+  out_id = lc.ids[lane];
+  out_x = order_value(lc.keys[lane]);
 }
 
-template <int ES, bool VEC, bool TOP>
+template <int ES, bool TOP>
 __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
   __shared__ int lists[TOP ? 4 * kLpList : 1];
   const int i = blockIdx.x, lane = threadIdx.x;
@@ -325,7 +471,7 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
         S1 += f * q.s;
         W1 += f * (q.w + d * q.s);
       } else {
-        S1 += q.s;  // 0, or NaN
+        S1 += (double)q.s;  // 0, or NaN
       }
     }
     S = wave_total_d(S1);
@@ -348,8 +494,7 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
     int id = -1;
     float x = -INFINITY;
     if (good)
-      top_of_row<ES, VEC>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, P.top, lane, lists, lists + kLpList,
-                          lists + 2 * kLpList, lists + 3 * kLpList, id, x);
+      top_of_row<ES>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, P.top, lane, lists, id, x);
     if (lane < P.top) {
       P.top_ids[(int64_t)i * P.top + lane] = id;
       P.top_lp[(int64_t)i * P.top + lane] =
@@ -358,25 +503,20 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
   }
 }
 
-template <int ES, bool VEC, bool TOP>
+template <int ES, bool TOP>
 static hipError_t launch_logprobs_typed(const LogprobsParams& P, hipStream_t stream) {
   const int64_t rows = (int64_t)P.B * P.R;
-  hipLaunchKernelGGL((logprobs_stats_kernel<ES, VEC, TOP>), dim3((unsigned)(rows * P.C)), dim3(kWG), 0, stream, P);
+  hipLaunchKernelGGL((logprobs_stats_kernel<ES, TOP>), dim3((unsigned)(rows * P.C)), dim3(kWG), 0, stream, P);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((logprobs_finish_kernel<ES, VEC, TOP>), dim3((unsigned)rows), dim3(64), 0, stream, P);
+  hipLaunchKernelGGL((logprobs_finish_kernel<ES, TOP>), dim3((unsigned)rows), dim3(64), 0, stream, P);
   return hipGetLastError();
 }
 
-hipError_t launch_logprobs(const LogprobsParams& P, int dtype, bool vec, hipStream_t stream) {
-  if (dtype == SPEC_BF16) {
-    if (P.top > 0)
-      return vec ? launch_logprobs_typed<2, true, true>(P, stream) : launch_logprobs_typed<2, false, true>(P, stream);
-    return vec ? launch_logprobs_typed<2, true, false>(P, stream) : launch_logprobs_typed<2, false, false>(P, stream);
-  }
-  if (P.top > 0)
-    return vec ? launch_logprobs_typed<4, true, true>(P, stream) : launch_logprobs_typed<4, false, true>(P, stream);
-  return vec ? launch_logprobs_typed<4, true, false>(P, stream) : launch_logprobs_typed<4, false, false>(P, stream);
+hipError_t launch_logprobs(const LogprobsParams& P, int dtype, hipStream_t stream) {
+  if (dtype == SPEC_BF16)
+    return P.top > 0 ? launch_logprobs_typed<2, true>(P, stream) : launch_logprobs_typed<2, false>(P, stream);
+  return P.top > 0 ? launch_logprobs_typed<4, true>(P, stream) : launch_logprobs_typed<4, false>(P, stream);
 }
 
 }  // namespace specv

@@ -13,12 +13,12 @@ namespace specv {
 
 // ------------------------------------------------------ log probabilities --
 struct LpRecord {  // one 4096-logit segment of a row
-  double s;        // sum of 2^((x - m) * log2(e) / T)
-  double w;        // sum of the same times its exponent
   float m;         // largest logit
-  int32_t pad;
+  float s;         // sum of 2^((x - m) * log2(e) / T)
+  float w;         // sum of the same times its exponent
+  float pad;
 };
-static_assert(sizeof(LpRecord) == 24, "LpRecord layout");
+static_assert(sizeof(LpRecord) == 16, "LpRecord layout");
 
 constexpr int kLpCells = 64;     // cells of 64 consecutive logits in a segment
 constexpr int kLpChunkSegs = 8;  // segments per workgroup of the statistics pass
@@ -37,7 +37,7 @@ struct LogprobsParams {
   float* cells;    // [B * R, nseg, kLpCells] largest logit of each cell (top > 0)
 };
 
-hipError_t launch_logprobs(const LogprobsParams& P, int dtype, bool vec, hipStream_t stream);
+hipError_t launch_logprobs(const LogprobsParams& P, int dtype, hipStream_t stream);
 
 // ------------------------------------------------------------ paged cache --
 struct CacheView {

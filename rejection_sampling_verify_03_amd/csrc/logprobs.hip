@@ -15,14 +15,16 @@
 //      writes the maximum of every cell of 64 consecutive logits, 1/64 of the
 //      row.
 //
-//  logprobs_finish  one wave per row: merges the segments' records and finds
+//  logprobs_finish  one wave per row (for rows that one workgroup holds, its
+//      first wave): merges the segments' records and finds
 //      the alternatives through the cells: the n largest logits lie in the n
 //      cells with the largest maxima (lower cell first on ties: a cell's
 //      logits all stand in front of the next cell's).  A threshold that at
-//      least n cells reach (the n-th largest of the 64 lanes' maxima) picks
-//      a few more than n cells, whose logits are read again; those that reach
-//      it are sorted.
+//      least n of the 64 lanes' maxima reach picks a few more than n cells,
+//      whose logits are read again; those that reach it are sorted.
 #include <limits.h>
+
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "ops_kernels.hpp"
@@ -150,18 +152,331 @@ __device__ __forceinline__ void add_group(const float (&e)[8], const float (&t)[
   W += a + b;
 }
 
+// A float's place in the order of floats as a signed integer (-0 as +0).
+__device__ __forceinline__ int order_key(float x) {
+  const int k = __float_as_int(x + 0.0f);
+  return k < 0 ? (int)0x80000000 - k : k;
+}
+__device__ __forceinline__ float order_value(int k) {
+  return __int_as_float(k < 0 ? (int)0x80000000 - k : k);
+}
+
+// A bound that at least n of the 64 * K keys of a wave reach (1 <= n <=
+// 64 * K), and as few more as kSpare where the keys differ: the range below
+// the largest key is widened until it holds n, then halved.
+constexpr int kSpare = 8;
+template <int K>
+__device__ __forceinline__ int reach_bound(const int (&k)[K], int n) {
+  auto count = [&](int bound) {
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < K; ++q) c += __builtin_popcountll(__ballot(k[q] >= bound));
+    return c;
+  };
+  int most = k[0];
+#pragma unroll
+  for (int q = 1; q < K; ++q) most = max(most, k[q]);
+  int64_t hi = wave_max_i(most), lo = hi;
+  int c = 0;
+  for (int64_t step = 1 << 20;; step <<= 2) {  // an eighth of a power of two first
+    lo = max(hi - step, (int64_t)INT_MIN);
+    c = count((int)lo);
+    if (c >= n) break;  // (at INT_MIN all 64 * K do)
+    hi = lo - 1;
+  }
+  while (c > n + kSpare && lo < hi) {
+    const int64_t mid = (lo + hi + 1) >> 1;
+    const int m = count((int)mid);
+    if (m >= n) {
+      lo = mid;
+      c = m;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  return (int)lo;
+}
+
+constexpr int kLpList = 256;  // candidates a wave can hold, 4 per lane
+
+// Candidates in LDS, in ascending order of their ids: all whose key is above
+// the threshold, and of those equal to it the first n.  What the list cannot
+// hold is counted all the same.
+struct LpList {
+  int* keys;
+  int* ids;
+  int count, equal;  // appended (or past the end), of them equal to the threshold
+};
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Appends from each lane Q items with consecutive ids from `id` on; lanes in
+// ascending order hold ascending ids.
+template <int Q>
+__device__ __forceinline__ void collect(LpList& st, const int (&key)[Q], int id, int thr, int n) {
+  int most = key[0];
+#pragma unroll
+  for (int q = 1; q < Q; ++q) most = max(most, key[q]);
+  if (!__ballot(most >= thr)) return;
+  int rank = st.equal, equal = 0;  // of this lane's first item among those equal to the threshold
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const uint64_t b = __ballot(key[q] == thr);
+    rank += lanes_below(b);
+    equal += __builtin_popcountll(b);
+  }
+  st.equal += equal;
+  bool take[Q];
+  int at = st.count;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    take[q] = key[q] > thr || (key[q] == thr && rank < n);
+    rank += key[q] == thr;
+    const uint64_t b = __ballot(take[q]);
+    at += lanes_below(b);
+    st.count += __builtin_popcountll(b);
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (take[q] && at < kLpList) {
+      st.keys[at] = key[q];
+      st.ids[at] = id + q;
+    }
+    at += take[q];
+  }
+}
+
+// A bound that at least n of a full list's keys reach, and not all of them: a
+// threshold above the one that the list was collected with.
+__device__ __forceinline__ int raise_threshold(const int* keys, int lane, int n) {
+  int k[kLpList / 64];
+#pragma unroll
+  for (int q = 0; q < kLpList / 64; ++q) k[q] = keys[q * 64 + lane];
+  return reach_bound<kLpList / 64>(k, n);
+}
+
+// The alternatives of one row: ids and values of the n largest logits above
+// -inf (lane p the p-th), -1 where there are fewer.  A row is one wave's chain
+// of steps: the reads of a step are on their way together, and the loops are
+// kept rolled (unrolled, the wave waits for its own instructions).
+constexpr int kLpWindow = 16;  // loads of 256 cells held at a time: 4096 cells, a row of up to 262144 logits
+template <int ES>
+struct LpLists {  // a wave's room in LDS
+  int keys[2][kLpList], ids[2][kLpList];  // candidate cells, candidate logits
+  typename std::conditional<ES == 2, uint2, uint4>::type cells[kLpWindow * 64];  // four to a lane, as stored
+};
+
+template <int ES>
+__device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* row, const float* cells, int n,
+                                           int lane, LpLists<ES>& L, int& out_id, float& out_x) {
+  const int ncell = P.nseg * kLpCells;  // at most 2^25, a multiple of 64
+  const int kNone = order_key(-INFINITY);
+  const int windows = (ncell + kLpWindow * 256 - 1) / (kLpWindow * 256);
+  float lm = -INFINITY;   // the lane's largest
+  f32x4 head{-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // its first four
+  auto load_window = [&](int w) {
+    f32x4 c[kLpWindow];
+#pragma unroll
+    for (int j = 0; j < kLpWindow; ++j) {
+      const int at = (w * kLpWindow + j) * 256 + lane * 4;
+      c[j] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (at < ncell) c[j] = *reinterpret_cast<const f32x4*>(cells + at);
+    }
+    if (w == 0) head = c[0];
+#pragma unroll
+    for (int j = 0; j < kLpWindow; ++j) {
+      lm = fmaxf(fmaxf(fmaxf(c[j].x, c[j].y), fmaxf(c[j].z, c[j].w)), lm);
+      if constexpr (ES == 2)  // exact in bf16
+        L.cells[j * 64 + lane] = uint2{(__float_as_uint(c[j].x) >> 16) | (__float_as_uint(c[j].y) & 0xffff0000u),
+                                       (__float_as_uint(c[j].z) >> 16) | (__float_as_uint(c[j].w) & 0xffff0000u)};
+      else
+        L.cells[j * 64 + lane] = uint4{__float_as_uint(c[j].x), __float_as_uint(c[j].y), __float_as_uint(c[j].z),
+                                       __float_as_uint(c[j].w)};
+    }
+  };
+  // a threshold that at least n cells reach (or -inf: every cell above it)
+  for (int w = 0; w < windows; ++w) load_window(w);
+  int thr;
+  if (ncell <= 256) {
+    const int mk[4] = {order_key(head.x), order_key(head.y), order_key(head.z), order_key(head.w)};
+    thr = reach_bound<4>(mk, n);
+  } else {
+    const int mk[1] = {order_key(lm)};
+    thr = reach_bound<1>(mk, n);
+  }
+  thr = max(thr, kNone + 1);
+  LpList lc{L.keys[0], L.ids[0], 0, 0};
+  for (;;) {
+    lc.count = lc.equal = 0;
+    for (int w = 0; w < windows; ++w) {
+      if (windows > 1) load_window(w);
+      const int loads = min(kLpWindow, (ncell - w * kLpWindow * 256 + 255) / 256);
+#pragma unroll 1
+      for (int j = 0; j < loads; ++j) {
+        int key[4];
+        if constexpr (ES == 2) {
+          const uint2 v = L.cells[j * 64 + lane];
+          key[0] = order_key(__uint_as_float(v.x << 16));
+          key[1] = order_key(__uint_as_float(v.x & 0xffff0000u));
+          key[2] = order_key(__uint_as_float(v.y << 16));
+          key[3] = order_key(__uint_as_float(v.y & 0xffff0000u));
+        } else {
+          const uint4 v = L.cells[j * 64 + lane];
+          key[0] = order_key(__uint_as_float(v.x));
+          key[1] = order_key(__uint_as_float(v.y));
+          key[2] = order_key(__uint_as_float(v.z));
+          key[3] = order_key(__uint_as_float(v.w));
+        }
+        collect<4>(lc, key, (w * kLpWindow + j) * 256 + lane * 4, thr, n);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (lc.count <= kLpList) break;
+    thr = raise_threshold(lc.keys, lane, n);
+  }
+  // the cells' logits that reach the threshold: 8 lanes to a cell, 8 cells a
+  // load, the next load on its way; the cells stand in ascending order
+  LpList le{L.keys[1], L.ids[1], 0, 0};
+  auto first_of = [&](int c0) {
+    const int at = c0 + (lane >> 3);
+    return at < lc.count ? lc.ids[at] * 64 + (lane & 7) * 8 : P.V;
+  };
+  for (;;) {
+    le.count = le.equal = 0;
+    int e1 = first_of(0);
+    RawGroup<ES, true> r1 = load_any_bounded<ES>(row, e1, P.V);
+#pragma unroll 1
+    for (int c0 = 0; c0 < lc.count; c0 += 8) {
+      const int e0 = e1;
+      float x[8];
+      int key[8];
+      unpack_group<ES, true>(r1, x);
+      if (c0 + 8 < lc.count) {
+        e1 = first_of(c0 + 8);
+        r1 = load_any_bounded<ES>(row, e1, P.V);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) key[q] = order_key(x[q]);
+      // before anything is collected the threshold may rise to what n lanes reach
+      if (c0 == 0) {
+        int most = key[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) most = max(most, key[q]);
+        const int mk[1] = {most};
+        thr = max(thr, reach_bound<1>(mk, n));
+      }
+      collect<8>(le, key, e0, thr, n);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (le.count <= kLpList) break;
+    thr = raise_threshold(le.keys, lane, n);
+  }
+  // sorted by rank: the place of an item is the number of items in front
+  const int ne = le.count;
+  lc.keys[lane] = kNone;
+  lc.ids[lane] = -1;
+  __builtin_amdgcn_wave_barrier();
+  for (int at = lane; at < ne; at += 64) {
+    const int key = le.keys[at];
+    int rank = 0;
+#pragma unroll 8
+    for (int o = 0; o < ne; ++o) rank += le.keys[o] > key || (le.keys[o] == key && o < at);
+    if (rank < n) {
+      lc.keys[rank] = key;
+      lc.ids[rank] = le.ids[at];
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  out_id = lc.ids[lane];
+  out_x = order_value(lc.keys[lane]);
+}
+
+// One wave: row i's records joined, its outputs written.
 template <int ES, bool TOP>
+__device__ __forceinline__ void finish_row(const LogprobsParams& P, int i, int lane, LpLists<ES>* lists) {
+  const int b = i / P.R, r = i - b * P.R;
+  const int tok = P.tokens[i];
+  const float T = row_temperature(P, b);
+  const float nan = __builtin_nanf("");
+  const bool usable = tok >= 0 && tok < P.V && temperature_valid(T);
+  double M = -INFINITY, S = 0.0, W = 0.0;
+  if (usable) {
+    // the records' sums, each brought to the row's maximum: the exponents
+    // shift by d = (m - M) * s <= 0, so S by 2^d and W to 2^d (W + d S)
+    const LpRecord* rec = P.rec + (int64_t)i * P.nseg;
+    const double s = 1.4426950408889634074 / (double)T;
+    float mm = -INFINITY;
+    for (int j = lane; j < P.nseg; j += 64) mm = fmaxf(mm, rec[j].m);
+    mm = wave_max_f(mm);
+    M = mm;
+    double S1 = 0.0, W1 = 0.0;
+    for (int j = lane; j < P.nseg; j += 64) {
+      const LpRecord q = rec[j];
+      if (q.m > -INFINITY) {
+        const double d = fmax(((double)q.m - M) * s, -4000.0);
+        const double f = exp2(d);
+        S1 += f * q.s;
+        W1 += f * (q.w + d * q.s);
+      } else {
+        S1 += (double)q.s;  // 0, or NaN
+      }
+    }
+    S = wave_total_d(S1);
+    W = wave_total_d(W1);
+  }
+  const bool good = usable && S > 0.0 && S <= DBL_MAX && fabs(M) <= FLT_MAX;
+  const char* row = P.logits + (b * P.req + r * P.row) * ES;
+  const double lnS = good ? log(S) : 0.0;
+  if (lane == 0) {
+    float lp = tok == -1 ? 0.f : nan, ent = lp;
+    if (good) {
+      const double x = load_one<ES>(row, tok);
+      lp = (float)((x - M) / (double)T - lnS);
+      ent = (float)fmax(lnS - 0.69314718055994530942 * (W / S), 0.0);
+    }
+    P.logprobs[i] = lp;
+    if (P.entropy) P.entropy[i] = ent;
+  }
+  if constexpr (TOP) {
+    int id = -1;
+    float x = -INFINITY;
+    if (good)
+      top_of_row<ES>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, P.top, lane, *lists, id, x);
+    if (lane < P.top) {
+      P.top_ids[(int64_t)i * P.top + lane] = id;
+      P.top_lp[(int64_t)i * P.top + lane] =
+          good ? (float)(((double)x - M) / (double)T - lnS) : (tok == -1 ? 0.f : nan);
+    }
+  }
+}
+
+template <int ES, bool TOP>
+__global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
+  if constexpr (TOP) {
+    __shared__ LpLists<ES> lists;
+    finish_row<ES, true>(P, blockIdx.x, threadIdx.x, &lists);
+  } else {
+    finish_row<ES, false>(P, blockIdx.x, threadIdx.x, nullptr);
+  }
+}
+
+// WHOLE: a workgroup holds a whole row (P.C == 1), and its first wave finishes
+// it (no second launch: 4 us less of the 15 us of a small batch).
+template <int ES, bool TOP, bool WHOLE>
 __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
   const int c = blockIdx.x % P.C;
   const int i = blockIdx.x / P.C;  // row b * R + r
   const int b = i / P.R, r = i - b * P.R;
   const int tok = P.tokens[i];
   const float T = row_temperature(P, b);
-  if (tok < 0 || tok >= P.V || !temperature_valid(T)) return;  // the finish reports it
+  const bool usable = tok >= 0 && tok < P.V && temperature_valid(T);  // the finish reports the others
+  if (!WHOLE && !usable) return;
   const char* row = P.logits + (b * P.req + r * P.row) * ES;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float s = (float)(1.4426950408889634074 / (double)T);
-  const int j1 = min(P.nseg, (c + 1) * kLpChunkSegs);
+  const int j1 = usable ? min(P.nseg, (c + 1) * kLpChunkSegs) : 0;
   for (int j = c * kLpChunkSegs + wave; j < j1; j += kWaves) {
     const int s0 = j * kSeg;
     RawGroup<ES, true> rg[kSegGroups];
@@ -246,259 +561,14 @@ __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
     W = wave_total_f(W);
     if (lane == 0) P.rec[rec] = LpRecord{m, S, W, 0.f};
   }
-}
-
-// A float's place in the order of floats as a signed integer (-0 as +0).
-__device__ __forceinline__ int order_key(float x) {
-  const int k = __float_as_int(x + 0.0f);
-  return k < 0 ? (int)0x80000000 - k : k;
-}
-__device__ __forceinline__ float order_value(int k) {
-  return __int_as_float(k < 0 ? (int)0x80000000 - k : k);
-}
-
-// The n-th largest of the 64 * K keys of a wave (1 <= n <= 64 * K), by
-// halving the range that holds it.
-template <int K>
-__device__ __forceinline__ int nth_largest(const int (&k)[K], int n) {
-  int lo = INT_MIN, hi = INT_MAX;  // the largest bound that at least n keys reach
-  while (lo < hi) {
-    const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-    int cnt = 0;
-#pragma unroll
-    for (int q = 0; q < K; ++q) cnt += __builtin_popcountll(__ballot(k[q] >= mid));
-    if (cnt >= n)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
-}
-
-constexpr int kLpList = 256;  // candidates a wave can hold, 4 per lane
-
-// Candidates in LDS, in ascending order of their ids: all whose key is above
-// the threshold, and of those equal to it the first n.  What the list cannot
-// hold is counted all the same.
-struct LpList {
-  int* keys;
-  int* ids;
-  int count, equal;  // appended (or past the end), of them equal to the threshold
-};
-
-__device__ __forceinline__ int lanes_below(uint64_t mask) {
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-}
-
-// Appends from each lane Q items with consecutive ids from `id` on; lanes in
-// ascending order hold ascending ids.
-template <int Q>
-__device__ __forceinline__ void collect(LpList& st, const int (&key)[Q], int id, int thr, int n) {
-  int most = key[0];
-#pragma unroll
-  for (int q = 1; q < Q; ++q) most = max(most, key[q]);
-  if (!__ballot(most >= thr)) return;
-  int rank = st.equal, equal = 0;  // of this lane's first item among those equal to the threshold
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const uint64_t b = __ballot(key[q] == thr);
-    rank += lanes_below(b);
-    equal += __builtin_popcountll(b);
-  }
-  st.equal += equal;
-  bool take[Q];
-  int at = st.count;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    take[q] = key[q] > thr || (key[q] == thr && rank < n);
-    rank += key[q] == thr;
-    const uint64_t b = __ballot(take[q]);
-    at += lanes_below(b);
-    st.count += __builtin_popcountll(b);
-  }
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    if (take[q] && at < kLpList) {
-      st.keys[at] = key[q];
-      st.ids[at] = id + q;
-    }
-    at += take[q];
-  }
-}
-
-// The n-th largest key of a full list: a threshold above the one it was
-// collected with that at least n of all items still reach.
-__device__ __forceinline__ int raise_threshold(const int* keys, int lane, int n) {
-  int k[kLpList / 64];
-#pragma unroll
-  for (int q = 0; q < kLpList / 64; ++q) k[q] = keys[q * 64 + lane];
-  return nth_largest<kLpList / 64>(k, n);
-}
-
-// The alternatives of one row: ids and values of the n largest logits above
-// -inf (lane p the p-th), -1 where there are fewer.  Every read of a step is
-// on its way before the first is used: a row is one wave's chain of steps.
-constexpr int kLpWindow = 16;  // loads of 256 cells held at a time: 4096 cells, a row of up to 262144 logits
-template <int ES>
-__device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* row, const float* cells, int n,
-                                           int lane, int* lists, int& out_id, float& out_x) {
-  const int ncell = P.nseg * kLpCells;  // at most 2^25, a multiple of 64
-  const int kNone = order_key(-INFINITY);
-  const int windows = (ncell + kLpWindow * 256 - 1) / (kLpWindow * 256);
-  f32x4 c[kLpWindow];
-  auto load_window = [&](int w) {
-#pragma unroll
-    for (int j = 0; j < kLpWindow; ++j) {
-      const int at = (w * kLpWindow + j) * 256 + lane * 4;
-      c[j] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (at < ncell) c[j] = *reinterpret_cast<const f32x4*>(cells + at);
-    }
-  };
-  // a threshold that at least n cells reach (or -inf: every cell above it)
-  float lm = -INFINITY;
-  for (int w = 0; w < windows; ++w) {
-    load_window(w);
-#pragma unroll
-    for (int j = 0; j < kLpWindow; ++j) lm = fmaxf(fmaxf(fmaxf(c[j].x, c[j].y), fmaxf(c[j].z, c[j].w)), lm);
-  }
-  int thr;
-  if (ncell <= 256) {
-    const int mk[4] = {order_key(c[0].x), order_key(c[0].y), order_key(c[0].z), order_key(c[0].w)};
-    thr = nth_largest<4>(mk, n);
-  } else {
-    const int mk[1] = {order_key(lm)};
-    thr = nth_largest<1>(mk, n);
-  }
-  thr = max(thr, kNone + 1);
-  LpList lc{lists, lists + kLpList, 0, 0};
-  for (;;) {
-    lc.count = lc.equal = 0;
-    for (int w = 0; w < windows; ++w) {
-      if (windows > 1) load_window(w);
-#pragma unroll
-      for (int j = 0; j < kLpWindow; ++j) {
-        const int key[4] = {order_key(c[j].x), order_key(c[j].y), order_key(c[j].z), order_key(c[j].w)};
-        collect<4>(lc, key, (w * kLpWindow + j) * 256 + lane * 4, thr, n);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (lc.count <= kLpList) break;
-    thr = raise_threshold(lc.keys, lane, n);
-  }
-  // the cells' logits that reach the threshold: 8 lanes to a cell, 8 cells a
-  // load, 4 loads at a time; the cells stand in ascending order
-  LpList le{lists + 2 * kLpList, lists + 3 * kLpList, 0, 0};
-  for (;;) {
-    le.count = le.equal = 0;
-    for (int c0 = 0; c0 < lc.count; c0 += 32) {
-      RawGroup<ES, true> rg[4];
-      int e0[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = c0 + j * 8 + (lane >> 3);
-        e0[j] = at < lc.count ? lc.ids[at] * 64 + (lane & 7) * 8 : P.V;
-        rg[j] = load_any_bounded<ES>(row, e0[j], P.V);
-      }
-      int key[4][8];
-      int most = INT_MIN;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[8];
-        unpack_group<ES, true>(rg[j], x);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          key[j][q] = order_key(x[q]);
-          most = max(most, key[j][q]);
-        }
-      }
-      // before anything is collected the threshold may rise to what n lanes reach
-      if (c0 == 0) {
-        const int mk[1] = {most};
-        thr = max(thr, nth_largest<1>(mk, n));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) collect<8>(le, key[j], e0[j], thr, n);
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (le.count <= kLpList) break;
-    thr = raise_threshold(le.keys, lane, n);
-  }
-  // sorted by rank: the place of an item is the number of items in front
-  const int ne = le.count;
-  lc.keys[lane] = kNone;
-  lc.ids[lane] = -1;
-  __builtin_amdgcn_wave_barrier();
-  for (int at = lane; at < ne; at += 64) {
-    const int key = le.keys[at];
-    int rank = 0;
-#pragma unroll 8
-    for (int o = 0; o < ne; ++o) rank += le.keys[o] > key || (le.keys[o] == key && o < at);
-    if (rank < n) {
-      lc.keys[rank] = key;
-      lc.ids[rank] = le.ids[at];
-    }
-  }
-  __builtin_amdgcn_wave_barrier();
-  out_id = lc.ids[lane];
-  out_x = order_value(lc.keys[lane]);
-}
-
-template <int ES, bool TOP>
-__global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
-  __shared__ int lists[TOP ? 4 * kLpList : 1];
-  const int i = blockIdx.x, lane = threadIdx.x;
-  const int b = i / P.R, r = i - b * P.R;
-  const int tok = P.tokens[i];
-  const float T = row_temperature(P, b);
-  const float nan = __builtin_nanf("");
-  const bool usable = tok >= 0 && tok < P.V && temperature_valid(T);
-  double M = -INFINITY, S = 0.0, W = 0.0;
-  if (usable) {
-    // the records' sums, each brought to the row's maximum: the exponents
-    // shift by d = (m - M) * s <= 0, so S by 2^d and W to 2^d (W + d S)
-    const LpRecord* rec = P.rec + (int64_t)i * P.nseg;
-    const double s = 1.4426950408889634074 / (double)T;
-    float mm = -INFINITY;
-    for (int j = lane; j < P.nseg; j += 64) mm = fmaxf(mm, rec[j].m);
-    mm = wave_max_f(mm);
-    M = mm;
-    double S1 = 0.0, W1 = 0.0;
-    for (int j = lane; j < P.nseg; j += 64) {
-      const LpRecord q = rec[j];
-      if (q.m > -INFINITY) {
-        const double d = fmax(((double)q.m - M) * s, -4000.0);
-        const double f = exp2(d);
-        S1 += f * q.s;
-        W1 += f * (q.w + d * q.s);
-      } else {
-        S1 += (double)q.s;  // 0, or NaN
-      }
-    }
-    S = wave_total_d(S1);
-    W = wave_total_d(W1);
-  }
-  const bool good = usable && S > 0.0 && S <= DBL_MAX && fabs(M) <= FLT_MAX;
-  const char* row = P.logits + (b * P.req + r * P.row) * ES;
-  const double lnS = good ? log(S) : 0.0;
-  if (lane == 0) {
-    float lp = tok == -1 ? 0.f : nan, ent = lp;
-    if (good) {
-      const double x = load_one<ES>(row, tok);
-      lp = (float)((x - M) / (double)T - lnS);
-      ent = (float)fmax(lnS - 0.69314718055994530942 * (W / S), 0.0);
-    }
-    P.logprobs[i] = lp;
-    if (P.entropy) P.entropy[i] = ent;
-  }
-  if constexpr (TOP) {
-    int id = -1;
-    float x = -INFINITY;
-    if (good)
-      top_of_row<ES>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, P.top, lane, lists, id, x);
-    if (lane < P.top) {
-      P.top_ids[(int64_t)i * P.top + lane] = id;
-      P.top_lp[(int64_t)i * P.top + lane] =
-          good ? (float)(((double)x - M) / (double)T - lnS) : (tok == -1 ? 0.f : nan);
+  if constexpr (WHOLE) {
+    __threadfence_block();
+    __syncthreads();
+    if constexpr (TOP) {
+      __shared__ LpLists<ES> lists;
+      if (wave == 0) finish_row<ES, true>(P, i, lane, &lists);
+    } else {
+      if (wave == 0) finish_row<ES, false>(P, i, lane, nullptr);
     }
   }
 }
@@ -506,7 +576,11 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
 template <int ES, bool TOP>
 static hipError_t launch_logprobs_typed(const LogprobsParams& P, hipStream_t stream) {
   const int64_t rows = (int64_t)P.B * P.R;
-  hipLaunchKernelGGL((logprobs_stats_kernel<ES, TOP>), dim3((unsigned)(rows * P.C)), dim3(kWG), 0, stream, P);
+  if (P.C == 1) {
+    hipLaunchKernelGGL((logprobs_stats_kernel<ES, TOP, true>), dim3((unsigned)rows), dim3(kWG), 0, stream, P);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((logprobs_stats_kernel<ES, TOP, false>), dim3((unsigned)(rows * P.C)), dim3(kWG), 0, stream, P);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((logprobs_finish_kernel<ES, TOP>), dim3((unsigned)rows), dim3(64), 0, stream, P);

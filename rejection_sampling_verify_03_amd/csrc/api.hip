@@ -353,7 +353,8 @@ AttnPlan attn_plan(const spec_attn_args* a) {
 size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
   if (p.chunks == 0 || a->B == 0) return 0;
   const size_t parts = (size_t)p.chunks * 2 * a->cache.heads * 16 * p.rt;
-  return align256(parts * a->cache.head_dim * sizeof(float)) + align256(parts * sizeof(float2));
+  return align256(parts * a->cache.head_dim * sizeof(float)) + align256(parts * sizeof(float2)) +
+         align256((size_t)a->B * p.nrb * sizeof(int2));
 }
 
 int attn_check(const spec_attn_args* a, AttnPlan& plan) {
@@ -372,7 +373,7 @@ int attn_check(const spec_attn_args* a, AttnPlan& plan) {
   const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;  // <= 2^31 * 2^10 * 2^26 checked in steps
   if ((int64_t)a->B * a->cache.heads > INT32_MAX || grid / plan.nrb != (int64_t)a->B * a->cache.heads ||
       grid > INT32_MAX || !fits_dispatch((plan.groups + 7) / 8 * 8 * plan.items, kThreads) ||
-      (plan.chunks > 0 && !fits_dispatch(grid, kThreads)))
+      (plan.chunks > 0 && !fits_dispatch(grid * plan.rt, kThreads)))
     return SPEC_EINVAL;
   const size_t need = attn_ws_bytes(a, plan);
   if (need > 0) {
@@ -779,10 +780,13 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.lse = a->lse;
   P.po = static_cast<float*>(a->workspace);
   P.pm = nullptr;
-  if (plan.chunks > 0)
-    P.pm = reinterpret_cast<float2*>(
-        static_cast<char*>(a->workspace) +
-        align256((size_t)plan.chunks * 2 * a->cache.heads * 16 * plan.rt * a->cache.head_dim * sizeof(float)));
+  P.runs = nullptr;
+  if (plan.chunks > 0) {
+    const size_t parts = (size_t)plan.chunks * 2 * a->cache.heads * 16 * plan.rt;
+    char* ws = static_cast<char*>(a->workspace) + align256(parts * a->cache.head_dim * sizeof(float));
+    P.pm = reinterpret_cast<float2*>(ws);
+    P.runs = reinterpret_cast<int2*>(ws + align256(parts * sizeof(float2)));
+  }
   P.qvec = aligned16(a->q) && a->q_token_stride % 8 == 0 && a->q_head_stride % 8 == 0;
   return launch_attn(P, plan, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }

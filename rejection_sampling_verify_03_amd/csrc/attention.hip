@@ -658,6 +658,11 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     }
   }
   }
+  // which runs hold the unit, for the join (one workgroup of the heads tells it)
+  if (P->chunks > 0 && head == 0 && threadIdx.x == 0 && un.tiles > 0) {
+    if (at == 0) P->runs[v].x = grp * 2 + !run_begin;
+    if (at + len == un.tiles) P->runs[v].y = grp;
+  }
   // the next unit of the run
   left -= len;
   at = 0;
@@ -667,36 +672,52 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 }
 
 // Joins the runs of a unit that several hold: one workgroup per (unit, KV
-// head), 4 dims a thread.
-__global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams, int block_rows) {
+// head, 16 rows), 4 dims a thread.
+template <int COLS>  // threads to a row
+__global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams, int row_tiles) {
   const Params P = params_again();
-  const int v = blockIdx.x / P->c.heads, head = blockIdx.x % P->c.heads, lane = threadIdx.x & 63;
-  const Unit u = unit_of(P, v, block_rows);
-  if (u.tiles <= 1) return;
-  const int64_t base = tiles_before(P, v, block_rows, lane);
-  const int64_t per = chunk_tiles(P, tiles_before(P, P->B * P->nrb, block_rows, lane));
-  const int j0 = (int)(base / per), j1 = (int)((base + u.tiles - 1) / per);
-  if (j0 == j1) return;  // written whole
-  const bool late = base > j0 * per;  // its first run began with another unit
-  const int cols = P->c.dim >> 2;
-  for (int cell = threadIdx.x; cell < u.rows * cols; cell += kWG) {
-    const int k = cell / cols, d = (cell - k * cols) * 4;
+  const int rt = blockIdx.x % row_tiles, x = blockIdx.x / row_tiles;
+  const int v = x / P->c.heads, head = x % P->c.heads;
+  const int2 runs = P->runs[v];  // (of a unit without rows: never written, and not used)
+  const Unit u = unit_of(P, v, row_tiles * 16);
+  const int j0 = runs.x >> 1, j1 = runs.y;
+  if (u.bad || u.tiles <= 1 || j0 == j1) return;  // written whole
+  const bool late = runs.x & 1;  // its first run began with another unit
+  const int d = (threadIdx.x % COLS) * 4;
+  for (int kk = threadIdx.x / COLS; kk < 16; kk += kWG / COLS) {
+    const int k = rt * 16 + kk;
+    if (k >= u.rows || d >= P->c.dim) continue;
     const int t = div_group(P, u.h0 + k);
     const int hq = head * P->G + u.h0 + k - t * P->G;
     const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
-    const float sk = P->sinks ? P->sinks[hq] * 1.44269504088896341f : kNoRef;
-    float mx = sk;
-#pragma unroll 8
-    for (int j = j0; j <= j1; ++j) mx = fmaxf(mx, P->pm[part_row(P, j, late && j == j0, head, block_rows, k)].x);
-    float l = P->sinks ? exp2_fast(sk - mx) : 0.f;
+    // eight runs' sums on their way at a time
+    float mx = P->sinks ? P->sinks[hq] * 1.44269504088896341f : kNoRef;
+    float l = P->sinks ? 1.f : 0.f;
     f32x4 o{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int j = j0; j <= j1; ++j) {
-      const int64_t part = part_row(P, j, late && j == j0, head, block_rows, k);
-      const float2 p = P->pm[part];
-      const float f = exp2_fast(p.x - mx);
-      l += p.y * f;
-      o += *reinterpret_cast<const f32x4*>(P->po + part * P->c.dim + d) * f;
+    for (int j = j0; j <= j1; j += 8) {
+      float2 p[8];
+      f32x4 a[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int jj = min(j + q, j1);
+        const int64_t part = part_row(P, jj, late && jj == j0, head, row_tiles * 16, k);
+        p[q] = P->pm[part];
+        a[q] = *reinterpret_cast<const f32x4*>(P->po + part * P->c.dim + d);
+        if (j + q > j1) p[q] = float2{kNoRef, 0.f};
+      }
+      float m = mx;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, p[q].x);
+      const float f = exp2_fast(mx - m);
+      l *= f;
+      o *= f;
+      mx = m;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float w = j + q > j1 ? 0.f : exp2_fast(p[q].x - m);
+        l += p[q].y * w;
+        o += j + q > j1 ? f32x4{0.f, 0.f, 0.f, 0.f} : a[q] * w;
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     uint32_t w[2];
@@ -769,7 +790,13 @@ hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t st
   else
     e = launch_attn_rows<256>(P, plan.rt, stream);
   if (e != hipSuccess || plan.chunks == 0) return e;
-  hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(P.B * P.nrb * P.c.heads)), dim3(kWG), 0, stream, P, plan.rt * 16);
+  const dim3 grid((unsigned)(P.B * P.nrb * P.c.heads * plan.rt));
+  if (P.c.dim <= 64)
+    hipLaunchKernelGGL((attn_join_kernel<16>), grid, dim3(kWG), 0, stream, P, plan.rt);
+  else if (P.c.dim <= 128)
+    hipLaunchKernelGGL((attn_join_kernel<32>), grid, dim3(kWG), 0, stream, P, plan.rt);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<64>), grid, dim3(kWG), 0, stream, P, plan.rt);
   return hipGetLastError();
 }
 

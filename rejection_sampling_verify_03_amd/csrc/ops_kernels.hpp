@@ -91,6 +91,7 @@ struct AttnParams {
   float* lse;
   float* po;   // [chunks, 2, heads, 16 * rt, dim] partial sums (chunks > 0)
   float2* pm;  // [chunks, 2, heads, 16 * rt] their reference exponents and sums of weights
+  int2* runs;  // [B * nrb] the runs that hold each unit: (first * 2 + whether it began with another unit, last)
   int32_t qvec;
 };
 

@@ -646,8 +646,8 @@ typedef struct {
 } spec_attn_args;
 
 /* Bytes of device workspace for these sizes (the sizes alone are read: B, N,
- * q_heads, max_q, max_ctx, window and cache.heads, head_dim, block_size; 0
- * also where they are invalid); stateless, no initialisation; calls that
+ * q_heads, max_q, max_ctx, window and cache.heads, head_dim, token_stride,
+ * head_stride; 0 also where they are invalid); stateless, no initialisation; calls that
  * overlap on one workspace race. */
 size_t spec_attn_workspace_bytes(const spec_attn_args* args);
 int spec_attn_launch(const spec_attn_args* args, hipStream_t stream);

@@ -347,7 +347,7 @@ bool attn_sizes_ok(const spec_attn_args* a) {
 
 AttnPlan attn_plan(const spec_attn_args* a) {
   return plan_attn(a->B, a->q_heads / a->cache.heads, a->cache.heads, a->cache.head_dim, a->max_q, a->max_ctx,
-                   a->window);
+                   a->window, a->cache.head_stride < a->cache.token_stride);
 }
 
 size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
@@ -762,6 +762,7 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.max_blocks = a->max_blocks;
   P.nrb = plan.nrb;
   P.chunks = plan.chunks;
+  P.hw = plan.hw;
   P.items = (int32_t)plan.items;
   P.groups = (int32_t)plan.groups;
   P.q_flip = a->scale < 0.f ? 0x80008000u : 0u;

@@ -8,8 +8,8 @@
 //
 // The rows of one KV head, token-major (row m = token m / G, head m % G), are
 // cut into blocks of 16 * RT; one 256-thread workgroup takes a block and a
-// range of keys, each of its four waves every fourth tile of 32 keys, on its
-// own: keys and values go from memory to the matrix units through registers
+// range of keys, each of its four waves every fourth tile of 32 keys (or, for
+// few rows, a KV head of its own), on its own: keys and values go from memory to the matrix units through registers
 // alone, no barrier stands in the loop, and the waves' sums are joined once
 // at the end.  Where there are few blocks with long contexts, the tiles of
 // all blocks, end to end, are cut into equal runs, one to each workgroup that
@@ -204,22 +204,27 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   x = grp * P->items + x % P->items;
   const int units = P->B * P->nrb;
 
+  // the waves share out hw heads and the tiles: wave w takes head w % hw and
+  // every (kWaves / hw)-th tile
+  const int hw = RT == 1 ? P->hw : 1, hs = wave & (hw - 1), ks = RT == 1 ? wave / hw : wave, kways = kWaves / hw;
+  const int hgroups = P->c.heads / hw;
+
   // the run of tiles [at, at + left) of unit v, v + 1, ... that this workgroup
-  // takes for its head: a whole unit, or (P->chunks > 0) one of the equal runs
-  int v, at = 0, head;
+  // takes for its heads: a whole unit, or (P->chunks > 0) one of the equal runs
+  int v, at = 0, head0;
   int left = INT_MAX;
   if (P->chunks == 0) {
     const int rb = x % P->nrb;
     x /= P->nrb;
-    head = x % P->c.heads;
-    v = (x / P->c.heads) * P->nrb + rb;
+    head0 = x % hgroups * hw;
+    v = (x / hgroups) * P->nrb + rb;
   } else {
     const int lane = threadIdx.x & 63;
-    head = x % P->c.heads;
+    head0 = x % hgroups * hw;
     const int64_t total = tiles_before(P, units, RT * 16, lane);
     left = (int)chunk_tiles(P, total);  // (units * 2^25 tiles over at least 8 runs, units <= 4096: below 2^31 for
                                         // any cache that fits the card)
-    const int64_t first = (int64_t)(x / P->c.heads) * left;
+    const int64_t first = (int64_t)(x / hgroups) * left;
     if (first >= total) return;
     // the unit that holds tile `first`
     double base = 0.0;
@@ -257,23 +262,26 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   const Unit un = unit_of(P, v, RT * 16);
   const int len = min(left, un.tiles - at);  // of this unit
   if (un.bad && un.tiles > 0) {
-    for (int64_t m = tid; m < (int64_t)un.n * G; m += kWG) {
-      const int64_t row = (int64_t)(un.q0 + m / G) * P->Hq + head * G + m % G;
+    const int gw = G * hw;  // (query heads of the workgroup's heads stand together)
+    for (int64_t m = tid; m < (int64_t)un.n * gw; m += kWG) {
+      const int64_t row = (int64_t)(un.q0 + m / gw) * P->Hq + head0 * G + m % gw;
       for (int d = 0; d < P->c.dim; ++d) P->out[row * P->c.dim + d] = 0x7fc0;
       if (P->lse) P->lse[row] = __builtin_nanf("");
     }
   } else if (un.tiles > 0) {
   const int k_beg = un.lo + at * kTileKeys, k_end = min(un.hi, k_beg + len * kTileKeys);
   const bool joined = len < un.tiles;  // other runs hold more of this unit's keys
-  const int nt = (len - wave + kWaves - 1) / kWaves;
+  const int head = head0 + hs;  // this wave's
+  const int nt = (len - ks + kways - 1) / kways;
 
   // Q, to become the fragments of the first product in LDS: fragment (rt, c),
   // lane l: row 16 rt + l % 16, dims 64 (c / 2) + 16 (l / 16) + 8 (c % 2) ..+ 8
-  constexpr int QF = (RT * C * 64 + kWG - 1) / kWG;
+  // (RT = 1: a wave's own head's, which stay in its registers)
+  constexpr int QF = RT == 1 ? C : (RT * C * 64 + kWG - 1) / kWG;
   u32x4 qreg[QF];
 #pragma unroll
   for (int i = 0; i < QF; ++i) {
-    const int f = tid + i * kWG;
+    const int f = RT == 1 ? i * 64 + lane : tid + i * kWG;
     const int l = f & 63, cc = (f >> 6) % C, rt = (f >> 6) / C;
     const int k = rt * 16 + (l & 15);
     const int d = (cc >> 1) * 64 + (l >> 4) * 16 + (cc & 1) * 8;
@@ -321,7 +329,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   auto look_up = [&](int i0) {
     const Params P = params_again();
     const int32_t* bt = P->bt + (int64_t)un.b * P->bt_stride;
-    const int key = k_beg + ((i0 + (lane >> 1)) * kWaves + wave) * kTileKeys + (lane & 1) * 16;
+    const int key = k_beg + ((i0 + (lane >> 1)) * kways + ks) * kTileKeys + (lane & 1) * 16;
     const int lb = key >> P->c.bs_shift, in = key & ((1 << P->c.bs_shift) - 1);
     int page = -1;
     if (key < k_end && lb < P->max_blocks) page = bt[lb];
@@ -410,8 +418,8 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   auto tile = [&](Buffer& t, int i) {
     // more than a few fragments of Q are read from LDS for every tile rather
     // than kept in registers (the compiler would move the reads out of the loop)
-    if constexpr (RT * C > 4) asm volatile("" ::: "memory");
-    const int key0 = k_beg + (i * kWaves + wave) * kTileKeys;
+    if constexpr (RT > 1 && RT * C > 4) asm volatile("" ::: "memory");
+    const int key0 = k_beg + (i * kways + ks) * kTileKeys;
     const uint32_t okt = t.ok;
     // every row of the block sees every key of the tile
     const bool whole = okt == 3u && key0 + kTileKeys - 1 <= un.p_lo && (window == 0 || key0 > un.p_hi - window);
@@ -434,8 +442,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
       for (int cc = 0; cc < C; ++cc)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka[cc], __builtin_bit_cast(bf16x8, qf[(rt * C + cc) * 64]),
-                                                             s[rt][u], 0, 0, 0);
+          s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              ka[cc], __builtin_bit_cast(bf16x8, RT == 1 ? qreg[RT == 1 ? cc : 0] : qf[(rt * C + cc) * 64]), s[rt][u],
+              0, 0, 0);
     }
     load_k(t, min(i + NB, nt - 1));
 
@@ -574,10 +583,11 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
       load_v(buf[i], i);
     }
 #pragma unroll
-  for (int i = 0; i < QF; ++i)
-    if (tid + i * kWG < RT * C * 64)
-      reinterpret_cast<u32x4*>(s_mem)[tid + i * kWG] = (qreg[i] & P->q_keep) ^ P->q_flip;
-  __syncthreads();
+  for (int i = 0; i < QF; ++i) {
+    qreg[i] = (qreg[i] & P->q_keep) ^ P->q_flip;
+    if (RT > 1 && tid + i * kWG < RT * C * 64) reinterpret_cast<u32x4*>(s_mem)[tid + i * kWG] = qreg[i];
+  }
+  if (RT > 1) __syncthreads();
   // every tile's loads are unconditional (the last ones' read a tile again):
   // behind a condition the compiler could not count the loads in flight, and
   // would wait for the values just asked for before it uses the keys
@@ -605,8 +615,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     float top = kNoRef;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_ref[w][rt * 16 + r]);
+    for (int w = hs; w < kWaves; w += hw) top = fmaxf(top, s_ref[w][rt * 16 + r]);
     const float f = exp2_fast(ref[rt] - top);
     if (rt > 0) __syncthreads();
 #pragma unroll
@@ -617,26 +626,25 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
             f32x4{acc[rt][dt][q] * f, acc[rt][dt + 1][q] * f, acc[rt][dt + 2][q] * f, acc[rt][dt + 3][q] * f};
     __syncthreads();
     // 4 dims a thread
-    for (int cell = tid; cell < 16 * (DP / 4); cell += kWG) {
-      const int rr = cell / (DP / 4), d = (cell % (DP / 4)) * 4;
+    for (int cell = tid; cell < hw * 16 * (DP / 4); cell += kWG) {
+      const int w0 = cell / (16 * (DP / 4)), rr = cell / (DP / 4) % 16, d = (cell % (DP / 4)) * 4;
       const int k = rt * 16 + rr;
       if (k >= un.rows || d >= P->c.dim) continue;
       f32x4 o{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) o += *reinterpret_cast<const f32x4*>(part + (w * 16 + rr) * DP + d);
       float mx = kNoRef;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_ref[w][rt * 16 + rr]);
+      for (int w = w0; w < kWaves; w += hw) {
+        o += *reinterpret_cast<const f32x4*>(part + (w * 16 + rr) * DP + d);
+        mx = fmaxf(mx, s_ref[w][rt * 16 + rr]);
+      }
       float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) l += s_sum[w][rt * 16 + rr] * exp2_fast(s_ref[w][rt * 16 + rr] - mx);
+      for (int w = w0; w < kWaves; w += hw) l += s_sum[w][rt * 16 + rr] * exp2_fast(s_ref[w][rt * 16 + rr] - mx);
       const int t = div_group(P, un.h0 + k);
-      const int hq = head * G + un.h0 + k - t * G;
+      const int hq = (head0 + w0) * G + un.h0 + k - t * G;
       const int64_t row = (int64_t)(un.q0 + un.t0 + t) * P->Hq + hq;
       if (joined) {
-        const int64_t part = part_row(P, grp, !run_begin, head, RT * 16, k);
-        *reinterpret_cast<f32x4*>(P->po + part * P->c.dim + d) = o;
-        if (d == 0) P->pm[part] = float2{mx, l};
+        const int64_t pr = part_row(P, grp, !run_begin, head0 + w0, RT * 16, k);
+        *reinterpret_cast<f32x4*>(P->po + pr * P->c.dim + d) = o;
+        if (d == 0) P->pm[pr] = float2{mx, l};
       } else {
         if (P->sinks) {
           const float sk = P->sinks[hq] * 1.44269504088896341f;
@@ -659,7 +667,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   }
   }
   // which runs hold the unit, for the join (one workgroup of the heads tells it)
-  if (P->chunks > 0 && head == 0 && threadIdx.x == 0 && un.tiles > 0) {
+  if (P->chunks > 0 && head0 == 0 && threadIdx.x == 0 && un.tiles > 0) {
     if (at == 0) P->runs[v].x = grp * 2 + !run_begin;
     if (at + len == un.tiles) P->runs[v].y = grp;
   }
@@ -672,52 +680,85 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 }
 
 // Joins the runs of a unit that several hold: one workgroup per (unit, KV
-// head, 16 rows), 4 dims a thread.
-template <int COLS>  // threads to a row
-__global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams, int row_tiles) {
+// head, 16 rows), 4 dims a thread, the runs of a row shared out to what
+// threads are left (a decode step of a few long contexts has few rows and many
+// runs; there the workgroup is large).
+template <int COLS, int NT>  // threads to a row, to a workgroup
+__global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams, int row_tiles) {
+  constexpr int NS = NT / COLS;
+  __shared__ float4 s_o[NT];
+  __shared__ float2 s_ml[NT];
   const Params P = params_again();
   const int rt = blockIdx.x % row_tiles, x = blockIdx.x / row_tiles;
   const int v = x / P->c.heads, head = x % P->c.heads;
   const int2 runs = P->runs[v];  // (of a unit without rows: never written, and not used)
   const Unit u = unit_of(P, v, row_tiles * 16);
   const int j0 = runs.x >> 1, j1 = runs.y;
-  if (u.bad || u.tiles <= 1 || j0 == j1) return;  // written whole
+  const int rows = min(16, u.rows - rt * 16);
+  if (u.bad || u.tiles <= 1 || rows <= 0 || j0 == j1) return;  // written whole
   const bool late = runs.x & 1;  // its first run began with another unit
-  const int d = (threadIdx.x % COLS) * 4;
-  for (int kk = threadIdx.x / COLS; kk < 16; kk += kWG / COLS) {
-    const int k = rt * 16 + kk;
-    if (k >= u.rows || d >= P->c.dim) continue;
-    const int t = div_group(P, u.h0 + k);
-    const int hq = head * P->G + u.h0 + k - t * P->G;
-    const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
+  const int shift = rows > 8 ? 4 : rows > 4 ? 3 : rows > 2 ? 2 : rows > 1 ? 1 : 0;  // rows, rounded up to 2^shift
+  const int tid = threadIdx.x, slot = tid / COLS, d = (tid % COLS) * 4;
+  const bool wide = NS >= (1 << shift);  // (else the rows are taken in turn, each by one thread a column)
+  const int ways = wide ? NS >> shift : 1, way = wide ? slot >> shift : 0;
+  for (int r0 = 0; r0 < rows; r0 += NS) {
+    const int k = rt * 16 + (wide ? slot & ((1 << shift) - 1) : r0 + slot);
+    const bool on = k < u.rows && k < rt * 16 + 16 && d < P->c.dim;
     // eight runs' sums on their way at a time
-    float mx = P->sinks ? P->sinks[hq] * 1.44269504088896341f : kNoRef;
-    float l = P->sinks ? 1.f : 0.f;
+    float mx = kNoRef, l = 0.f;
     f32x4 o{0.f, 0.f, 0.f, 0.f};
-    for (int j = j0; j <= j1; j += 8) {
+    for (int j = j0 + way; on && j <= j1; j += 8 * ways) {
       float2 p[8];
       f32x4 a[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const int jj = min(j + q, j1);
+        const int jj = min(j + q * ways, j1);
         const int64_t part = part_row(P, jj, late && jj == j0, head, row_tiles * 16, k);
         p[q] = P->pm[part];
         a[q] = *reinterpret_cast<const f32x4*>(P->po + part * P->c.dim + d);
-        if (j + q > j1) p[q] = float2{kNoRef, 0.f};
       }
       float m = mx;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = fmaxf(m, p[q].x);
+      for (int q = 0; q < 8; ++q) m = j + q * ways <= j1 ? fmaxf(m, p[q].x) : m;
       const float f = exp2_fast(mx - m);
       l *= f;
       o *= f;
       mx = m;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float w = j + q > j1 ? 0.f : exp2_fast(p[q].x - m);
-        l += p[q].y * w;
-        o += j + q > j1 ? f32x4{0.f, 0.f, 0.f, 0.f} : a[q] * w;
+      for (int q = 0; q < 8; ++q)
+        if (j + q * ways <= j1) {
+          const float w = exp2_fast(p[q].x - m);
+          l += p[q].y * w;
+          o += a[q] * w;
+        }
+    }
+    if (ways > 1) {
+      s_o[tid] = float4{o.x, o.y, o.z, o.w};
+      s_ml[tid] = float2{mx, l};
+      __syncthreads();
+      if (way == 0) {
+        for (int w = 1; w < ways; ++w) {
+          const int at = tid + (w << shift) * COLS;
+          const float2 p = s_ml[at];
+          const float4 q = s_o[at];
+          const float m = fmaxf(mx, p.x);
+          const float f = exp2_fast(mx - m), g = exp2_fast(p.x - m);
+          l = l * f + p.y * g;
+          o = o * f + f32x4{q.x, q.y, q.z, q.w} * g;
+          mx = m;
+        }
       }
+    }
+    if (!on || way != 0) continue;
+    const int t = div_group(P, u.h0 + k);
+    const int hq = head * P->G + u.h0 + k - t * P->G;
+    const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
+    if (P->sinks) {
+      const float sk = P->sinks[hq] * 1.44269504088896341f;
+      const float m = fmaxf(mx, sk), f = exp2_fast(mx - m);
+      l = l * f + exp2_fast(sk - m);
+      o *= f;
+      mx = m;
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     uint32_t w[2];
@@ -729,7 +770,8 @@ __global__ __launch_bounds__(kWG) void attn_join_kernel(AttnParams, int row_tile
   }
 }
 
-AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window) {
+AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window,
+                   bool heads_in) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * G;
   const int64_t tiles = (rows + 15) / 16;
@@ -742,6 +784,7 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
   if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
   const int64_t units = (int64_t)B * p.nrb;
   const int slots = 256 * (dim <= 64 && p.rt == 1 ? 4 : dim <= 64 && p.rt == 2 ? 3 : 2);  // resident workgroups
+  p.hw = 1;
   if (keys <= 1024 || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
     // short contexts, very many units, or many blocks of long prompts: a unit
     // to a workgroup; the blocks of one head on one XCD, for its keys
@@ -749,9 +792,15 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
     p.items = p.nrb;
     p.groups = (int64_t)B * heads;
   } else {
-    // equal runs, as many as are resident at once; a run's heads on one XCD
-    p.chunks = slots / heads > 8 ? slots / heads / 8 * 8 : 8;
-    p.items = heads;
+    // equal runs, as many as are resident at once; a run's heads on one XCD.
+    // With few rows (small partial sums), long runs and a token's heads side
+    // by side a wave takes a head of its own, so that a workgroup reads them
+    // together.
+    if (p.rt == 1 && heads_in && units * keys / kTileKeys * heads >= (int64_t)slots * kWaves * 32)
+      p.hw = heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
+    const int hgroups = heads / p.hw;
+    p.chunks = slots / hgroups > 8 ? slots / hgroups / 8 * 8 : 8;
+    p.items = hgroups;
     p.groups = p.chunks;
   }
   return p;
@@ -781,6 +830,16 @@ static hipError_t launch_attn_rows(const AttnParams& P, int rt, hipStream_t stre
   return hipErrorInvalidValue;
 }
 
+template <int COLS>
+static hipError_t launch_join(const AttnParams& P, const AttnPlan& plan, hipStream_t stream) {
+  const dim3 grid((unsigned)(P.B * P.nrb * P.c.heads * plan.rt));
+  if (plan.chunks > 8 * P.B * P.nrb)  // many runs to a unit
+    hipLaunchKernelGGL((attn_join_kernel<COLS, 1024>), grid, dim3(1024), 0, stream, P, plan.rt);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<COLS, kWG>), grid, dim3(kWG), 0, stream, P, plan.rt);
+  return hipGetLastError();
+}
+
 hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream) {
   hipError_t e;
   if (P.c.dim <= 64)
@@ -790,14 +849,8 @@ hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t st
   else
     e = launch_attn_rows<256>(P, plan.rt, stream);
   if (e != hipSuccess || plan.chunks == 0) return e;
-  const dim3 grid((unsigned)(P.B * P.nrb * P.c.heads * plan.rt));
-  if (P.c.dim <= 64)
-    hipLaunchKernelGGL((attn_join_kernel<16>), grid, dim3(kWG), 0, stream, P, plan.rt);
-  else if (P.c.dim <= 128)
-    hipLaunchKernelGGL((attn_join_kernel<32>), grid, dim3(kWG), 0, stream, P, plan.rt);
-  else
-    hipLaunchKernelGGL((attn_join_kernel<64>), grid, dim3(kWG), 0, stream, P, plan.rt);
-  return hipGetLastError();
+  return P.c.dim <= 64 ? launch_join<16>(P, plan, stream)
+                       : P.c.dim <= 128 ? launch_join<32>(P, plan, stream) : launch_join<64>(P, plan, stream);
 }
 
 }  // namespace specv

@@ -74,6 +74,7 @@ struct AttnParams {
   uint32_t g_inv;       // 65535 / G + 1
   int32_t max_q, max_ctx, window, max_blocks;
   int32_t nrb, chunks;              // row blocks per (request, KV head); equal runs of tiles (0: a unit each)
+  int32_t hw;                       // KV heads of a workgroup (1, 2 or 4)
   int32_t items, groups;            // workgroups kept on one XCD, and how many such sets
   // the scores are scale2 * q . k with scale2 = |scale| * log2(e) > 0: a
   // negative scale is the sign of q (q_flip: the sign bits of two bf16), a
@@ -96,11 +97,13 @@ struct AttnParams {
 };
 
 struct AttnPlan {
-  int32_t rt, nrb, chunks;
+  int32_t rt, nrb, chunks, hw;
   int64_t items, groups;
 };
 // How the rows of a (request, KV head) and its keys are cut into workgroups.
-AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window);
+// heads_in: the heads of a token stand together in the cache.
+AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window,
+                   bool heads_in);
 hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream);
 
 }  // namespace specv

@@ -322,6 +322,9 @@ int kv_write_check(const spec_kv_write_args* a) {
   if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
   if (a->k_token_stride < 0 || a->k_head_stride < 0 || a->v_token_stride < 0 || a->v_head_stride < 0)
     return SPEC_EINVAL;
+  const int64_t chunk = kv_write_chunk(a->N);
+  if (!fits_dispatch(((int64_t)a->N + chunk - 1) / chunk * ((2 * a->cache.heads + 3) / 4), kThreads))
+    return SPEC_EINVAL;
   return SPEC_OK;
 }
 
@@ -332,6 +335,8 @@ int kv_read_check(const spec_kv_read_args* a) {
   if (rc != SPEC_OK) return rc;
   if (a->N == 0) return SPEC_OK;
   if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
+  const int64_t per = kv_read_per(a->N, a->cache.heads, a->cache.head_dim);
+  if (!fits_dispatch(((int64_t)a->N + per - 1) / per, kThreads)) return SPEC_EINVAL;
   return SPEC_OK;
 }
 
@@ -708,12 +713,10 @@ int spec_logprobs_launch(const spec_logprobs_args* a, hipStream_t stream) {
 int spec_kv_write_launch(const spec_kv_write_args* a, hipStream_t stream) {
   const int rc = kv_write_check(a);
   if (rc != SPEC_OK || a->N == 0) return rc;
-  const int es = a->dtype == SPEC_BF16 ? 2 : 4;
   KvWriteParams P;
   P.c = cache_view(a->cache);
   P.N = a->N;
-  // few entries: few to a workgroup, so that they spread over the card
-  P.chunk = a->N >= 8192 ? 64 : a->N >= 1024 ? 16 : 4;
+  P.chunk = kv_write_chunk(a->N);
   P.src[0] = static_cast<const char*>(a->key);
   P.src[1] = static_cast<const char*>(a->value);
   P.tok[0] = a->k_token_stride;
@@ -721,10 +724,7 @@ int spec_kv_write_launch(const spec_kv_write_args* a, hipStream_t stream) {
   P.tok[1] = a->v_token_stride;
   P.hd[1] = a->v_head_stride;
   P.slots = a->slots;
-  const bool vec = aligned16(a->key) && aligned16(a->value) && (a->k_token_stride * es) % 16 == 0 &&
-                   (a->k_head_stride * es) % 16 == 0 && (a->v_token_stride * es) % 16 == 0 &&
-                   (a->v_head_stride * es) % 16 == 0;
-  return launch_kv_write(P, a->dtype, vec, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+  return launch_kv_write(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }
 
 int spec_kv_read_launch(const spec_kv_read_args* a, hipStream_t stream) {
@@ -733,6 +733,7 @@ int spec_kv_read_launch(const spec_kv_read_args* a, hipStream_t stream) {
   KvReadParams P;
   P.c = cache_view(a->cache);
   P.N = a->N;
+  P.per = kv_read_per(a->N, a->cache.heads, a->cache.head_dim);
   P.dst[0] = static_cast<char*>(a->key);
   P.dst[1] = static_cast<char*>(a->value);
   P.slots = a->slots;

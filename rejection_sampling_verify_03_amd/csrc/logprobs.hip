@@ -71,23 +71,7 @@ __device__ __forceinline__ float row_temperature(const LogprobsParams& P, int b)
   return T == 0.0f ? 1.0f : T;
 }
 
-// 8 logits as stored, from any element on: the hardware's 16-byte loads need
-// no alignment, so rows of any length and stride take the same path.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-template <int ES>
-__device__ __forceinline__ RawGroup<ES, true> load_any(const char* row, int64_t e0) {
-  RawGroup<ES, true> r;
-  if constexpr (ES == 2) {
-    r.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + e0 * 2));
-  } else {
-    r.a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4));
-    r.b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4 + 16));
-  }
-  return r;
-}
-
-// The same, with -inf for those past the end of the row.
+// 8 logits as stored, with -inf for those past the end of the row.
 template <int ES>
 __device__ __forceinline__ RawGroup<ES, true> load_any_bounded(const char* row, int e0, int V) {
   if (e0 < V && e0 + 8 <= V) return load_any<ES>(row, e0);

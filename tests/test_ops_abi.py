@@ -130,6 +130,15 @@ def test_write_and_read_refusals(sv, kw, status):
         a.cache, a.N, a.dtype, a.key, a.value, a.slots = cache_args(sv), 4, sv.SPEC_BF16, P, P, P
         setattr(a, stride, -1)
         assert sv.spec_kv_write_launch(a, None) == sv.SPEC_EINVAL
+    # grids past one dispatch of 2^32 work-items
+    a = sv.SpecKVWriteArgs()
+    a.cache, a.dtype, a.key, a.value, a.slots = cache_args(sv, heads=1024, token_stride=2 ** 16, block_stride=2 ** 20,
+                                                           scale_block_stride=1024), sv.SPEC_BF16, P, P, P
+    a.N = 2 ** 30
+    assert sv.spec_kv_write_launch(a, None) == sv.SPEC_EINVAL
+    r = sv.SpecKVReadArgs()
+    r.cache, r.N, r.dtype, r.key, r.value, r.slots = a.cache, 2 ** 30, sv.SPEC_BF16, P, P, P
+    assert sv.spec_kv_read_launch(r, None) == sv.SPEC_EINVAL
     assert sv.lib.spec_kv_write_launch(None, None) == sv.SPEC_EINVAL
     assert sv.lib.spec_kv_read_launch(None, None) == sv.SPEC_EINVAL
 

@@ -759,7 +759,7 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.g_inv = 65535u / (uint32_t)P.G + 1u;
   P.max_q = a->max_q;
   P.max_ctx = a->max_ctx;
-  P.window = a->window;
+  P.window = a->window < (1 << 30) ? a->window : 1 << 30;  // (no context is longer)
   P.max_blocks = a->max_blocks;
   P.nrb = plan.nrb;
   P.chunks = plan.chunks;

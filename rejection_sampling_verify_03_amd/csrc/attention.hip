@@ -187,6 +187,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   constexpr int C = DP / 32;   // steps of the sum over dims
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
   constexpr int W = DP / 64;   // 16-byte loads of a lane's share of a key
+  constexpr bool QREG = RT == 1 && C <= 4;  // Q's fragments stay in registers
   // tiles in flight: two where the registers hold them
   constexpr int NB = 1;
   constexpr int kWindow = 32;  // tiles whose pages a wave holds at a time, a subtile to a lane
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   // the run of tiles [at, at + left) of unit v, v + 1, ... that this workgroup
   // takes for its heads: a whole unit, or (P->chunks > 0) one of the equal runs
   int v, at = 0, head0;
-  int left = INT_MAX;
+  int64_t left = INT64_MAX;
   if (P->chunks == 0) {
     const int rb = x % P->nrb;
     x /= P->nrb;
@@ -222,8 +223,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     const int lane = threadIdx.x & 63;
     head0 = x % hgroups * hw;
     const int64_t total = tiles_before(P, units, RT * 16, lane);
-    left = (int)chunk_tiles(P, total);  // (units * 2^25 tiles over at least 8 runs, units <= 4096: below 2^31 for
-                                        // any cache that fits the card)
+    left = chunk_tiles(P, total);
     const int64_t first = (int64_t)(x / hgroups) * left;
     if (first >= total) return;
     // the unit that holds tile `first`
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     koff[w] = (uint32_t)(r * tok_stride + (w * 64 + g * 16 < dim ? w * 64 + g * 16 : 0));
   const uint32_t voff = (uint32_t)(4 * g * tok_stride + (r * (DP / 16) < dim ? r * (DP / 16) : 0));
   const Unit un = unit_of(P, v, RT * 16);
-  const int len = min(left, un.tiles - at);  // of this unit
+  const int len = (int)min(left, (int64_t)(un.tiles - at));  // of this unit
   if (un.bad && un.tiles > 0) {
     const int gw = G * hw;  // (query heads of the workgroup's heads stand together)
     for (int64_t m = tid; m < (int64_t)un.n * gw; m += kWG) {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 
   // Q, to become the fragments of the first product in LDS: fragment (rt, c),
   // lane l: row 16 rt + l % 16, dims 64 (c / 2) + 16 (l / 16) + 8 (c % 2) ..+ 8
-  // (RT = 1: a wave's own head's, which stay in its registers)
+  // (RT = 1: a wave's own head's)
   constexpr int QF = RT == 1 ? C : (RT * C * 64 + kWG - 1) / kWG;
   u32x4 qreg[QF];
 #pragma unroll
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   const float scale2 = P->scale2;
   const int window = P->window;
   const uint8_t *k_codes = P->c.codes[0], *v_codes = P->c.codes[1];
-  const u32x4* qf = reinterpret_cast<const u32x4*>(s_mem) + lane;
+  const u32x4* qf = reinterpret_cast<const u32x4*>(s_mem) + (RT == 1 ? wave * C * 64 : 0) + lane;
 
   // Lane l knows subtile l % 2 of tile i0 + l / 2 of this wave: where its keys
   // begin, whether their block exists, and (!FINE) their scales.
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   auto tile = [&](Buffer& t, int i) {
     // more than a few fragments of Q are read from LDS for every tile rather
     // than kept in registers (the compiler would move the reads out of the loop)
-    if constexpr (RT > 1 && RT * C > 4) asm volatile("" ::: "memory");
+    if constexpr (!QREG && RT * C > 4) asm volatile("" ::: "memory");
     const int key0 = k_beg + (i * kways + ks) * kTileKeys;
     const uint32_t okt = t.ok;
     // every row of the block sees every key of the tile
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              ka[cc], __builtin_bit_cast(bf16x8, RT == 1 ? qreg[RT == 1 ? cc : 0] : qf[(rt * C + cc) * 64]), s[rt][u],
+              ka[cc], __builtin_bit_cast(bf16x8, QREG ? qreg[QREG ? cc : 0] : qf[(rt * C + cc) * 64]), s[rt][u],
               0, 0, 0);
     }
     load_k(t, min(i + NB, nt - 1));
@@ -586,8 +586,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   for (int i = 0; i < QF; ++i) {
     qreg[i] = (qreg[i] & P->q_keep) ^ P->q_flip;
     if (RT > 1 && tid + i * kWG < RT * C * 64) reinterpret_cast<u32x4*>(s_mem)[tid + i * kWG] = qreg[i];
+    if (RT == 1 && !QREG) reinterpret_cast<u32x4*>(s_mem)[(wave * C + i) * 64 + lane] = qreg[i];
   }
-  if (RT > 1) __syncthreads();
+  if (!QREG) __syncthreads();
   // every tile's loads are unconditional (the last ones' read a tile again):
   // behind a condition the compiler could not count the loads in flight, and
   // would wait for the values just asked for before it uses the keys
@@ -783,9 +784,9 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
   int64_t keys = max_ctx;
   if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
   const int64_t units = (int64_t)B * p.nrb;
-  const int slots = 256 * (dim <= 64 && p.rt == 1 ? 4 : dim <= 64 && p.rt == 2 ? 3 : 2);  // resident workgroups
+  const int slots = 256 * (dim <= 64 && p.rt <= 2 ? 3 : 2);  // resident workgroups
   p.hw = 1;
-  if (keys <= 1024 || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
+  if (keys <= 1024 || (keys <= 2048 && units * heads <= slots) || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
     // short contexts, very many units, or many blocks of long prompts: a unit
     // to a workgroup; the blocks of one head on one XCD, for its keys
     p.chunks = 0;

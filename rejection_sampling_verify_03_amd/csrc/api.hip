@@ -694,6 +694,8 @@ int spec_logprobs_launch(const spec_logprobs_args* a, hipStream_t stream) {
   P.V = a->V;
   P.nseg = (int32_t)(((int64_t)a->V + kSeg - 1) / kSeg);
   P.C = (P.nseg + kLpChunkSegs - 1) / kLpChunkSegs;
+  P.by_C = FastDiv::by((uint32_t)P.C);
+  P.by_R = FastDiv::by((uint32_t)P.R);
   P.top = a->top;
   P.logits = static_cast<const char*>(a->logits);
   P.req = a->req_stride;

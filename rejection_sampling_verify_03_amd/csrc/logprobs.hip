@@ -94,32 +94,8 @@ __device__ __forceinline__ RawGroup<ES, true> load_any_bounded(const char* row, 
   return r;
 }
 
-// The places n and up of a group as `pad` (bf16: its upper half).
-template <int ES>
-__device__ __forceinline__ void pad_group(RawGroup<ES, true>& r, int n, float pad) {
-  if constexpr (ES == 2) {
-    const uint32_t p = __float_as_uint(pad) >> 16;
-    uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 2 * i + 1 < n ? w[i] : (w[i] & 0xffffu) | (p << 16);
-      w[i] = 2 * i < n ? w[i] : (w[i] & 0xffff0000u) | p;
-    }
-    r.v = u32x4{w[0], w[1], w[2], w[3]};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.a[i] = i < n ? r.a[i] : pad;
-      r.b[i] = i + 4 < n ? r.b[i] : pad;
-    }
-  }
-}
-
 // The largest of 8 logits, three to an instruction (a NaN shows in S).
-template <int ES>
-__device__ __forceinline__ float group_max(const RawGroup<ES, true>& r) {
-  float x[8];
-  unpack_group<ES, true>(r, x);
+__device__ __forceinline__ float group_max(const float (&x)[8]) {
   const float a = fmaxf(fmaxf(x[0], x[1]), x[2]), b = fmaxf(fmaxf(x[3], x[4]), x[5]);
   return fmaxf(fmaxf(fmaxf(x[6], x[7]), a), b);
 }
@@ -380,7 +356,7 @@ __device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* 
 // One wave: row i's records joined, its outputs written.
 template <int ES, bool TOP>
 __device__ __forceinline__ void finish_row(const LogprobsParams& P, int i, int lane, LpLists<ES>* lists) {
-  const int b = i / P.R, r = i - b * P.R;
+  const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
   const int tok = P.tokens[i];
   const float T = row_temperature(P, b);
   const float nan = __builtin_nanf("");
@@ -450,9 +426,9 @@ __global__ __launch_bounds__(64) void logprobs_finish_kernel(LogprobsParams P) {
 // it (no second launch: 4 us less of the 15 us of a small batch).
 template <int ES, bool TOP, bool WHOLE>
 __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
-  const int c = blockIdx.x % P.C;
-  const int i = blockIdx.x / P.C;  // row b * R + r
-  const int b = i / P.R, r = i - b * P.R;
+  const int i = (int)P.by_C.of(blockIdx.x);  // row b * R + r
+  const int c = (int)blockIdx.x - i * P.C;
+  const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
   const int tok = P.tokens[i];
   const float T = row_temperature(P, b);
   const bool usable = tok >= 0 && tok < P.V && temperature_valid(T);  // the finish reports the others
@@ -474,10 +450,15 @@ __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
         rg[g] = load_any_bounded<ES>(row, e, P.V);
       }
     }
-    float gm[kSegGroups], m = -INFINITY;
+    // widened once: the kernel is bound by its vector instructions, and a
+    // second widening would be a tenth of them
+    float x[kSegGroups][8], gm[kSegGroups], m = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kSegGroups; ++g) {
-      gm[g] = group_max<ES>(rg[g]);
+      unpack_group<ES, true>(rg[g], x[g]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) asm volatile("" : "+v"(x[g][q]));  // (kept, not widened anew)
+      gm[g] = group_max(x[g]);
       m = fmaxf(m, gm[g]);
     }
     m = wave_max_f(m);
@@ -495,21 +476,21 @@ __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
       // but finite
       const float pad = m - 16384.f / s;
 #pragma unroll
-      for (int g = 0; g < kSegGroups; ++g) pad_group<ES>(rg[g], P.V - (s0 + (g * 64 + lane) * 8), pad);
+      for (int g = 0; g < kSegGroups; ++g)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[g][q] = s0 + (g * 64 + lane) * 8 + q < P.V ? x[g][q] : pad;
     }
     bool again = !(fabsf(c) <= 0x1p24f);
     if (!again) {
 #pragma unroll
       for (int g = 0; g < kSegGroups; ++g) {
-        opaque_group<ES, true>(rg[g]);
-        float x[8], e[8];
-        unpack_group<ES, true>(rg[g], x);
+        float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = __builtin_fmaf(x[i], s, -c);
-          e[i] = __builtin_amdgcn_exp2f(x[i]);
+        for (int q = 0; q < 8; ++q) {
+          x[g][q] = __builtin_fmaf(x[g][q], s, -c);
+          e[q] = __builtin_amdgcn_exp2f(x[g][q]);
         }
-        add_group(e, x, S, W);
+        add_group(e, x[g], S, W);
       }
       const float f = __builtin_amdgcn_exp2f(-eps);
       W = __builtin_fmaf(-eps, S, W) * f;
@@ -524,20 +505,20 @@ __global__ __launch_bounds__(kWG) void logprobs_stats_kernel(LogprobsParams P) {
       S = W = 0.f;
 #pragma unroll 1
       for (int g = 0; g < kSegGroups && s0 + g * 512 < P.V; ++g) {
-        float x[8], e[8];
-        unpack_group<ES, true>(load_any_bounded<ES>(row, s0 + (g * 64 + lane) * 8, P.V), x);
+        float y[8], e[8];
+        unpack_group<ES, true>(load_any_bounded<ES>(row, s0 + (g * 64 + lane) * 8, P.V), y);
         if (m > -INFINITY) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float t = (x[i] - m) * s;
+            const float t = (y[i] - m) * s;
             e[i] = __builtin_amdgcn_exp2f(t);
-            x[i] = fmaxf(t, -16384.f);
+            y[i] = fmaxf(t, -16384.f);
           }
-          add_group(e, x, S, W);
+          add_group(e, y, S, W);
         } else {
           // only -inf adds nothing, but a NaN or +inf may hide among it
 #pragma unroll
-          for (int i = 0; i < 8; ++i) S = x[i] == -INFINITY ? S : __builtin_nanf("");
+          for (int i = 0; i < 8; ++i) S = y[i] == -INFINITY ? S : __builtin_nanf("");
         }
       }
     }

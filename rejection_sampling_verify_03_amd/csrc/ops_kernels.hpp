@@ -23,8 +23,25 @@ static_assert(sizeof(LpRecord) == 16, "LpRecord layout");
 constexpr int kLpCells = 64;     // cells of 64 consecutive logits in a segment
 constexpr int kLpChunkSegs = 8;  // segments per workgroup of the statistics pass
 
+// n / d for 0 <= n < 2^31 as a product and a shift (a scalar division is some
+// forty vector instructions, in every wave): with 2^s the largest power of two
+// below d, mul = ceil(2^(32+s) / d) < 2^32 is off by less than d from exact,
+// which stays below one quotient for n < 2^31.
+struct FastDiv {
+  uint32_t mul, shift;  // mul 0: d = 1
+  __host__ __device__ static FastDiv by(uint32_t d) {
+    uint32_t s = 0;
+    while (d > 1 && (2u << s) < d) ++s;
+    return d > 1 ? FastDiv{(uint32_t)(((1ull << (32 + s)) + d - 1) / d), s} : FastDiv{0, 0};
+  }
+  __host__ __device__ uint32_t of(uint32_t n) const {
+    return mul ? (uint32_t)(((uint64_t)n * mul) >> 32) >> shift : n;
+  }
+};
+
 struct LogprobsParams {
   int32_t B, R, V, nseg, C, top;  // C: chunks of kLpChunkSegs segments per row
+  FastDiv by_C, by_R;
   const char* logits;
   int64_t req, row;
   const int32_t* tokens;

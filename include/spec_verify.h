@@ -1,7 +1,9 @@
 /*
  * spec_verify.h -- C ABI of the MI355X (gfx950) speculative-decoding hot path:
  * batched modified-rejection-sampling verification and the P-EAGLE
- * parallel-drafting batch expansion with its hidden-state gather.
+ * parallel-drafting batch expansion with its hidden-state gather; and the
+ * operators around it in a decode step: token log probabilities, the 8-bit
+ * paged KV cache behind the slot mapping, and attention over that cache.
  *
  * Conventions for every entry point
  *  - Pointers marked "device" are HIP device pointers; the library never
@@ -34,9 +36,10 @@ typedef enum {
   SPEC_OK = 0,
   SPEC_EINVAL = -1,     /* null pointer, size or stride out of range (also a batch whose kernel
                            grids would exceed one dispatch's 2^32 work-items) */
-  SPEC_EDTYPE = -2,     /* unknown logits dtype */
-  SPEC_EALIGN = -3,     /* workspace (or a statistics record array) not 16-byte aligned */
-  SPEC_EWORKSPACE = -4, /* workspace smaller than spec_verify_workspace_bytes() */
+  SPEC_EDTYPE = -2,     /* unknown dtype, or one that the call does not take */
+  SPEC_EALIGN = -3,     /* workspace, statistics record array, cache codes or strides, or attention
+                           output not 16-byte aligned */
+  SPEC_EWORKSPACE = -4, /* workspace smaller than the call's *_workspace_bytes() */
   SPEC_ELAUNCH = -5     /* the HIP runtime refused a launch */
 } spec_status;
 

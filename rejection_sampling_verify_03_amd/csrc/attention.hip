@@ -9,9 +9,9 @@
 // The rows of one KV head, token-major (row m = token m / G, head m % G), are
 // cut into blocks of 16 * RT; one 256-thread workgroup takes a block and a
 // range of keys, each of its four waves every fourth tile of 32 keys (or, for
-// few rows, a KV head of its own), on its own: keys and values go from memory to the matrix units through registers
-// alone, no barrier stands in the loop, and the waves' sums are joined once
-// at the end.  Where there are few blocks with long contexts, the tiles of
+// few rows, a KV head of its own), on its own: keys and values go from memory
+// to the matrix units through registers alone, no barrier stands in the loop,
+// and the waves' sums are joined once at the end.  Where there are few blocks with long contexts, the tiles of
 // all blocks, end to end, are cut into equal runs, one to each workgroup that
 // the card holds at once, whatever the lengths of the contexts; a second
 // kernel joins the blocks that several runs hold.
@@ -24,9 +24,9 @@
 // that is where the second product wants P^T: the weights never leave their
 // lanes.  The order of the sum over dims is free too: lane group g takes
 // dims 64 w + 16 g ..+ 16 of the keys, so that keys are read in 16-byte loads
-// of which four lanes' stand together.  The codes widen to bf16 exactly, scale included (one instruction
-// for two); the values' bytes, which lie along dims, are first transposed
-// four by four in registers.
+// of which four lanes' stand together.  The codes widen to bf16 exactly, scale
+// included (one instruction for two); the values' bytes, which lie along dims,
+// are first transposed four by four in registers.
 //
 // Weights are 2^(s_j log2(e) - ref) with a reference per row that moves only
 // when a score passes it by 2^8: up to there the fp32 sums and the bf16
@@ -34,6 +34,19 @@
 // rounded to bf16 for the second product (a relative error of at most 2^-8
 // each, of no common sign, as the output's own rounding); their sum is kept
 // in fp32 from the unrounded weights, so lse keeps fp32's accuracy.
+//
+// Bounds, measured (MI355X).  Single tokens over long contexts: memory (three
+// contexts of up to 131072 tokens, 691 MB, in 140 us; 131 us of it the main
+// kernel, 5.3 TB/s; with all pages in L2 the call takes 83 us).  The
+// verification batch, 72 rows to a KV head: instructions (126 us; 121 with all
+// pages in L2; vector instructions in 56 % of the cycles, matrix instructions
+// in 22 %).  A 2048-token chunk over 8192 tokens: the same (390 us, 0.8 PFLOP/s;
+// vector 65 %, matrix 34 %: the two hardly overlap on two waves to a SIMD).
+// RT is what 256 registers hold without spilling much: 5 row tiles at 64 dims
+// (the 72 rows of nine tokens and a group of eight in one block; 3 tiles: 175
+// us), 3 at 128 (4 spill: 992 us for the chunk against 382).  A second tile on
+// its way in registers was no faster (133 against 133 us, long contexts 150
+// against 141).
 #include <limits.h>
 
 #include "cache_device.hpp"
@@ -130,7 +143,8 @@ __device__ __forceinline__ int64_t tiles_before(Params P, int v0, int block_rows
 }
 
 // Tiles to a chunk: all units' tiles, end to end, are cut into P->chunks equal
-// runs, none shorter than kMinChunk.
+// runs, none shorter than kMinChunk (32: 94 us against 82 for 64 contexts of
+// 4096 tokens; 8: no faster).
 constexpr int kMinChunk = 16;
 __device__ __forceinline__ int64_t chunk_tiles(Params P, int64_t total) {
   return max((total + P->chunks - 1) / P->chunks, (int64_t)kMinChunk);
@@ -188,8 +202,6 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
   constexpr int W = DP / 64;   // 16-byte loads of a lane's share of a key
   constexpr bool QREG = RT == 1 && C <= 4;  // Q's fragments stay in registers
-  // tiles in flight: two where the registers hold them
-  constexpr int NB = 1;
   constexpr int kWindow = 32;  // tiles whose pages a wave holds at a time, a subtile to a lane
   __shared__ __align__(16) char s_mem[(RT * C * 64 * 16 > kWaves * 16 * DP * 4) ? RT * C * 64 * 16
                                                                                 : kWaves * 16 * DP * 4];
@@ -358,8 +370,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     uint32_t kfine[2], vfine[2];  // (FINE) scale bytes of key r, and of keys 4 g ..+ 4
     float ksc[2], vsc[2];
     uint32_t ok;
-  } buf[NB];
-  auto load_k = [&](Buffer& t, int i) {
+  } buf;
+  auto load_k = [&](int i) {
+    Buffer& t = buf;
     if ((i & (kWindow - 1)) == 0) look_up(i);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -376,7 +389,8 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     }
     t.ok = (uint32_t)(okv >> ((i & (kWindow - 1)) << 1)) & 3u;
   };
-  auto load_v = [&](Buffer& t, int i) {
+  auto load_v = [&](int i) {
+    Buffer& t = buf;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int l = ((i & (kWindow - 1)) << 1) + u;
@@ -415,7 +429,8 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     }
   };
 
-  auto tile = [&](Buffer& t, int i) {
+  auto tile = [&](int i) {
+    Buffer& t = buf;
     // more than a few fragments of Q are read from LDS for every tile rather
     // than kept in registers (the compiler would move the reads out of the loop)
     if constexpr (!QREG && RT * C > 4) asm volatile("" ::: "memory");
@@ -446,7 +461,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
               ka[cc], __builtin_bit_cast(bf16x8, QREG ? qreg[QREG ? cc : 0] : qf[(rt * C + cc) * 64]), s[rt][u],
               0, 0, 0);
     }
-    load_k(t, min(i + NB, nt - 1));
+    load_k(min(i + 1, nt - 1));
 
     // a tile that some row sees only in part: scores not seen become -inf;
     // nothing of the keys that no row sees may enter (0 * NaN, 0 * inf), and a
@@ -573,15 +588,13 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
           acc[rt][4 * dw + dd] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pb[rt], acc[rt][4 * dw + dd], 0, 0, 0);
       }
     }
-    load_v(t, min(i + NB, nt - 1));
+    load_v(min(i + 1, nt - 1));
   };
-  // (in this order the first tiles are on their way before Q is waited for)
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-    if (i < nt) {
-      load_k(buf[i], i);
-      load_v(buf[i], i);
-    }
+  // (in this order the first tile is on its way before Q is waited for)
+  if (nt > 0) {
+    load_k(0);
+    load_v(0);
+  }
 #pragma unroll
   for (int i = 0; i < QF; ++i) {
     qreg[i] = (qreg[i] & P->q_keep) ^ P->q_flip;
@@ -592,12 +605,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   // every tile's loads are unconditional (the last ones' read a tile again):
   // behind a condition the compiler could not count the loads in flight, and
   // would wait for the values just asked for before it uses the keys
-  for (int i = 0; i < nt; i += NB) {
-    tile(buf[0], i);
-    if constexpr (NB > 1) {
-      if (i + 1 < nt) tile(buf[NB - 1], i + 1);
-    }
-  }
+  for (int i = 0; i < nt; ++i) tile(i);
 
   P = params_again();
   // the four waves' sums joined: lane l holds of row l % 16 the dims
@@ -784,11 +792,15 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
   int64_t keys = max_ctx;
   if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
   const int64_t units = (int64_t)B * p.nrb;
-  const int slots = 256 * (dim <= 64 && p.rt <= 2 ? 3 : 2);  // resident workgroups
+  // workgroups that the card holds at once, by the kernels' registers (at 64
+  // dims and one row tile 4 to a CU would fit in part: 118 us against 107 for
+  // 256 contexts of 2048 tokens)
+  const int slots = 256 * (dim <= 64 && p.rt <= 2 ? 3 : 2);
   p.hw = 1;
   if (keys <= 1024 || (keys <= 2048 && units * heads <= slots) || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
-    // short contexts, very many units, or many blocks of long prompts: a unit
-    // to a workgroup; the blocks of one head on one XCD, for its keys
+    // short contexts (8 of 1500 tokens: 19 us against 24 in runs, but 256 of
+    // 2048: 117 against 107), very many units, or many blocks of long prompts:
+    // a unit to a workgroup; the blocks of one head on one XCD, for its keys
     p.chunks = 0;
     p.items = p.nrb;
     p.groups = (int64_t)B * heads;
@@ -796,7 +808,8 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
     // equal runs, as many as are resident at once; a run's heads on one XCD.
     // With few rows (small partial sums), long runs and a token's heads side
     // by side a wave takes a head of its own, so that a workgroup reads them
-    // together.
+    // together (three contexts of 131072 tokens: 141 us against 167; where
+    // tokens stand inside heads it is the other way, 150 against 133).
     if (p.rt == 1 && heads_in && units * keys / kTileKeys * heads >= (int64_t)slots * kWaves * 32)
       p.hw = heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
     const int hgroups = heads / p.hw;
@@ -834,7 +847,9 @@ static hipError_t launch_attn_rows(const AttnParams& P, int rt, hipStream_t stre
 template <int COLS>
 static hipError_t launch_join(const AttnParams& P, const AttnPlan& plan, hipStream_t stream) {
   const dim3 grid((unsigned)(P.B * P.nrb * P.c.heads * plan.rt));
-  if (plan.chunks > 8 * P.B * P.nrb)  // many runs to a unit
+  // many runs to a unit: 10 us against 25 for three units of 85 runs; few runs
+  // and many units: 10 us with small workgroups
+  if (plan.chunks > 8 * P.B * P.nrb)
     hipLaunchKernelGGL((attn_join_kernel<COLS, 1024>), grid, dim3(1024), 0, stream, P, plan.rt);
   else
     hipLaunchKernelGGL((attn_join_kernel<COLS, kWG>), grid, dim3(kWG), 0, stream, P, plan.rt);

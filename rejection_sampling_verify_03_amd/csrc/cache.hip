@@ -7,7 +7,14 @@
 // leads: the wave that meets it gathers the group's entries, reduces their
 // largest magnitude, settles the exponent with the one the group has, moves
 // the earlier tokens' codes if it grew, and writes the new codes.  No
-// atomics, no second launch, and one owner for each group's bytes.
+// global atomics, no second launch, and one owner for each group's bytes.
+//
+// Both are bound by memory.  Measured (MI355X): 32771 tokens of 8 heads of 128
+// bf16 written in 36 us (143 MB read and written, 3.9 TB/s; a device copy
+// reaches 4.7), 131072 tokens read back in 140 us (806 MB, 5.7 TB/s).  A write
+// holds eight steps of a group in registers: four made it 20 % slower (groups
+// of 32 tokens are then read twice), and heads that interleave keys and values
+// over the waves cost a tenth (a wave's neighbours then read elsewhere).
 #include <limits.h>
 
 #include "cache_device.hpp"

@@ -22,6 +22,15 @@
 //      logits all stand in front of the next cell's).  A threshold that at
 //      least n of the 64 lanes' maxima reach picks a few more than n cells,
 //      whose logits are read again; those that reach it are sorted.
+//
+// Bounds, measured (MI355X): the statistics pass is bound by its vector
+// instructions (a logit costs 8 of them and an exponential; they are issued
+// in 95 % of the cycles) just above the rate of memory: 2304 rows of 151936
+// bf16 logits without alternatives take 125 us (6.3 TB/s), the 1327 live rows
+// of a verified batch with 5 alternatives 92 us (4.4 TB/s), of which the finish
+// is 15 us, one chain of three reads of memory.  Segments of 4096 logits, as
+// in draft.hip: 64 registers of logits a lane leave five waves to a SIMD.
+// Four segments to a workgroup were 7 % slower there, sixteen 3 %.
 #include <limits.h>
 
 #include <type_traits>

@@ -301,3 +301,132 @@ def test_a_round_of_speculative_decoding(sv):
     assert np.all(np.abs(r.logprobs.cpu().double().numpy() - lp) <= tol)
     assert np.array_equal(r.top_ids.cpu().numpy(), ids)
     assert np.array_equal((tok >= 0).sum(1).cpu().numpy(), acc.cpu().numpy() + 1)
+
+
+# The cut of the work follows the bounds that the caller gives (max_ctx,
+# max_q), not the lengths on the device: a bound far above them takes the cut
+# of long contexts (equal runs, a head to a wave, large joins) at small sizes.
+FAR = 1 << 22
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("heads,G", [(1, 16), (2, 3), (4, 8), (8, 1), (12, 2)])
+def test_runs_of_tiles_and_heads_to_waves(sv, dim, heads, G):
+    for st, order in ((16, "tokens"), (1, "tokens"), (16, "heads")):
+        c = Case([1, 1, 0, 1], [700, 33, 0, 1100], G, heads, dim, 16, st, dim + heads + st, order=order)
+        c.check(sv, max_ctx=FAR, sinks=st == 1)
+    c.check(sv, max_ctx=FAR, window=1030)
+
+
+@pytest.mark.parametrize("dim,n,G", [(64, 9, 8), (64, 40, 4), (128, 30, 4), (256, 20, 3)])
+def test_runs_with_several_blocks_of_rows(sv, dim, n, G):
+    c = Case([n, n // 3, 1, n], [n + 1500, n, 500, n - 5], G, 2, dim, 32, 32, dim + n)
+    c.check(sv, max_ctx=FAR)
+    c.check(sv, max_ctx=FAR, sinks=True, window=1030)
+
+
+@pytest.mark.parametrize("order", ["tokens", "heads"])
+def test_long_runs_of_many_heads(sv, order):
+    """Fewer runs than the shortest ones would make: with many heads a run
+    has more tiles, and a wave's look-up window ends inside it."""
+    Case([1, 2, 1], [4100, 37, 3333], 1, 64, 16, 16, 16, 85, order=order).check(sv, max_ctx=FAR)
+
+
+def test_runs_captured_and_replayed(sv):
+    """Two graphs whose calls share one workspace, replayed in turn with the
+    program's own calls between them; lengths on the device change."""
+    cs = [Case([1, 1], [900, 1300], 8, 2, 64, 16, 16, 86), Case([3, 1], [1100, 200], 4, 4, 128, 16, 1, 87)]
+    args = [(c.q.cuda(), c.cache(sv), c.table.cuda(), c.q_start.cuda(), c.ctx.cuda()) for c in cs]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def go(i, **kw):
+        return sv.kv_attention(*args[i], max_q=cs[i].max_q, max_ctx=FAR, return_lse=True, **kw)
+    for i in range(2):
+        go(i, workspace=ws)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in cs], []
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            outs.append(go(i, workspace=ws))
+    for lens in (([900, 1300], [1100, 200]), ([17, 1001], [5, 0]), ([1, 0], [1100, 199])):
+        for i in range(2):
+            args[i][4].copy_(torch.tensor(lens[i], dtype=torch.int32))
+            args[i][0].copy_(args[i][0].flip(0))
+            graphs[i].replay()
+        eager = [go(i) for i in range(2)]
+        torch.cuda.synchronize()
+        for (o, z), (eo, ez) in zip(outs, eager):
+            assert torch.equal(o, eo) and torch.equal(z, ez)
+
+
+def test_runs_keep_what_is_not_seen_out(sv):
+    c = Case([3, 1], [1037, 970], 4, 4, 64, 16, 16, 80)
+    last = int(c.table[0, 64])
+    for t in (c.k, c.v):
+        t[last, 13:] = 0x7F
+    c.table[1, 3] = -1
+    out, lse = c.check(sv, max_ctx=FAR)
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+    c.v[last, 12, 2, 7] = 0x7F   # the last token's value: position 1036
+    out, _ = c.call(sv, max_ctx=FAR)
+    torch.cuda.synchronize()
+    bad = torch.isnan(out.float()).cpu()
+    assert bool(bad[2, 8:12, 7].all()) and int(bad.sum()) == 4
+
+
+def test_runs_with_unusable_and_empty_requests(sv):
+    c = Case([1, 2, 0, 1, 1], [400, 300, 10, 0, 900], 4, 4, 64, 16, 16, 81)
+    c.ctx[1] = -3
+    out, lse = c.call(sv, max_ctx=FAR)
+    torch.cuda.synchronize()
+    c.ctx[1] = 300
+    o, z, otol, ltol = c.want()
+    o[1:3], z[1:3] = np.nan, np.nan
+    compare(out, lse, o, z, otol, ltol)
+    c.ctx[:] = 0
+    out, lse = c.check(sv, max_ctx=FAR)
+    assert not bool(out.any())
+
+
+def test_many_requests(sv):
+    """Ragged batches of hundreds (in runs) and thousands (a workgroup each)."""
+    g = torch.Generator().manual_seed(82)
+    for B, most in ((300, 200), (4200, 20)):
+        ctx = torch.randint(0, most, (B,), generator=g).tolist()
+        lens = [min(int(v), 3) for v in torch.randint(0, 4, (B,), generator=g)]
+        Case(lens, ctx, 2, 1, 32, 16, 16, B).check(sv, max_ctx=FAR)
+
+
+def test_two_streams_at_once(sv):
+    a, b = Case([1, 1], [3000, 1700], 8, 2, 64, 16, 16, 83), Case([2, 1], [2500, 4100], 4, 4, 128, 16, 1, 84)
+    plain = [c.call(sv, max_ctx=FAR) for c in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [c.call(sv, max_ctx=FAR, stream=s) for c, s in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        for (o, z), (po, pz) in zip(got, plain):
+            assert torch.equal(o, po) and torch.equal(z, pz)
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_scores_past_the_range_of_fp32(sv, far):
+    """Above it: the row is NaN; below it: the key has no weight."""
+    c = Case([1, 1], [40, 70], 2, 1, 64, 16, 16, 88)
+    c.k[:], c.ks[:] = 0, 127
+    one = 0x38  # 1.0
+    at = int(c.table[1, 1])  # positions 16..31 of request 1, of which 20 is aligned with q
+    c.k[at, 4, 0, :] = one
+    c.ks[at] = 247  # 2^120
+    c.q[:] = 1.0
+    c.q[1, 0, :], c.q[1, 1, :] = 2.0 ** 20, -2.0 ** 20
+    out, lse = c.call(sv, max_ctx=FAR if far else c.max_ctx)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(out[1, 0]).all()) and bool(torch.isnan(lse[1, 0]))
+    assert not bool(torch.isnan(out[0]).any())
+    # 69 keys of score 0 and one of no weight
+    j = np.array([t for t in range(70) if t != 20])
+    v = oo.kv_values(c.v.numpy(), c.vs.numpy(), c.table[1].numpy()[j // 16] * 16 + j % 16, 16)[:, 0]
+    want, tol = v.mean(0), np.abs(v.mean(0)) * 2.0 ** -8 + np.abs(v).mean(0) * 80 * oo.U
+    assert np.all(np.abs(out[1, 1].cpu().double().numpy() - want) <= tol)
+    assert abs(float(lse[1, 1]) - math.log(69)) <= 8 * oo.U * math.log(69)

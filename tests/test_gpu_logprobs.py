@@ -59,6 +59,19 @@ def test_shapes(sv, B, R, V, top, dtype):
     check(sv, *make(B, R, V, dtype, B * 7 + R * 11 + V), top)
 
 
+@pytest.mark.parametrize("V,top", [(262144, 5), (262145, 20), (300001, 32), (1 << 20, 20)])
+def test_vocabularies_past_one_window_of_cells(sv, V, top):
+    check(sv, *make(1, 2, V, torch.bfloat16, V % 1000), top)
+    x = torch.full((1, 1, V), -4.0)
+    x[0, 0, ::64] = 3.0  # more cells of equal maxima than a list holds
+    x[0, 0, V - 1] = 5.0
+    check(sv, x, torch.tensor([[V - 1]], dtype=torch.int32), None, top)
+
+
+def test_many_rows(sv):
+    check(sv, *make(700, 5, 130, torch.float32, 6), 3)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_rows_without_tokens_and_unusable_rows(sv, dtype):
     logits, tokens, temperature = make(12, 3, 5000, dtype, 5)

@@ -536,7 +536,9 @@ int spec_logprobs_launch(const spec_logprobs_args* args, hipStream_t stream);
  * c is c * 2^(byte - 127).  (e4m3 is a floating-point format: a scale that is
  * no power of two would gain it no precision, and with powers of two a value
  * is exact in bf16 and a growing scale moves codes without rounding them,
- * but for the smallest.)
+ * but for the smallest.)  A write makes bytes of 10 to 247.  A byte of 0, that
+ * of memory not written yet, gives values of 0; other bytes that a write does
+ * not make are read where fp32 (bf16) holds the values, 255 is unspecified.
  * Layout: code of head h, element d at
  *   codes + block * block_stride + token * token_stride + h * head_stride + d,
  * scale byte of group g of a block at
@@ -615,6 +617,8 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  *   out = sum_j exp(s_j - z) v_j,  lse = z
  * (without sinks that term is absent).  A token that sees nothing gets out 0
  * and lse = sinks[h], or -inf without sinks.
+ * The scores are computed in fp32: one above its range makes its row NaN, one
+ * below it counts as -inf.
  * Codes of positions that a token does not see never reach its output, NaN
  * among them.  A request whose ctx_len is negative or above max_ctx or
  * max_blocks * block_size, or whose n_b is above max_q, is a data error: NaN
@@ -632,7 +636,7 @@ typedef struct {
   int32_t max_ctx;             /* upper bound of ctx_len, 0..2^30 */
   int32_t window;              /* 0 = none */
   int32_t dtype;               /* SPEC_BF16: q and out */
-  float scale;                 /* finite */
+  float scale;                 /* finite, below 2.3e38 */
   const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
   int64_t q_token_stride, q_head_stride;  /* elements, >= 0 */
   const int32_t* q_start;      /* device [B + 1] */

@@ -347,7 +347,7 @@ bool attn_sizes_ok(const spec_attn_args* a) {
   const spec_kv_cache& c = a->cache;
   if (c.heads < 1 || c.heads > 1024 || c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16) return false;
   if (a->q_heads < c.heads || a->q_heads % c.heads || a->q_heads / c.heads > 64) return false;
-  return true;
+  return (int64_t)a->B * c.heads <= INT32_MAX;  // (times the blocks of rows, at most 2^26, within 64 bits)
 }
 
 AttnPlan attn_plan(const spec_attn_args* a) {
@@ -367,7 +367,7 @@ int attn_check(const spec_attn_args* a, AttnPlan& plan) {
   if (a->dtype != SPEC_BF16) return SPEC_EDTYPE;
   const int rc = cache_check(a->cache);
   if (rc != SPEC_OK) return rc;
-  if (!(a->scale >= -FLT_MAX && a->scale <= FLT_MAX)) return SPEC_EINVAL;
+  if (!(fabsf(a->scale) <= FLT_MAX / 1.4427f)) return SPEC_EINVAL;  // (the kernel takes scale * log2(e))
   if (a->max_blocks < 0 || a->bt_row_stride < a->max_blocks) return SPEC_EINVAL;
   if (a->B == 0 || a->N == 0) return SPEC_OK;
   if (!a->q || !a->q_start || !a->ctx_len || !a->out) return SPEC_EINVAL;
@@ -375,9 +375,8 @@ int attn_check(const spec_attn_args* a, AttnPlan& plan) {
   if (a->q_token_stride < 0 || a->q_head_stride < 0) return SPEC_EINVAL;
   if (!aligned16(a->out)) return SPEC_EALIGN;
   plan = attn_plan(a);
-  const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;  // <= 2^31 * 2^10 * 2^26 checked in steps
-  if ((int64_t)a->B * a->cache.heads > INT32_MAX || grid / plan.nrb != (int64_t)a->B * a->cache.heads ||
-      grid > INT32_MAX || !fits_dispatch((plan.groups + 7) / 8 * 8 * plan.items, kThreads) ||
+  const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;
+  if (grid > INT32_MAX || !fits_dispatch((plan.groups + 7) / 8 * 8 * plan.items, kThreads) ||
       (plan.chunks > 0 && !fits_dispatch(grid * plan.rt, kThreads)))
     return SPEC_EINVAL;
   const size_t need = attn_ws_bytes(a, plan);

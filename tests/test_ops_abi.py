@@ -216,3 +216,13 @@ def test_oracle_group_exponent():
         x[0, 0, 3] = -amax
         oo.kv_write(codes, scales, x, [0], 16)
         assert int(scales[0, 0, 0]) - 127 == e
+
+
+def test_attention_sizes_past_64_bits(sv):
+    """Sizes whose products pass what the plan counts in are refused."""
+    for kw in (dict(B=2 ** 31 - 1, q_heads=128, max_q=2 ** 24, max_ctx=2 ** 30), dict(B=2 ** 31 - 1, max_q=2 ** 24)):
+        a = attn_args(sv, **kw)
+        a.cache.heads = 2
+        assert sv.spec_attn_launch(a, None) == sv.SPEC_EINVAL and sv.spec_attn_workspace_bytes(a) == 0
+    assert sv.spec_attn_launch(attn_args(sv, scale=3e38), None) == sv.SPEC_EINVAL
+    assert sv.spec_attn_launch(attn_args(sv, scale=-3e38), None) == sv.SPEC_EINVAL

@@ -205,3 +205,16 @@ def test_graph_replays(sv):
         torch.cuda.synchronize()
         assert torch.equal(cache.k, ref.k) and torch.equal(cache.v_scale, ref.v_scale)
         assert torch.equal(k, ek) and torch.equal(v, ev)
+
+
+def test_long_runs_of_skipped_entries(sv):
+    """Runs of skipped entries longer than what one reading of the list takes,
+    between a group's entries, in front of them and behind the last."""
+    cache = filled(sv, 6, 16, 1, 32, 16, 12)
+    slots = torch.full((5000,), -1)
+    for i, s in ((700, 18), (1291, 19), (2400, 20), (2401, 33), (3500, 34), (3501, 2), (4120, 80), (4999, 81)):
+        slots[i] = s
+    check_write(sv, cache, *tokens(5000, 1, 32, torch.bfloat16, 13), slots)
+    slots = torch.full((3000,), -1)
+    slots[0], slots[2999] = 64, 65
+    check_write(sv, cache, *tokens(3000, 1, 32, torch.float32, 14), slots)

@@ -27,8 +27,9 @@
 // instructions (a logit costs 8 of them and an exponential; they are issued
 // in 95 % of the cycles) just above the rate of memory: 2304 rows of 151936
 // bf16 logits without alternatives take 125 us (6.3 TB/s), the 1327 live rows
-// of a verified batch with 5 alternatives 92 us (4.4 TB/s), of which the finish
-// is 15 us, one chain of three reads of memory.  Segments of 4096 logits, as
+// of a verified batch with 5 alternatives 87 us (4.7 TB/s), of which the finish
+// is 11 us, one wave's chain of steps: 4 to the joined sums, 3 to the threshold,
+// the rest to find, read and sort the candidates.  Segments of 4096 logits, as
 // in draft.hip: 64 registers of logits a lane leave five waves to a SIMD.
 // Four segments to a workgroup were 7 % slower there, sixteen 3 %.
 #include <limits.h>
@@ -228,45 +229,46 @@ __device__ __forceinline__ int raise_threshold(const int* keys, int lane, int n)
 
 // The alternatives of one row: ids and values of the n largest logits above
 // -inf (lane p the p-th), -1 where there are fewer.  A row is one wave's chain
-// of steps: the reads of a step are on their way together, and the loops are
-// kept rolled (unrolled, the wave waits for its own instructions).
+// of steps.  top_short takes rows whose cells fit a window and whose
+// candidates are few, all others (ties of thousands, very long rows) top_long.
 constexpr int kLpWindow = 16;  // loads of 256 cells held at a time: 4096 cells, a row of up to 262144 logits
+constexpr int kLpShort = 8;    // loads of 8 cells that top_short holds: 64 candidate cells
 template <int ES>
 struct LpLists {  // a wave's room in LDS
-  int keys[2][kLpList], ids[2][kLpList];  // candidate cells, candidate logits
-  typename std::conditional<ES == 2, uint2, uint4>::type cells[kLpWindow * 64];  // four to a lane, as stored
+  alignas(16) int keys[2][kLpList];
+  alignas(16) int ids[2][kLpList];  // candidate cells, candidate logits
+  union {
+    typename std::conditional<ES == 2, uint2, uint4>::type cells[kLpWindow * 64];  // four to a lane, as stored
+    RawGroup<ES, true> logits[kLpShort * 64];                                      // eight to a lane, as stored
+  };
 };
 
-template <int ES>
-__device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* row, const float* cells, int n,
-                                           int lane, LpLists<ES>& L, int& out_id, float& out_x) {
-  const int ncell = P.nseg * kLpCells;  // at most 2^25, a multiple of 64
-  const int kNone = order_key(-INFINITY);
-  const int windows = (ncell + kLpWindow * 256 - 1) / (kLpWindow * 256);
-  float lm = -INFINITY;   // the lane's largest
-  f32x4 head{-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // its first four
-  auto load_window = [&](int w) {
-    f32x4 c[kLpWindow];
+__device__ __forceinline__ int wave_scan_i(int x) {
+  x += dpp_i<0x111, 0xf>(x, 0);
+  x += dpp_i<0x112, 0xf>(x, 0);
+  x += dpp_i<0x114, 0xf>(x, 0);
+  x += dpp_i<0x118, 0xf>(x, 0);
+  x += dpp_i<0x142, 0xa>(x, 0);
+  x += dpp_i<0x143, 0xc>(x, 0);
+  return x;
+}
+
+// The first window of a row's cells, four to a lane and load; -inf past them.
+struct LpCellWindow {
+  f32x4 c[kLpWindow];
+};
+__device__ __forceinline__ void load_cells(LpCellWindow& w, const float* cells, int first, int ncell, int lane) {
 #pragma unroll
-    for (int j = 0; j < kLpWindow; ++j) {
-      const int at = (w * kLpWindow + j) * 256 + lane * 4;
-      c[j] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (at < ncell) c[j] = *reinterpret_cast<const f32x4*>(cells + at);
-    }
-    if (w == 0) head = c[0];
-#pragma unroll
-    for (int j = 0; j < kLpWindow; ++j) {
-      lm = fmaxf(fmaxf(fmaxf(c[j].x, c[j].y), fmaxf(c[j].z, c[j].w)), lm);
-      if constexpr (ES == 2)  // exact in bf16
-        L.cells[j * 64 + lane] = uint2{(__float_as_uint(c[j].x) >> 16) | (__float_as_uint(c[j].y) & 0xffff0000u),
-                                       (__float_as_uint(c[j].z) >> 16) | (__float_as_uint(c[j].w) & 0xffff0000u)};
-      else
-        L.cells[j * 64 + lane] = uint4{__float_as_uint(c[j].x), __float_as_uint(c[j].y), __float_as_uint(c[j].z),
-                                       __float_as_uint(c[j].w)};
-    }
-  };
-  // a threshold that at least n cells reach (or -inf: every cell above it)
-  for (int w = 0; w < windows; ++w) load_window(w);
+  for (int j = 0; j < kLpWindow; ++j) {
+    const int at = first + j * 256 + lane * 4;
+    w.c[j] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (at < ncell) w.c[j] = *reinterpret_cast<const f32x4*>(cells + at);
+  }
+}
+
+// The keys of a row's cells, the lanes' largest: a threshold that at least n
+// cells reach (or every cell above -inf).
+__device__ __forceinline__ int cell_threshold(const f32x4& head, float lm, int ncell, int n) {
   int thr;
   if (ncell <= 256) {
     const int mk[4] = {order_key(head.x), order_key(head.y), order_key(head.z), order_key(head.w)};
@@ -275,7 +277,131 @@ __device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* 
     const int mk[1] = {order_key(lm)};
     thr = reach_bound<1>(mk, n);
   }
-  thr = max(thr, kNone + 1);
+  return max(thr, order_key(-INFINITY) + 1);
+}
+
+// The candidates of a row in any order into L.keys[1], L.ids[1]; their number,
+// or -1 where there are too many.  A lane marks what it holds in a mask, and a
+// sum over the lanes gives each its places: no step waits for another's count
+// (appending 256 cells at a time cost 5 us of the finish's 16, and eight cells'
+// logits at a time another 5).
+template <int ES>
+__device__ __forceinline__ int top_short(const LogprobsParams& P, const char* row, const LpCellWindow& win, int n,
+                                         int lane, LpLists<ES>& L) {
+  float lm = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kLpWindow; ++j)
+    lm = fmaxf(fmaxf(fmaxf(win.c[j].x, win.c[j].y), fmaxf(win.c[j].z, win.c[j].w)), lm);
+  int thr = cell_threshold(win.c[0], lm, P.nseg * kLpCells, n);
+  auto places = [&](uint64_t hit, int& total) {  // where this lane's hits go
+    const int mine = __builtin_popcountll(hit), end = wave_scan_i(mine);
+    total = lane_i(end, 63);
+    return end - mine;
+  };
+  uint32_t lo = 0, hi = 0;
+  const float t0 = order_value(thr);
+#pragma unroll
+  for (int j = 0; j < kLpWindow; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) (j < 8 ? lo : hi) |= win.c[j][q] >= t0 ? 1u << (4 * (j & 7) + q) : 0u;
+  uint64_t hit = ((uint64_t)hi << 32) | lo;
+  int ncand, at = places(hit, ncand);
+  if (ncand > kLpShort * 8) return -1;
+  for (; hit; hit &= hit - 1, ++at) {
+    const int k = __builtin_ctzll(hit);
+    L.ids[0][at] = (k >> 2) * 256 + lane * 4 + (k & 3);
+  }
+  __builtin_amdgcn_wave_barrier();
+  // the cells' logits, 8 lanes to a cell: the last 8 of the row where a lane's
+  // would pass its end, of which it takes what is its own
+  RawGroup<ES, true> r[kLpShort];
+  int first[kLpShort];
+#pragma unroll
+  for (int j = 0; j < kLpShort; ++j) {
+    const int c = j * 8 + (lane >> 3);
+    first[j] = INT_MAX;
+    if (j * 8 < ncand) {
+      if (c < ncand) first[j] = L.ids[0][c] * 64 + (lane & 7) * 8;
+      r[j] = load_any<ES>(row, min(first[j], P.V - 8));
+    }
+  }
+  float most = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kLpShort; ++j)
+    if (j * 8 < ncand) {
+      float x[8];
+      unpack_group<ES, true>(r[j], x);
+      L.logits[j * 64 + lane] = r[j];
+      if (__ballot(first[j] > P.V - 8)) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = first[j] - q > P.V - 8 ? -INFINITY : x[q];
+      }
+      most = fmaxf(most, group_max(x));
+    }
+  // the threshold may rise to what n lanes reach
+  const int mk[1] = {order_key(most)};
+  thr = max(thr, reach_bound<1>(mk, n));
+  const float t1 = order_value(thr);
+  lo = hi = 0;
+#pragma unroll
+  for (int j = 0; j < kLpShort; ++j)
+    if (j * 8 < ncand) {
+      float x[8];
+      uint32_t m = 0;
+      unpack_group<ES, true>(r[j], x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m |= x[q] >= t1 ? 1u << q : 0u;
+      const int own = min(max(first[j] - (P.V - 8), 0), 8);  // the first of them that is its own
+      m = (m >> own) << own;
+      (j < 4 ? lo : hi) |= m << (8 * (j & 3));
+    }
+  hit = ((uint64_t)hi << 32) | lo;
+  int ne;
+  at = places(hit, ne);
+  if (ne > kLpList) return -1;
+  __builtin_amdgcn_wave_barrier();
+  for (; hit; hit &= hit - 1, ++at) {
+    const int k = __builtin_ctzll(hit), j = k >> 3, q = k & 7;
+    const int c = j * 8 + (lane >> 3);
+    const char* g = reinterpret_cast<const char*>(&L.logits[j * 64 + lane]);
+    uint32_t bits = 0;  // (bf16: its upper half)
+    __builtin_memcpy(reinterpret_cast<char*>(&bits) + 4 - ES, g + q * ES, ES);
+    L.keys[1][at] = order_key(__uint_as_float(bits));
+    L.ids[1][at] = min(L.ids[0][c] * 64 + (lane & 7) * 8, P.V - 8) + q;
+  }
+  __builtin_amdgcn_wave_barrier();
+  return ne;
+}
+
+// The same for any row, the candidates in ascending order of their ids and of
+// those equal to the threshold the first n; the loops are kept rolled
+// (unrolled, the wave waits for its own instructions).
+template <int ES>
+__device__ __forceinline__ int top_long(const LogprobsParams& P, const char* row, const float* cells, int n, int lane,
+                                        LpLists<ES>& L) {
+  const int ncell = P.nseg * kLpCells;  // at most 2^25, a multiple of 64
+  const int windows = (ncell + kLpWindow * 256 - 1) / (kLpWindow * 256);
+  float lm = -INFINITY;   // the lane's largest
+  f32x4 head;             // its first four
+  auto load_window = [&](int w) {
+    LpCellWindow win;
+    load_cells(win, cells, w * kLpWindow * 256, ncell, lane);
+    if (w == 0) head = win.c[0];
+#pragma unroll
+    for (int j = 0; j < kLpWindow; ++j) {
+      const f32x4 c = win.c[j];
+      lm = fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), lm);
+      if constexpr (ES == 2)  // exact in bf16
+        L.cells[j * 64 + lane] = uint2{(__float_as_uint(c.x) >> 16) | (__float_as_uint(c.y) & 0xffff0000u),
+                                       (__float_as_uint(c.z) >> 16) | (__float_as_uint(c.w) & 0xffff0000u)};
+      else
+        L.cells[j * 64 + lane] = uint4{__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(c.z),
+                                       __float_as_uint(c.w)};
+    }
+  };
+#pragma unroll 1
+  for (int w = 0; w < windows; ++w) load_window(w);
+  int thr = cell_threshold(head, lm, ncell, n);
   LpList lc{L.keys[0], L.ids[0], 0, 0};
   for (;;) {
     lc.count = lc.equal = 0;
@@ -342,24 +468,35 @@ __device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* 
     if (le.count <= kLpList) break;
     thr = raise_threshold(le.keys, lane, n);
   }
+  return le.count;
+}
+
+template <int ES>
+__device__ __forceinline__ void top_of_row(const LogprobsParams& P, const char* row, const float* cells,
+                                           const LpCellWindow& win, int n, int lane, LpLists<ES>& L, int& out_id,
+                                           float& out_x) {
+  int ne = -1;
+  if (P.nseg * kLpCells <= kLpWindow * 256 && P.V >= 8) ne = top_short<ES>(P, row, win, n, lane, L);
+  if (ne < 0) ne = top_long<ES>(P, row, cells, n, lane, L);
   // sorted by rank: the place of an item is the number of items in front
-  const int ne = le.count;
-  lc.keys[lane] = kNone;
-  lc.ids[lane] = -1;
+  const int* keys = L.keys[1];
+  const int* ids = L.ids[1];
+  L.keys[0][lane] = order_key(-INFINITY);
+  L.ids[0][lane] = -1;
   __builtin_amdgcn_wave_barrier();
   for (int at = lane; at < ne; at += 64) {
-    const int key = le.keys[at];
+    const int key = keys[at], id = ids[at];
     int rank = 0;
 #pragma unroll 8
-    for (int o = 0; o < ne; ++o) rank += le.keys[o] > key || (le.keys[o] == key && o < at);
+    for (int o = 0; o < ne; ++o) rank += keys[o] > key || (keys[o] == key && ids[o] < id);
     if (rank < n) {
-      lc.keys[rank] = key;
-      lc.ids[rank] = le.ids[at];
+      L.keys[0][rank] = key;
+      L.ids[0][rank] = id;
     }
   }
   __builtin_amdgcn_wave_barrier();
-  out_id = lc.ids[lane];
-  out_x = order_value(lc.keys[lane]);
+  out_id = L.ids[0][lane];
+  out_x = order_value(L.keys[0][lane]);
 }
 
 // One wave: row i's records joined, its outputs written.
@@ -370,19 +507,27 @@ __device__ __forceinline__ void finish_row(const LogprobsParams& P, int i, int l
   const float T = row_temperature(P, b);
   const float nan = __builtin_nanf("");
   const bool usable = tok >= 0 && tok < P.V && temperature_valid(T);
+  const char* row = P.logits + (b * P.req + r * P.row) * ES;
   double M = -INFINITY, S = 0.0, W = 0.0;
+  float x_tok = 0.f;
+  LpCellWindow win;
   if (usable) {
+    // what the row needs first is on its way together: its records, the
+    // token's logit, the cells
+    const LpRecord* rec = P.rec + (int64_t)i * P.nseg;
+    LpRecord q = rec[min(lane, P.nseg - 1)];
+    x_tok = load_one<ES>(row, tok);
+    if constexpr (TOP) load_cells(win, P.cells + (int64_t)i * P.nseg * kLpCells, 0, P.nseg * kLpCells, lane);
+    if (lane >= P.nseg) q = LpRecord{-INFINITY, 0.f, 0.f, 0.f};
     // the records' sums, each brought to the row's maximum: the exponents
     // shift by d = (m - M) * s <= 0, so S by 2^d and W to 2^d (W + d S)
-    const LpRecord* rec = P.rec + (int64_t)i * P.nseg;
     const double s = 1.4426950408889634074 / (double)T;
-    float mm = -INFINITY;
-    for (int j = lane; j < P.nseg; j += 64) mm = fmaxf(mm, rec[j].m);
+    float mm = q.m;
+    for (int j = lane + 64; j < P.nseg; j += 64) mm = fmaxf(mm, rec[j].m);
     mm = wave_max_f(mm);
     M = mm;
     double S1 = 0.0, W1 = 0.0;
-    for (int j = lane; j < P.nseg; j += 64) {
-      const LpRecord q = rec[j];
+    for (int j = lane;;) {
       if (q.m > -INFINITY) {
         const double d = fmax(((double)q.m - M) * s, -4000.0);
         const double f = exp2(d);
@@ -391,18 +536,19 @@ __device__ __forceinline__ void finish_row(const LogprobsParams& P, int i, int l
       } else {
         S1 += (double)q.s;  // 0, or NaN
       }
+      j += 64;
+      if (j >= P.nseg) break;
+      q = rec[j];
     }
     S = wave_total_d(S1);
     W = wave_total_d(W1);
   }
   const bool good = usable && S > 0.0 && S <= DBL_MAX && fabs(M) <= FLT_MAX;
-  const char* row = P.logits + (b * P.req + r * P.row) * ES;
   const double lnS = good ? log(S) : 0.0;
   if (lane == 0) {
     float lp = tok == -1 ? 0.f : nan, ent = lp;
     if (good) {
-      const double x = load_one<ES>(row, tok);
-      lp = (float)((x - M) / (double)T - lnS);
+      lp = (float)(((double)x_tok - M) / (double)T - lnS);
       ent = (float)fmax(lnS - 0.69314718055994530942 * (W / S), 0.0);
     }
     P.logprobs[i] = lp;
@@ -412,7 +558,7 @@ __device__ __forceinline__ void finish_row(const LogprobsParams& P, int i, int l
     int id = -1;
     float x = -INFINITY;
     if (good)
-      top_of_row<ES>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, P.top, lane, *lists, id, x);
+      top_of_row<ES>(P, row, P.cells + (int64_t)i * P.nseg * kLpCells, win, P.top, lane, *lists, id, x);
     if (lane < P.top) {
       P.top_ids[(int64_t)i * P.top + lane] = id;
       P.top_lp[(int64_t)i * P.top + lane] =

@@ -399,11 +399,12 @@ def test_many_requests(sv):
 
 def test_two_streams_at_once(sv):
     a, b = Case([1, 1], [3000, 1700], 8, 2, 64, 16, 16, 83), Case([2, 1], [2500, 4100], 4, 4, 128, 16, 1, 84)
-    plain = [c.call(sv, max_ctx=FAR) for c in (a, b)]
-    torch.cuda.synchronize()
+    args = [(c.q.cuda(), c.cache(sv), c.table.cuda(), c.q_start.cuda(), c.ctx.cuda(), c.max_q) for c in (a, b)]
+    plain = [sv.kv_attention(*x, max_ctx=FAR, return_lse=True) for x in args]
+    torch.cuda.synchronize()  # (the streams below wait for nothing: all inputs are there)
     streams = [torch.cuda.Stream() for _ in range(2)]
     for _ in range(3):
-        got = [c.call(sv, max_ctx=FAR, stream=s) for c, s in zip((a, b), streams)]
+        got = [sv.kv_attention(*x, max_ctx=FAR, return_lse=True, stream=s) for x, s in zip(args, streams)]
         torch.cuda.synchronize()
         for (o, z), (po, pz) in zip(got, plain):
             assert torch.equal(o, po) and torch.equal(z, pz)

@@ -618,7 +618,8 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  * (without sinks that term is absent).  A token that sees nothing gets out 0
  * and lse = sinks[h], or -inf without sinks.
  * The scores are computed in fp32: one above its range makes its row NaN, one
- * below it counts as -inf.
+ * below it counts as -inf.  The sums of values too, with weights of up to 2^8:
+ * 2^8 * ctx_len * max |v| has to lie in its range.
  * Codes of positions that a token does not see never reach its output, NaN
  * among them.  A request whose ctx_len is negative or above max_ctx or
  * max_blocks * block_size, or whose n_b is above max_q, is a data error: NaN

@@ -193,3 +193,30 @@ def test_graph_replays_and_other_streams(sv):
     other = sv.token_logprobs(lg, tk, tp, top=8, stream=side)
     side.synchronize()
     assert torch.equal(other.top_ids, eager.top_ids) and torch.equal(other.logprobs, eager.logprobs)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [8, 9, 15, 63, 66, 71, 4097, 4103, 5003, 32765, 70001, 262139])
+def test_alternatives_at_the_end_of_a_row(sv, V, dtype):
+    """The last logits, whose loads reach back over the row's end, lead; then
+    the same with the row's ends -inf, and with equal ones."""
+    for top in (1, 5, 20, 32):
+        x, tokens, _ = make(2, 2, V, dtype, V + top)
+        last = min(V, 40)
+        x[:, 0, V - last:] = 20.0 + torch.randperm(last, generator=torch.Generator().manual_seed(V)).to(dtype) / 4
+        x[:, 1, V - last:] = 20.0
+        x[1, 1, V - last // 2:] = -math.inf
+        tokens[1, 1] = V - last // 2 - 1
+        check(sv, x, tokens, None, top)
+
+
+def test_more_candidates_than_a_list(sv):
+    """Equal logits in 60 to 70 cells, and 250 to 260 of them in few cells."""
+    for cells in (60, 64, 65, 70):
+        x = torch.randn(1, 1, 40000, generator=torch.Generator().manual_seed(cells)).to(torch.bfloat16)
+        x[0, 0, 37:37 + 64 * 8 * cells:64 * 8] = 9.0
+        check(sv, x, torch.tensor([[37]], dtype=torch.int32), None, 32)
+    for equal in (250, 256, 257, 260):
+        x = torch.randn(1, 1, 40000, generator=torch.Generator().manual_seed(equal)).to(torch.bfloat16)
+        x[0, 0, 1001:1001 + equal] = 9.0
+        check(sv, x, torch.tensor([[1001]], dtype=torch.int32), None, 32)

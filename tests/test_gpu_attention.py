@@ -431,3 +431,47 @@ def test_scores_past_the_range_of_fp32(sv, far):
     want, tol = v.mean(0), np.abs(v.mean(0)) * 2.0 ** -8 + np.abs(v).mean(0) * 80 * oo.U
     assert np.all(np.abs(out[1, 1].cpu().double().numpy() - want) <= tol)
     assert abs(float(lse[1, 1]) - math.log(69)) <= 8 * oo.U * math.log(69)
+
+
+def test_tables_without_columns_and_batches_of_nothing(sv):
+    c = Case([2, 1], [0, 0], 2, 2, 64, 16, 16, 89)
+    c.table = torch.empty(2, 0, dtype=torch.int32)
+    out, lse = c.call(sv)
+    torch.cuda.synchronize()
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+    c.ctx[1] = 1  # more than the table holds
+    out, _ = c.call(sv, max_ctx=FAR)
+    torch.cuda.synchronize()
+    assert not bool(out[:2].any()) and bool(torch.isnan(out[2].float()).all())
+    cache = c.cache(sv)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, _ = sv.kv_attention(q, cache, torch.empty(0, 3, **i32), torch.zeros(1, **i32), torch.empty(0, **i32), max_q=1)
+    assert out.shape == q.shape
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(0, dtype=torch.int64, device="cuda")
+    sv.kv_write(cache, none, none, slots)
+    assert sv.kv_read(cache, slots)[0].shape == none.shape
+    r = sv.token_logprobs(torch.empty(0, 3, 100, device="cuda"), torch.empty(0, 3, **i32), top=2)
+    assert r.top_ids.shape == (0, 3, 2)
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_output_in_place_of_the_queries(sv, far):
+    c = Case([3, 40, 1], [900, 70, 1300], 4, 2, 64, 16, 16, 90)
+    kw = dict(max_ctx=FAR) if far else {}
+    out, _ = c.call(sv, **kw)
+    q = c.q.cuda()
+    got, _ = c.call(sv, q=q, out=q, **kw)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(got, out)
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_requests_that_share_pages(sv, far):
+    """A common prefix: two tables name the same blocks; and one block named
+    by several entries of a table."""
+    c = Case([1, 2, 1], [800, 640, 330], 4, 2, 128, 16, 16, 91)
+    c.table[1, :40] = c.table[0, :40]
+    c.table[2, 3:9] = c.table[2, 2]
+    c.check(sv, **(dict(max_ctx=FAR) if far else {}))

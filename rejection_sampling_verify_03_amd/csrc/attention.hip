@@ -98,13 +98,22 @@ struct Unit {
 // x < 2^16 / G (x < 16 * RT + G here).
 __device__ __forceinline__ int div_group(Params P, int x) { return (int)(((uint32_t)x * P->g_inv) >> 16); }
 
-__device__ __forceinline__ Unit unit_of(Params P, int v, int block_rows) {
+struct UnitData {
+  int b, q0, q1, ctx;
+};
+
+__device__ __forceinline__ UnitData load_unit(Params P, int v) {
+  const int b = v / P->nrb;
+  return UnitData{b, P->q_start[b], P->q_start[b + 1], P->ctx_len[b]};
+}
+
+__device__ __forceinline__ Unit unit_from(Params P, int v, const UnitData& data, int block_rows) {
   Unit u;
-  u.b = v / P->nrb;
+  u.b = data.b;
   const int rb = v - u.b * P->nrb;
-  u.q0 = P->q_start[u.b];
-  const int q1 = P->q_start[u.b + 1];
-  u.ctx = P->ctx_len[u.b];
+  u.q0 = data.q0;
+  const int q1 = data.q1;
+  u.ctx = data.ctx;
   u.n = q1 - u.q0;
   u.tiles = 0;
   u.t0 = u.h0 = u.rows = u.lo = u.hi = u.p_lo = u.p_hi = 0;
@@ -129,23 +138,21 @@ __device__ __forceinline__ Unit unit_of(Params P, int v, int block_rows) {
   return u;
 }
 
+__device__ __forceinline__ Unit unit_of(Params P, int v, int block_rows) {
+  return unit_from(P, v, load_unit(P, v), block_rows);
+}
+
 // A value that is the same in every lane, held in scalar registers.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return ((int64_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x);
 }
 
-// The tiles of all units in front of unit v0 (or of all, v0 = their number).
-__device__ __forceinline__ int64_t tiles_before(Params P, int v0, int block_rows, int lane) {
-  double t = 0.0;
-  for (int v = lane; v < v0; v += 64) t += (double)unit_of(P, v, block_rows).tiles;
-  return uniform64((int64_t)wave_total_d(t));
-}
-
 // Tiles to a chunk: all units' tiles, end to end, are cut into P->chunks equal
 // runs, none shorter than kMinChunk (32: 94 us against 82 for 64 contexts of
 // 4096 tokens; 8: no faster).
 constexpr int kMinChunk = 16;
+constexpr int kMaxRunUnits = 65536;  // a workgroup's room for their tiles, 64 units to a place
 __device__ __forceinline__ int64_t chunk_tiles(Params P, int64_t total) {
   return max((total + P->chunks - 1) / P->chunks, (int64_t)kMinChunk);
 }
@@ -232,27 +239,54 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     head0 = x % hgroups * hw;
     v = (x / hgroups) * P->nrb + rb;
   } else {
+    // the tiles of every 64 units, four of a wave's blocks on their way at a
+    // time, then the block and the unit that hold the run's first tile
+    // (one wave over all of them: 2000 contexts of 1500, two heads, 135 us against 106)
     const int lane = threadIdx.x & 63;
     head0 = x % hgroups * hw;
-    const int64_t total = tiles_before(P, units, RT * 16, lane);
+    double* s_tiles = reinterpret_cast<double*>(s_mem);
+    static_assert(sizeof(s_mem) >= kMaxRunUnits / 64 * sizeof(double), "a place for each 64 units");
+    const int blocks = (units + 63) / 64;
+    auto tiles_of = [&](int v, const UnitData& data) {
+      return v < units ? (double)unit_from(P, v, data, RT * 16).tiles : 0.0;
+    };
+    for (int k = wave; k < blocks; k += 4 * kWaves) {
+      UnitData data[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) data[q] = load_unit(P, min((k + q * kWaves) * 64 + lane, units - 1));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const double t = wave_total_d(tiles_of((k + q * kWaves) * 64 + lane, data[q]));
+        if (lane == 0 && k + q * kWaves < blocks) s_tiles[k + q * kWaves] = t;
+      }
+    }
+    __syncthreads();
+    double sum = 0.0;
+    for (int k = lane; k < blocks; k += 64) sum += s_tiles[k];
+    const int64_t total = uniform64((int64_t)wave_total_d(sum));
     left = chunk_tiles(P, total);
     const int64_t first = (int64_t)(x / hgroups) * left;
     if (first >= total) return;
-    // the unit that holds tile `first`
     double base = 0.0;
-    int v0 = 0;
-    for (;; v0 += 64) {
-      const double t = v0 + lane < units ? (double)unit_of(P, v0 + lane, RT * 16).tiles : 0.0;
+    int k = 0;
+    for (int k0 = 0;; k0 += 64) {  // (first < total: some block ends behind it)
+      const double t = k0 + lane < blocks ? s_tiles[k0 + lane] : 0.0;
       const double end = wave_scan_d(t);
       const uint64_t past = __ballot(base + end > (double)first);
       if (past) {
         const int l = __builtin_ctzll(past);
-        v = v0 + l;
-        at = uniform((int)((double)first - (base + lane_d(end - t, l))));
+        k = k0 + l;
+        base += lane_d(end - t, l);
         break;
       }
       base += lane_d(end, 63);
     }
+    const double t = tiles_of(k * 64 + lane, load_unit(P, min(k * 64 + lane, units - 1)));
+    const double end = wave_scan_d(t);
+    const int l = __builtin_ctzll(__ballot(base + end > (double)first));
+    v = k * 64 + l;
+    at = uniform((int)((double)first - (base + lane_d(end - t, l))));
+    __syncthreads();  // (Q takes that memory next)
   }
 
   for (bool run_begin = true;; run_begin = false) {
@@ -796,22 +830,35 @@ AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max
   // dims and one row tile 4 to a CU would fit in part: 118 us against 107 for
   // 256 contexts of 2048 tokens)
   const int slots = 256 * (dim <= 64 && p.rt <= 2 ? 3 : 2);
+  // heads that stand side by side in a token, to a wave each: a workgroup reads
+  // them together
+  const int hw = p.rt > 1 || !heads_in ? 1 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
   p.hw = 1;
-  if (keys <= 1024 || (keys <= 2048 && units * heads <= slots) || units > 4096 || (p.nrb > 1 && units * heads >= 2 * slots)) {
+  if (keys <= 1024 || (keys <= 2048 && units * heads <= slots) ||
+      (keys <= 4096 && units * (heads / hw) >= 2 * slots) || units > kMaxRunUnits ||
+      (p.nrb > 1 && units * heads >= 2 * slots)) {
+    // a unit to a workgroup, the blocks of one head on one XCD, for its keys:
     // short contexts (8 of 1500 tokens: 19 us against 24 in runs, but 256 of
-    // 2048: 117 against 107), very many units, or many blocks of long prompts:
-    // a unit to a workgroup; the blocks of one head on one XCD, for its keys
+    // 2048: 117 against 107), so many units that the card is full of them (2000
+    // with two heads of up to 1500 tokens: 82 us against 103, 8000 with one: 144
+    // against 207; a few long ones among many would be its last), more units
+    // than the runs' beginnings are searched for in, or many blocks of long
+    // prompts (two chunks of 2048 tokens in contexts of 8192: 391 us against 530)
     p.chunks = 0;
+    // (512 requests of up to 1000 tokens, 8 heads of 64, which half fill a line
+    // each: 77 us against 108; where it leaves workgroups idle, fewer heads)
+    p.hw = hw;
+    while (p.hw > 1 && units * (heads / p.hw) < slots) p.hw /= 2;
     p.items = p.nrb;
-    p.groups = (int64_t)B * heads;
+    p.groups = (int64_t)B * (heads / p.hw);
   } else {
     // equal runs, as many as are resident at once; a run's heads on one XCD.
     // With few rows (small partial sums), long runs and a token's heads side
     // by side a wave takes a head of its own, so that a workgroup reads them
     // together (three contexts of 131072 tokens: 141 us against 167; where
     // tokens stand inside heads it is the other way, 150 against 133).
-    if (p.rt == 1 && heads_in && units * keys / kTileKeys * heads >= (int64_t)slots * kWaves * 32)
-      p.hw = heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
+    if (units * keys / kTileKeys * heads >= (int64_t)slots * kWaves * 32)
+      p.hw = hw;
     const int hgroups = heads / p.hw;
     p.chunks = slots / hgroups > 8 ? slots / hgroups / 8 * 8 : 8;
     p.items = hgroups;

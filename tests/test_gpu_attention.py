@@ -475,3 +475,25 @@ def test_requests_that_share_pages(sv, far):
     c.table[1, :40] = c.table[0, :40]
     c.table[2, 3:9] = c.table[2, 2]
     c.check(sv, **(dict(max_ctx=FAR) if far else {}))
+
+
+@pytest.mark.parametrize("dim,st,order", [(64, 16, "tokens"), (64, 1, "tokens"), (80, 4, "tokens"), (128, 16, "tokens"),
+                                          (256, 2, "tokens"), (64, 16, "heads")])
+@pytest.mark.parametrize("B,heads,G", [(800, 4, 1), (420, 2, 3), (800, 2, 16), (200, 12, 1)])
+def test_many_requests_with_heads_to_waves(sv, B, heads, G, dim, st, order):
+    """Batches that fill the card: a workgroup takes several heads of a
+    request, a wave each; with empty and unusable requests among them."""
+    g = torch.Generator().manual_seed(B + dim)
+    ctx = torch.randint(0, 90, (B,), generator=g).tolist()
+    lens = torch.randint(0, 2, (B,), generator=g).tolist()
+    lens[5], ctx[5] = 1, 40
+    c = Case(lens, ctx, G, heads, dim, 16, st, B + dim + st, order=order)
+    o, z, otol, ltol = c.want(window=50)
+    row = int(c.q_start[5])
+    c.ctx[5] = -1
+    o[row], z[row] = np.nan, np.nan
+    out, lse = c.call(sv, window=50, max_ctx=1000)
+    torch.cuda.synchronize()
+    on = np.arange(int(c.q_start[-1]))
+    assert len(on) == out.shape[0]
+    compare(out, lse, o, z, otol, ltol)

@@ -164,7 +164,7 @@ def attn_args(sv, **kw):
     (dict(ctx_len=None), "SPEC_EINVAL"), (dict(block_table=None), "SPEC_EINVAL"), (dict(out=None), "SPEC_EINVAL"),
     (dict(out=P + 4), "SPEC_EALIGN"), (dict(max_blocks=-1), "SPEC_EINVAL"), (dict(bt_row_stride=6), "SPEC_EINVAL"),
     (dict(q_token_stride=-1), "SPEC_EINVAL"), (dict(q_head_stride=-64), "SPEC_EINVAL"),
-    (dict(B=2 ** 30, max_q=2 ** 24), "SPEC_EINVAL"), (dict(B=2 ** 23, N=2 ** 23), "SPEC_EINVAL")])
+    (dict(B=2 ** 30, max_q=2 ** 24), "SPEC_EINVAL"), (dict(B=2 ** 25, N=2 ** 25), "SPEC_EINVAL")])
 def test_attention_refusals(sv, kw, status):
     assert sv.spec_attn_launch(attn_args(sv, **kw), None) == getattr(sv, status)
 

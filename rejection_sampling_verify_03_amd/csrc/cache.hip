@@ -18,6 +18,7 @@
 #include <limits.h>
 
 #include "cache_device.hpp"
+#include "unaligned.hpp"
 
 namespace specv {
 

@@ -111,22 +111,6 @@ __device__ __forceinline__ RawGroup<ES, VEC> load_raw(const char* __restrict__ r
   return r;
 }
 
-// The same from any element on: the hardware's 16-byte loads need no
-// alignment, so rows of any length and stride can take one path.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-template <int ES>
-__device__ __forceinline__ RawGroup<ES, true> load_any(const char* __restrict__ row, int64_t e0) {
-  RawGroup<ES, true> r;
-  if constexpr (ES == 2) {
-    r.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + e0 * 2));
-  } else {
-    r.a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4));
-    r.b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(row + e0 * 4 + 16));
-  }
-  return r;
-}
-
 template <int ES, bool VEC>
 __device__ __forceinline__ void unpack_group(const RawGroup<ES, VEC>& r, float x[8]) {
   if constexpr (!VEC) {

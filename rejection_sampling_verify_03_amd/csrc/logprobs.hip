@@ -38,6 +38,7 @@
 
 #include "device_common.hpp"
 #include "ops_kernels.hpp"
+#include "unaligned.hpp"
 
 namespace specv {
 

@@ -616,7 +616,9 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  *   s_j = scale * q . k_j,  z = ln(sum_j exp(s_j) + exp(sinks[h])),
  *   out = sum_j exp(s_j - z) v_j,  lse = z
  * (without sinks that term is absent).  A token that sees nothing gets out 0
- * and lse = sinks[h], or -inf without sinks.
+ * and lse = sinks[h], or -inf without sinks.  A sink may be any number, the
+ * largest and the infinite ones among them: one of +inf takes all the weight
+ * (out 0, lse +inf), one of -inf none.
  * The scores are computed in fp32: one above its range makes its row NaN, one
  * below it counts as -inf.  The sums of values too, with weights of up to 2^8:
  * 2^8 * ctx_len * max |v| has to lie in its range.

@@ -202,6 +202,37 @@ __device__ __forceinline__ int64_t part_row(Params P, int j, bool later, int hea
   return (((int64_t)j * 2 + later) * P->c.heads + head) * block_rows + k;
 }
 
+// What a row's sums of weights become: the factor of its sums of values, and
+// its lse.  mx: their reference (log2); l: the sum of the weights, 0 if the row
+// saw nothing.  Where the sink leads, or stands alone, lse is taken from the
+// sink itself, so that it holds for sinks whose log2 is past fp32, and for
+// infinite ones; where a score leads, such a sink adds nothing.
+struct RowEnd {
+  float f, lse;
+};
+__device__ __forceinline__ RowEnd row_end(Params P, int hq, float mx, float l) {
+  constexpr float kLn2 = 0.693147180559945309f;
+  if (P->sinks) {
+    const float sink = P->sinks[hq], sk = sink * 1.44269504088896341f;
+    if (l == 0.f || sk > mx) {
+      const float f = l == 0.f ? 0.f : exp2_fast(mx - sk), sum = l * f + 1.0f;
+      return RowEnd{f / sum, sink + __builtin_amdgcn_logf(sum) * kLn2};
+    }
+    l += exp2_fast(sk - mx);
+  }
+  return l == 0.f ? RowEnd{0.f, -INFINITY} : RowEnd{1.0f / l, (mx + __builtin_amdgcn_logf(l)) * kLn2};
+}
+
+// 4 dims of a row to the output, and with the first ones its lse.
+__device__ __forceinline__ void store_row(Params P, int64_t row, int d, f32x4 o, RowEnd end) {
+  uint32_t w[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{o[2 * q] * end.f, o[2 * q + 1] * end.f}, bf16x2));
+  *reinterpret_cast<u32x2*>(P->out + row * P->c.dim + d) = u32x2{w[0], w[1]};
+  if (d == 0 && P->lse) P->lse[row] = end.lse;
+}
+
 // FINE: scale_tokens < 16, a scale for each key; otherwise one for each 16.
 template <int DP, int RT, bool FINE>
 __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
@@ -689,22 +720,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
         *reinterpret_cast<f32x4*>(P->po + pr * P->c.dim + d) = o;
         if (d == 0) P->pm[pr] = float2{mx, l};
       } else {
-        if (P->sinks) {
-          const float sk = P->sinks[hq] * 1.44269504088896341f;
-          const float top2 = fmaxf(mx, sk);
-          const float fa = exp2_fast(mx - top2);
-          l = l * fa + exp2_fast(sk - top2);
-          o *= fa;
-          mx = top2;
-        }
-        // a row that sees nothing: l = 0
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        uint32_t w[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{o[2 * q] * inv, o[2 * q + 1] * inv}, bf16x2));
-        *reinterpret_cast<u32x2*>(P->out + row * P->c.dim + d) = u32x2{w[0], w[1]};
-        if (d == 0 && P->lse) P->lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+        store_row(P, row, d, o, row_end(P, hq, mx, l));
       }
     }
   }
@@ -796,20 +812,7 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams, int row_tiles
     const int t = div_group(P, u.h0 + k);
     const int hq = head * P->G + u.h0 + k - t * P->G;
     const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
-    if (P->sinks) {
-      const float sk = P->sinks[hq] * 1.44269504088896341f;
-      const float m = fmaxf(mx, sk), f = exp2_fast(mx - m);
-      l = l * f + exp2_fast(sk - m);
-      o *= f;
-      mx = m;
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    uint32_t w[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{o[2 * q] * inv, o[2 * q + 1] * inv}, bf16x2));
-    *reinterpret_cast<u32x2*>(P->out + row * P->c.dim + d) = u32x2{w[0], w[1]};
-    if (d == 0 && P->lse) P->lse[row] = l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+    store_row(P, row, d, o, row_end(P, hq, mx, l));
   }
 }
 

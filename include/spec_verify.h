@@ -537,8 +537,9 @@ int spec_logprobs_launch(const spec_logprobs_args* args, hipStream_t stream);
  * no power of two would gain it no precision, and with powers of two a value
  * is exact in bf16 and a growing scale moves codes without rounding them,
  * but for the smallest.)  A write makes bytes of 10 to 247.  A byte of 0, that
- * of memory not written yet, gives values of 0; other bytes that a write does
- * not make are read where fp32 (bf16) holds the values, 255 is unspecified.
+ * of memory not written yet, gives values of 0 whatever the codes, NaN ones
+ * among them; other bytes that a write does not make are read where fp32
+ * (bf16) holds the values, 255 is unspecified.
  * Layout: code of head h, element d at
  *   codes + block * block_stride + token * token_stride + h * head_stride + d,
  * scale byte of group g of a block at
@@ -568,7 +569,7 @@ typedef struct {
  * the group's first token is among the written ones the group begins anew
  * with scale 2^e; otherwise the scale becomes the larger of 2^e and what it
  * was, and where it grew, the tokens in front of the first written one are
- * requantised (tokens behind it that this call does not write are stale in a
+ * requantised (to codes of 0 where it was a byte of 0; tokens behind it that this call does not write are stale in a
  * cache written in order: drafts that were rejected; their codes stay).
  * Values are rounded to nearest, ties to even; a NaN or infinite element is
  * stored as NaN.

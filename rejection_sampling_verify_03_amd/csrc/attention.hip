@@ -180,6 +180,9 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Whether some byte is 0.
+__device__ __forceinline__ bool zero_byte(uint32_t w) { return ((w - 0x01010101u) & ~w & 0x80808080u) != 0; }
+
 // The largest of a lane's eight scores, three to an instruction.
 __device__ __forceinline__ float max_of(const f32x4 (&s)[2]) {
   const float a = fmaxf(fmaxf(s[0][0], s[0][1]), s[0][2]), b = fmaxf(fmaxf(s[0][3], s[1][0]), s[1][1]);
@@ -402,7 +405,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   // Lane l knows subtile l % 2 of tile i0 + l / 2 of this wave: where its keys
   // begin, whether their block exists, and (!FINE) their scales.
   int pg_lo = 0, pg_hi = 0, sc_lo = 0, sc_hi = 0, ksv = 0, vsv = 0;
-  uint64_t okv = 0;
+  uint64_t okv = 0, knone = 0, vnone = 0;  // (knone, vnone: !FINE, scale bytes of 0)
   auto look_up = [&](int i0) {
     const Params P = params_again();
     const int32_t* bt = P->bt + (int64_t)un.b * P->bt_stride;
@@ -423,6 +426,8 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     } else {
       ksv = P->c.scales[0][so];
       vsv = P->c.scales[1][so];
+      knone = __ballot(ok && ksv == 0);
+      vnone = __ballot(ok && vsv == 0);
     }
   };
   auto lane64 = [&](int lo, int hi, int l) { return ((int64_t)lane_i(hi, l) << 32) | (uint32_t)lane_i(lo, l); };
@@ -434,7 +439,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     uint32_t v[8][W];
     uint32_t kfine[2], vfine[2];  // (FINE) scale bytes of key r, and of keys 4 g ..+ 4
     float ksc[2], vsc[2];
-    uint32_t ok;
+    uint32_t ok;  // bits: 0, 1 the subtiles' blocks exist; 2, 3 their keys' scale is 0; 4, 5 their values'
   } buf;
   auto load_k = [&](int i) {
     Buffer& t = buf;
@@ -452,7 +457,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
         t.ksc[u] = scale_of((uint32_t)lane_i(ksv, l));
       }
     }
-    t.ok = (uint32_t)(okv >> ((i & (kWindow - 1)) << 1)) & 3u;
+    const int l0 = (i & (kWindow - 1)) << 1;
+    t.ok = (uint32_t)(okv >> l0) & 3u;
+    if constexpr (!FINE) t.ok |= ((uint32_t)(knone >> l0) & 3u) << 2 | ((uint32_t)(vnone >> l0) & 3u) << 4;
   };
   auto load_v = [&](int i) {
     Buffer& t = buf;
@@ -500,7 +507,17 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     // than kept in registers (the compiler would move the reads out of the loop)
     if constexpr (!QREG && RT * C > 4) asm volatile("" ::: "memory");
     const int key0 = k_beg + (i * kways + ks) * kTileKeys;
-    const uint32_t okt = t.ok;
+    const uint32_t okt = t.ok & 3u;
+    // a scale byte of 0 (never written): values of 0, whatever the codes
+    const uint32_t v_none = t.ok >> 4;
+    if (FINE ? __ballot(t.kfine[0] == 0 || t.kfine[1] == 0) != 0 : (t.ok & 12u) != 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool none = FINE ? t.kfine[u] == 0 : ((t.ok >> (2 + u)) & 1u) != 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) t.k[u][w] = none ? u32x4{0, 0, 0, 0} : t.k[u][w];
+      }
+    }
     // every row of the block sees every key of the tile
     const bool whole = okt == 3u && key0 + kTileKeys - 1 <= un.p_lo && (window == 0 || key0 > un.p_hi - window);
 
@@ -527,6 +544,16 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
               0, 0, 0);
     }
     load_k(min(i + 1, nt - 1));
+    if (FINE ? __ballot(zero_byte(t.vfine[0]) || zero_byte(t.vfine[1])) != 0 : v_none != 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool none = FINE ? ((t.vfine[u] >> (8 * j)) & 0xffu) == 0 : ((v_none >> u) & 1u) != 0;
+#pragma unroll
+          for (int w = 0; w < W; ++w) t.v[4 * u + j][w] = none ? 0u : t.v[4 * u + j][w];
+        }
+    }
 
     // a tile that some row sees only in part: scores not seen become -inf;
     // nothing of the keys that no row sees may enter (0 * NaN, 0 * inf), and a

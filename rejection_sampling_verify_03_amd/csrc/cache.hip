@@ -103,7 +103,9 @@ __device__ __forceinline__ void write_group(const KvWriteParams& P, int kv, int 
   int e = group_exponent(wave_max_f(amax));
   if (first > 0) {
     if (e > old) {
-      // the tokens in front move to the larger scale
+      // the tokens in front move to the larger scale; in front of a byte of 0
+      // nothing was written, whatever codes stand there
+      const bool none = old == -kScaleBias;
       const float f = two_to(max(old - e, -126));
       for (int t0 = 0; t0 < first; t0 += tps) {
         const int t = t0 + tl;
@@ -115,7 +117,7 @@ __device__ __forceinline__ void write_group(const KvWriteParams& P, int kv, int 
           decode4(w.y, b);
           w.x = encode4(a[0] * f, a[1] * f, a[2] * f, a[3] * f);
           w.y = encode4(b[0] * f, b[1] * f, b[2] * f, b[3] * f);
-          *p = w;
+          *p = none ? u32x2{0, 0} : w;
         }
       }
     } else {
@@ -245,8 +247,9 @@ __global__ __launch_bounds__(kWG) void kv_read_kernel(KvReadParams P) {
       for (int kv = 0; kv < 2; ++kv) {
         const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c.codes[kv] + at));
         const float sc = scale_of(c.scales[kv][sat]);
-        w[kv][q] = in ? v : u32x2{0, 0};
-        f[kv][q] = in ? sc : 0.f;
+        const bool some = in && sc > 0.f;  // (0: never written, whatever the codes)
+        w[kv][q] = some ? v : u32x2{0, 0};
+        f[kv][q] = some ? sc : 0.f;
       }
     }
 #pragma unroll

@@ -15,7 +15,8 @@ constexpr int kScaleBias = 127;
 // then still a normal number in bf16 and fp32, so values read back exactly.
 constexpr int kScaleMin = -117;
 
-// 2^(byte - 127); a byte of 0, which only memory never written has, as 0.
+// 2^(byte - 127); a byte of 0, which only memory never written has, as 0 (its
+// codes, which may be NaN, are taken as 0 too).
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // 2^e for e in [-126, 127].

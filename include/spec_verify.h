@@ -569,8 +569,9 @@ typedef struct {
  * the group's first token is among the written ones the group begins anew
  * with scale 2^e; otherwise the scale becomes the larger of 2^e and what it
  * was, and where it grew, the tokens in front of the first written one are
- * requantised (to codes of 0 where it was a byte of 0; tokens behind it that this call does not write are stale in a
- * cache written in order: drafts that were rejected; their codes stay).
+ * requantised (to codes of 0 where it was a byte of 0; tokens behind it that
+ * this call does not write are stale in a cache written in order: drafts that
+ * were rejected; their codes stay).
  * Values are rounded to nearest, ties to even; a NaN or infinite element is
  * stored as NaN.
  * Precondition: the entries of one group stand together in the list (skipped

@@ -124,7 +124,7 @@ __device__ __forceinline__ void write_group(const KvWriteParams& P, int kv, int 
       e = old;
     }
   }
-  const float f = two_to(-e);
+  const float f = e < 127 ? two_to(-e) : 0x1p-127f;  // (127 only where the group had a byte of 254)
   for (int s0 = 0; s0 < steps; s0 += kWriteSteps) {
     if (steps > kWriteSteps) load_steps(s0);
 #pragma unroll

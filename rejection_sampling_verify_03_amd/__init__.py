@@ -870,11 +870,13 @@ class KVCache:
         if k.dim() != 4 or k_scale.dim() != 3:
             raise ValueError("codes must be [num_blocks, block_size, heads, head_dim], scales [num_blocks, heads, "
                              "groups]")
+        torch = _torch()
+        if k.dtype not in (torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype or \
+                k_scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or v_scale.dtype != k_scale.dtype:
+            raise TypeError("codes must be uint8 or float8_e4m3fn, scales uint8 or float8_e8m0fnu, alike for k and v")
         dev = _gpu_device(k)
         if v.device != dev or k_scale.device != dev or v_scale.device != dev:
             raise ValueError("all tensors must be on the same GPU")
-        if k.itemsize != 1 or v.dtype != k.dtype or k_scale.itemsize != 1 or v_scale.dtype != k_scale.dtype:
-            raise TypeError("codes and scales must be 8-bit tensors, alike for k and v")
         nb, bs, heads, dim = k.shape
         snb, sheads, groups = k_scale.shape
         st, sst = k.stride(), k_scale.stride()

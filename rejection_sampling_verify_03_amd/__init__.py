@@ -303,6 +303,8 @@ def spec_shard_draw_launch(args, stream_ptr):
 
 
 def spec_logprobs_workspace_bytes(B, R, V, top):
+    if not _fits32(B, R, V, top):
+        return 0  # (as for any invalid shape)
     return int(lib.spec_logprobs_workspace_bytes(int(B), int(R), int(V), int(top)))
 
 
@@ -747,6 +749,16 @@ class _on:
             self.ctx.__exit__(*exc)
 
 
+def _fits32(*sizes):
+    return max(sizes) <= 0x7fffffff and min(sizes) >= -0x80000000
+
+
+def _int32(*sizes):
+    """The library counts in 32 bits, and ctypes drops what is above them."""
+    if not _fits32(*sizes):
+        raise ValueError("a size past 32 bits among %s" % list(sizes))
+
+
 def _gpu_device(t):
     if not t.is_cuda:
         raise ValueError("all tensors must be on the GPU")
@@ -794,9 +806,10 @@ def token_logprobs_args(logits, tokens, temperature, out, workspace):
     stride (an expanded request dimension shares rows), tokens [B, R] int32,
     temperature [B] float32 or None, out a TokenLogprobs."""
     torch = _torch()
-    dev = _gpu_device(logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
+    _int32(*logits.shape)
+    dev = _gpu_device(logits)
     B, R, _ = logits.shape
     if out.entropy is not None:
         _want(out.entropy, torch.float32, (B, R), dev, "entropy")
@@ -829,9 +842,10 @@ def token_logprobs(logits, tokens, temperature=None, top=0, entropy=True, worksp
     verification with logits its target.  Enqueued on `stream` or the tensors'
     device's current stream; returns a TokenLogprobs (`out`, where given, says
     with its shapes what is computed)."""
-    dev = _gpu_device(logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
+    _int32(*logits.shape)
+    dev = _gpu_device(logits)
     if not 0 <= top <= SPEC_MAX_TOP:
         raise ValueError("top must be in 0..%d" % SPEC_MAX_TOP)
     with _on(dev, stream) as s:
@@ -874,6 +888,7 @@ class KVCache:
         if k.dtype not in (torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype or \
                 k_scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or v_scale.dtype != k_scale.dtype:
             raise TypeError("codes must be uint8 or float8_e4m3fn, scales uint8 or float8_e8m0fnu, alike for k and v")
+        _int32(*k.shape)
         dev = _gpu_device(k)
         if v.device != dev or k_scale.device != dev or v_scale.device != dev:
             raise ValueError("all tensors must be on the same GPU")
@@ -918,6 +933,7 @@ def kv_write_args(cache, key, value, slots):
     """Fill a SpecKVWriteArgs (no copies): key and value [N, heads, head_dim]
     with unit stride along head_dim, slots [N] int64 (-1: not written)."""
     N, dev = slots.shape[0], cache.device
+    _int32(N)
     shape = (N, cache.heads, cache.head_dim)
     k0, k1, k2 = key.stride() if key.dim() == 3 else (0, 0, 0)
     v0, v1, v2 = value.stride() if value.dim() == 3 else (0, 0, 0)
@@ -947,6 +963,7 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
     default) or float32, zeros where a slot is -1."""
     torch = _torch()
     N, dev = slots.shape[0], cache.device
+    _int32(N)
     shape = (N, cache.heads, cache.head_dim)
     with _on(cache.device, stream) as s:
         if out is None:
@@ -985,6 +1002,7 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
     if q.device != dev or block_table.device != dev:
         raise ValueError("all tensors must be on the same GPU")
     max_blocks = block_table.shape[1]
+    _int32(B, N, Hq, max_q, max_ctx, window, max_blocks)
     ws = _want_workspace(workspace, dev)
     return SpecAttnArgs(
         cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q.stride(0), q.stride(1),

@@ -574,6 +574,8 @@ typedef struct {
  * were rejected; their codes stay).
  * Values are rounded to nearest, ties to even; a NaN or infinite element is
  * stored as NaN.
+ * A cache whose keys and values are the same memory can be read and attended
+ * over, but not written (SPEC_EINVAL).
  * Precondition: the entries of one group stand together in the list (skipped
  * entries between them do not matter), as a slot mapping has them; of equal
  * slots the last entry counts.  A list that breaks this leaves unspecified

@@ -325,6 +325,8 @@ int kv_write_check(const spec_kv_write_args* a) {
   const int64_t chunk = kv_write_chunk(a->N);
   if (!fits_dispatch(((int64_t)a->N + chunk - 1) / chunk * ((2 * a->cache.heads + 3) / 4), kThreads))
     return SPEC_EINVAL;
+  // keys and values are written by different waves
+  if (a->cache.k_codes == a->cache.v_codes || a->cache.k_scales == a->cache.v_scales) return SPEC_EINVAL;
   return SPEC_OK;
 }
 

@@ -87,3 +87,19 @@ def test_attention_tables_past_32_bits(sv):
         sv.kv_attention_args(q, cache, table, start, ctx, out=q, **kw)
     with pytest.raises(ValueError, match="32 bits"):
         sv.kv_attention_args(q[:3], cache, torch.empty(2, 2 ** 32 + 3, **i32), start, ctx, out=q[:3], **kw)
+
+
+def test_writes_to_keys_and_values_in_one_place(sv):
+    """Two owners of the same bytes: refused (one address for both; the
+    launch is refused before anything is enqueued)."""
+    P = 1 << 20
+    for same in ("codes", "scales"):
+        a = sv.SpecKVWriteArgs()
+        c = a.cache
+        c.num_blocks, c.block_size, c.scale_tokens, c.heads, c.head_dim = 10, 16, 16, 2, 64
+        c.k_codes, c.v_codes, c.k_scales, c.v_scales = P, 2 * P, 3 * P, 4 * P
+        c.block_stride, c.token_stride, c.head_stride = 2048, 128, 64
+        c.scale_block_stride, c.scale_head_stride = 2, 1
+        setattr(c, "v_" + same, getattr(c, "k_" + same))
+        a.N, a.dtype, a.key, a.value, a.slots = 4, sv.SPEC_BF16, P, P, P
+        assert sv.spec_kv_write_launch(a, None) == sv.SPEC_EINVAL

@@ -56,7 +56,7 @@ namespace specv {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTileKeys = 32;
+static_assert(kAttnWaves == kWaves, "waves of a workgroup");
 constexpr float kNoRef = -FLT_MAX;   // the reference of a row that has seen nothing
 constexpr float kRefSlack = 8.0f;   // how far (log2) a score may pass the reference
 
@@ -148,15 +148,6 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return ((int64_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x);
 }
 
-// Tiles to a chunk: all units' tiles, end to end, are cut into P->chunks equal
-// runs, none shorter than kMinChunk (32: 94 us against 82 for 64 contexts of
-// 4096 tokens; 8: no faster).
-constexpr int kMinChunk = 16;
-constexpr int kMaxRunUnits = 65536;  // a workgroup's room for their tiles, 64 units to a place
-__device__ __forceinline__ int64_t chunk_tiles(Params P, int64_t total) {
-  return max((total + P->chunks - 1) / P->chunks, (int64_t)kMinChunk);
-}
-
 __device__ __forceinline__ bf16x8 pack8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
 }
@@ -243,7 +234,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
   constexpr int W = DP / 64;   // 16-byte loads of a lane's share of a key
   constexpr bool QREG = RT == 1 && C <= 4;  // Q's fragments stay in registers
-  constexpr int kWindow = 32;  // tiles whose pages a wave holds at a time, a subtile to a lane
+  constexpr int kWindow = kAttnWindow;  // a subtile to a lane
   __shared__ __align__(16) char s_mem[(RT * C * 64 * 16 > kWaves * 16 * DP * 4) ? RT * C * 64 * 16
                                                                                 : kWaves * 16 * DP * 4];
   __shared__ float s_ref[kWaves][RT * 16], s_sum[kWaves][RT * 16];
@@ -260,7 +251,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 
   // the waves share out hw heads and the tiles: wave w takes head w % hw and
   // every (kWaves / hw)-th tile
-  const int hw = RT == 1 ? P->hw : 1, hs = wave & (hw - 1), ks = RT == 1 ? wave / hw : wave, kways = kWaves / hw;
+  const int hw = RT == 1 ? P->hw : 1, hs = wave & (hw - 1), ks = RT == 1 ? wave / hw : wave, kways = kAttnWaves / hw;
   const int hgroups = P->c.heads / hw;
 
   // the run of tiles [at, at + left) of unit v, v + 1, ... that this workgroup
@@ -298,7 +289,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     double sum = 0.0;
     for (int k = lane; k < blocks; k += 64) sum += s_tiles[k];
     const int64_t total = uniform64((int64_t)wave_total_d(sum));
-    left = chunk_tiles(P, total);
+    left = attn_run_tiles(total, P->chunks);
     const int64_t first = (int64_t)(x / hgroups) * left;
     if (first >= total) return;
     double base = 0.0;
@@ -841,60 +832,6 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams, int row_tiles
     const int64_t row = (int64_t)(u.q0 + u.t0 + t) * P->Hq + hq;
     store_row(P, row, d, o, row_end(P, hq, mx, l));
   }
-}
-
-AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window,
-                   bool heads_in) {
-  AttnPlan p;
-  const int64_t rows = (int64_t)max_q * G;
-  const int64_t tiles = (rows + 15) / 16;
-  const int rt_max = dim > 128 ? 1 : dim > 64 ? 3 : 5;
-  p.nrb = (int32_t)((tiles + rt_max - 1) / rt_max);
-  p.rt = (int32_t)((tiles + p.nrb - 1) / p.nrb);
-  p.nrb = (int32_t)((tiles + p.rt - 1) / p.rt);
-  // keys that one block of rows can see
-  int64_t keys = max_ctx;
-  if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
-  const int64_t units = (int64_t)B * p.nrb;
-  // workgroups that the card holds at once, by the kernels' registers (at 64
-  // dims and one row tile 4 to a CU would fit in part: 118 us against 107 for
-  // 256 contexts of 2048 tokens)
-  const int slots = 256 * (dim <= 64 && p.rt <= 2 ? 3 : 2);
-  // heads that stand side by side in a token, to a wave each: a workgroup reads
-  // them together
-  const int hw = p.rt > 1 || !heads_in ? 1 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
-  p.hw = 1;
-  if (keys <= 1024 || (keys <= 2048 && units * heads <= slots) ||
-      (keys <= 4096 && units * (heads / hw) >= 2 * slots) || units > kMaxRunUnits ||
-      (p.nrb > 1 && units * heads >= 2 * slots)) {
-    // a unit to a workgroup, the blocks of one head on one XCD, for its keys:
-    // short contexts (8 of 1500 tokens: 19 us against 24 in runs, but 256 of
-    // 2048: 117 against 107), so many units that the card is full of them (2000
-    // with two heads of up to 1500 tokens: 82 us against 103, 8000 with one: 144
-    // against 207; a few long ones among many would be its last), more units
-    // than the runs' beginnings are searched for in, or many blocks of long
-    // prompts (two chunks of 2048 tokens in contexts of 8192: 391 us against 530)
-    p.chunks = 0;
-    // (512 requests of up to 1000 tokens, 8 heads of 64, which half fill a line
-    // each: 77 us against 108; where it leaves workgroups idle, fewer heads)
-    p.hw = hw;
-    while (p.hw > 1 && units * (heads / p.hw) < slots) p.hw /= 2;
-    p.items = p.nrb;
-    p.groups = (int64_t)B * (heads / p.hw);
-  } else {
-    // equal runs, as many as are resident at once; a run's heads on one XCD.
-    // With few rows (small partial sums), long runs and a token's heads side
-    // by side a wave takes a head of its own, so that a workgroup reads them
-    // together (three contexts of 131072 tokens: 141 us against 167; where
-    // tokens stand inside heads it is the other way, 150 against 133).
-    if (units * keys / kTileKeys * heads >= (int64_t)slots * kWaves * 32)
-      p.hw = hw;
-    const int hgroups = heads / p.hw;
-    p.chunks = slots / hgroups > 8 ? slots / hgroups / 8 * 8 : 8;
-    p.items = hgroups;
-    p.groups = p.chunks;
-  }
-  return p;
 }
 
 template <int DP, int RT>

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attention_plan.hpp"
 #include "spec_verify.h"
 #include "verify_layout.hpp"
 
@@ -124,14 +125,6 @@ struct AttnParams {
   int32_t qvec;
 };
 
-struct AttnPlan {
-  int32_t rt, nrb, chunks, hw;
-  int64_t items, groups;
-};
-// How the rows of a (request, KV head) and its keys are cut into workgroups.
-// heads_in: the heads of a token stand together in the cache.
-AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window,
-                   bool heads_in);
 hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream);
 
 }  // namespace specv

@@ -573,7 +573,8 @@ typedef struct {
  * this call does not write are stale in a cache written in order: drafts that
  * were rejected; their codes stay).
  * Values are rounded to nearest, ties to even; a NaN or infinite element is
- * stored as NaN.
+ * stored as NaN.  (A finite one of 1.9375 * 2^127 or more rounds to 2^128,
+ * which bf16 and fp32 read as infinite.)
  * A cache whose keys and values are the same memory can be read and attended
  * over, but not written (SPEC_EINVAL).
  * Precondition: the entries of one group stand together in the list (skipped
@@ -625,7 +626,8 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  * (out 0, lse +inf), one of -inf none.
  * The scores are computed in fp32: one above its range makes its row NaN, one
  * below it counts as -inf.  The sums of values too, with weights of up to 2^8:
- * 2^8 * ctx_len * max |v| has to lie in its range.
+ * 2^8 * ctx_len * max |v| has to lie in its range, over all positions that
+ * some new token of the request sees.
  * Codes of positions that a token does not see never reach its output, NaN
  * among them.  A request whose ctx_len is negative or above max_ctx or
  * max_blocks * block_size, or whose n_b is above max_q, is a data error: NaN

@@ -32,8 +32,11 @@
 // when a score passes it by 2^8: up to there the fp32 sums and the bf16
 // weights lose nothing, and the sums are rarely rescaled.  The weights are
 // rounded to bf16 for the second product (a relative error of at most 2^-8
-// each, of no common sign, as the output's own rounding); their sum is kept
-// in fp32 from the unrounded weights, so lse keeps fp32's accuracy.
+// each, of no common sign, as the output's own rounding: the matrix units take
+// both factors in one type, and the values are exact in bf16); where a scale
+// covers fewer than 16 tokens it is multiplied into the weight before that,
+// which is exact down to 2^-126.  Their sum is kept in fp32 from the unrounded
+// weights, so lse keeps fp32's accuracy.
 //
 // Bounds, measured (MI355X).  Single tokens over long contexts: memory (three
 // contexts of up to 131072 tokens, 691 MB, in 140 us; 131 us of it the main

@@ -193,9 +193,11 @@ double spec_verify_phase_cost(int32_t B, int32_t K, int32_t V, int32_t dtype);
  * for any shape it is large enough for; calls that overlap on one workspace
  * race.  What it carries from one call to the next: the invalid-request count
  * that spec_workspace_error reads, and a launch counter with per-request
- * words of the dynamic early exit, which tag what a launch wrote so that it
- * is told apart from anything older and from memory never written (zero bytes
- * never carry a tag).  Leftover bytes can only make that mode read more
+ * words of the dynamic early exit.  What a launch of that mode writes carries
+ * a tag made of the counter (which tells replays of a captured call apart),
+ * the workspace's address and the number of the call in the process, so that
+ * it is told apart from anything older, whatever the counter's memory held,
+ * and from memory never written (zero bytes never carry a tag).  Leftover bytes can only make that mode read more
  * rows, never change an output (a request's rows up to its stop are read
  * unless leftover words match this launch's tags by chance: its 56-bit tag
  * in a state word, or its 48-bit tags in all eight words of a record, which

@@ -5,6 +5,7 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "spec_verify.h"
@@ -543,9 +544,18 @@ static VerifyParams verify_params(const spec_verify_args* a, bool& vec) {
   P.err = reinterpret_cast<int32_t*>(ws + L.off_err);
   P.state = reinterpret_cast<int32_t*>(ws + L.off_state);
   P.epoch = reinterpret_cast<uint64_t*>(ws + L.off_epoch);
-  // a workspace's launches are tagged by its counter plus this salt (an odd
-  // multiple of the address: different workspaces, different salts)
-  P.salt = (uint64_t)(uintptr_t)a->workspace * 0x9E3779B97F4A7C15ull;
+  // A workspace's launches are tagged by its counter plus this salt, from the
+  // workspace's address and the number of this call in the process, which no
+  // leftover memory can repeat: of a workspace allocated again at the same
+  // address the counter may hold a value that an earlier launch ran at, whose
+  // records still stand (in a test of that, 110 of 192 requests invalid without
+  // the call's number).  Replays of a captured call share its number and differ
+  // in the counter.  2^64 over the golden ratio
+  // and over the root of two: multiples by differences d stay 2^64 / (3 d)
+  // away from 0, so that small differences of the three do not cancel.
+  static std::atomic<uint64_t> calls{0};
+  P.salt = (uint64_t)(uintptr_t)a->workspace * 0x9E3779B97F4A7C15ull +
+           (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0xB504F333F9DE6485ull;
   P.dstate = reinterpret_cast<uint64_t*>(ws + L.off_dstate);
   P.trec = reinterpret_cast<TaggedPartial*>(ws + L.off_trec);
   P.dyn = a->phase_starts == SPEC_PHASES_DYNAMIC;

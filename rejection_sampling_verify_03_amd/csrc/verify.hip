@@ -116,11 +116,12 @@ __device__ __forceinline__ void dstate_read(uint64_t w, uint64_t E, int K, int& 
 
 // The tag E of a launch: the workspace's launch counter (byte 8, advanced by
 // the last kernel of every launch) plus a salt taken from the workspace's
-// address.  The counter of a workspace that was never used holds whatever
-// the memory held, and two such workspaces -- say two allocations of one
-// allocator, each carved from memory a third one used before -- can hold the
-// same value while one's record area holds the other's records; the salt
-// keeps their launches apart.
+// address and the number of the call in its process.  The counter of a
+// workspace that was never used holds whatever the memory held, and two such
+// workspaces -- say two allocations of one allocator, each carved from memory
+// a third one used before, or one after the other at one address -- can hold
+// the same value while one's record area holds the other's records; the salt
+// keeps their launches apart, and the counter the replays of a captured call.
 __device__ __forceinline__ uint64_t launch_tag(const VerifyParams& P) { return *P.epoch + P.salt; }
 
 // The 48-bit tags of launch E in the words of a record, each odd (so that
@@ -398,7 +399,7 @@ __device__ void decide(const VerifyParams& P, int b, bool write, ReqDesc& D) {
     if (threadIdx.x == 0) {
       // position n passed after all: the state word was not written in this launch
       sh.a = (f && a > n) ? -1 : a;
-      if (write) P.dstate[b] = dstate_word(E + 1, 0, 0);  // the next launch starts from nothing
+      if (write) P.dstate[b] = 0;  // the next launch starts from nothing, whatever its tag
     }
     __syncthreads();
     decide_finish<ES>(P, b, write, D, sh);

@@ -66,8 +66,8 @@ struct VerifyParams {
   int32_t last_lo, phased;
   // dynamic early exit (dyn): decisions taken inside the row pass as its
   // chunks finish.  epoch: the launch counter, which with salt (from the
-  // workspace's address) gives the launch's tag E that its tagged records and
-  // state words carry; dstate [B]: per request (E << 8) | (2 n + f),
+  // workspace's address and the call's number) gives the launch's tag E that
+  // its tagged records and state words carry; dstate [B]: per request (E << 8) | (2 n + f),
   // positions before n known accepted and, with f, position n stops the
   // request; trec: tagged copies of rowp; dyn_shift: request groups between a
   // request's chunks of a position and its decider slot

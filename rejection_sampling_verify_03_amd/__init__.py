@@ -844,12 +844,13 @@ def token_logprobs(logits, tokens, temperature=None, top=0, entropy=True, worksp
     with its shapes what is computed)."""
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V]")
-    _int32(*logits.shape)
+    B, R, V = logits.shape
+    if (B | R | V) > 0x7fffffff:
+        _int32(B, R, V)
     dev = _gpu_device(logits)
     if not 0 <= top <= SPEC_MAX_TOP:
         raise ValueError("top must be in 0..%d" % SPEC_MAX_TOP)
     with _on(dev, stream) as s:
-        B, R, V = logits.shape
         if out is not None:
             top = out.top_ids.shape[-1]
         if workspace is None:
@@ -933,7 +934,8 @@ def kv_write_args(cache, key, value, slots):
     """Fill a SpecKVWriteArgs (no copies): key and value [N, heads, head_dim]
     with unit stride along head_dim, slots [N] int64 (-1: not written)."""
     N, dev = slots.shape[0], cache.device
-    _int32(N)
+    if N > 0x7fffffff:
+        _int32(N)
     shape = (N, cache.heads, cache.head_dim)
     k0, k1, k2 = key.stride() if key.dim() == 3 else (0, 0, 0)
     v0, v1, v2 = value.stride() if value.dim() == 3 else (0, 0, 0)
@@ -963,7 +965,8 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
     default) or float32, zeros where a slot is -1."""
     torch = _torch()
     N, dev = slots.shape[0], cache.device
-    _int32(N)
+    if N > 0x7fffffff:
+        _int32(N)
     shape = (N, cache.heads, cache.head_dim)
     with _on(cache.device, stream) as s:
         if out is None:
@@ -1002,7 +1005,8 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
     if q.device != dev or block_table.device != dev:
         raise ValueError("all tensors must be on the same GPU")
     max_blocks = block_table.shape[1]
-    _int32(B, N, Hq, max_q, max_ctx, window, max_blocks)
+    if not 0 <= (B | N | Hq | max_q | max_ctx | window | max_blocks) <= 0x7fffffff:  # (some bit above the 31, or a sign)
+        _int32(B, N, Hq, max_q, max_ctx, window, max_blocks)
     ws = _want_workspace(workspace, dev)
     return SpecAttnArgs(
         cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q.stride(0), q.stride(1),

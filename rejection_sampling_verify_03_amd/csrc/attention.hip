@@ -11,10 +11,11 @@
 // range of keys, each of its four waves every fourth tile of 32 keys (or, for
 // few rows, a KV head of its own), on its own: keys and values go from memory
 // to the matrix units through registers alone, no barrier stands in the loop,
-// and the waves' sums are joined once at the end.  Where there are few blocks with long contexts, the tiles of
-// all blocks, end to end, are cut into equal runs, one to each workgroup that
-// the card holds at once, whatever the lengths of the contexts; a second
-// kernel joins the blocks that several runs hold.
+// and the waves' sums are joined once at the end.  Where there are few blocks
+// with long contexts, the tiles of all blocks, end to end, are cut into equal
+// runs, one to each workgroup that the card holds at once, whatever the lengths
+// of the contexts; a second kernel joins the blocks that several runs hold
+// (attention_plan.hpp).
 //
 // Both products run on v_mfma_f32_16x16x32_bf16 in the transposed order:
 //   S^T (keys x rows) = K Q^T,   O^T (dims x rows) += V^T P^T,
@@ -40,14 +41,19 @@
 //
 // Bounds, measured (MI355X).  Single tokens over long contexts: memory (three
 // contexts of up to 131072 tokens, 691 MB, in 140 us; 131 us of it the main
-// kernel, 5.3 TB/s; with all pages in L2 the call takes 83 us).  The
-// verification batch, 72 rows to a KV head: instructions (126 us; 121 with all
-// pages in L2; vector instructions in 56 % of the cycles, matrix instructions
-// in 22 %).  A 2048-token chunk over 8192 tokens: the same (390 us, 0.8 PFLOP/s;
-// vector 65 %, matrix 34 %: the two hardly overlap on two waves to a SIMD).
-// RT is what 256 registers hold without spilling much: 5 row tiles at 64 dims
-// (the 72 rows of nine tokens and a group of eight in one block; 3 tiles: 175
-// us), 3 at 128 (4 spill: 992 us for the chunk against 382).  A second tile on
+// kernel, 5.3 TB/s; with all pages in L2 the call takes 84 us).  The
+// verification batch, 72 rows to a KV head: instructions (128 us; 6 % less with
+// all pages in L2; vector instructions in 55 % of the cycles, matrix
+// instructions in 21 %).  A 2048-token chunk over 8192 tokens: the same (387 us,
+// 0.8 PFLOP/s; vector 65 %, matrix 34 %: the two hardly overlap on two waves to
+// a SIMD).  A prompt of 2048 tokens under a window of 128, where a wave has one
+// or two tiles to a block: the fixed costs of a block (69 us, of 5 for bytes).
+// RT is what 256 registers hold with few spilled: 5 row tiles at 64 dims (the 72
+// rows of nine tokens and a group of eight in one block, 2 registers spilled
+// with fine scales; 3 tiles: 175 us), 3 at 128 (7 spilled, 25 with fine scales;
+// with 4 the chunk takes 992 us against 382), 1 at 256 (19, 27): there the
+// verification batch is five units to a KV head, each of which reads the whole
+// context (726 us with heads of 256, 251 with 128).  A second tile on
 // its way in registers was no faster (133 against 133 us, long contexts 150
 // against 141).
 #include <limits.h>

@@ -7,7 +7,8 @@
 // so one pass that keeps (m, S, W) gives both.  A lane sums its 64 terms in
 // fp32, and so do the lanes of a segment; segments are joined in double.
 //
-// Two kernels, one read of each row:
+// Two kernels, one read of each row whose logits are finite (a segment that
+// holds one of -inf is read and summed a second time):
 //
 //  logprobs_stats   one 256-thread workgroup per (row, 8 segments), a wave per
 //      4096-logit segment: the segment stays in registers while its maximum
@@ -24,12 +25,14 @@
 //      whose logits are read again; those that reach it are sorted.
 //
 // Bounds, measured (MI355X): the statistics pass is bound by its vector
-// instructions (a logit costs 8 of them and an exponential; they are issued
-// in 95 % of the cycles) just above the rate of memory: 2304 rows of 151936
-// bf16 logits without alternatives take 125 us (6.3 TB/s), the 1327 live rows
-// of a verified batch with 5 alternatives 87 us (4.7 TB/s), of which the finish
-// is 11 us, one wave's chain of steps: 4 to the joined sums, 3 to the threshold,
-// the rest to find, read and sort the candidates.  Segments of 4096 logits, as
+// instructions (a logit costs 8 of them and an exponential, which takes four
+// slots; they fill 96 % of the slots) just above the rate of memory: 2304 rows
+// of 151936 bf16 logits without alternatives take 123 us (6.4 TB/s), the 1327
+// live rows of a verified batch with 5 alternatives 84 us (4.8 TB/s), of which
+// the finish is 11 us, one wave's chain of steps: 4 to the joined sums, 3 to the
+// threshold, the rest to find, read and sort the candidates.  Masked rows cost
+// more: the same 1327 rows with a logit of -inf in every segment take 157 us,
+// with 8 such logits to a row 106.  Segments of 4096 logits, as
 // in draft.hip: 64 registers of logits a lane leave five waves to a SIMD.
 // Four segments to a workgroup were 7 % slower there, sixteen 3 %.
 #include <limits.h>

@@ -550,9 +550,9 @@ static VerifyParams verify_params(const spec_verify_args* a, bool& vec) {
   // address the counter may hold a value that an earlier launch ran at, whose
   // records still stand (in a test of that, 110 of 192 requests invalid without
   // the call's number).  Replays of a captured call share its number and differ
-  // in the counter.  2^64 over the golden ratio
-  // and over the root of two: multiples by differences d stay 2^64 / (3 d)
-  // away from 0, so that small differences of the three do not cancel.
+  // in the counter.  2^64 over the golden ratio and over the root of two: d
+  // times either stays 2^64 / (3 d) away from 0, so that small differences of
+  // the address or the number do not cancel against the counter's.
   static std::atomic<uint64_t> calls{0};
   P.salt = (uint64_t)(uintptr_t)a->workspace * 0x9E3779B97F4A7C15ull +
            (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0xB504F333F9DE6485ull;

@@ -2,8 +2,9 @@
  * spec_verify.h -- C ABI of the MI355X (gfx950) speculative-decoding hot path:
  * batched modified-rejection-sampling verification and the P-EAGLE
  * parallel-drafting batch expansion with its hidden-state gather; and the
- * operators around it in a decode step: token log probabilities, the 8-bit
- * paged KV cache behind the slot mapping, and attention over that cache.
+ * operators around it in a decode step: token log probabilities, sampling from
+ * cut distributions, rotary positions, the paged KV caches behind the slot
+ * mapping (8 and 4 bits), and attention over them.
  *
  * Conventions for every entry point
  *  - Pointers marked "device" are HIP device pointers; the library never
@@ -670,6 +671,221 @@ typedef struct {
  * overlap on one workspace race. */
 size_t spec_attn_workspace_bytes(const spec_attn_args* args);
 int spec_attn_launch(const spec_attn_args* args, hipStream_t stream);
+
+/* ------------------------------------------- sampling from cut distributions
+ *
+ * Tokens from the distribution softmax(x / T) of a row of logits x, cut to its
+ * likelier tokens and scaled up again ("explainer" page, section
+ * "修正拒绝采样": drafts are drawn from q; a serving API lets a request cut it).
+ * With m the row's largest logit, w_v = exp((x_v - m) / T), and the tokens in
+ * the order of falling logits (equal ones: the lower index first), the row
+ * keeps the shortest of three prefixes of that order:
+ *   top_k: its first top_k tokens (0, or V and more: all);
+ *   top_p: the tokens in front of which less than top_p of the first top_k's
+ *          sum of w stands (1 and more: all);
+ *   min_p: those with w_v >= min_p (0: all).
+ * With the uniform number u in [0, 1) the token is the first one, by index,
+ * whose sum of kept w, up to and with its own, is above u times the sum of all
+ * kept.  T = 0 takes the lowest index of the largest logit, whatever the cut
+ * (a NaN logit counts as -inf, and a row with nothing above -inf gives 0).
+ * Weights are taken to a multiple of 2^-f of the largest, f = 63 - (bits of
+ * V), at most 51 (45 for V = 2^17 to 2^18 - 1): what is below counts as 0.
+ *
+ * Data errors give token -1: a temperature that is negative, NaN, infinite or
+ * positive below FLT_MIN; top_k < 0; top_p not above 0, or NaN; min_p outside
+ * [0, 1], or NaN; u outside [0, 1), or NaN; an entry of the row table outside
+ * [0, rows); and with T > 0 a row with a NaN or +inf logit or without a finite
+ * one.
+ */
+typedef struct {
+  int32_t B;                /* requests, >= 0 */
+  int32_t R;                /* rows per request, >= 0 */
+  int32_t V;                /* vocabulary size, 1..SPEC_MAX_V */
+  int32_t dtype;            /* spec_dtype of the logits */
+  const void* logits;       /* device [B, R, V], or with a row table [rows, V] */
+  int64_t req_stride;       /* elements between requests, 0 (shared rows) or >= R * row_stride (unused
+                               with a row table) */
+  int64_t row_stride;       /* elements between rows, >= V */
+  const int32_t* row_index; /* device [B, R]: row r of request b is row row_index[b, r] of the logits;
+                               or NULL */
+  int32_t rows;             /* rows of the logits (with a row table), >= 0 */
+  const float* temperature; /* device [B] */
+  const int32_t* top_k;     /* device [B] or NULL (0) */
+  const float* top_p;       /* device [B] or NULL (1) */
+  const float* min_p;       /* device [B] or NULL (0) */
+  const float* uniforms;    /* device [B, R] */
+  int32_t* tokens;          /* device out [B, R] */
+  void* workspace;          /* device, >= spec_sample_workspace_bytes(B, R, V), 16-byte aligned */
+  size_t workspace_bytes;
+} spec_sample_args;
+
+/* Bytes of device workspace for a sampling or a truncation of these sizes (0
+ * for an invalid shape); stateless, no initialisation; calls that overlap on
+ * one workspace race. */
+size_t spec_sample_workspace_bytes(int32_t B, int32_t R, int32_t V);
+int spec_sample_launch(const spec_sample_args* args, hipStream_t stream);
+
+/* The same cut applied to logits: out = the logits with -inf in the place of
+ * the tokens that are not kept, so that a verification of tokens that were
+ * drawn from cut distributions finds them cut (its target rows, and its draft
+ * rows, cut as the tokens were).  A row of a request with T = 0, and a row
+ * with a NaN or +inf logit or without a finite one, stays as it is; a row
+ * whose request's settings are data errors (above) becomes NaN, which a
+ * verification reports.  out may be the logits themselves (in place, with
+ * their strides), or memory that does not overlap them.
+ */
+typedef struct {
+  int32_t B, R, V;          /* as above */
+  int32_t dtype;            /* spec_dtype of the logits and of out */
+  const void* logits;       /* device [B, R, V] */
+  int64_t req_stride, row_stride;
+  const float* temperature; /* device [B] */
+  const int32_t* top_k;     /* device [B] or NULL */
+  const float* top_p;       /* device [B] or NULL */
+  const float* min_p;       /* device [B] or NULL */
+  void* out;                /* device out [B, R, V] */
+  int64_t out_req_stride;   /* elements, >= R * out_row_stride */
+  int64_t out_row_stride;   /* elements, >= V */
+  void* workspace;          /* device, >= spec_sample_workspace_bytes(B, R, V), 16-byte aligned */
+  size_t workspace_bytes;
+} spec_truncate_args;
+
+int spec_truncate_launch(const spec_truncate_args* args, hipStream_t stream);
+
+/* ----------------------------------------------------------- rotary positions
+ *
+ * Queries and keys turned to their positions (those an expansion emits, or a
+ * prompt's): with the angle a = position * inv_freq[i], pair i of each head,
+ * (x, y), becomes
+ *   (x cos a - y sin a, y cos a + x sin a) * scale,
+ * pairs (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1), i < rot_dim / 2;
+ * the elements of a head from rot_dim on stay as they are.  A negative position
+ * turns back.  The angle is the fp64 product; its cosine and sine and the
+ * products with them are taken in fp64 (|a| up to 2^31) and rounded once.
+ */
+typedef struct {
+  int32_t N;                   /* tokens, >= 0 */
+  int32_t q_heads, k_heads;    /* heads, 0..1024 each (0: that tensor is absent) */
+  int32_t head_dim;            /* a multiple of 8, 8..256 */
+  int32_t rot_dim;             /* a multiple of 16, 16..head_dim */
+  int32_t interleaved;         /* pairs side by side */
+  int32_t dtype;               /* spec_dtype of all four tensors */
+  const double* inv_freq;      /* device [rot_dim / 2] */
+  double scale;                /* finite */
+  const int32_t* positions;    /* device [N] */
+  const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
+  int64_t q_token_stride, q_head_stride;  /* elements, >= 0 */
+  const void* k;               /* device [N, k_heads, head_dim] */
+  int64_t k_token_stride, k_head_stride;
+  void* q_out;                 /* device out: q itself with its strides, or memory that does not overlap */
+  int64_t q_out_token_stride, q_out_head_stride;  /* elements, >= 0; no two elements in one place */
+  void* k_out;                 /* device out, alike */
+  int64_t k_out_token_stride, k_out_head_stride;
+} spec_rope_args;
+
+int spec_rope_launch(const spec_rope_args* args, hipStream_t stream);
+
+/* ------------------------------------------------------ 4-bit paged KV cache
+ *
+ * The cache behind the slot mapping of spec_expand_launch in 4 bits: slot s is
+ * token s % block_size of physical block s / block_size.  Keys and values are
+ * OCP e2m1 codes, the even element of a pair in the low half of its byte; 32
+ * consecutive elements of a token and head share a power of two, an exponent
+ * byte b: the value of code c is c * 2^(b - 127), NaN where b is 255 (the
+ * microscaled format MXFP4).  Layout: the byte of elements 2 i and 2 i + 1 of
+ * head h at
+ *   codes + block * block_stride + token * token_stride + h * head_stride + i,
+ * the exponent byte of elements 32 g ..+ 32 at
+ *   scales + block * scale_block_stride + h * scale_head_stride + g * block_size + token.
+ * Memory never written holds whatever values its bytes say.
+ */
+typedef struct {
+  int32_t num_blocks;          /* physical blocks, >= 1 */
+  int32_t block_size;          /* tokens per block: a power of two, 16..1024 */
+  int32_t heads;               /* KV heads, 1..1024 */
+  int32_t head_dim;            /* multiple of 32, 32..256 */
+  uint8_t* k_codes;            /* device, 16-byte aligned */
+  uint8_t* v_codes;            /* device, 16-byte aligned, the strides of k_codes */
+  int64_t block_stride;        /* bytes, multiples of 16; tokens and heads of a block in either */
+  int64_t token_stride;        /* order, without overlap; token_stride at most 2^26 */
+  int64_t head_stride;
+  uint8_t* k_scales;           /* device */
+  uint8_t* v_scales;           /* device, the strides of k_scales */
+  int64_t scale_block_stride;  /* bytes, >= heads * scale_head_stride */
+  int64_t scale_head_stride;   /* bytes, >= head_dim / 32 * block_size */
+} spec_kv4_cache;
+
+/* Write: token i's keys and values go to slot slots[i]; entries outside
+ * [0, num_blocks * block_size) (the -1 of a slot mapping) are not written.  With
+ * rot_dim > 0 the keys are first turned to positions[i] as by spec_rope_launch,
+ * and so are queries, if there are any (q_heads > 0), for every entry, written
+ * or not; what the keys become is not rounded in between.  32 elements get the
+ * smallest exponent e with |x| <= 6 * 2^e, at least -117, and are rounded to
+ * nearest, ties to even; with a NaN or an infinity among them, all 32 are
+ * stored as NaN.  (One of 1.75 * 2^127 or more rounds to 2^128, which bf16 and
+ * fp32 read as infinite.)
+ * Of equal slots next to each other the last entry counts; equal slots apart
+ * from each other leave a mixture of their entries.
+ */
+typedef struct {
+  spec_kv4_cache cache;
+  int32_t N;                   /* entries, >= 0 */
+  int32_t dtype;               /* spec_dtype of key, value and q */
+  const void* key;             /* device [N, heads, head_dim], unit stride in head_dim */
+  const void* value;           /* device [N, heads, head_dim] */
+  int64_t k_token_stride, k_head_stride;  /* elements, >= 0 */
+  int64_t v_token_stride, v_head_stride;
+  const int64_t* slots;        /* device [N] */
+  int32_t rot_dim;             /* a multiple of 16 up to head_dim; 0: nothing is turned */
+  int32_t interleaved;
+  const double* inv_freq;      /* device [rot_dim / 2] */
+  double scale;                /* finite */
+  const int32_t* positions;    /* device [N] */
+  int32_t q_heads;             /* 0..1024 */
+  const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
+  int64_t q_token_stride, q_head_stride;
+  void* q_out;                 /* device out: q itself with its strides, or memory that does not overlap */
+  int64_t q_out_token_stride, q_out_head_stride;
+} spec_kv4_write_args;
+
+int spec_kv4_write_launch(const spec_kv4_write_args* args, hipStream_t stream);
+
+/* Read: key[i], value[i] = the values at slot slots[i] in the given type
+ * (exact in both), zeros for entries outside the cache. */
+typedef struct {
+  spec_kv4_cache cache;
+  int32_t N;                   /* entries, >= 0 */
+  int32_t dtype;               /* spec_dtype of key and value */
+  void* key;                   /* device out [N, heads, head_dim], contiguous */
+  void* value;                 /* device out [N, heads, head_dim], contiguous */
+  const int64_t* slots;        /* device [N] */
+} spec_kv4_read_args;
+
+int spec_kv4_read_launch(const spec_kv4_read_args* args, hipStream_t stream);
+
+/* Attention over the 4-bit cache: spec_attn_launch in everything else.  (An
+ * element of a key or value that is NaN makes the rows that see it NaN.) */
+typedef struct {
+  spec_kv4_cache cache;
+  int32_t B, N, q_heads, max_q, max_ctx, window;
+  int32_t dtype;               /* SPEC_BF16: q and out */
+  float scale;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* block_table;
+  int64_t bt_row_stride;
+  int32_t max_blocks;
+  const float* sinks;
+  void* out;
+  float* lse;
+  void* workspace;             /* device, >= spec_attn4_workspace_bytes(args) */
+  size_t workspace_bytes;
+} spec_attn4_args;
+
+size_t spec_attn4_workspace_bytes(const spec_attn4_args* args);
+int spec_attn4_launch(const spec_attn4_args* args, hipStream_t stream);
 
 /* Human-readable name of a spec_status value (static storage). */
 const char* spec_status_string(int status);

@@ -32,6 +32,8 @@ EXPORTED = ("spec_verify_workspace_bytes", "spec_verify_plan_phases", "spec_veri
             "spec_shard_phase_launch", "spec_shard_decide_launch", "spec_shard_draw_launch",
             "spec_logprobs_workspace_bytes", "spec_logprobs_launch", "spec_kv_write_launch",
             "spec_kv_read_launch", "spec_attn_workspace_bytes", "spec_attn_launch",
+            "spec_sample_workspace_bytes", "spec_sample_launch", "spec_truncate_launch", "spec_rope_launch",
+            "spec_kv4_write_launch", "spec_kv4_read_launch", "spec_attn4_workspace_bytes", "spec_attn4_launch",
             "spec_workspace_error", "spec_status_string")
 
 
@@ -149,6 +151,76 @@ class SpecAttnArgs(ctypes.Structure):
     ]
 
 
+class SpecSampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("R", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("req_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+        ("row_index", ctypes.c_void_p), ("rows", ctypes.c_int32),
+        ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p), ("uniforms", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SpecTruncateArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("R", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("req_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("out_req_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SpecRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("inv_freq", ctypes.c_void_p), ("scale", ctypes.c_double), ("positions", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("k_out", ctypes.c_void_p), ("k_out_token_stride", ctypes.c_int64), ("k_out_head_stride", ctypes.c_int64),
+    ]
+
+
+class SpecKV4Cache(ctypes.Structure):
+    _fields_ = [
+        ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+    ]
+
+
+class SpecKV4WriteArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SpecKV4Cache), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("key", ctypes.c_void_p), ("value", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+        ("scale", ctypes.c_double), ("positions", ctypes.c_void_p),
+        ("q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p), ("q_out_token_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+    ]
+
+
+class SpecKV4ReadArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", SpecKV4Cache), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("key", ctypes.c_void_p), ("value", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+    ]
+
+
+class SpecAttn4Args(ctypes.Structure):
+    _fields_ = [("cache", SpecKV4Cache)] + SpecAttnArgs._fields_[1:]
+
+
 def _load():
     # torch ships its own HIP runtime under the same SONAME as the system one;
     # loading torch first makes this library bind to that single runtime
@@ -193,8 +265,15 @@ def _load():
     L.spec_logprobs_workspace_bytes.restype = ctypes.c_size_t
     L.spec_attn_workspace_bytes.argtypes = [ctypes.POINTER(SpecAttnArgs)]
     L.spec_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_sample_workspace_bytes.argtypes = [ctypes.c_int32] * 3
+    L.spec_sample_workspace_bytes.restype = ctypes.c_size_t
+    L.spec_attn4_workspace_bytes.argtypes = [ctypes.POINTER(SpecAttn4Args)]
+    L.spec_attn4_workspace_bytes.restype = ctypes.c_size_t
     for name, struct in (("spec_logprobs_launch", SpecLogprobsArgs), ("spec_kv_write_launch", SpecKVWriteArgs),
-                         ("spec_kv_read_launch", SpecKVReadArgs), ("spec_attn_launch", SpecAttnArgs)):
+                         ("spec_kv_read_launch", SpecKVReadArgs), ("spec_attn_launch", SpecAttnArgs),
+                         ("spec_sample_launch", SpecSampleArgs), ("spec_truncate_launch", SpecTruncateArgs),
+                         ("spec_rope_launch", SpecRopeArgs), ("spec_kv4_write_launch", SpecKV4WriteArgs),
+                         ("spec_kv4_read_launch", SpecKV4ReadArgs), ("spec_attn4_launch", SpecAttn4Args)):
         getattr(L, name).argtypes = [ctypes.POINTER(struct), ctypes.c_void_p]
         getattr(L, name).restype = ctypes.c_int
     L.spec_status_string.argtypes = [ctypes.c_int]
@@ -327,6 +406,42 @@ def spec_attn_workspace_bytes(args):
 
 def spec_attn_launch(args, stream_ptr):
     return int(lib.spec_attn_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_sample_workspace_bytes(B, R, V):
+    """Workspace of a sampling or a truncation."""
+    if not _fits32(B, R, V):
+        return 0  # (as for any invalid shape)
+    return int(lib.spec_sample_workspace_bytes(int(B), int(R), int(V)))
+
+
+def spec_sample_launch(args, stream_ptr):
+    return int(lib.spec_sample_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_truncate_launch(args, stream_ptr):
+    return int(lib.spec_truncate_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_rope_launch(args, stream_ptr):
+    return int(lib.spec_rope_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_kv4_write_launch(args, stream_ptr):
+    return int(lib.spec_kv4_write_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_kv4_read_launch(args, stream_ptr):
+    return int(lib.spec_kv4_read_launch(ctypes.byref(args), stream_ptr))
+
+
+def spec_attn4_workspace_bytes(args):
+    """Workspace of an attention over a 4-bit cache from the sizes in its argument block."""
+    return int(lib.spec_attn4_workspace_bytes(ctypes.byref(args)))
+
+
+def spec_attn4_launch(args, stream_ptr):
+    return int(lib.spec_attn4_launch(ctypes.byref(args), stream_ptr))
 
 
 def spec_status_string(status):
@@ -921,6 +1036,57 @@ def make_kv_cache(num_blocks, block_size, heads, head_dim, scale_tokens=None, de
     return KVCache(*codes, *scales)
 
 
+class KVCache4:
+    """A paged cache of keys and values in 4 bits: codes k, v (uint8, or
+    float4_e2m1fn_x2) [num_blocks, block_size, heads, head_dim / 2], the even
+    element of a byte in its low half, and exponents k_scale, v_scale (uint8, or
+    float8_e8m0fnu) [num_blocks, heads, head_dim / 32, block_size], one for 32
+    elements of a token and head; the value of a code is code * 2^(byte - 127),
+    NaN where the byte is 255.  Blocks may hold their tokens outside their heads
+    or inside (a transposed view); k and v share strides, and so do their
+    scales.  block_size is a power of two from 16 to 1024, head_dim a multiple
+    of 32 up to 256."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "block_size", "heads", "head_dim", "device", "args")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or k_scale.dim() != 4:
+            raise ValueError("codes must be [num_blocks, block_size, heads, head_dim / 2], scales [num_blocks, heads, "
+                             "head_dim / 32, block_size]")
+        torch = _torch()
+        if k.dtype not in (torch.uint8, torch.float4_e2m1fn_x2) or v.dtype != k.dtype or \
+                k_scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or v_scale.dtype != k_scale.dtype:
+            raise TypeError("codes must be uint8 or float4_e2m1fn_x2, scales uint8 or float8_e8m0fnu, alike for k and v")
+        _int32(*k.shape)
+        dev = _gpu_device(k)
+        if v.device != dev or k_scale.device != dev or v_scale.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        nb, bs, heads, half = k.shape
+        st, sst = k.stride(), k_scale.stride()
+        if v.shape != k.shape or v.stride() != st or v_scale.shape != k_scale.shape or v_scale.stride() != sst or \
+                k_scale.shape != (nb, heads, half // 16, bs) or half % 16:
+            raise ValueError("k and v (and their scales) must agree in shape and strides")
+        if st[3] != 1 or sst[3] != 1 or (half > 16 and sst[2] != bs):
+            raise ValueError("codes must be contiguous along head_dim, the scales of a block and head too")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_blocks, self.block_size, self.heads, self.head_dim, self.device = nb, bs, heads, 2 * half, dev
+        self.args = SpecKV4Cache(nb, bs, heads, 2 * half, k.data_ptr(), v.data_ptr(), st[0], st[1],
+                                 st[2] if heads > 1 else half, k_scale.data_ptr(), v_scale.data_ptr(), sst[0],
+                                 sst[1] if heads > 1 else half // 16 * bs)
+
+
+def make_kv4_cache(num_blocks, block_size, heads, head_dim, device="cuda"):
+    """A KVCache4 of zeros, each block's tokens inside its heads (what the
+    attention reads fastest)."""
+    torch = _torch()
+    if head_dim < 32 or head_dim % 32:
+        raise ValueError("head_dim must be a multiple of 32")
+    codes = [torch.zeros(num_blocks, heads, block_size, head_dim // 2, dtype=torch.uint8, device=device).transpose(1, 2)
+             for _ in range(2)]
+    scales = [torch.zeros(num_blocks, heads, head_dim // 32, block_size, dtype=torch.uint8, device=device)
+              for _ in range(2)]
+    return KVCache4(*codes, *scales)
+
+
 def _kv_dtype(dtype):
     torch = _torch()
     if dtype == torch.bfloat16:
@@ -950,11 +1116,14 @@ def kv_write_args(cache, key, value, slots):
 
 
 def kv_write(cache, key, value, slots, stream=None):
-    """Quantise keys and values [N, heads, head_dim] into the cache at slots
-    [N] int64 (the slot_mapping of an expansion; -1 is skipped); returns the
-    cache."""
+    """Quantise keys and values [N, heads, head_dim] into the cache (a KVCache
+    or a KVCache4) at slots [N] int64 (the slot_mapping of an expansion; -1 is
+    skipped); returns the cache."""
     with _on(cache.device, stream) as s:
-        rc = lib.spec_kv_write_launch(kv_write_args(cache, key, value, slots), s)
+        if type(cache) is KVCache4:
+            rc = lib.spec_kv4_write_launch(kv4_write_args(cache, key, value, slots), s)
+        else:
+            rc = lib.spec_kv_write_launch(kv_write_args(cache, key, value, slots), s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return cache
@@ -977,9 +1146,11 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
             dt = key.dtype if dtype is None else dtype
             _want(key, dt, shape, dev, "key")
             _want(value, dt, shape, dev, "value")
-        a = SpecKVReadArgs(cache.args, N, _kv_dtype(dt), key.data_ptr(), value.data_ptr(),
-                           _want(slots, torch.int64, (N,), dev, "slots"))
-        rc = lib.spec_kv_read_launch(a, s)
+        four = type(cache) is KVCache4
+        a = (SpecKV4ReadArgs if four else SpecKVReadArgs)(cache.args, N, _kv_dtype(dt), key.data_ptr(),
+                                                          value.data_ptr(),
+                                                          _want(slots, torch.int64, (N,), dev, "slots"))
+        rc = lib.spec_kv4_read_launch(a, s) if four else lib.spec_kv_read_launch(a, s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return key, value
@@ -987,7 +1158,7 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
 
 def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse=None, window=0,
                       sinks=None, workspace=None):
-    """Fill a SpecAttnArgs (no copies): q [N, q_heads, head_dim] bfloat16 with
+    """Fill a SpecAttnArgs, or for a KVCache4 a SpecAttn4Args (no copies): q [N, q_heads, head_dim] bfloat16 with
     unit stride along head_dim, block_table [B, max_blocks] int32 (row stride
     free), q_start [B + 1] and ctx_len [B] int32, sinks [q_heads] float32,
     out [N, q_heads, head_dim] bfloat16, lse [N, q_heads] float32."""
@@ -1008,7 +1179,7 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
     if not 0 <= (B | N | Hq | max_q | max_ctx | window | max_blocks) <= 0x7fffffff:  # (some bit above the 31, or a sign)
         _int32(B, N, Hq, max_q, max_ctx, window, max_blocks)
     ws = _want_workspace(workspace, dev)
-    return SpecAttnArgs(
+    return (SpecAttn4Args if type(cache) is KVCache4 else SpecAttnArgs)(
         cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q.stride(0), q.stride(1),
         _want(q_start, torch.int32, (B + 1,), dev, "q_start"), _want(ctx_len, torch.int32, (B,), dev, "ctx_len"),
         block_table.data_ptr(), block_table.stride(0) if B > 1 else max_blocks, max_blocks,
@@ -1019,8 +1190,8 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
 
 def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, scale=None, window=0, sinks=None,
                  return_lse=False, workspace=None, stream=None, out=None):
-    """Attention of the new tokens q [N, q_heads, head_dim] of B requests
-    (request b: rows q_start[b]..q_start[b+1] - 1) over their cached contexts
+    """Attention over a KVCache or a KVCache4 of the new tokens q [N, q_heads,
+    head_dim] of B requests (request b: rows q_start[b]..q_start[b+1] - 1) over their cached contexts
     of ctx_len[b] tokens, the new ones included and last.  max_q and max_ctx
     bound the new tokens and the context of a request (max_ctx defaults to
     what the block table holds); scale defaults to head_dim ** -0.5; window >
@@ -1033,6 +1204,7 @@ def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, s
         max_ctx = min(block_table.shape[-1] * cache.block_size, 1 << 30)
     if scale is None:
         scale = cache.head_dim ** -0.5
+    four = type(cache) is KVCache4
     with _on(cache.device, stream) as s:
         if out is None:
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
@@ -1040,11 +1212,278 @@ def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, s
         a = kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse, window, sinks,
                               workspace)
         if workspace is None:
-            n = lib.spec_attn_workspace_bytes(a)
+            n = lib.spec_attn4_workspace_bytes(a) if four else lib.spec_attn_workspace_bytes(a)
             if n:
                 workspace = torch.empty(n, dtype=torch.uint8, device=dev)
                 a.workspace, a.workspace_bytes = workspace.data_ptr(), n
-        rc = lib.spec_attn_launch(a, s)
+        rc = lib.spec_attn4_launch(a, s) if four else lib.spec_attn_launch(a, s)
     if rc != SPEC_OK:
         raise SpecError(rc)
     return out, lse
+
+
+# ------------------------------------------- rotary positions, 4-bit writes
+class Rope:
+    """How heads are turned to positions: inv_freq [rot_dim / 2] float64 on the
+    GPU, the angle of each pair at position 1; scale, the factor of the turned
+    elements; interleaved: pairs (2 i, 2 i + 1) in place of (i, i + rot_dim / 2).
+    make_rope gives the usual tables."""
+    __slots__ = ("inv_freq", "scale", "interleaved", "rot_dim", "ptr")
+
+    def __init__(self, inv_freq, scale=1.0, interleaved=False):
+        if inv_freq.dtype != _torch().float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous float64 [rot_dim / 2]")
+        _gpu_device(inv_freq)
+        self.inv_freq, self.scale, self.interleaved = inv_freq, float(scale), bool(interleaved)
+        self.rot_dim, self.ptr = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+
+
+def make_rope(rot_dim, base=10000.0, scaling=None, factor=1.0, trained=None, interleaved=False, beta_fast=32.0,
+              beta_slow=1.0, device="cuda"):
+    """A Rope of the angles base ** (-2 i / rot_dim), for contexts `factor`
+    times the trained ones: scaling None (as they are), "linear" (every angle
+    divided by factor), "ntk" (the base raised so that the slowest pair is
+    divided by factor, the fastest by 1), or "yarn" (pairs that turn at least
+    beta_fast times over the `trained` positions as they are, pairs that turn at
+    most beta_slow times divided by factor, a ramp between; turned elements
+    times 0.1 ln(factor) + 1)."""
+    import math
+    torch = _torch()
+    if rot_dim < 16 or rot_dim % 16:
+        raise ValueError("rot_dim must be a multiple of 16")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1, factor at least 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = float(base) ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if trained is None or trained < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs the trained positions, and beta_fast above beta_slow")
+
+        def pair_of(turns):  # the pair that turns so often over the trained positions
+            return rot_dim * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rot_dim - 1)
+        ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        f = f * (1 - ramp) + f / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return Rope(f.to(device), scale, interleaved)
+
+
+def _heads(t, N, dim, dtype, dev, name):
+    """A tensor [N, heads, dim] with unit stride along dim: its heads, address and strides."""
+    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != dim or (t.stride(2) != 1 and dim > 1):
+        raise ValueError("%s must be [N, heads, head_dim], contiguous along head_dim" % name)
+    if t.dtype != dtype:
+        raise TypeError("queries and keys must share a dtype")
+    if t.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    return t.shape[1], t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def rope_args(q, k, positions, rope, q_out, k_out):
+    """Fill a SpecRopeArgs (no copies): q, k and their outputs [N, heads,
+    head_dim] with unit stride along head_dim (k and k_out may be None),
+    positions [N] int32."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be [N, heads, head_dim], contiguous along head_dim")
+    dev = _gpu_device(q)
+    N, _, dim = q.shape
+    _int32(*q.shape)
+    dt = _kv_dtype(q.dtype)
+    if rope.inv_freq.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    hq, qp, q0, q1 = _heads(q, N, dim, q.dtype, dev, "q")
+    hqo, qop, qo0, qo1 = _heads(q_out, N, dim, q.dtype, dev, "q_out")
+    hk, kp, k0, k1, hko, kop, ko0, ko1 = (0, None, 0, 0) * 2
+    if k is not None:
+        hk, kp, k0, k1 = _heads(k, N, dim, q.dtype, dev, "k")
+        hko, kop, ko0, ko1 = _heads(k_out, N, dim, q.dtype, dev, "k_out")
+    if hqo != hq or hko != hk:
+        raise ValueError("the outputs must have the inputs' shapes")
+    return SpecRopeArgs(N, hq, hk, dim, rope.rot_dim, rope.interleaved, dt, rope.ptr, rope.scale,
+                        _want(positions, torch.int32, (N,), dev, "positions"), qp, q0, q1, kp, k0, k1, qop, qo0, qo1,
+                        kop, ko0, ko1)
+
+
+def rope(q, k, positions, rope, out=None, stream=None):
+    """Queries and keys [N, heads, head_dim] (bfloat16 or float32; k may be
+    None) turned to positions [N] int32 as `rope`, a Rope, says.  Returns (q,
+    k), new tensors or those of `out`, a pair which may be (q, k) themselves."""
+    torch = _torch()
+    dev = _gpu_device(q)
+    with _on(dev, stream) as s:
+        if out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
+        else:
+            q_out, k_out = out
+        rc = lib.spec_rope_launch(rope_args(q, k, positions, rope, q_out, k_out), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return q_out, k_out
+
+
+def kv4_write_args(cache, key, value, slots, positions=None, rope=None, q=None, q_out=None):
+    """Fill a SpecKV4WriteArgs (no copies): key and value [N, heads, head_dim]
+    with unit stride along head_dim, slots [N] int64 (-1: not written); with a
+    Rope the keys are turned to positions [N] int32 first, and queries q [N,
+    q_heads, head_dim] into q_out."""
+    torch = _torch()
+    N, dev = slots.shape[0], cache.device
+    if N > 0x7fffffff:
+        _int32(N)
+    shape, dim = (N, cache.heads, cache.head_dim), cache.head_dim
+    k0, k1, k2 = key.stride() if key.dim() == 3 else (0, 0, 0)
+    v0, v1, v2 = value.stride() if value.dim() == 3 else (0, 0, 0)
+    if key.shape != shape or value.shape != shape or k2 != 1 or v2 != 1:
+        raise ValueError("key and value must be [N, heads, head_dim], contiguous along head_dim")
+    if key.dtype != value.dtype:
+        raise TypeError("key and value must share a dtype")
+    if key.device != dev or value.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    a = SpecKV4WriteArgs(cache.args, N, _kv_dtype(key.dtype), key.data_ptr(), value.data_ptr(), k0, k1, v0, v1,
+                         _want(slots, torch.int64, (N,), dev, "slots"))
+    if rope is not None:
+        if rope.inv_freq.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        a.rot_dim, a.interleaved, a.inv_freq, a.scale = rope.rot_dim, rope.interleaved, rope.ptr, rope.scale
+        a.positions = _want(positions, torch.int32, (N,), dev, "positions")
+    if q is not None:
+        if rope is None:
+            raise ValueError("queries are turned as a Rope says: none is given")
+        _int32(*q.shape)
+        a.q_heads, a.q, a.q_token_stride, a.q_head_stride = _heads(q, N, dim, key.dtype, dev, "q")
+        n, a.q_out, a.q_out_token_stride, a.q_out_head_stride = _heads(q_out, N, dim, key.dtype, dev, "q_out")
+        if n != a.q_heads:
+            raise ValueError("the output must have the queries' shape")
+    return a
+
+
+def rope_kv_write(cache, q, key, value, positions, slots, rope, q_out=None, stream=None):
+    """rope() of queries [N, q_heads, head_dim] and keys, and kv_write() of the
+    keys and values [N, heads, head_dim] into a KVCache4, in one launch: the
+    queries and keys turned to positions [N] int32, the keys (not rounded in
+    between) and values quantised into the cache at slots [N] int64 (-1 is
+    skipped).  q may be None.  Returns the turned queries (q_out, which may be
+    q itself)."""
+    if type(cache) is not KVCache4:
+        raise TypeError("the cache must be a KVCache4 (for a KVCache: rope(), then kv_write())")
+    with _on(cache.device, stream) as s:
+        if q is not None and q_out is None:
+            q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+        rc = lib.spec_kv4_write_launch(kv4_write_args(cache, key, value, slots, positions, rope, q, q_out), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return q_out
+
+
+# --------------------------------------- sampling from cut distributions
+def _per_request(t, dtype, B, dev, name):
+    return None if t is None else _want(t, dtype, (B,), dev, name)
+
+
+def sample_args(logits, uniforms, temperature, top_k, top_p, min_p, tokens, workspace, row_index=None):
+    """Fill a SpecSampleArgs (no copies): logits [B, R, V] with unit column
+    stride (an expanded request dimension shares rows), or with row_index [B, R]
+    int32 [rows, V]; uniforms [B, R] float32, temperature, top_p, min_p [B]
+    float32, top_k [B] int32 (the last three may be None), tokens [B, R] int32."""
+    torch = _torch()
+    dev = _gpu_device(logits)
+    if logits.dim() != (3 if row_index is None else 2) or uniforms.dim() != 2:
+        raise ValueError("logits must be [B, R, V] ([rows, V] with a row table), uniforms [B, R]")
+    B, R = uniforms.shape
+    V = logits.shape[-1]
+    _int32(B, R, *logits.shape)
+    st = logits.stride()
+    if st[-1] != 1 and V > 1:
+        raise ValueError("logits must have contiguous rows")
+    if row_index is None:
+        if logits.shape[:2] != uniforms.shape:
+            raise ValueError("logits and uniforms must agree in requests and rows")
+        req, row, rows, index = st[0] if B > 1 else 0, st[1] if R > 1 else V, 0, None
+    else:
+        rows = logits.shape[0]
+        req, row, index = 0, st[0] if rows > 1 else V, _want(row_index, torch.int32, (B, R), dev, "row_index")
+    ws = _want_workspace(workspace, dev)
+    return SpecSampleArgs(
+        B, R, V, _logit_dtype(logits), logits.data_ptr(), req, row, index, rows,
+        _want(temperature, torch.float32, (B,), dev, "temperature"), _per_request(top_k, torch.int32, B, dev, "top_k"),
+        _per_request(top_p, torch.float32, B, dev, "top_p"), _per_request(min_p, torch.float32, B, dev, "min_p"),
+        _want(uniforms, torch.float32, (B, R), dev, "uniforms"), _want(tokens, torch.int32, (B, R), dev, "tokens"),
+        ws[0], ws[1])
+
+
+def sample(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None, row_index=None, workspace=None,
+           stream=None, out=None):
+    """A token for each row of logits [B, R, V], or of rows row_index [B, R]
+    int32 of logits [rows, V], from softmax(logits / temperature[b]) cut to the
+    top_k[b] likeliest tokens (0: all), to the likeliest that reach top_p[b] of
+    their mass (1: all) and to those of at least min_p[b] times the largest
+    probability (0: all), by one uniform number of [0, 1) a row, uniforms [B, R]
+    float32.  Equal logits count in the order of their indices.  Returns tokens
+    [B, R] int32, -1 where a row or its settings cannot be used."""
+    torch = _torch()
+    dev = _gpu_device(logits)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(uniforms.shape, dtype=torch.int32, device=dev)
+        if workspace is None:
+            B, R = uniforms.shape if uniforms.dim() == 2 else (0, 0)
+            workspace = torch.empty(max(spec_sample_workspace_bytes(B, R, logits.shape[-1]), 16), dtype=torch.uint8,
+                                    device=dev)
+        rc = lib.spec_sample_launch(sample_args(logits, uniforms, temperature, top_k, top_p, min_p, out, workspace,
+                                                row_index), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return out
+
+
+def truncate_args(logits, temperature, top_k, top_p, min_p, out, workspace):
+    """Fill a SpecTruncateArgs (no copies): logits and out [B, R, V] with unit
+    column stride, the settings as for sample_args."""
+    torch = _torch()
+    dev = _gpu_device(logits)
+    if logits.dim() != 3 or out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("logits must be [B, R, V], out alike")
+    if out.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    _int32(*logits.shape)
+    B, R, V = logits.shape
+    (s0, s1, s2), (o0, o1, o2) = logits.stride(), out.stride()
+    if (s2 != 1 or o2 != 1) and V > 1:
+        raise ValueError("logits and out must have contiguous rows")
+    s0, s1, o0, o1 = s0 if B > 1 else 0, s1 if R > 1 else V, o0 if B > 1 else 0, o1 if R > 1 else V
+    ws = _want_workspace(workspace, dev)
+    return SpecTruncateArgs(
+        B, R, V, _logit_dtype(logits), logits.data_ptr(), s0, s1,
+        _want(temperature, torch.float32, (B,), dev, "temperature"), _per_request(top_k, torch.int32, B, dev, "top_k"),
+        _per_request(top_p, torch.float32, B, dev, "top_p"), _per_request(min_p, torch.float32, B, dev, "min_p"),
+        out.data_ptr(), o0, o1, ws[0], ws[1])
+
+
+def truncate_logits(logits, temperature, top_k=None, top_p=None, min_p=None, workspace=None, stream=None, out=None):
+    """logits [B, R, V] with -inf in the place of every token that sample()
+    would leave out with the same settings: the target (and draft) rows for a
+    verification of tokens drawn from cut distributions.  Rows of requests with
+    temperature 0 stay as they are.  Returns `out`, a new tensor by default,
+    which may be the logits themselves."""
+    torch = _torch()
+    dev = _gpu_device(logits)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(spec_sample_workspace_bytes(*logits.shape), 16), dtype=torch.uint8, device=dev)
+        rc = lib.spec_truncate_launch(truncate_args(logits, temperature, top_k, top_p, min_p, out, workspace), s)
+    if rc != SPEC_OK:
+        raise SpecError(rc)
+    return out

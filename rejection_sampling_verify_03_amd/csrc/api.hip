@@ -343,6 +343,213 @@ int kv_read_check(const spec_kv_read_args* a) {
   return SPEC_OK;
 }
 
+// ------------------------------------------------ sampling, 4-bit cache, rotation
+size_t cut_ws_bytes(int32_t B, int32_t R, int32_t V) {
+  const size_t rows = (size_t)B * R, segs = rows * (((size_t)V + kSeg - 1) / kSeg);
+  return align256(segs * sizeof(CutRecord)) + align256(segs * 64 * sizeof(float)) + align256(rows * sizeof(uint64_t));
+}
+
+bool cut_shape_ok(int32_t B, int32_t R, int32_t V) {
+  if (B < 0 || R < 0 || V < 1 || V > SPEC_MAX_V) return false;
+  const int64_t rows = (int64_t)B * R, nseg = ((int64_t)V + kSeg - 1) / kSeg;
+  const int64_t C = (nseg + kCutChunkSegs - 1) / kCutChunkSegs;
+  return rows <= INT32_MAX && rows * C <= INT32_MAX && fits_dispatch(rows * C, kThreads) && fits_dispatch(rows, 1024);
+}
+
+// The sizes, settings and workspace that a sampling and a truncation share.
+template <class Args>
+int cut_check(const Args* a) {
+  if (!a || !cut_shape_ok(a->B, a->R, a->V)) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (a->B == 0 || a->R == 0) return SPEC_OK;
+  if (!a->logits || !a->temperature || !a->workspace) return SPEC_EINVAL;
+  if (a->row_stride < a->V) return SPEC_EINVAL;
+  if (!aligned16(a->workspace)) return SPEC_EALIGN;
+  if (a->workspace_bytes < cut_ws_bytes(a->B, a->R, a->V)) return SPEC_EWORKSPACE;
+  return SPEC_OK;
+}
+
+template <class Args>
+CutParams cut_params(const Args* a) {
+  CutParams P = {};
+  P.B = a->B;
+  P.R = a->R;
+  P.V = a->V;
+  P.nseg = (int32_t)(((int64_t)a->V + kSeg - 1) / kSeg);
+  P.C = (P.nseg + kCutChunkSegs - 1) / kCutChunkSegs;
+  while (((int64_t)1 << P.ibits) < a->V) ++P.ibits;
+  // V weights of at most 2^frac within 63 bits, each within the 52 of a double
+  int bits = P.ibits;
+  if (((int64_t)1 << bits) == a->V) ++bits;
+  P.frac = 63 - bits < 51 ? 63 - bits : 51;
+  P.by_C = FastDiv::by((uint32_t)P.C);
+  P.by_R = FastDiv::by((uint32_t)P.R);
+  P.logits = static_cast<const char*>(a->logits);
+  P.req = a->req_stride;
+  P.row = a->row_stride;
+  P.temperature = a->temperature;
+  P.top_k = a->top_k;
+  P.top_p = a->top_p;
+  P.min_p = a->min_p;
+  const size_t segs = (size_t)a->B * a->R * P.nseg;
+  char* ws = static_cast<char*>(a->workspace);
+  P.rec = reinterpret_cast<CutRecord*>(ws);
+  P.cells = reinterpret_cast<float*>(ws + align256(segs * sizeof(CutRecord)));
+  P.last = reinterpret_cast<uint64_t*>(ws + align256(segs * sizeof(CutRecord)) + align256(segs * 64 * sizeof(float)));
+  return P;
+}
+
+int cache4_check(const spec_kv4_cache& c) {
+  if (c.num_blocks < 1 || !power_of_two(c.block_size, 16, 1024) || c.heads < 1 || c.heads > 1024 || c.head_dim < 32 ||
+      c.head_dim > 256 || c.head_dim % 32)
+    return SPEC_EINVAL;
+  if (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales) return SPEC_EINVAL;
+  if (!aligned16(c.k_codes) || !aligned16(c.v_codes)) return SPEC_EALIGN;
+  if (c.block_stride % 16 || c.token_stride % 16 || c.head_stride % 16) return SPEC_EALIGN;
+  const int64_t bytes = c.head_dim / 2;
+  constexpr int64_t kMost = (int64_t)1 << 42;  // (as for 8 bits)
+  if (c.token_stride < bytes || c.head_stride < bytes) return SPEC_EINVAL;
+  if (c.token_stride > ((int64_t)1 << 26) || c.head_stride > kMost) return SPEC_EINVAL;
+  const int64_t tokens = (int64_t)(c.block_size - 1) * c.token_stride, heads = (int64_t)(c.heads - 1) * c.head_stride;
+  const bool heads_in = c.token_stride >= heads + bytes, tokens_in = c.head_stride >= tokens + bytes;
+  if (!(heads_in || tokens_in || c.heads == 1)) return SPEC_EINVAL;
+  if (c.num_blocks > 1 && c.block_stride < tokens + heads + bytes) return SPEC_EINVAL;
+  if (c.scale_head_stride < (int64_t)(c.head_dim / 32) * c.block_size || c.scale_head_stride > kMost) return SPEC_EINVAL;
+  if (c.scale_block_stride < c.heads * c.scale_head_stride && c.num_blocks > 1) return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
+CacheView cache4_view(const spec_kv4_cache& c) {
+  CacheView v;
+  v.num_blocks = c.num_blocks;
+  v.heads = c.heads;
+  v.dim = c.head_dim;
+  v.bs_shift = log2_of(c.block_size);
+  v.st_shift = 0;
+  v.codes[0] = c.k_codes;
+  v.codes[1] = c.v_codes;
+  v.scales[0] = c.k_scales;
+  v.scales[1] = c.v_scales;
+  v.block = c.block_stride;
+  v.token = c.token_stride;
+  v.head = c.head_stride;
+  v.sblock = c.scale_block_stride;
+  v.shead = c.scale_head_stride;
+  return v;
+}
+
+// One rotated tensor: its input and output.
+bool turned_ok(const void* in, int64_t tok, int64_t head, const void* out, int64_t out_tok, int64_t out_head) {
+  if (!in || !out || tok < 0 || head < 0 || out_tok < 0 || out_head < 0) return false;
+  return in != out || (tok == out_tok && head == out_head);
+}
+
+// How the tokens and heads of a rotation are shared out; false: too many.
+bool rope_split(RopeParams& P) {
+  const int64_t per = kThreads / (P.dim / 8), heads = (int64_t)P.heads[0] + (P.write ? 2 : 1) * (int64_t)P.heads[1];
+  const int64_t rounds = (heads + per - 1) / per;
+  P.tokens = 1;
+  P.shares = (int32_t)rounds;
+  return fits_dispatch((((int64_t)P.N + P.tokens - 1) / P.tokens) * P.shares, kThreads);
+}
+
+int rope_check(const spec_rope_args* a, RopeParams& P) {
+  if (!a || a->N < 0 || a->q_heads < 0 || a->q_heads > 1024 || a->k_heads < 0 || a->k_heads > 1024) return SPEC_EINVAL;
+  if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8) return SPEC_EINVAL;
+  if (a->rot_dim < 16 || a->rot_dim > a->head_dim || a->rot_dim % 16) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (!(fabs(a->scale) <= DBL_MAX)) return SPEC_EINVAL;
+  if (a->N == 0 || a->q_heads + a->k_heads == 0) return SPEC_OK;
+  if (!a->inv_freq || !a->positions) return SPEC_EINVAL;
+  if (a->q_heads > 0 && !turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride,
+                                   a->q_out_head_stride))
+    return SPEC_EINVAL;
+  if (a->k_heads > 0 && !turned_ok(a->k, a->k_token_stride, a->k_head_stride, a->k_out, a->k_out_token_stride,
+                                   a->k_out_head_stride))
+    return SPEC_EINVAL;
+  P = {};
+  P.N = a->N;
+  P.heads[0] = a->q_heads;
+  P.heads[1] = a->k_heads;
+  P.dim = a->head_dim;
+  P.half = a->rot_dim / 2;
+  P.inter = a->interleaved != 0;
+  P.positions = a->positions;
+  P.inv_freq = a->inv_freq;
+  P.scale = a->scale;
+  P.src[0] = static_cast<const char*>(a->q);
+  P.tok[0] = a->q_token_stride;
+  P.hd[0] = a->q_head_stride;
+  P.src[1] = static_cast<const char*>(a->k);
+  P.tok[1] = a->k_token_stride;
+  P.hd[1] = a->k_head_stride;
+  P.dst[0] = static_cast<char*>(a->q_out);
+  P.dtok[0] = a->q_out_token_stride;
+  P.dhd[0] = a->q_out_head_stride;
+  P.dst[1] = static_cast<char*>(a->k_out);
+  P.dtok[1] = a->k_out_token_stride;
+  P.dhd[1] = a->k_out_head_stride;
+  return rope_split(P) ? SPEC_OK : SPEC_EINVAL;
+}
+
+int kv4_write_check(const spec_kv4_write_args* a, RopeParams& P) {
+  if (!a || a->N < 0) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  const int rc = cache4_check(a->cache);
+  if (rc != SPEC_OK) return rc;
+  if (a->rot_dim < 0 || a->rot_dim > a->cache.head_dim || a->rot_dim % 16) return SPEC_EINVAL;
+  if (a->q_heads < 0 || a->q_heads > 1024 || (a->q_heads > 0 && a->rot_dim == 0)) return SPEC_EINVAL;
+  if (a->rot_dim > 0 && !(fabs(a->scale) <= DBL_MAX)) return SPEC_EINVAL;
+  // keys and values are written by different lanes
+  if (a->cache.k_codes == a->cache.v_codes || a->cache.k_scales == a->cache.v_scales) return SPEC_EINVAL;
+  if (a->N == 0) return SPEC_OK;
+  if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
+  if (a->k_token_stride < 0 || a->k_head_stride < 0 || a->v_token_stride < 0 || a->v_head_stride < 0)
+    return SPEC_EINVAL;
+  if (a->rot_dim > 0 && (!a->inv_freq || !a->positions)) return SPEC_EINVAL;
+  if (a->q_heads > 0 && !turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride,
+                                   a->q_out_head_stride))
+    return SPEC_EINVAL;
+  P = {};
+  P.c = cache4_view(a->cache);
+  P.N = a->N;
+  P.heads[0] = a->q_heads;
+  P.heads[1] = a->cache.heads;
+  P.dim = a->cache.head_dim;
+  P.half = a->rot_dim / 2;
+  P.inter = a->rot_dim == 0 || a->interleaved != 0;  // (nothing turned: no lane needs another's elements)
+  P.write = 1;
+  P.positions = a->positions;
+  P.inv_freq = a->inv_freq;
+  P.scale = a->scale;
+  P.src[0] = static_cast<const char*>(a->q);
+  P.tok[0] = a->q_token_stride;
+  P.hd[0] = a->q_head_stride;
+  P.src[1] = static_cast<const char*>(a->key);
+  P.tok[1] = a->k_token_stride;
+  P.hd[1] = a->k_head_stride;
+  P.src[2] = static_cast<const char*>(a->value);
+  P.tok[2] = a->v_token_stride;
+  P.hd[2] = a->v_head_stride;
+  P.dst[0] = static_cast<char*>(a->q_out);
+  P.dtok[0] = a->q_out_token_stride;
+  P.dhd[0] = a->q_out_head_stride;
+  P.slots = a->slots;
+  return rope_split(P) ? SPEC_OK : SPEC_EINVAL;
+}
+
+int kv4_read_check(const spec_kv4_read_args* a) {
+  if (!a || a->N < 0) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  const int rc = cache4_check(a->cache);
+  if (rc != SPEC_OK) return rc;
+  if (a->N == 0) return SPEC_OK;
+  if (!a->key || !a->value || !a->slots) return SPEC_EINVAL;
+  const int64_t per = kv_read_per(a->N, a->cache.heads, a->cache.head_dim);
+  if (!fits_dispatch(((int64_t)a->N + per - 1) / per, kThreads)) return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
 bool attn_sizes_ok(const spec_attn_args* a) {
   if (a->B < 0 || a->N < 0 || a->max_q < 1 || a->max_q > (1 << 24) || a->max_ctx < 0 || a->max_ctx > (1 << 30) ||
       a->window < 0)
@@ -365,11 +572,11 @@ size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
          align256((size_t)a->B * p.nrb * sizeof(int2));
 }
 
-int attn_check(const spec_attn_args* a, AttnPlan& plan) {
-  if (!a || !attn_sizes_ok(a)) return SPEC_EINVAL;
+// cache_rc: what the check of the cache says.
+int attn_check(const spec_attn_args* a, int cache_rc, AttnPlan& plan) {
+  if (!attn_sizes_ok(a)) return SPEC_EINVAL;
   if (a->dtype != SPEC_BF16) return SPEC_EDTYPE;
-  const int rc = cache_check(a->cache);
-  if (rc != SPEC_OK) return rc;
+  if (cache_rc != SPEC_OK) return cache_rc;
   if (!(fabsf(a->scale) <= FLT_MAX / 1.4427f)) return SPEC_EINVAL;  // (the kernel takes scale * log2(e))
   if (a->max_blocks < 0 || a->bt_row_stride < a->max_blocks) return SPEC_EINVAL;
   if (a->B == 0 || a->N == 0) return SPEC_OK;
@@ -389,6 +596,43 @@ int attn_check(const spec_attn_args* a, AttnPlan& plan) {
     if (a->workspace_bytes < need) return SPEC_EWORKSPACE;
   }
   return SPEC_OK;
+}
+
+int attn_launch(const spec_attn_args* a, const AttnPlan& plan, const CacheView& view, bool four, hipStream_t stream);
+
+// An attention over the 4-bit cache as one over a cache of 8 bits: what is not
+// the cache, and of the cache what its plan reads.
+spec_attn_args attn_of(const spec_attn4_args* a) {
+  spec_attn_args b = {};
+  b.cache.num_blocks = a->cache.num_blocks;
+  b.cache.block_size = a->cache.block_size;
+  b.cache.scale_tokens = 1;
+  b.cache.heads = a->cache.heads;
+  b.cache.head_dim = a->cache.head_dim;
+  b.cache.token_stride = a->cache.token_stride;
+  b.cache.head_stride = a->cache.head_stride;
+  b.B = a->B;
+  b.N = a->N;
+  b.q_heads = a->q_heads;
+  b.max_q = a->max_q;
+  b.max_ctx = a->max_ctx;
+  b.window = a->window;
+  b.dtype = a->dtype;
+  b.scale = a->scale;
+  b.q = a->q;
+  b.q_token_stride = a->q_token_stride;
+  b.q_head_stride = a->q_head_stride;
+  b.q_start = a->q_start;
+  b.ctx_len = a->ctx_len;
+  b.block_table = a->block_table;
+  b.bt_row_stride = a->bt_row_stride;
+  b.max_blocks = a->max_blocks;
+  b.sinks = a->sinks;
+  b.out = a->out;
+  b.lse = a->lse;
+  b.workspace = a->workspace;
+  b.workspace_bytes = a->workspace_bytes;
+  return b;
 }
 
 }  // namespace
@@ -760,11 +1004,95 @@ size_t spec_attn_workspace_bytes(const spec_attn_args* a) {
 }
 
 int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
+  if (!a) return SPEC_EINVAL;
   AttnPlan plan;
-  const int rc = attn_check(a, plan);
+  const int rc = attn_check(a, cache_check(a->cache), plan);
   if (rc != SPEC_OK || a->B == 0 || a->N == 0) return rc;
+  return attn_launch(a, plan, cache_view(a->cache), false, stream);
+}
+
+size_t spec_attn4_workspace_bytes(const spec_attn4_args* a) {
+  if (!a || a->cache.head_dim % 32) return 0;
+  const spec_attn_args b = attn_of(a);
+  return spec_attn_workspace_bytes(&b);
+}
+
+int spec_attn4_launch(const spec_attn4_args* a, hipStream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  const spec_attn_args b = attn_of(a);
+  AttnPlan plan;
+  const int rc = attn_check(&b, cache4_check(a->cache), plan);
+  if (rc != SPEC_OK || a->B == 0 || a->N == 0) return rc;
+  return attn_launch(&b, plan, cache4_view(a->cache), true, stream);
+}
+
+int spec_sample_launch(const spec_sample_args* a, hipStream_t stream) {
+  int rc = cut_check(a);
+  if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
+  if (!a->uniforms || !a->tokens) return SPEC_EINVAL;
+  if (a->row_index ? a->rows < 0 : a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;
+  CutParams P = cut_params(a);
+  P.row_index = a->row_index;
+  P.rows = a->rows;
+  P.uniforms = a->uniforms;
+  P.tokens = a->tokens;
+  return launch_cut(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+size_t spec_sample_workspace_bytes(int32_t B, int32_t R, int32_t V) {
+  return cut_shape_ok(B, R, V) ? cut_ws_bytes(B, R, V) : 0;
+}
+
+int spec_truncate_launch(const spec_truncate_args* a, hipStream_t stream) {
+  int rc = cut_check(a);
+  if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
+  if (!a->out) return SPEC_EINVAL;
+  if (a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;
+  if (a->out_row_stride < a->V || (a->B > 1 && a->out_req_stride / a->R < a->out_row_stride)) return SPEC_EINVAL;
+  if (a->out == a->logits && (a->out_row_stride != a->row_stride || (a->B > 1 && a->out_req_stride != a->req_stride)))
+    return SPEC_EINVAL;
+  CutParams P = cut_params(a);
+  P.out = static_cast<char*>(a->out);
+  P.out_req = a->out_req_stride;
+  P.out_row = a->out_row_stride;
+  return launch_cut(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+int spec_rope_launch(const spec_rope_args* a, hipStream_t stream) {
+  RopeParams P;
+  const int rc = rope_check(a, P);
+  if (rc != SPEC_OK || a->N == 0 || a->q_heads + a->k_heads == 0) return rc;
+  return launch_rope(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+int spec_kv4_write_launch(const spec_kv4_write_args* a, hipStream_t stream) {
+  RopeParams P;
+  const int rc = kv4_write_check(a, P);
+  if (rc != SPEC_OK || a->N == 0) return rc;
+  return launch_rope(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+int spec_kv4_read_launch(const spec_kv4_read_args* a, hipStream_t stream) {
+  const int rc = kv4_read_check(a);
+  if (rc != SPEC_OK || a->N == 0) return rc;
+  KvReadParams P;
+  P.c = cache4_view(a->cache);
+  P.N = a->N;
+  P.per = kv_read_per(a->N, a->cache.heads, a->cache.head_dim);
+  P.dst[0] = static_cast<char*>(a->key);
+  P.dst[1] = static_cast<char*>(a->value);
+  P.slots = a->slots;
+  return launch_kv4_read(P, a->dtype, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
+}
+
+}  // extern "C"
+
+// The kernel parameters of a checked attention (B, N >= 1), and its launch.
+namespace {
+int attn_launch(const spec_attn_args* a, const AttnPlan& plan, const CacheView& view, bool four, hipStream_t stream) {
   AttnParams P;
-  P.c = cache_view(a->cache);
+  P.c = view;
+  P.four = four;
   P.B = a->B;
   P.N = a->N;
   P.Hq = a->q_heads;
@@ -805,6 +1133,9 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   P.qvec = aligned16(a->q) && a->q_token_stride % 8 == 0 && a->q_head_stride % 8 == 0;
   return launch_attn(P, plan, stream) == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }
+}  // namespace
+
+extern "C" {
 
 int spec_workspace_error(const void* workspace, hipStream_t stream) {
   if (workspace == nullptr) return SPEC_EINVAL;

@@ -58,11 +58,12 @@
 // against 141).
 #include <limits.h>
 
+#include <type_traits>
+
 #include "cache_device.hpp"
 
 namespace specv {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 static_assert(kAttnWaves == kWaves, "waves of a workgroup");
@@ -236,12 +237,18 @@ __device__ __forceinline__ void store_row(Params P, int64_t row, int d, f32x4 o,
   if (d == 0 && P->lse) P->lse[row] = end.lse;
 }
 
-// FINE: scale_tokens < 16, a scale for each key; otherwise one for each 16.
-template <int DP, int RT, bool FINE>
+// How the cache holds its values: 8 bits with a scale for each 16 keys or more,
+// with a scale for each key (scale_tokens < 16), or 4 bits with a scale for each
+// 32 dims of a key.
+enum CacheForm { kCoarse8, kFine8, kFour };
+
+template <int DP, int RT, CacheForm FORM>
 __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
+  constexpr bool FINE = FORM != kCoarse8, FOUR = FORM == kFour;
   constexpr int C = DP / 32;   // steps of the sum over dims
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
-  constexpr int W = DP / 64;   // 16-byte loads of a lane's share of a key
+  // a lane's share of a key in loads of KD dims, and dwords of its share of a value
+  constexpr int KD = FOUR && DP > 64 ? 32 : 16, WK = DP / (4 * KD), WV = FOUR ? (DP + 127) / 128 : DP / 64;
   constexpr bool QREG = RT == 1 && C <= 4;  // Q's fragments stay in registers
   constexpr int kWindow = kAttnWindow;  // a subtile to a lane
   __shared__ __align__(16) char s_mem[(RT * C * 64 * 16 > kWaves * 16 * DP * 4) ? RT * C * 64 * 16
@@ -334,11 +341,16 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   const int tok_stride = (int)P->c.token;
   // a lane whose dims are past the head's takes the key's first ones instead:
   // Q is 0 there, and those dims of the output are not stored
-  uint32_t koff[W];
+  uint32_t koff[WK], kso[FOUR ? WK : 1];  // kso, vso: (4 bits) where their scales stand
 #pragma unroll
-  for (int w = 0; w < W; ++w)
-    koff[w] = (uint32_t)(r * tok_stride + (w * 64 + g * 16 < dim ? w * 64 + g * 16 : 0));
-  const uint32_t voff = (uint32_t)(4 * g * tok_stride + (r * (DP / 16) < dim ? r * (DP / 16) : 0));
+  for (int w = 0; w < WK; ++w) {
+    const int d = (w * 4 + g) * KD, from = d < dim ? d : 0;
+    koff[w] = (uint32_t)(r * tok_stride + (FOUR ? from / 2 : from));
+    if constexpr (FOUR) kso[w] = (uint32_t)(((from >> 5) << P->c.bs_shift) + r);
+  }
+  const int vd = r * (DP / 16) < dim ? r * (DP / 16) : 0;
+  const uint32_t voff = (uint32_t)(4 * g * tok_stride + (FOUR ? vd / 2 : vd));
+  const uint32_t vso = FOUR ? (uint32_t)(((vd >> 5) << P->c.bs_shift) + 4 * g) : 0;
   const Unit un = unit_of(P, v, RT * 16);
   const int len = (int)min(left, (int64_t)(un.tiles - at));  // of this unit
   if (un.bad && un.tiles > 0) {
@@ -355,8 +367,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   const int nt = (len - ks + kways - 1) / kways;
 
   // Q, to become the fragments of the first product in LDS: fragment (rt, c),
-  // lane l: row 16 rt + l % 16, dims 64 (c / 2) + 16 (l / 16) + 8 (c % 2) ..+ 8
-  // (RT = 1: a wave's own head's)
+  // lane l: row 16 rt + l % 16, dims 64 (c / 2) + 16 (l / 16) + 8 (c % 2) ..+ 8, or
+  // with loads of 32 dims 128 (c / 4) + 32 (l / 16) + 8 (c % 4) ..+ 8 (RT = 1: a
+  // wave's own head's)
   constexpr int QF = RT == 1 ? C : (RT * C * 64 + kWG - 1) / kWG;
   u32x4 qreg[QF];
 #pragma unroll
@@ -364,7 +377,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     const int f = RT == 1 ? i * 64 + lane : tid + i * kWG;
     const int l = f & 63, cc = (f >> 6) % C, rt = (f >> 6) / C;
     const int k = rt * 16 + (l & 15);
-    const int d = (cc >> 1) * 64 + (l >> 4) * 16 + (cc & 1) * 8;
+    const int d = ((cc / (KD / 8)) * 4 + (l >> 4)) * KD + (cc % (KD / 8)) * 8;
     qreg[i] = u32x4{0, 0, 0, 0};
     if (k < un.rows && d < P->c.dim) {
       const int t = div_group(P, un.h0 + k);
@@ -417,7 +430,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     page = ok ? page : 0;
     okv = __ballot(ok);
     const int64_t po = (int64_t)page * P->c.block + (int64_t)head * P->c.head + (int64_t)in * P->c.token;
-    const int64_t so = (int64_t)page * P->c.sblock + (int64_t)head * P->c.shead + (in >> P->c.st_shift);
+    const int64_t so = (int64_t)page * P->c.sblock + (int64_t)head * P->c.shead + (FOUR ? in : in >> P->c.st_shift);
     pg_lo = (int)po;
     pg_hi = (int)(po >> 32);
     if constexpr (FINE) {
@@ -432,12 +445,13 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
   };
   auto lane64 = [&](int lo, int hi, int l) { return ((int64_t)lane_i(hi, l) << 32) | (uint32_t)lane_i(lo, l); };
 
-  // subtile u: key l % 16, dims 64 w + 16 g ..+ 16; slot j's key, dims
+  // subtile u: key l % 16, dims KD (4 w + g) ..+ KD; slot j's key, dims
   // [r DP/16, (r+1) DP/16)
+  using KeyLoad = std::conditional_t<FOUR && KD == 16, u32x2, u32x4>;
   struct Buffer {
-    u32x4 k[2][W];
-    uint32_t v[8][W];
-    uint32_t kfine[2], vfine[2];  // (FINE) scale bytes of key r, and of keys 4 g ..+ 4
+    KeyLoad k[2][WK];
+    uint32_t v[8][WV];
+    uint32_t kfine[2][FOUR ? WK : 1], vfine[2];  // (FINE) scale bytes of key r, and of keys 4 g ..+ 4
     float ksc[2], vsc[2];
     uint32_t ok;  // bits: 0, 1 the subtiles' blocks exist; 2, 3 their keys' scale is 0; 4, 5 their values'
   } buf;
@@ -449,10 +463,14 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
       const int l = ((i & (kWindow - 1)) << 1) + u;
       const uint8_t* kb = k_codes + lane64(pg_lo, pg_hi, l);
 #pragma unroll
-      for (int w = 0; w < W; ++w) t.k[u][w] = *reinterpret_cast<const u32x4*>(kb + koff[w]);
-      if constexpr (FINE) {
+      for (int w = 0; w < WK; ++w) t.k[u][w] = *reinterpret_cast<const KeyLoad*>(kb + koff[w]);
+      if constexpr (FOUR) {
+        const uint8_t* sb = P->c.scales[0] + lane64(sc_lo, sc_hi, l);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) t.kfine[u][w] = sb[kso[w]];
+      } else if constexpr (FINE) {
         const int64_t so = lane64(sc_lo, sc_hi, l);
-        t.kfine[u] = P->c.scales[0][so + (uint32_t)(r >> P->c.st_shift)];
+        t.kfine[u][0] = P->c.scales[0][so + (uint32_t)(r >> P->c.st_shift)];
       } else {
         t.ksc[u] = scale_of((uint32_t)lane_i(ksv, l));
       }
@@ -470,9 +488,11 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint8_t* p = vb + (int64_t)j * tok_stride;
-        if constexpr (W == 1) {
+        if constexpr (FOUR && DP == 64) {
+          t.v[4 * u + j][0] = *reinterpret_cast<const uint16_t*>(p + voff);
+        } else if constexpr (WV == 1) {
           t.v[4 * u + j][0] = *reinterpret_cast<const uint32_t*>(p + voff);
-        } else if constexpr (W == 2) {
+        } else if constexpr (WV == 2) {
           const u32x2 w = *reinterpret_cast<const u32x2*>(p + voff);
           t.v[4 * u + j][0] = w.x;
           t.v[4 * u + j][1] = w.y;
@@ -484,7 +504,9 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
           t.v[4 * u + j][3] = w.w;
         }
       }
-      if constexpr (FINE) {
+      if constexpr (FOUR) {
+        __builtin_memcpy(&t.vfine[u], P->c.scales[1] + lane64(sc_lo, sc_hi, l) + vso, 4);
+      } else if constexpr (FINE) {
         const uint8_t* sb = P->c.scales[1] + lane64(sc_lo, sc_hi, l) + (uint32_t)((4 * g) >> P->c.st_shift);
         if (P->c.st_shift == 0) {
           uint32_t w;
@@ -508,14 +530,16 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     if constexpr (!QREG && RT * C > 4) asm volatile("" ::: "memory");
     const int key0 = k_beg + (i * kways + ks) * kTileKeys;
     const uint32_t okt = t.ok & 3u;
-    // a scale byte of 0 (never written): values of 0, whatever the codes
+    // (8 bits) a scale byte of 0 (never written): values of 0, whatever the codes
     const uint32_t v_none = t.ok >> 4;
-    if (FINE ? __ballot(t.kfine[0] == 0 || t.kfine[1] == 0) != 0 : (t.ok & 12u) != 0) {
+    if constexpr (!FOUR) {
+      if (FINE ? __ballot(t.kfine[0][0] == 0 || t.kfine[1][0] == 0) != 0 : (t.ok & 12u) != 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool none = FINE ? t.kfine[u] == 0 : ((t.ok >> (2 + u)) & 1u) != 0;
+        for (int u = 0; u < 2; ++u) {
+          const bool none = FINE ? t.kfine[u][0] == 0 : ((t.ok >> (2 + u)) & 1u) != 0;
 #pragma unroll
-        for (int w = 0; w < W; ++w) t.k[u][w] = none ? u32x4{0, 0, 0, 0} : t.k[u][w];
+          for (int w = 0; w < WK; ++w) t.k[u][w] = none ? KeyLoad{} : t.k[u][w];
+        }
       }
     }
     // every row of the block sees every key of the tile
@@ -525,13 +549,19 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     f32x4 s[RT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float sc = FINE ? scale_of(t.kfine[u]) : t.ksc[u];
       bf16x8 ka[C];
 #pragma unroll
       for (int cc = 0; cc < C; ++cc) {
-        const u32x4 w4 = t.k[u][cc / 2];
-        const uint32_t w0 = (cc & 1) ? w4.z : w4.x, w1 = (cc & 1) ? w4.w : w4.y;
-        ka[cc] = pack8(widen2<false>(w0, sc), widen2<true>(w0, sc), widen2<false>(w1, sc), widen2<true>(w1, sc));
+        if constexpr (FOUR) {
+          const float sc = scale_of(t.kfine[u][cc / (KD / 8)]);
+          const uint32_t w = t.k[u][cc / (KD / 8)][cc % (KD / 8)];
+          ka[cc] = pack8(widen4<0>(w, sc), widen4<1>(w, sc), widen4<2>(w, sc), widen4<3>(w, sc));
+        } else {
+          const float sc = FINE ? scale_of(t.kfine[u][0]) : t.ksc[u];
+          const u32x4 w4 = t.k[u][cc / 2];
+          const uint32_t w0 = (cc & 1) ? w4.z : w4.x, w1 = (cc & 1) ? w4.w : w4.y;
+          ka[cc] = pack8(widen2<false>(w0, sc), widen2<true>(w0, sc), widen2<false>(w1, sc), widen2<true>(w1, sc));
+        }
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -544,15 +574,17 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
               0, 0, 0);
     }
     load_k(min(i + 1, nt - 1));
-    if (FINE ? __ballot(zero_byte(t.vfine[0]) || zero_byte(t.vfine[1])) != 0 : v_none != 0) {
+    if constexpr (!FOUR) {
+      if (FINE ? __ballot(zero_byte(t.vfine[0]) || zero_byte(t.vfine[1])) != 0 : v_none != 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool none = FINE ? ((t.vfine[u] >> (8 * j)) & 0xffu) == 0 : ((v_none >> u) & 1u) != 0;
+          for (int j = 0; j < 4; ++j) {
+            const bool none = FINE ? ((t.vfine[u] >> (8 * j)) & 0xffu) == 0 : ((v_none >> u) & 1u) != 0;
 #pragma unroll
-          for (int w = 0; w < W; ++w) t.v[4 * u + j][w] = none ? 0u : t.v[4 * u + j][w];
-        }
+            for (int w = 0; w < WV; ++w) t.v[4 * u + j][w] = none ? 0u : t.v[4 * u + j][w];
+          }
+      }
     }
 
     // a tile that some row sees only in part: scores not seen become -inf;
@@ -571,12 +603,13 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
           const bool any = there && key <= un.p_hi && (window == 0 || key > un.p_lo - window);
           some |= any;
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
+          for (int w = 0; w < WV; ++w) {
             t.v[4 * u + j][w] = any ? t.v[4 * u + j][w] : 0u;
-            nans |= nan_bytes(t.v[4 * u + j][w]) != 0;
+            if constexpr (!FOUR) nans |= nan_bytes(t.v[4 * u + j][w]) != 0;
           }
           if constexpr (FINE) fine |= any ? t.vfine[u] & (0xffu << (8 * j)) : (uint32_t)kScaleBias << (8 * j);
         }
+        if constexpr (FOUR) nans |= zero_byte(~fine);  // (a scale byte of 255)
         if constexpr (FINE) t.vfine[u] = fine;
         if constexpr (!FINE) t.vsc[u] = __ballot(some) ? t.vsc[u] : 1.0f;
         __builtin_amdgcn_sched_barrier(0);  // (few conditions at a time: each is a pair of scalar registers)
@@ -622,7 +655,7 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[4 * u + j] = exp2_fast(__builtin_fmaf(s[rt][u][j], scale2, -ref[rt]));
       sum[rt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      if constexpr (FINE) {
+      if constexpr (FINE && !FOUR) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] *= scale_of((t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu);
       }
@@ -641,14 +674,22 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
       for (int d = lane; d < DP; d += 64) mask[d] = 0;
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bit = 1u << (16 * (j >> 2) + 4 * g + (j & 3));
+        if constexpr (FOUR) {  // all dims of the scale
+          if (((t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu) == 255u) {
+            for (int d = 0; d < DT; ++d) atomicOr(&mask[r * DT + d], bit);
+            t.vfine[j >> 2] ^= 0x80u << (8 * (j & 3));  // (of 2^0; the codes may be any)
+          }
+        } else {
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const uint32_t nb = nan_bytes(t.v[j][w]);
-          for (uint32_t m = nb; m; m &= m - 1)
-            atomicOr(&mask[r * DT + 4 * w + (__builtin_ctz(m) >> 3)], 1u << (16 * (j >> 2) + 4 * g + (j & 3)));
-          t.v[j][w] &= ~((nb >> 7) * 0xffu);
+          for (int w = 0; w < WV; ++w) {
+            const uint32_t nb = nan_bytes(t.v[j][w]);
+            for (uint32_t m = nb; m; m &= m - 1) atomicOr(&mask[r * DT + 4 * w + (__builtin_ctz(m) >> 3)], bit);
+            t.v[j][w] &= ~((nb >> 7) * 0xffu);
+          }
         }
+      }
       __builtin_amdgcn_wave_barrier();
       uint32_t see[RT];
 #pragma unroll
@@ -665,9 +706,35 @@ __global__ __launch_bounds__(kWG, 2) void attn_kernel(AttnParams) {
     }
 
     // O^T
+    if constexpr (FOUR) {
+      // two dims of a key to a byte: widened with the key's scale, then two keys
+      // of a dim put together
+      float vs[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vs[j] = scale_of((t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu);
+#pragma unroll
+      for (int b = 0; b < DT / 2; ++b) {
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = widen4_at(t.v[2 * j][b / 4], vs[2 * j], b % 4),
+                         c = widen4_at(t.v[2 * j + 1][b / 4], vs[2 * j + 1], b % 4);
+          even[j] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+          odd[j] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+        }
+        const bf16x8 va = pack8(even[0], even[1], even[2], even[3]), vb = pack8(odd[0], odd[1], odd[2], odd[3]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          acc[rt][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pb[rt], acc[rt][2 * b], 0, 0, 0);
+          acc[rt][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pb[rt], acc[rt][2 * b + 1], 0, 0, 0);
+        }
+      }
+      load_v(min(i + 1, nt - 1));
+      return;
+    }
     const float v0 = FINE ? 1.0f : t.vsc[0], v1 = FINE ? 1.0f : t.vsc[1];
 #pragma unroll
-    for (int dw = 0; dw < W; ++dw) {
+    for (int dw = 0; dw < (FOUR ? 0 : WV); ++dw) {
       uint32_t lo[4], hi[4];
       transpose4(t.v[0][dw], t.v[1][dw], t.v[2][dw], t.v[3][dw], lo);
       transpose4(t.v[4][dw], t.v[5][dw], t.v[6][dw], t.v[7][dw], hi);
@@ -846,10 +913,12 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(AttnParams, int row_tiles
 template <int DP, int RT>
 static hipError_t launch_attn_typed(const AttnParams& P, hipStream_t stream) {
   const dim3 grid((unsigned)(((int64_t)P.groups + 7) / 8 * 8 * P.items));
-  if (P.c.st_shift < 4)
-    hipLaunchKernelGGL((attn_kernel<DP, RT, true>), grid, dim3(kWG), 0, stream, P);
+  if (P.four)
+    hipLaunchKernelGGL((attn_kernel<DP, RT, kFour>), grid, dim3(kWG), 0, stream, P);
+  else if (P.c.st_shift < 4)
+    hipLaunchKernelGGL((attn_kernel<DP, RT, kFine8>), grid, dim3(kWG), 0, stream, P);
   else
-    hipLaunchKernelGGL((attn_kernel<DP, RT, false>), grid, dim3(kWG), 0, stream, P);
+    hipLaunchKernelGGL((attn_kernel<DP, RT, kCoarse8>), grid, dim3(kWG), 0, stream, P);
   return hipGetLastError();
 }
 

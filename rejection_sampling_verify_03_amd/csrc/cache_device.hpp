@@ -9,6 +9,7 @@ namespace specv {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kScaleBias = 127;
 // The smallest exponent a written group gets: the smallest code, 2^-9, is
@@ -46,6 +47,25 @@ __device__ __forceinline__ void decode4(uint32_t w, float x[4]) {
   x[1] = lo.y;
   x[2] = hi.x;
   x[3] = hi.y;
+}
+
+// Two fp32 values as bf16, rounded to nearest even, the first in the low half.
+__device__ __forceinline__ uint32_t round_bf16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+// Byte SEL of a word of e2m1 codes as two bf16 values, the scale's exponent
+// applied: exact down to the subnormal ones; an exponent byte of 255 gives NaN
+// whatever the codes.
+template <int SEL>
+__device__ __forceinline__ uint32_t widen4(uint32_t codes, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, SEL));
+}
+
+// (byte b, a constant after unrolling)
+__device__ __forceinline__ uint32_t widen4_at(uint32_t codes, float scale, int b) {
+  return b == 0 ? widen4<0>(codes, scale)
+                : b == 1 ? widen4<1>(codes, scale) : b == 2 ? widen4<2>(codes, scale) : widen4<3>(codes, scale);
 }
 
 }  // namespace specv

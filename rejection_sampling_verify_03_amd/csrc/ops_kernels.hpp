@@ -57,6 +57,40 @@ struct LogprobsParams {
 
 hipError_t launch_logprobs(const LogprobsParams& P, int dtype, hipStream_t stream);
 
+// ------------------------------------- sampling from cut distributions --
+struct CutRecord {  // one 4096-logit segment of a row
+  float m;          // largest logit
+  int32_t nan;      // whether some logit is a NaN
+  double s;         // sum of exp((x - m) / T), where it is needed
+};
+static_assert(sizeof(CutRecord) == 16, "CutRecord layout");
+
+constexpr int kCutChunkSegs = 8;         // segments per workgroup of the passes over all rows
+constexpr uint64_t kCutAll = ~1ull;      // a row's last kept rank: the row stays as it is
+constexpr uint64_t kCutBad = ~0ull;      // its settings cannot be used
+
+struct CutParams {
+  int32_t B, R, V, nseg, C;  // C: chunks of kCutChunkSegs segments per row
+  int32_t ibits, frac;       // bits of an index; weights are whole numbers of 2^-frac
+  FastDiv by_C, by_R;
+  const char* logits;
+  int64_t req, row;
+  const int32_t* row_index;  // or null
+  int32_t rows;
+  const float* temperature;
+  const int32_t* top_k;  // or null, as the next two
+  const float* top_p;
+  const float* min_p;
+  const float* uniforms;
+  int32_t* tokens;  // null: truncate
+  char* out;
+  int64_t out_req, out_row;
+  CutRecord* rec;  // [B * R, nseg]
+  float* cells;    // [B * R, nseg, 64] largest logit of each lane's 64 of a segment
+  uint64_t* last;  // [B * R] (truncate) rank of the last kept token
+};
+hipError_t launch_cut(const CutParams& P, int dtype, hipStream_t stream);
+
 // ------------------------------------------------------------ paged cache --
 struct CacheView {
   int32_t num_blocks, heads, dim;
@@ -95,6 +129,28 @@ inline int32_t kv_read_per(int32_t N, int32_t heads, int32_t dim) {
 inline int32_t kv_write_chunk(int32_t N) { return N >= 8192 ? 32 : N >= 1024 ? 16 : 4; }
 hipError_t launch_kv_write(const KvWriteParams& P, int dtype, hipStream_t stream);
 hipError_t launch_kv_read(const KvReadParams& P, int dtype, bool vec, hipStream_t stream);
+// (of a cache of 4 bits: the view's scales are [heads, dim / 32, block_size] of a block, st_shift unused)
+hipError_t launch_kv4_read(const KvReadParams& P, int dtype, hipStream_t stream);
+
+// ------------------------------------- rotary positions, the 4-bit write --
+constexpr int kRopeAngles = 256;  // cosines and sines that a workgroup holds
+struct RopeParams {
+  CacheView c;          // (write)
+  int32_t N, heads[2];  // tokens; query and key heads (values have the keys')
+  int32_t dim, half;    // half: rotated pairs of a head
+  int32_t inter, write; // pairs side by side; keys and values go to the cache
+  int32_t tokens;       // of a workgroup, at most kRopeAngles / half
+  int32_t shares;       // workgroups to a set of tokens
+  const int32_t* positions;
+  const double* inv_freq;
+  double scale;
+  const char* src[3];   // queries, keys, values
+  int64_t tok[3], hd[3];  // strides in elements
+  char* dst[2];
+  int64_t dtok[2], dhd[2];
+  const int64_t* slots;
+};
+hipError_t launch_rope(const RopeParams& P, int dtype, hipStream_t stream);
 
 // -------------------------------------------------------------- attention --
 struct AttnParams {
@@ -123,6 +179,7 @@ struct AttnParams {
   float2* pm;  // [chunks, 2, heads, 16 * rt] their reference exponents and sums of weights
   int2* runs;  // [B * nrb] the runs that hold each unit: (first * 2 + whether it began with another unit, last)
   int32_t qvec;
+  int32_t four;  // the cache holds 4 bits
 };
 
 hipError_t launch_attn(const AttnParams& P, const AttnPlan& plan, hipStream_t stream);

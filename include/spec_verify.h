@@ -689,7 +689,7 @@ int spec_attn_launch(const spec_attn_args* args, hipStream_t stream);
  * kept.  T = 0 takes the lowest index of the largest logit, whatever the cut
  * (a NaN logit counts as -inf, and a row with nothing above -inf gives 0).
  * Weights are taken to a multiple of 2^-f of the largest, f = 63 - (bits of
- * V), at most 51 (45 for V = 2^17 to 2^18 - 1): what is below counts as 0.
+ * V), at most 48 (45 for V = 2^17 to 2^18 - 1): what is below counts as 0.
  *
  * Data errors give token -1: a temperature that is negative, NaN, infinite or
  * positive below FLT_MIN; top_k < 0; top_p not above 0, or NaN; min_p outside

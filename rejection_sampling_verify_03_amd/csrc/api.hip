@@ -344,9 +344,8 @@ int kv_read_check(const spec_kv_read_args* a) {
 }
 
 // ------------------------------------------------ sampling, 4-bit cache, rotation
-size_t cut_ws_bytes(int32_t B, int32_t R, int32_t V) {
-  const size_t rows = (size_t)B * R, segs = rows * (((size_t)V + kSeg - 1) / kSeg);
-  return align256(segs * sizeof(CutRecord)) + align256(segs * 64 * sizeof(float)) + align256(rows * sizeof(uint64_t));
+size_t cut_ws_bytes(int32_t B, int32_t R) {
+  return align256((size_t)B * R * sizeof(uint64_t));
 }
 
 bool cut_shape_ok(int32_t B, int32_t R, int32_t V) {
@@ -365,7 +364,7 @@ int cut_check(const Args* a) {
   if (!a->logits || !a->temperature || !a->workspace) return SPEC_EINVAL;
   if (a->row_stride < a->V) return SPEC_EINVAL;
   if (!aligned16(a->workspace)) return SPEC_EALIGN;
-  if (a->workspace_bytes < cut_ws_bytes(a->B, a->R, a->V)) return SPEC_EWORKSPACE;
+  if (a->workspace_bytes < cut_ws_bytes(a->B, a->R)) return SPEC_EWORKSPACE;
   return SPEC_OK;
 }
 
@@ -375,13 +374,12 @@ CutParams cut_params(const Args* a) {
   P.B = a->B;
   P.R = a->R;
   P.V = a->V;
-  P.nseg = (int32_t)(((int64_t)a->V + kSeg - 1) / kSeg);
-  P.C = (P.nseg + kCutChunkSegs - 1) / kCutChunkSegs;
+  P.C = (int32_t)((((int64_t)a->V + kSeg - 1) / kSeg + kCutChunkSegs - 1) / kCutChunkSegs);
   while (((int64_t)1 << P.ibits) < a->V) ++P.ibits;
-  // V weights of at most 2^frac within 63 bits, each within the 52 of a double
+  // V weights of at most 2^frac within 63 bits, eight within the 52 of a double
   int bits = P.ibits;
   if (((int64_t)1 << bits) == a->V) ++bits;
-  P.frac = 63 - bits < 51 ? 63 - bits : 51;
+  P.frac = 63 - bits < 48 ? 63 - bits : 48;
   P.by_C = FastDiv::by((uint32_t)P.C);
   P.by_R = FastDiv::by((uint32_t)P.R);
   P.logits = static_cast<const char*>(a->logits);
@@ -391,11 +389,7 @@ CutParams cut_params(const Args* a) {
   P.top_k = a->top_k;
   P.top_p = a->top_p;
   P.min_p = a->min_p;
-  const size_t segs = (size_t)a->B * a->R * P.nseg;
-  char* ws = static_cast<char*>(a->workspace);
-  P.rec = reinterpret_cast<CutRecord*>(ws);
-  P.cells = reinterpret_cast<float*>(ws + align256(segs * sizeof(CutRecord)));
-  P.last = reinterpret_cast<uint64_t*>(ws + align256(segs * sizeof(CutRecord)) + align256(segs * 64 * sizeof(float)));
+  P.last = static_cast<uint64_t*>(a->workspace);
   return P;
 }
 
@@ -1040,7 +1034,7 @@ int spec_sample_launch(const spec_sample_args* a, hipStream_t stream) {
 }
 
 size_t spec_sample_workspace_bytes(int32_t B, int32_t R, int32_t V) {
-  return cut_shape_ok(B, R, V) ? cut_ws_bytes(B, R, V) : 0;
+  return cut_shape_ok(B, R, V) ? cut_ws_bytes(B, R) : 0;
 }
 
 int spec_truncate_launch(const spec_truncate_args* a, hipStream_t stream) {

@@ -58,19 +58,12 @@ struct LogprobsParams {
 hipError_t launch_logprobs(const LogprobsParams& P, int dtype, hipStream_t stream);
 
 // ------------------------------------- sampling from cut distributions --
-struct CutRecord {  // one 4096-logit segment of a row
-  float m;          // largest logit
-  int32_t nan;      // whether some logit is a NaN
-  double s;         // sum of exp((x - m) / T), where it is needed
-};
-static_assert(sizeof(CutRecord) == 16, "CutRecord layout");
-
-constexpr int kCutChunkSegs = 8;         // segments per workgroup of the passes over all rows
-constexpr uint64_t kCutAll = ~1ull;      // a row's last kept rank: the row stays as it is
+constexpr int kCutChunkSegs = 8;         // segments per workgroup of the pass that writes cut rows
+constexpr uint64_t kCutAll = ~1ull;      // a row's last kept key: the row stays as it is
 constexpr uint64_t kCutBad = ~0ull;      // its settings cannot be used
 
 struct CutParams {
-  int32_t B, R, V, nseg, C;  // C: chunks of kCutChunkSegs segments per row
+  int32_t B, R, V, C;   // C: chunks of kCutChunkSegs segments per row
   int32_t ibits, frac;       // bits of an index; weights are whole numbers of 2^-frac
   FastDiv by_C, by_R;
   const char* logits;
@@ -85,9 +78,7 @@ struct CutParams {
   int32_t* tokens;  // null: truncate
   char* out;
   int64_t out_req, out_row;
-  CutRecord* rec;  // [B * R, nseg]
-  float* cells;    // [B * R, nseg, 64] largest logit of each lane's 64 of a segment
-  uint64_t* last;  // [B * R] (truncate) rank of the last kept token
+  uint64_t* last;  // [B * R] (truncate) key of the last kept token
 };
 hipError_t launch_cut(const CutParams& P, int dtype, hipStream_t stream);
 

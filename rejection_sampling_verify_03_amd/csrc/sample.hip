@@ -15,36 +15,30 @@
 // their order: histograms by atomic additions in LDS give the same bits every
 // time.
 //
-// Three kernels, the first reads each row once:
+// One workgroup takes a row.  Its first pass counts the logits in bins of their
+// upper bits, in the order of the logits: a bin of bf16 logits is a single
+// value, so the bins' counts give every sum of weights with one exponential a
+// bin; fp32 logits, whose bins hold several values, are weighed one by one in a
+// second pass where top p asks for it.  The bin in which the count or the mass
+// reaches a border is known from one scan.  Where the tokens up to it are few
+// they are gathered into LDS and everything else happens there; otherwise the
+// border is found inside its bin (the c-th of equal logits by their index, or
+// the logits of the bin gathered), and the token by the sums of kept weights
+// over ranges of indices, then inside the range.
 //
-//  cut_stats   a wave to a segment of 4096 logits: the largest logit of each
-//      cell (the 64 logits of a lane), of the segment, whether there is a NaN,
-//      and where no top_k bounds the row the sum of its weights (fp64).
-//
-//  cut_finish  a workgroup to a row.  The k-th largest cell bounds the k-th
-//      largest logit from below, so only the cells above it are read again, and
-//      their logits above the bound (a few more than k) are candidates in LDS.
-//      Every border is then found by a radix search: a histogram of the weights
-//      (or of ones) over 2048 ranges of the key, a scan for the range in which
-//      the sum crosses the border, and so on inside it.  The key is the place
-//      in the order (distance of the logit from the largest, then the index), or
-//      the index for the token.  Where the candidates are too many for LDS, the
-//      same searches go over the row itself, and continue in LDS inside the range found.
-//
-//  truncate    writes the row, with -inf behind the last kept token.
 #include <limits.h>
+
+#include <type_traits>
 
 #include "ops_kernels.hpp"
 #include "unaligned.hpp"
 
 namespace specv {
 
-constexpr int kCutThreads = 1024;             // of cut_finish
-constexpr int kCutWaves = kCutThreads / 64;
-constexpr int kBins = 2048;
-constexpr int kCand = 4096;                   // candidates held in LDS
-constexpr int kGuess = 512;                   // cells taken at first where only the mass bounds the row
+constexpr int kRangeBits = 10, kRanges = 1 << kRangeBits;  // of a search's histogram
+constexpr int kCand = 2048;                                // candidates held in LDS
 typedef unsigned long long u64;
+constexpr u64 kNone = ~0ull;
 
 // What a request asks for.
 struct Cut {
@@ -52,7 +46,6 @@ struct Cut {
   int k;          // 0: all
   bool ok;        // usable
   bool greedy, all;  // T = 0; nothing is left out
-  bool mass;      // the sum of all weights is needed
 };
 
 __device__ __forceinline__ Cut cut_of(const CutParams& P, int b) {
@@ -65,7 +58,6 @@ __device__ __forceinline__ Cut cut_of(const CutParams& P, int b) {
   if (c.k >= P.V) c.k = 0;
   c.greedy = c.T == 0.0f;
   c.all = c.k == 0 && c.p >= 1.0f && c.mn == 0.0f;
-  c.mass = !c.greedy && c.k == 0 && (c.p < 1.0f || c.mn == 0.0f);
   return c;
 }
 
@@ -122,24 +114,6 @@ __device__ __forceinline__ float value_at(uint32_t o) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// ------------------------------------------------------------- statistics --
-template <int ES>
-__device__ __forceinline__ uint32_t magnitude(const RawGroup<ES, true>& g) {  // the largest, as bits
-  uint32_t a = 0;
-  if constexpr (ES == 2) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 m{0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, g.v[i] & 0x7fff7fffu));
-    a = (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a = max(max(a, __float_as_uint(g.a[i]) & 0x7fffffffu), __float_as_uint(g.b[i]) & 0x7fffffffu);
-  }
-  return a;
-}
-
 // 8 logits from e on, -inf past the row's end.
 template <int ES>
 __device__ __forceinline__ RawGroup<ES, true> load_end(const char* lg, int64_t e, int V) {
@@ -189,56 +163,6 @@ __device__ __forceinline__ void store_end(char* dst, int64_t e, int V, const flo
   }
 }
 
-template <int ES>
-__global__ __launch_bounds__(kWG) void cut_stats_kernel(CutParams P) {
-  const int i = (int)P.by_C.of(blockIdx.x), chunk = blockIdx.x - i * P.C;
-  const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
-  const Cut cut = cut_of(P, b);
-  if (!cut.ok || (P.tokens == nullptr && (cut.greedy || cut.all))) return;  // (the finish does not read them)
-  const char* lg = row_of(P, b, r, ES);
-  if (!lg) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int j1 = min(P.nseg, (chunk + 1) * kCutChunkSegs);
-  const double s = cut.mass ? 1.4426950408889634074 / (double)cut.T : 0.0;
-  for (int j = chunk * kCutChunkSegs + wave; j < j1; j += kWaves) {
-    const int64_t s0 = (int64_t)j * kSeg;
-    RawGroup<ES, true> g[kSegGroups];
-    if (s0 + kSeg <= P.V) {  // eight loads in a row, none under a branch
-#pragma unroll
-      for (int q = 0; q < kSegGroups; ++q) g[q] = load_any<ES>(lg, s0 + (q * 64 + lane) * 8);
-    } else {
-#pragma unroll
-      for (int q = 0; q < kSegGroups; ++q) g[q] = load_end<ES>(lg, s0 + (q * 64 + lane) * 8, P.V);
-    }
-    float gm = -INFINITY;
-    uint32_t big = 0;
-#pragma unroll
-    for (int q = 0; q < kSegGroups; ++q) {
-      float x[8];
-      unpack_group<ES, true>(g[q], x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) gm = fmaxf(gm, x[e]);
-      big = max(big, magnitude<ES>(g[q]));
-    }
-    P.cells[((int64_t)i * P.nseg + j) * 64 + lane] = gm;
-    CutRecord rec{wave_max_f(gm), __ballot(big > 0x7f800000u) != 0 ? 1 : 0, 0.0};
-    if (cut.mass && rec.m > -INFINITY) {
-      const double m = rec.m;
-      double sum = 0.0;
-#pragma unroll 1
-      for (int q = 0; q < kSegGroups; ++q) {
-        float x[8];
-        unpack_group<ES, true>(g[q], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += pow2(((double)x[e] - m) * s, 0);
-      }
-      rec.s = wave_total_d(sum);
-    }
-    if (lane == 0) P.rec[(int64_t)i * P.nseg + j] = rec;
-  }
-}
-
-// --------------------------------------------------------------- searches --
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ u64 dpp_u64(u64 x) {  // fill 0
   const uint32_t lo = (uint32_t)dpp_i<CTRL, ROW_MASK>((int)(uint32_t)x, 0);
@@ -255,17 +179,6 @@ __device__ __forceinline__ u64 wave_scan_u64(u64 x) {  // inclusive, in lane ord
   return x;
 }
 
-struct CutShared {
-  u64 hist[kBins];
-  u64 cand[kCand];      // keys of rank
-  u64 wave[kCutWaves];
-  double wave_d[kCutWaves];
-  float wave_f[kCutWaves];
-  u64 before, total, lo, hi;
-  int bin, count;
-  uint32_t far;
-};
-
 // A border: the smallest prefix whose weight reaches it.
 struct Border {
   enum Kind { kFixed, kShare, kAbove } kind;
@@ -278,261 +191,472 @@ struct Border {
   }
 };
 
-// What the searches of a row share.
-struct RowView {
-  const char* lg;
-  int V, ibits, frac;
-  float m;
-  uint32_t top;  // place of m
-  double s;      // log2(e) / T
+
+// ------------------------------------------------------------------- bins --
+// The bins of logits by sign and upper bits, in falling order: 2^kFine to an
+// octave from 2^-20 to 2^7 in magnitude, and three that hold what is left: from
+// 2^7 on (bin 0), below 2^-20 in magnitude (the middle one), from -2^7 down.
+// They are kept by slot, the clamped magnitude of either sign: slots 0 and kHalf
+// are both the middle bin's (counts are moved to the first).
+template <int ES>
+struct Bins {
+  static constexpr int kFine = ES == 2 ? 7 : 6, kShift = 23 - kFine;  // (bf16: all the bits there are)
+  static constexpr uint32_t kLo = 107u << kFine, kHi = 134u << kFine;
+  static constexpr int kMid = (int)(kHi - kLo) + 1, kN = 2 * kMid + 1;
+  static constexpr int kHalf = kMid + 1, kSlots = 2 * kHalf;
+  static __device__ __forceinline__ int slot(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return (int)(min(max((u & 0x7fffffffu) >> kShift, kLo - 1), kHi) - (kLo - 1) + (u >> 31) * kHalf);
+  }
+  static __device__ __forceinline__ int slot_of(int bin) { return bin <= kMid ? kMid - bin : kHalf + bin - kMid; }
+  static __device__ __forceinline__ int of(float x) {
+    const int s = slot(x);
+    return s < kHalf ? kMid - s : kMid + s - kHalf;
+  }
+  // whether all its logits are one value, and that value
+  static __device__ __forceinline__ bool single(int bin) { return ES == 2 && bin > 0 && bin < kN - 1 && bin != kMid; }
+  static __device__ __forceinline__ float value(int bin) {
+    const uint32_t mag = kLo - 1 + (uint32_t)abs(bin - kMid);
+    return __uint_as_float((mag << kShift) | (bin > kMid ? 0x80000000u : 0u));
+  }
+  // the smallest value that the bin can hold
+  static __device__ __forceinline__ float least(int bin) {
+    if (bin == kN - 1) return -INFINITY;
+    if (bin == kMid) return -__uint_as_float((kLo << kShift) - (ES == 2 ? 0x10000u : 1u));
+    const uint32_t mag = kLo - 1 + (uint32_t)abs(bin - kMid);
+    return bin < kMid ? __uint_as_float(mag << kShift)
+                      : -__uint_as_float(ES == 2 ? mag << kShift : ((mag + 1) << kShift) - 1);
+  }
+};
+static_assert((Bins<4>::kSlots + 1) / 2 + Bins<4>::kSlots <= Bins<2>::kSlots,
+              "counts and masses of fp32 in the place of bf16's weights");
+
+// SMALL: rows of up to kCand logits, all of them candidates.
+template <bool SMALL>
+struct CutShared {
+  // by slot.  bf16: counts (u32), later weights (double); fp32: counts, and
+  // behind them masses
+  u64 bins[SMALL ? 1 : Bins<2>::kSlots];
+  union {
+    u64 ranges[kRanges];
+    struct {  // a range's candidates
+      u64 few[64], few_mass[64], few_upto[64];
+    };
+  };
+  u64 cand[kCand];  // keys of rank; (bf16) counts of equal logits by range
+  u64 wave[2][16];
+  float wave_f[16];
+  uint32_t wave_u[16];
+  u64 before, through, special[3];
+  int bin, count;
 };
 
-// The key of rank of logit x at index e: 0.. for the row's largest.
+// The slots of 8 bf16 logits, two to an instruction.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void slots8(const RawGroup<2, true>& g, uint32_t (&slot)[8]) {
+  using B = Bins<2>;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 lo = (uint16_t)(B::kLo - 1), hi = (uint16_t)B::kHi, half = (uint16_t)B::kHalf;
+    const uint32_t two = g.v[i];
+    u16x2 mag = __builtin_bit_cast(u16x2, two & 0x7fff7fffu);
+    const u16x2 sign = __builtin_bit_cast(u16x2, two) >> (uint16_t)15;
+    mag = __builtin_elementwise_min(__builtin_elementwise_max(mag, lo), hi) - lo + sign * half;
+    const uint32_t both = __builtin_bit_cast(uint32_t, mag);
+    slot[2 * i] = both & 0xffffu;
+    slot[2 * i + 1] = both >> 16;
+  }
+}
+
+// A bound from below on logits, as the test of a group of 8 takes it: bf16
+// values above zero rise with their bits as signed numbers, those below zero
+// fall with them as unsigned ones.
 template <int ES>
-__device__ __forceinline__ u64 rank_key(const RowView& w, float x, int e) {
-  return ((u64)(w.top - place<ES>(x)) << w.ibits) | (uint32_t)e;
-}
-template <int ES>
-__device__ __forceinline__ float key_logit(const RowView& w, u64 key) {
-  return value_at<ES>(w.top - (uint32_t)(key >> w.ibits));
-}
-template <bool MASS>
-__device__ __forceinline__ u64 weight_of(const RowView& w, float x) {
-  return MASS ? whole(pow2(((double)x - (double)w.m) * w.s, w.frac)) : 1;
-}
+struct Floor {
+  float x;
+  uint32_t both;  // (bf16) its bits in both halves
+  bool above;     // (bf16) above zero
+  __device__ __forceinline__ explicit Floor(float f) : x(f) {
+    uint32_t u = __float_as_uint(f) >> 16;
+    above = f > 0.f;
+    if (f == 0.f) u = 0x8000u;
+    both = u | u << 16;
+  }
+  // whether some logit of the group may reach it
+  __device__ __forceinline__ bool reached(const RawGroup<ES, true>& g) const {
+    if constexpr (ES == 2) {
+      typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+      const uint32_t two[4] = {g.v.x, g.v.y, g.v.z, g.v.w};
+      if (above) {
+        i16x2 m = __builtin_bit_cast(i16x2, two[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(i16x2, two[i]));
+        return max(m.x, m.y) >= (int16_t)(both & 0xffffu);
+      }
+      u16x2 m = __builtin_bit_cast(u16x2, two[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = __builtin_elementwise_min(m, __builtin_bit_cast(u16x2, two[i]));
+      return min(m.x, m.y) <= (uint16_t)(both & 0xffffu);
+    } else {
+      float m = g.a[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = fmaxf(m, g.a[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, g.b[i]);
+      return m >= x;
+    }
+  }
+};
 
 struct Crossing {
   int bin;  // -1: the border is above the total
-  u64 before, total, border;
+  u64 before, border, through;
 };
 
-// The range of the histogram in which the sum reaches the border (all threads;
-// the histogram is complete when it is called, and free when it returns).
-__device__ __forceinline__ Crossing find_crossing(CutShared& S, const Border& border, u64 offset) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  __syncthreads();
-  const u64 h0 = S.hist[2 * t], h1 = S.hist[2 * t + 1], v = h0 + h1;
-  const u64 x = wave_scan_u64(v);
-  if (lane == 63) S.wave[wave] = x;
-  if (t == 0) S.bin = -1;
-  __syncthreads();
-  u64 base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kCutWaves; ++w) {
-    const u64 y = S.wave[w];
-    base += w < wave ? y : 0;
-    total += y;
-  }
-  const u64 at = border.of(total) - offset, before = base + x - v;
-  if (before < at && at <= before + v) {
-    S.bin = at <= before + h0 ? 2 * t : 2 * t + 1;
-    S.before = at <= before + h0 ? before : before + h0;
-  }
-  __syncthreads();
-  const Crossing c{S.bin, S.before, total, at + offset};
-  __syncthreads();
-  return c;
+__device__ __forceinline__ u64 lane_u64(u64 x, int l) {
+  return ((u64)(uint32_t)lane_i((int)(x >> 32), l) << 32) | (uint32_t)lane_i((int)x, l);
 }
-
-__device__ __forceinline__ void clear_hist(CutShared& S) {
-  S.hist[threadIdx.x] = 0;
-  S.hist[threadIdx.x + kCutThreads] = 0;
-  __syncthreads();
-}
-
-constexpr u64 kNone = ~0ull;
 
 __device__ __forceinline__ int bits_of(u64 x) { return 64 - __clzll((long long)x); }
 
-// Among the candidates in LDS with a key of rank up to `last`, the key (of
-// rank, or the index) at which the sum of weights (or the count) reaches the
-// border; kNone if it never does.  Keys lie in [lo, hi]; `offset` stands in
-// front of them.
-template <int ES, bool INDEX, bool MASS>
-__device__ __forceinline__ u64 search_lds(CutShared& S, const RowView& w, int n, u64 last, u64 lo, u64 hi, Border border,
-                          u64 offset) {
-  for (;;) {
-    const int shift = max(bits_of(hi - lo) - 11, 0);
-    clear_hist(S);
-    for (int i = threadIdx.x; i < n; i += kCutThreads) {
-      const u64 rank = S.cand[i];
-      const u64 key = INDEX ? rank & ((1ull << w.ibits) - 1) : rank;
-      if (rank <= last && key >= lo && key <= hi)
-        atomicAdd(&S.hist[(key - lo) >> shift], weight_of<MASS>(w, key_logit<ES>(w, rank)));
-    }
-    const Crossing c = find_crossing(S, border, offset);
-    if (c.bin < 0) return kNone;
-    border = Border{Border::kFixed, c.border, 0.0};
-    offset += c.before;
-    lo += (u64)c.bin << shift;
-    if (shift == 0) return lo;
-    hi = min(hi, lo + (1ull << shift) - 1);
-  }
+// The key of rank of logit x at index e, rising in a row's order.
+template <int ES>
+__device__ __forceinline__ u64 key_of(float x, int e, int ibits) {
+  return ((u64)((ES == 2 ? 0xffffu : 0xffffffffu) - place<ES>(x)) << ibits) | (uint32_t)e;
 }
 
-// f(x, e) for every logit of the row.
-template <int ES, class F>
-__device__ __forceinline__ void each_logit(const RowView& w, F f) {
-  constexpr int kAhead = ES == 2 ? 4 : 2;
-  const int groups = (w.V + 7) >> 3;
-  for (int g0 = threadIdx.x; g0 < groups; g0 += kCutThreads * kAhead) {
-    RawGroup<ES, true> raw[kAhead];
+// A row and what its passes share; NT: threads of the workgroup.
+template <int ES, int NT, bool SMALL>
+struct CutRow {
+  using B = Bins<ES>;
+  static constexpr int kWavesNT = NT / 64;
+  static constexpr int kPer = (B::kN + NT - 1) / NT;  // bins of a thread
+
+  CutShared<SMALL>& S;
+  const char* lg;
+  int V, ibits, frac;
+  float m;
+  double s;  // log2(e) / T
+
+  // by slot
+  __device__ __forceinline__ uint32_t* counts() const { return reinterpret_cast<uint32_t*>(S.bins); }
+  __device__ __forceinline__ double* weights() const { return reinterpret_cast<double*>(S.bins); }
+  __device__ __forceinline__ u64* masses() const { return S.bins + (B::kSlots + 1) / 2; }
+
+  __device__ __forceinline__ u64 rank_key(float x, int e) const { return key_of<ES>(x, e, ibits); }
+  __device__ __forceinline__ float key_logit(u64 key) const {
+    return value_at<ES>((ES == 2 ? 0xffffu : 0xffffffffu) - (uint32_t)(key >> ibits));
+  }
+  __device__ __forceinline__ u64 index_mask() const { return (1ull << ibits) - 1; }
+  // The key of the last place that a bin's logits can have.
+  __device__ __forceinline__ u64 bin_end(int bin) const { return rank_key(B::least(bin), 0) | index_mask(); }
+
+  // The weight of a logit, a whole number.
+  __device__ __forceinline__ double weight_of(float x) const {
+    return __builtin_rint(pow2(((double)x - (double)m) * s, frac));
+  }
+  __device__ __forceinline__ u64 mass_of(float x) const { return whole(weight_of(x)); }
+
+  // Whether logits of -2^7 and below (the last bin's) may have a weight.
+  __device__ __forceinline__ bool low_weighs() const { return ((double)m + 128.0) * s < frac + 2; }
+
+  // f(raw, e) for the groups of 8 logits from index e on that hold some of
+  // [first, last]; past the row's end -inf.
+  template <class F>
+  __device__ __forceinline__ void each_group(int first, int last, F f) const {
+    constexpr int kAhead = ES == 2 ? 4 : 2;
+    const int g1 = (last >> 3) + 1, full = V >> 3;
+    RawGroup<ES, true> next[kAhead];
+    auto load = [&](int g0) {
+      if (full > 0) {  // (without a condition on each, so that they are on their way together)
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int g = g0 + q * kCutThreads;
-      if (g < groups) raw[q] = load_end<ES>(w.lg, (int64_t)g * 8, w.V);
+        for (int q = 0; q < kAhead; ++q) next[q] = load_any<ES>(lg, (int64_t)min(g0 + q * NT, full - 1) * 8);
+      }
+      if (g1 > full) {  // the row's last group is not whole
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+          if (g0 + q * NT == full) next[q] = load_end<ES>(lg, (int64_t)full * 8, V);
+      }
+    };
+    int g0 = (first >> 3) + threadIdx.x;
+    if (g0 < g1) load(g0);
+    for (; g0 < g1; g0 += NT * kAhead) {
+      RawGroup<ES, true> raw[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) raw[q] = next[q];
+      if (g0 + NT * kAhead < g1) load(g0 + NT * kAhead);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (g0 + q * NT < g1) f(raw[q], (g0 + q * NT) * 8);
     }
+  }
+
+  __device__ __forceinline__ float block_max(float x) const {
+    x = wave_max_f(x);
+    if ((threadIdx.x & 63) == 0) S.wave_f[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float y = S.wave_f[0];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int g = g0 + q * kCutThreads;
-      if (g >= groups) break;
+    for (int w = 1; w < kWavesNT; ++w) y = fmaxf(y, S.wave_f[w]);
+    __syncthreads();
+    return y;
+  }
+
+  // Of the places in thread order (a thread has the values at(0), ..., at(n - 1)
+  // and, beside each, other(i)) the one at which the sum reaches the border, with
+  // the sum of the others up to and with it.  All threads call it; what at()
+  // reads is complete, and free when it returns.
+  template <class At, class Other>
+  __device__ __forceinline__ Crossing find_crossing(const Border& border, u64 offset, int place0, int n, At at,
+                                                    Other other) const {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    __syncthreads();
+    u64 v = 0, o = 0;
+    for (int i = 0; i < n; ++i) {
+      v += at(i);
+      o += other(i);
+    }
+    const u64 x = wave_scan_u64(v), y = wave_scan_u64(o);
+    if (lane == 63) {
+      S.wave[0][wave] = x;
+      S.wave[1][wave] = y;
+    }
+    if (t == 0) S.bin = -1;
+    __syncthreads();
+    u64 base = 0, total = 0, obase = 0;
+#pragma unroll
+    for (int w = 0; w < kWavesNT; ++w) {
+      base += w < wave ? S.wave[0][w] : 0;
+      obase += w < wave ? S.wave[1][w] : 0;
+      total += S.wave[0][w];
+    }
+    const u64 to = border.of(total) - offset;
+    u64 sum = base + x - v, through = obase + y - o;
+    if (sum < to && to <= sum + v) {
+      int i = 0;
+      for (;; ++i) {
+        const u64 one = at(i);
+        through += other(i);
+        if (to <= sum + one) break;
+        sum += one;
+      }
+      S.bin = place0 + i;
+      S.before = sum;
+      S.through = through;
+    }
+    __syncthreads();
+    const Crossing c{S.bin, S.before, to + offset, S.through};
+    __syncthreads();
+    return c;
+  }
+
+  __device__ __forceinline__ Crossing find_range(const Border& border, u64 offset) const {
+    constexpr int kMine = kRanges / NT;
+    const int t = threadIdx.x * kMine;
+    return find_crossing(border, offset, t, kMine, [&](int i) { return S.ranges[t + i]; }, [](int) { return (u64)0; });
+  }
+
+  __device__ __forceinline__ void clear_ranges() const {
+    for (int i = threadIdx.x; i < kRanges; i += NT) S.ranges[i] = 0;
+    __syncthreads();
+  }
+
+  // The same among the n <= 64 in `few`: each one's sum up to itself, the pairs
+  // shared out to the waves.
+  template <bool INDEX, bool MASS>
+  __device__ __forceinline__ u64 search_few(int n, const Border& border, u64 offset) const {
+    constexpr int kShare = 64 / kWavesNT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto key_of_place = [&](int j) { return INDEX ? S.few[j] & index_mask() : S.few[j]; };
+    if (threadIdx.x < n) {
+      S.few_mass[lane] = MASS ? mass_of(key_logit(S.few[lane])) : 1;
+      S.few_upto[lane] = 0;
+    }
+    __syncthreads();
+    const u64 key = lane < n ? key_of_place(lane) : 0, mine = lane < n ? S.few_mass[lane] : 0;
+    u64 upto = 0;
+#pragma unroll
+    for (int q = 0; q < kShare; ++q) {
+      const int j = wave * kShare + q;
+      if (j < n && key_of_place(j) <= key) upto += S.few_mass[j];
+    }
+    if (lane < n && upto) atomicAdd(&S.few_upto[lane], upto);
+    __syncthreads();
+    upto = lane < n ? S.few_upto[lane] : 0;
+    const u64 to = border.of(lane_u64(wave_scan_u64(mine), 63)) - offset;
+    const uint64_t at = __ballot(lane < n && upto >= to && upto - mine < to);
+    __syncthreads();  // (they are free)
+    return at ? lane_u64(key, __builtin_ctzll(at)) : kNone;
+  }
+
+  // Among the candidates in LDS with a key of rank up to `last`, the key (of
+  // rank, or the index) at which the sum of weights (or the count) reaches the
+  // border; kNone if it never does.  Keys lie in [lo, hi]; `offset` stands in
+  // front of them.
+  template <bool INDEX, bool MASS>
+  __device__ __forceinline__ u64 search_lds(int n, u64 last, u64 lo, u64 hi, Border border, u64 offset) const {
+    for (;;) {
+      if (threadIdx.x == 0) S.count = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += NT) {
+        const u64 rank = S.cand[i];
+        const u64 key = INDEX ? rank & index_mask() : rank;
+        if (rank <= last && key >= lo && key <= hi) {
+          const int at = atomicAdd(&S.count, 1);
+          if (at < 64) S.few[at] = rank;
+        }
+      }
+      __syncthreads();
+      if (S.count <= 64) return search_few<INDEX, MASS>(S.count, border, offset);
+      const int shift = max(bits_of(hi - lo) - kRangeBits, 0);
+      clear_ranges();
+      for (int i = threadIdx.x; i < n; i += NT) {
+        const u64 rank = S.cand[i];
+        const u64 key = INDEX ? rank & index_mask() : rank;
+        if (rank <= last && key >= lo && key <= hi)
+          atomicAdd(&S.ranges[(key - lo) >> shift], MASS ? mass_of(key_logit(rank)) : 1ull);
+      }
+      const Crossing c = find_range(border, offset);
+      if (c.bin < 0) return kNone;
+      border = Border{Border::kFixed, c.border, 0.0};
+      offset += c.before;
+      lo += (u64)c.bin << shift;
+      if (shift == 0) return lo;
+      hi = min(hi, lo + (1ull << shift) - 1);
+    }
+  }
+
+  // The index in [lo, hi] at which the sum, with `offset` in front, reaches the
+  // border: sums over ranges of indices, then inside the range.  pass(lo, hi, f) calls f(e, sum) for the
+  // groups of [lo, hi] with their sum; one(x, e) is the part of a single logit.
+  template <class Pass, class One>
+  __device__ __forceinline__ int search_index(int lo, int hi, Border border, u64 offset, Pass pass, One one) const {
+    for (;;) {
+      const int shift = max(bits_of((u64)(hi - lo)) - kRangeBits, 0);
+      clear_ranges();
+      if (shift >= 3) {  // (ranges of whole groups)
+        pass(lo, hi, [&](int e, double sum) {
+          if (sum > 0.0) atomicAdd(&S.ranges[(e - lo) >> shift], (u64)sum);
+        });
+      } else {
+        each_group(lo, hi, [&](const RawGroup<ES, true>& raw, int e) {
+          float x[8];
+          unpack_group<ES, true>(raw, x);
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q)
+            if (e + q >= lo && e + q <= hi) {
+              const double y = one(x[q], e + q);
+              if (y > 0.0) atomicAdd(&S.ranges[(e + q - lo) >> shift], (u64)y);
+            }
+        });
+      }
+      const Crossing c = find_range(border, offset);
+      if (c.bin < 0) return -1;
+      border = Border{Border::kFixed, c.border, 0.0};
+      offset += c.before;
+      lo += c.bin << shift;
+      if (shift == 0) return lo;
+      hi = min(hi, lo + (1 << shift) - 1);
+    }
+  }
+
+  // The logits from `floor` up for which take(key) holds gathered into LDS, as
+  // many as fit: how many there are.
+  template <class Take>
+  __device__ __forceinline__ int gather(float floor, Take take) const {
+    __syncthreads();
+    if (threadIdx.x == 0) S.count = 0;
+    __syncthreads();
+    const Floor<ES> low(floor);
+    each_group(0, V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+      if (!low.reached(raw)) return;
       float x[8];
-      unpack_group<ES, true>(raw[q], x);
+      unpack_group<ES, true>(raw, x);
+      uint32_t hits = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (g * 8 + e < w.V) f(x[e], g * 8 + e);
-    }
+      for (int q = 0; q < 8; ++q) hits |= x[q] >= floor ? 1u << q : 0u;
+      for (; hits; hits &= hits - 1) {
+        const int q = __builtin_ctz(hits);
+        const u64 key = rank_key(select8(x, q), e + q);
+        if (e + q >= V || !take(key)) continue;
+        const int at = atomicAdd(&S.count, 1);
+        if (at < kCand) S.cand[at] = key;
+      }
+    });
+    __syncthreads();
+    const int n = S.count;
+    __syncthreads();
+    return n;
   }
-}
+  static __device__ __forceinline__ float select8(const float (&x)[8], int q) {
+    const float a = q & 1 ? x[1] : x[0], b = q & 1 ? x[3] : x[2], c = q & 1 ? x[5] : x[4], d = q & 1 ? x[7] : x[6];
+    const float e = q & 2 ? b : a, f = q & 2 ? d : c;
+    return q & 4 ? f : e;
+  }
 
-// Candidates gathered into LDS, with the range of their keys.
-struct Gather {
-  u64 lo = kNone, hi = 0;
-  __device__ __forceinline__ void take(CutShared& S, u64 rank, u64 key) {
-    const int at = atomicAdd(&S.count, 1);
-    if (at < kCand) S.cand[at] = rank;
-    lo = min(lo, key);
-    hi = max(hi, key);
+  // The key of rank at which the weights (or the count) of the logits of one bin
+  // up to `last` reach the border.
+  template <bool MASS>
+  __device__ __forceinline__ u64 search_bin(int bin, u64 last, u64 border) const {
+    const float floor = B::least(bin);
+    u64 lo = bin > 0 ? bin_end(bin - 1) + 1 : 0, hi = min(last, bin_end(bin)), offset = 0;
+    hi = min(hi, rank_key(-INFINITY, 0) | index_mask());
+    int n = gather(floor, [&](u64 key) { return key >= lo && key <= hi; });
+    const Border to{Border::kFixed, border, 0.0};
+    while (n > kCand) {  // their keys in finer ranges, over the row again
+      const int shift = max(bits_of(hi - lo) - kRangeBits, 0);
+      clear_ranges();
+      each_group(0, V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+        float x[8];
+        unpack_group<ES, true>(raw, x);
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          const u64 key = rank_key(x[q], e + q);
+          if (key >= lo && key <= hi && e + q < V) atomicAdd(&S.ranges[(key - lo) >> shift], MASS ? mass_of(x[q]) : 1ull);
+        }
+      });
+      const Crossing c = find_range(to, offset);
+      if (c.bin < 0) return kNone;
+      offset += c.before;
+      lo += (u64)c.bin << shift;
+      hi = min(hi, lo + (1ull << shift) - 1);
+      n = gather(floor, [&](u64 key) { return key >= lo && key <= hi; });
+    }
+    return search_lds<false, MASS>(n, last, lo, hi, to, offset);
+  }
+
+  // The c-th logit, by its index, among those in [lo, hi] equal to the value of a
+  // bin: its key of rank.
+  __device__ __forceinline__ u64 search_equal(int lo, int hi, int bin, u64 c) const {
+    const float v = B::value(bin);
+    const int at = search_index(
+        lo, hi, Border{Border::kFixed, c, 0.0}, 0,
+        [&](int l, int h, auto f) {
+          each_group(l, h, [&](const RawGroup<ES, true>& raw, int e) {
+            float x[8];
+            unpack_group<ES, true>(raw, x);
+            int k = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) k += x[q] == v;
+            f(e, (double)k);
+          });
+        },
+        [&](float x, int) { return x == v ? 1.0 : 0.0; });
+    return rank_key(v, at);
   }
 };
-__device__ __forceinline__ void gather_begin(CutShared& S) {
-  if (threadIdx.x == 0) {
-    S.count = 0;
-    S.lo = kNone;
-    S.hi = 0;
-  }
-  __syncthreads();
-}
-__device__ __forceinline__ void gather_end(CutShared& S, const Gather& g) {
-  if (g.lo <= g.hi) {
-    atomicMin(&S.lo, g.lo);
-    atomicMax(&S.hi, g.hi);
-  }
-  __syncthreads();
-}
-
-// search_lds over the row itself: a histogram of all its logits, the logits of
-// the range found gathered into LDS, and so on there.  `span`: the first
-// histogram over ranks has its ranges evenly over logits from m down to m -
-// span (all below in the last).
-template <int ES, bool INDEX, bool MASS>
-__device__ __forceinline__ u64 search_row(CutShared& S, const RowView& w, u64 last, float span, Border border) {
-  const float inv = INDEX ? 0.f : fminf((float)(kBins - 1) / span, FLT_MAX);
-  const int ishift = max(w.ibits - 11, 0);
-  auto bin_of = [&](float x, int e) {
-    if constexpr (INDEX) return e >> ishift;
-    return (int)fminf((w.m - x) * inv, (float)(kBins - 1));
-  };
-  clear_hist(S);
-  if constexpr (INDEX) {  // a group's logits mostly have one range
-    u64 sum = 0;
-    int at = -1;
-    each_logit<ES>(w, [&](float x, int e) {
-      const int bin = bin_of(x, e);
-      if (bin != at) {
-        if (sum) atomicAdd(&S.hist[at], sum);
-        sum = 0;
-        at = bin;
-      }
-      if (rank_key<ES>(w, x, e) <= last) sum += weight_of<MASS>(w, x);
-    });
-    if (sum) atomicAdd(&S.hist[at], sum);
-  } else {
-    each_logit<ES>(w, [&](float x, int e) {
-      if (rank_key<ES>(w, x, e) <= last) {
-        const u64 q = weight_of<MASS>(w, x);
-        if (q) atomicAdd(&S.hist[bin_of(x, e)], q);
-      }
-    });
-  }
-  Crossing c = find_crossing(S, border, 0);
-  if (c.bin < 0) return kNone;
-  border = Border{Border::kFixed, c.border, 0.0};
-  u64 offset = c.before;
-  const int bin = c.bin;
-  gather_begin(S);
-  Gather g;
-  each_logit<ES>(w, [&](float x, int e) {
-    const u64 rank = rank_key<ES>(w, x, e);
-    if (rank <= last && bin_of(x, e) == bin) g.take(S, rank, INDEX ? (u64)e : rank);
-  });
-  gather_end(S, g);
-  u64 lo = S.lo, hi = S.hi;
-  int n = S.count;
-  while (n > kCand) {  // (many equal logits) the range's keys in finer ranges, over the row again
-    const int shift = max(bits_of(hi - lo) - 11, 0);
-    clear_hist(S);
-    each_logit<ES>(w, [&](float x, int e) {
-      const u64 rank = rank_key<ES>(w, x, e), key = INDEX ? (u64)e : rank;
-      if (rank <= last && key >= lo && key <= hi) {
-        const u64 q = weight_of<MASS>(w, x);
-        if (q) atomicAdd(&S.hist[(key - lo) >> shift], q);
-      }
-    });
-    c = find_crossing(S, border, offset);
-    if (c.bin < 0) return kNone;
-    offset += c.before;
-    lo += (u64)c.bin << shift;
-    hi = min(hi, lo + (1ull << shift) - 1);
-    gather_begin(S);
-    Gather h;
-    each_logit<ES>(w, [&](float x, int e) {
-      const u64 rank = rank_key<ES>(w, x, e), key = INDEX ? (u64)e : rank;
-      if (rank <= last && key >= lo && key <= hi) h.take(S, rank, key);
-    });
-    gather_end(S, h);
-    lo = max(lo, S.lo);
-    hi = min(hi, S.hi);
-    n = S.count;
-  }
-  return search_lds<ES, INDEX, MASS>(S, w, n, last, lo, hi, border, offset);
-}
-
-// Reductions over the workgroup, the same in every thread.
-__device__ __forceinline__ float block_max_f(CutShared& S, float x) {
-  x = wave_max_f(x);
-  if ((threadIdx.x & 63) == 0) S.wave_f[threadIdx.x >> 6] = x;
-  __syncthreads();
-  float y = S.wave_f[0];
-#pragma unroll
-  for (int w = 1; w < kCutWaves; ++w) y = fmaxf(y, S.wave_f[w]);
-  __syncthreads();
-  return y;
-}
-__device__ __forceinline__ double block_sum_d(CutShared& S, double x) {
-  x = wave_total_d(x);
-  if ((threadIdx.x & 63) == 0) S.wave_d[threadIdx.x >> 6] = x;
-  __syncthreads();
-  double y = 0.0;
-#pragma unroll
-  for (int w = 0; w < kCutWaves; ++w) y += S.wave_d[w];
-  __syncthreads();
-  return y;
-}
 
 // ----------------------------------------------------------------- finish --
-template <int ES, bool DRAW>
-__global__ __launch_bounds__(kCutThreads) void cut_finish_kernel(CutParams P) {
-  __shared__ CutShared S;
+template <int ES, int NT, bool SMALL, bool DRAW>
+__global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
+  using B = Bins<ES>;
+  using Row = CutRow<ES, NT, SMALL>;
+  __shared__ CutShared<SMALL> S;
   const int i = blockIdx.x, tid = threadIdx.x;
   const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
   const Cut cut = cut_of(P, b);
   const float u = DRAW ? P.uniforms[i] : 0.f;
-  RowView w;
-  w.lg = row_of(P, b, r, ES);
-  w.V = P.V;
-  w.ibits = P.ibits;
-  w.frac = P.frac;
+  Row w{S, row_of(P, b, r, ES), P.V, P.ibits, P.frac, 0.f, 0.0};
   auto end = [&](int token, u64 last) {  // of the row
     if (tid == 0) {
       if constexpr (DRAW)
@@ -543,176 +667,326 @@ __global__ __launch_bounds__(kCutThreads) void cut_finish_kernel(CutParams P) {
   };
   if (!cut.ok || !w.lg || (DRAW && !(u >= 0.0f && u < 1.0f))) return end(-1, kCutBad);
   if (!DRAW && (cut.greedy || cut.all)) return end(-1, kCutAll);
-  const CutRecord* rec = P.rec + (int64_t)i * P.nseg;
+
+  if (DRAW && cut.greedy) {
+    VI best{-INFINITY, INT_MAX};
+    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+      float x[8];
+      unpack_group<ES, true>(raw, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) best = vi_pick(best, VI{x[q], e + q});
+    });
+    best = wave_argmax(vi_floor(best, 0));  // (a row with nothing above -inf: 0)
+    if ((tid & 63) == 0) {
+      S.wave_f[tid >> 6] = best.v;
+      S.wave_u[tid >> 6] = (uint32_t)best.i;
+    }
+    __syncthreads();
+    if (tid != 0) return;
+    for (int k = 1; k < Row::kWavesNT; ++k) best = vi_pick(best, VI{S.wave_f[k], (int)S.wave_u[k]});
+    return end(best.i, 0);
+  }
+
+  // the counts of the bins, the largest logit, and whether there is a NaN
+  const bool counted = !SMALL && (cut.k > 0 || cut.p < 1.0f);
+  uint32_t* counts = w.counts();
+  const int j0 = tid * Row::kPer, jn = max(0, min(Row::kPer, B::kN - j0));  // this thread's bins
   float m = -INFINITY;
-  bool nan = false;
-  for (int j = tid; j < P.nseg; j += kCutThreads) {
-    const CutRecord q = rec[j];
-    m = fmaxf(m, q.m);
-    nan |= q.nan != 0;
-  }
-  m = block_max_f(S, m);
-  nan = __syncthreads_or(nan);
-  if (cut.greedy ? m == -INFINITY : nan || !(fabsf(m) <= FLT_MAX)) return end(cut.greedy ? 0 : -1, kCutAll);
-  w.m = m;
-  w.top = place<ES>(m);
-  w.s = cut.greedy ? 0.0 : 1.4426950408889634074 / (double)cut.T;
-  const u64 index_mask = (1ull << w.ibits) - 1;
-  const float reach = (float)fmin((w.frac + 2) / fmax(w.s, 1e-300), (double)FLT_MAX);  // (no weight beyond)
-
-  if (DRAW && cut.all && !cut.greedy) {
-    // nothing left out: the segment from the segments' sums, then the token in it
-    auto units = [&](int j) { return (u64)ldexp(rec[j].s * pow2(((double)rec[j].m - (double)m) * w.s, 0), w.frac); };
-    int lo = 0, hi = P.nseg - 1;
-    u64 offset = 0;
-    Border at{Border::kAbove, 0, (double)u};
-    for (;;) {
-      const int shift = max(bits_of((u64)(hi - lo)) - 11, 0);
-      clear_hist(S);
-      for (int j = lo + tid; j <= hi; j += kCutThreads) atomicAdd(&S.hist[(j - lo) >> shift], units(j));
-      const Crossing c = find_crossing(S, at, offset);
-      at = Border{Border::kFixed, c.border, 0.0};
-      offset += c.before;
-      lo += c.bin << shift;
-      if (shift == 0) break;
-      hi = min(hi, lo + (1 << shift) - 1);
-    }
-    // in the segment the weights count from its own largest, 4096 of them in 62 bits
-    constexpr int kSegFrac = 50;
-    const double far = pow2(((double)rec[lo].m - (double)m) * w.s, 0);
-    const double rest = ldexp((double)(at.fixed - offset), kSegFrac - w.frac) / far;
-    w.m = rec[lo].m;
-    w.top = place<ES>(w.m);
-    w.frac = kSegFrac;
-    const int first = lo * kSeg, n = min(kSeg, P.V - first);
-    gather_begin(S);
-    u64 sum = 0;
-    for (int e = tid; e < n; e += kCutThreads) {
-      const float x = load_one<ES>(w.lg, first + e);
-      S.cand[e] = rank_key<ES>(w, x, first + e);
-      sum += weight_of<true>(w, x);
-    }
-    if (sum) atomicAdd(&S.hi, sum);
+  uint32_t big = 0, small = ~0u;
+  if (counted) {
+    for (int j = tid; j < B::kSlots; j += NT) counts[j] = 0;
     __syncthreads();
-    // (the segment's sum of rounded weights may fall short of the place found)
-    const u64 border = min(max((u64)ceil(fmin(rest, 0x1p62)), 1ull), S.hi);
+    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int) {
+      if constexpr (ES == 2) {
+        uint32_t slot[8];
+        slots8(raw, slot);
+        u16x2 mag{0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t two = raw.v[q] & 0x7fff7fffu;
+          mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, two));
+        }
+        big = max(big, (uint32_t)max(mag.x, mag.y) << 16);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) atomicAdd(&counts[slot[q]], 1u);
+      } else {
+        float x[8];
+        unpack_group<ES, true>(raw, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          m = fmaxf(m, x[q]);
+          big = max(big, __float_as_uint(x[q]) & 0x7fffffffu);
+          atomicAdd(&counts[B::slot(x[q])], 1u);
+        }
+      }
+    });
     __syncthreads();
-    const u64 e = search_lds<ES, true, true>(S, w, n, kNone, first, first + n - 1, Border{Border::kFixed, border, 0.0}, 0);
-    return end((int)e, 0);
+    if (tid == 0) {
+      counts[0] += counts[B::kHalf];  // zeros and the like of either sign
+      counts[B::kHalf] = 0;
+      const int last = B::slot_of(B::kN - 1);
+      counts[last] -= (8 - (P.V & 7)) & 7;  // (what the row's last group was filled up with)
+    }
+    __syncthreads();
+    if constexpr (ES == 2) {  // the largest logit from the first bin, where that is one value
+      int first = B::kN;
+      for (int j = jn - 1; j >= 0; --j)
+        if (counts[B::slot_of(j0 + j)]) first = j0 + j;
+      first = (int)-w.block_max((float)-first);
+      if (B::single(first)) m = B::value(first);
+    }
   }
+  if (!(m > -INFINITY) && (ES == 2 || !counted)) {
+    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+      float x[8];
+      unpack_group<ES, true>(raw, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t mag = __float_as_uint(x[q]) & 0x7fffffffu;
+        m = fmaxf(m, x[q]);
+        big = max(big, mag);
+        small = min(small, mag);
+        if (SMALL && e + q < P.V) S.cand[e + q] = w.rank_key(x[q], e + q);
+      }
+    });
+  }
+  w.m = w.block_max(m);
+  const bool nan = __syncthreads_or(big > 0x7f800000u);
+  if (nan || !(fabsf(w.m) <= FLT_MAX)) return end(-1, kCutAll);
+  w.s = 1.4426950408889634074 / (double)cut.T;
+  auto count_of = [&](int j) { return (u64)counts[B::slot_of(j0 + j)]; };
 
-  const int k = cut.greedy ? 1 : cut.k;
-  const float p = cut.greedy ? 1.0f : cut.p;
-  // how far (in places) from the largest logit the kept ones can be
-  uint32_t min_far = ~0u;  // by min_p
-  if (!cut.greedy && cut.mn > 0.0f) {
-    const double low = (double)m + (double)cut.T * log((double)cut.mn);
+  u64 last = kNone;  // the key of the last kept token
+  // the candidates in LDS, where they are all that can be kept, and the range of their keys
+  bool held = SMALL;
+  int n = SMALL ? P.V : 0;
+  const u64 lo = w.rank_key(w.m, 0);
+  u64 hi = w.rank_key(-INFINITY, 0) | w.index_mask();
+  // of the logits in the bin of the last kept token: how many stay, by their
+  // index, where the last one's index is still to be found (the bin, or -1)
+  int tie_bin = -1;
+  u64 ties = 0;
+  int k_bin = B::kN;
+  u64 k_rest = 0;
+  if (cut.k > 0) {
+    const Border to{Border::kFixed, (u64)cut.k, 0.0};
+    if constexpr (SMALL) {
+      last = w.template search_lds<false, false>(n, kNone, lo, hi, to, 0);
+    } else {
+      const Crossing c = w.find_crossing(to, 0, j0, jn, count_of, count_of);
+      k_bin = c.bin;
+      k_rest = (u64)cut.k - c.before;
+      last = w.bin_end(k_bin);
+      if (c.through <= kCand) {
+        n = w.gather(B::least(k_bin), [](u64) { return true; });
+        held = true;
+        hi = min(hi, last);
+        if (n > cut.k)
+          last = w.template search_lds<false, false>(n, kNone, k_bin > 0 ? w.bin_end(k_bin - 1) + 1 : 0, hi, to,
+                                                     c.before);
+      } else if (c.through > (u64)cut.k) {
+        if (B::single(k_bin)) {
+          tie_bin = k_bin;
+          ties = k_rest;
+        } else {
+          last = w.template search_bin<false>(k_bin, kNone, k_rest);
+        }
+      }
+    }
+  }
+  if (cut.p < 1.0f) {
+    const Border share{Border::kShare, 0, (double)cut.p};
+    if (held) {
+      last = min(last, w.template search_lds<false, true>(n, last, lo, hi, share, 0));
+    } else if constexpr (!SMALL) {
+      // the masses of bins with several values, logit by logit (those of -2^7 and below mostly have none)
+      u64* masses = w.masses();
+      if (tid < 3) S.special[tid] = 0;
+      if constexpr (ES == 4)
+        for (int j = tid; j < B::kSlots; j += NT) masses[j] = 0;
+      const bool low = counts[B::slot_of(B::kN - 1)] != 0 && w.low_weighs();
+      const bool some = ES == 4 || counts[B::slot_of(0)] != 0 || counts[B::slot_of(B::kMid)] != 0 || low;
+      __syncthreads();
+      if (some)
+        w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+          float x[8];
+          unpack_group<ES, true>(raw, x);
+#pragma unroll 2
+          for (int q = 0; q < 8; ++q) {
+            const int bin = B::of(x[q]);
+            if (!B::single(bin) && w.rank_key(x[q], e + q) <= last) {
+              const u64 y = w.mass_of(x[q]);
+              if (y) atomicAdd(ES == 4 ? &masses[B::slot_of(bin)] : &S.special[bin == 0 ? 0 : bin == B::kMid ? 1 : 2], y);
+            }
+          }
+        });
+      auto mass = [&](int j) -> u64 {
+        const int bin = j0 + j;
+        if constexpr (ES == 4) return masses[B::slot_of(bin)];
+        if (!B::single(bin)) return S.special[bin == 0 ? 0 : bin == B::kMid ? 1 : 2];
+        const u64 c = bin < k_bin ? counts[B::slot_of(bin)] : bin == k_bin ? k_rest : 0;
+        return c ? c * w.mass_of(B::value(bin)) : 0;
+      };
+      const Crossing c = w.find_crossing(share, 0, j0, jn, mass, count_of);
+      const u64 rest = c.border - c.before;
+      u64 one = 0, stay = 0;
+      if (B::single(c.bin)) {  // (of equal logits as many as reach it)
+        one = w.mass_of(B::value(c.bin));
+        stay = (rest + one - 1) / one;
+      }
+      if (c.through <= kCand) {
+        n = w.gather(B::least(c.bin), [&](u64 key) { return key <= last; });
+        held = true;
+        hi = min(hi, w.bin_end(c.bin));
+        const u64 from = c.bin > 0 ? w.bin_end(c.bin - 1) + 1 : 0;
+        last = min(last, one ? w.template search_lds<false, false>(n, last, from, hi, Border{Border::kFixed, stay, 0.0}, 0)
+                             : w.template search_lds<false, true>(n, last, from, hi, Border{Border::kFixed, rest, 0.0}, 0));
+        tie_bin = -1;
+      } else if (one) {
+        if (c.bin < k_bin) {  // (in the k-th token's bin the rest of that is known)
+          last = w.bin_end(c.bin);
+          tie_bin = -1;
+        }
+        if (stay < counts[B::slot_of(c.bin)]) {
+          tie_bin = c.bin;
+          ties = stay;
+        }
+      } else {
+        last = w.template search_bin<true>(c.bin, last, rest);
+        tie_bin = -1;
+      }
+    }
+  }
+  if (cut.mn > 0.0f) {
+    const double low = (double)w.m + (double)cut.T * log((double)cut.mn);
     const float f = fmaxf(__double2float_ru(low), -FLT_MAX);
     uint32_t q = place<ES>(f);
     if (ES == 2 && value_at<2>(q) < f) ++q;  // (the bf16 values not below it)
-    min_far = w.top - min(q, w.top);
-  }
-  // by the k-th largest cell, or where only the mass bounds the row, by a number of cells that mostly hold it
-  const float* cells = P.cells + (int64_t)i * P.nseg * 64;
-  const int ncell = P.nseg * 64;
-  const int want = k > 0 ? k : p < 1.0f ? min(kGuess, ncell) : 0;
-  uint32_t cell_far = ~0u;
-  if (want > 0 && want <= ncell) {
-    float least = INFINITY;
-    for (int c = tid; c < ncell; c += kCutThreads) {
-      const float x = cells[c];
-      least = fminf(least, x > -INFINITY ? x : INFINITY);
-    }
-    least = -block_max_f(S, -least);
-    const float inv = fminf((float)(kBins - 1) / (m - least), FLT_MAX);  // (0 / 0 for equal cells: range 0)
-    clear_hist(S);
-    auto bin_of = [&](float x) { return (int)fmaxf(fminf((m - x) * inv, (float)(kBins - 1)), 0.f); };
-    for (int c = tid; c < ncell; c += kCutThreads) atomicAdd(&S.hist[bin_of(cells[c])], 1ull);
-    const Crossing c = find_crossing(S, Border{Border::kFixed, (u64)want, 0.0}, 0);
-    if (tid == 0) S.far = 0;
-    __syncthreads();
-    uint32_t far = 0;
-    for (int j = tid; j < ncell; j += kCutThreads)
-      if (bin_of(cells[j]) <= c.bin) far = max(far, w.top - place<ES>(cells[j]));
-    if (far) atomicMax(&S.far, far);
-    __syncthreads();
-    cell_far = S.far;
-  }
-  // (a top_p of a top_k is a share of all its tokens, min_p or not)
-  const bool by_min = !(k > 0 && p < 1.0f);
-  const uint32_t far = by_min ? min(cell_far, min_far) : cell_far;
-  bool held = false;
-  gather_begin(S);
-  if (far != ~0u) {
-    Gather g;
-    for (int c = tid; c < ncell; c += kCutThreads) {
-      const float x = cells[c];
-      if (!(x >= -FLT_MAX) && !(x == m)) continue;
-      if (w.top - place<ES>(x) > far) continue;
-      const int s0 = (c >> 6) * kSeg + (c & 63) * 8;
-      RawGroup<ES, true> raw[kSegGroups];
-#pragma unroll
-      for (int q = 0; q < kSegGroups; ++q)
-        raw[q] = s0 + q * 512 < P.V ? load_end<ES>(w.lg, (int64_t)s0 + q * 512, P.V) : neg_inf_group<ES, true>();
-#pragma unroll 1
-      for (int q = 0; q < kSegGroups; ++q) {
-        float y[8];
-        unpack_group<ES, true>(raw[q], y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (y[e] <= m && w.top - place<ES>(y[e]) <= far && s0 + q * 512 + e < P.V) {
-            const u64 key = rank_key<ES>(w, y[e], s0 + q * 512 + e);
-            g.take(S, key, key);
-          }
-      }
-    }
-    gather_end(S, g);
-    held = S.count <= kCand;
-  }
-  __syncthreads();
-  const int n = S.count;
-  const u64 lo = S.lo, hi = S.hi;
-  __syncthreads();
-
-  u64 last = held ? hi : kNone;  // the rank of the last kept token
-  if (k > 0) {
-    const Border at{Border::kFixed, (u64)k, 0.0};
-    if (!held)
-      last = search_row<ES, false, false>(S, w, cut.greedy ? index_mask : kNone, reach, at);
-    else if (n > k)
-      last = search_lds<ES, false, false>(S, w, n, kNone, lo, hi, at, 0);
-  }
-  if (cut.greedy) return end((int)(last & index_mask), 0);
-  if (p < 1.0f) {
-    u64 at = kNone;
-    if (k > 0) {
-      const Border border{Border::kShare, 0, (double)p};
-      at = held ? search_lds<ES, false, true>(S, w, n, last, lo, hi, border, 0)
-                : search_row<ES, false, true>(S, w, last, reach, border);
-    } else {
-      if (held) {
-        double total = 0.0;
-        for (int j = tid; j < P.nseg; j += kCutThreads)
-          total += rec[j].s * pow2(((double)rec[j].m - (double)m) * w.s, 0);
-        total = ldexp(block_sum_d(S, total), w.frac);
-        const Border border{Border::kFixed, max((u64)ceil((double)p * total), 1ull), 0.0};
-        at = search_lds<ES, false, true>(S, w, n, kNone, lo, hi, border, 0);
-      }
-      // (not among the candidates: behind them, which matters where min_p did not bound them)
-      if (at == kNone && !(held && far == min_far)) {
-        at = search_row<ES, false, true>(S, w, kNone, reach, Border{Border::kShare, 0, (double)p});
-        last = kNone;
-        held = false;
-      }
-    }
+    const u64 at = ((u64)((ES == 2 ? 0xffffu : 0xffffffffu) - q) << w.ibits) | w.index_mask();
+    if (tie_bin >= 0 && at < w.rank_key(B::value(tie_bin), 0)) tie_bin = -1;
     last = min(last, at);
   }
-  if (min_far != ~0u) last = min(last, ((u64)min_far << w.ibits) | index_mask);
-  if constexpr (!DRAW) return end(0, last);
-  const Border at{Border::kAbove, 0, (double)u};
-  const u64 e = held ? search_lds<ES, true, true>(S, w, n, last, 0, (u64)P.V - 1, at, 0)
-                     : search_row<ES, true, true>(S, w, last, 0.f, at);
-  end((int)e, 0);
+  // (a draw finds the last index together with its sums, where it goes by ranges of whole groups)
+  const int shift = max(w.ibits - kRangeBits, 0);
+  if (!SMALL && tie_bin >= 0 && (!DRAW || shift < 3)) {
+    last = w.search_equal(0, P.V - 1, tie_bin, ties);
+    tie_bin = -1;
+  }
+  if constexpr (!DRAW) return end(0, min(last, (u64)kCutAll - 1));
+
+  const Border above{Border::kAbove, 0, (double)u};
+  if (held) return end((int)w.template search_lds<true, true>(n, last, 0, (u64)P.V - 1, above, 0), 0);
+  if constexpr (!SMALL) {
+    const float floor = last == kNone ? -INFINITY : w.key_logit(last);
+    auto one = [&](float x, int e) { return w.rank_key(x, e) <= last ? w.weight_of(x) : 0.0; };
+    int token;
+    if constexpr (ES == 2) {
+      // the weight of each bin, 0 behind the last kept one's and for bins of
+      // several values; of the last kept one it stands up to the last index
+      const int end_bin = B::of(floor);
+      const int end_at = last == kNone || !B::single(end_bin) ? INT_MAX - 8 : (int)(last & w.index_mask());
+      double* weights = w.weights();
+      __syncthreads();
+      // whether some of a bin of several values may stay, with a weight
+      const bool low = end_bin == B::kN - 1 && w.low_weighs();
+      const bool odd = __syncthreads_or(
+          counted ? counts[B::slot_of(0)] != 0 || counts[0] != 0 || (low && counts[B::slot_of(B::kN - 1)] != 0)
+                  : w.m >= 128.0f || small < (B::kLo << B::kShift) || (low && big >= (B::kHi << B::kShift)));
+      for (int j = tid; j < B::kN; j += NT)
+        weights[B::slot_of(j)] = j <= end_bin && j != tie_bin && B::single(j) ? w.weight_of(B::value(j)) : 0.0;
+      if (tid == 0) weights[B::kHalf] = 0.0;
+      const double end_weight = B::single(end_bin) ? w.weight_of(floor) : 0.0;
+      const Floor<2> kept(floor);
+      auto sum_of = [&](const RawGroup<2, true>& raw, const uint32_t (&slot)[8], int e) {
+        double sum = 0.0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum += weights[slot[q]];
+        if (odd) {
+          float x[8];
+          unpack_group<2, true>(raw, x);
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q)
+            if (!B::single(B::of(x[q]))) sum += one(x[q], e + q);
+        }
+        return sum;
+      };
+      auto pass = [&](int l, int h, auto f) {
+        w.each_group(l, h, [&](const RawGroup<2, true>& raw, int e) {
+          if (!kept.reached(raw)) return;
+          uint32_t slot[8];
+          slots8(raw, slot);
+          double sum = sum_of(raw, slot, e);
+          if (e + 7 > end_at) {
+            float x[8];
+            unpack_group<2, true>(raw, x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sum -= x[q] == floor && e + q > end_at ? end_weight : 0.0;
+          }
+          f(e, sum);
+        });
+      };
+      if (tie_bin >= 0) {
+        // the sums without the last bin's logits, and those counted beside
+        uint32_t* equal = reinterpret_cast<uint32_t*>(S.cand);
+        for (int j = tid; j < kRanges; j += NT) equal[j] = 0;
+        w.clear_ranges();
+        const uint32_t end_slot = (uint32_t)B::slot_of(tie_bin);
+        w.each_group(0, P.V - 1, [&](const RawGroup<2, true>& raw, int e) {
+          if (!kept.reached(raw)) return;
+          uint32_t slot[8], same = 0;
+          slots8(raw, slot);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) same += slot[q] == end_slot;
+          const double sum = sum_of(raw, slot, e);
+          if (sum > 0.0) atomicAdd(&S.ranges[e >> shift], (u64)sum);
+          if (same) atomicAdd(&equal[e >> shift], same);
+        });
+        constexpr int kMine = kRanges / NT;
+        const int t = tid * kMine;
+        const Crossing c = w.find_crossing(Border{Border::kFixed, ties, 0.0}, 0, t, kMine,
+                                           [&](int j) { return (u64)equal[t + j]; }, [](int) { return (u64)0; });
+        const u64 stay = ties - c.before, weight = (u64)end_weight;
+        const Crossing d = w.find_crossing(
+            above, 0, t, kMine,
+            [&](int j) { return S.ranges[t + j] + weight * (t + j < c.bin ? equal[t + j] : t + j == c.bin ? stay : 0); },
+            [](int) { return (u64)0; });
+        // what is left lies in a range each: its logits one by one
+        const int size = 1 << shift, l = c.bin << shift, l2 = d.bin << shift;
+        last = w.search_equal(l, min(P.V - 1, l + size - 1), tie_bin, stay);
+        token = w.search_index(l2, min(P.V - 1, l2 + size - 1), Border{Border::kFixed, d.border, 0.0}, d.before,
+                               [&](int a, int z, auto f) {
+                                 w.each_group(a, z, [&](const RawGroup<2, true>& raw, int e) {
+                                   float x[8];
+                                   unpack_group<2, true>(raw, x);
+                                   double sum = 0.0;
+#pragma unroll 1
+                                   for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
+                                   f(e, sum);
+                                 });
+                               },
+                               one);
+      } else {
+        token = w.search_index(0, P.V - 1, above, 0, pass, one);
+      }
+    } else {
+      const Floor<4> kept(floor);
+      token = w.search_index(
+          0, P.V - 1, above, 0,
+          [&](int l, int h, auto f) {
+            w.each_group(l, h, [&](const RawGroup<4, true>& raw, int e) {
+              if (!kept.reached(raw)) return;
+              float x[8];
+              unpack_group<4, true>(raw, x);
+              double sum = 0.0;
+#pragma unroll 2
+              for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
+              f(e, sum);
+            });
+          },
+          one);
+    }
+    end(token, 0);
+  }
 }
 
 // --------------------------------------------------------------- truncate --
@@ -724,16 +998,6 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
   const char* src = P.logits + ((int64_t)b * P.req + (int64_t)r * P.row) * ES;
   char* dst = P.out + ((int64_t)b * P.out_req + (int64_t)r * P.out_row) * ES;
   if (last == kCutAll && src == dst) return;
-  RowView w;
-  w.ibits = P.ibits;
-  w.top = 0;
-  if (last < kCutAll) {
-    float m = -INFINITY;
-    const CutRecord* rec = P.rec + (int64_t)i * P.nseg;
-    for (int j = threadIdx.x & 63; j < P.nseg; j += 64) m = fmaxf(m, rec[j].m);
-    w.m = wave_max_f(m);
-    w.top = place<ES>(w.m);
-  }
   const float fill = last == kCutBad ? __builtin_nanf("") : -INFINITY;
   const int64_t e1 = min((int64_t)P.V, ((int64_t)chunk + 1) * kCutChunkSegs * kSeg);
   for (int64_t e = (int64_t)chunk * kCutChunkSegs * kSeg + threadIdx.x * 8; e < e1; e += kWG * 8) {
@@ -743,7 +1007,7 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
     unpack_group<ES, true>(g, x);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const bool keep = last == kCutAll || (last < kCutAll && rank_key<ES>(w, x[q], (int)e + q) <= last);
+      const bool keep = last == kCutAll || (last < kCutAll && key_of<ES>(x[q], (int)e + q, P.ibits) <= last);
       some |= !keep;
       x[q] = keep ? x[q] : fill;
     }
@@ -752,20 +1016,24 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
   }
 }
 
+template <int ES, bool DRAW>
+static hipError_t launch_rows(const CutParams& P, unsigned rows, hipStream_t stream) {
+  if (P.V <= kCand)
+    hipLaunchKernelGGL((cut_kernel<ES, 256, true, DRAW>), dim3(rows), dim3(256), 0, stream, P);
+  else if (rows <= 256)
+    hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW>), dim3(rows), dim3(1024), 0, stream, P);
+  else
+    hipLaunchKernelGGL((cut_kernel<ES, 512, false, DRAW>), dim3(rows), dim3(512), 0, stream, P);
+  return hipGetLastError();
+}
+
 template <int ES>
 static hipError_t launch_cut_typed(const CutParams& P, hipStream_t stream) {
-  const unsigned rows = (unsigned)(P.B * P.R), chunks = rows * (unsigned)P.C;
-  hipLaunchKernelGGL((cut_stats_kernel<ES>), dim3(chunks), dim3(kWG), 0, stream, P);
-  hipError_t e = hipGetLastError();
+  const unsigned rows = (unsigned)(P.B * P.R);
+  if (P.tokens) return launch_rows<ES, true>(P, rows, stream);
+  const hipError_t e = launch_rows<ES, false>(P, rows, stream);
   if (e != hipSuccess) return e;
-  if (P.tokens) {
-    hipLaunchKernelGGL((cut_finish_kernel<ES, true>), dim3(rows), dim3(kCutThreads), 0, stream, P);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL((cut_finish_kernel<ES, false>), dim3(rows), dim3(kCutThreads), 0, stream, P);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((truncate_kernel<ES>), dim3(chunks), dim3(kWG), 0, stream, P);
+  hipLaunchKernelGGL((truncate_kernel<ES>), dim3(rows * (unsigned)P.C), dim3(kWG), 0, stream, P);
   return hipGetLastError();
 }
 

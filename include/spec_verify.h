@@ -772,7 +772,8 @@ typedef struct {
   int32_t dtype;               /* spec_dtype of all four tensors */
   const double* inv_freq;      /* device [rot_dim / 2] */
   double scale;                /* finite */
-  const int32_t* positions;    /* device [N] */
+  const void* positions;       /* device [N], int32_t or int64_t */
+  int32_t wide_positions;      /* int64_t, as an expansion's out_positions are */
   const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
   int64_t q_token_stride, q_head_stride;  /* elements, >= 0 */
   const void* k;               /* device [N, k_heads, head_dim] */
@@ -840,7 +841,8 @@ typedef struct {
   int32_t interleaved;
   const double* inv_freq;      /* device [rot_dim / 2] */
   double scale;                /* finite */
-  const int32_t* positions;    /* device [N] */
+  const void* positions;       /* device [N], int32_t or int64_t */
+  int32_t wide_positions;      /* int64_t, as an expansion's out_positions are */
   int32_t q_heads;             /* 0..1024 */
   const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
   int64_t q_token_stride, q_head_stride;

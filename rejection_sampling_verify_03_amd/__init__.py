@@ -178,6 +178,7 @@ class SpecRopeArgs(ctypes.Structure):
         ("N", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("inv_freq", ctypes.c_void_p), ("scale", ctypes.c_double), ("positions", ctypes.c_void_p),
+        ("wide_positions", ctypes.c_int32),
         ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
         ("k", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
         ("q_out", ctypes.c_void_p), ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
@@ -203,7 +204,7 @@ class SpecKV4WriteArgs(ctypes.Structure):
         ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
         ("slots", ctypes.c_void_p),
         ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
-        ("scale", ctypes.c_double), ("positions", ctypes.c_void_p),
+        ("scale", ctypes.c_double), ("positions", ctypes.c_void_p), ("wide_positions", ctypes.c_int32),
         ("q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
         ("q_head_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p), ("q_out_token_stride", ctypes.c_int64),
         ("q_out_head_stride", ctypes.c_int64),
@@ -1286,11 +1287,16 @@ def _heads(t, N, dim, dtype, dev, name):
     return t.shape[1], t.data_ptr(), t.stride(0), t.stride(1)
 
 
+def _positions(t, N, dev):
+    """The address of positions [N], int32 or int64, and whether they are int64."""
+    wide = t.dtype == _torch().int64
+    return _want(t, t.dtype if wide else _torch().int32, (N,), dev, "positions"), wide
+
+
 def rope_args(q, k, positions, rope, q_out, k_out):
     """Fill a SpecRopeArgs (no copies): q, k and their outputs [N, heads,
     head_dim] with unit stride along head_dim (k and k_out may be None),
-    positions [N] int32."""
-    torch = _torch()
+    positions [N] int32 or int64."""
     if q.dim() != 3:
         raise ValueError("q must be [N, heads, head_dim], contiguous along head_dim")
     dev = _gpu_device(q)
@@ -1307,14 +1313,14 @@ def rope_args(q, k, positions, rope, q_out, k_out):
         hko, kop, ko0, ko1 = _heads(k_out, N, dim, q.dtype, dev, "k_out")
     if hqo != hq or hko != hk:
         raise ValueError("the outputs must have the inputs' shapes")
-    return SpecRopeArgs(N, hq, hk, dim, rope.rot_dim, rope.interleaved, dt, rope.ptr, rope.scale,
-                        _want(positions, torch.int32, (N,), dev, "positions"), qp, q0, q1, kp, k0, k1, qop, qo0, qo1,
-                        kop, ko0, ko1)
+    at, wide = _positions(positions, N, dev)
+    return SpecRopeArgs(N, hq, hk, dim, rope.rot_dim, rope.interleaved, dt, rope.ptr, rope.scale, at, wide, qp, q0, q1,
+                        kp, k0, k1, qop, qo0, qo1, kop, ko0, ko1)
 
 
 def rope(q, k, positions, rope, out=None, stream=None):
     """Queries and keys [N, heads, head_dim] (bfloat16 or float32; k may be
-    None) turned to positions [N] int32 as `rope`, a Rope, says.  Returns (q,
+    None) turned to positions [N] int32 or int64 as `rope`, a Rope, says.  Returns (q,
     k), new tensors or those of `out`, a pair which may be (q, k) themselves."""
     torch = _torch()
     dev = _gpu_device(q)
@@ -1333,7 +1339,7 @@ def rope(q, k, positions, rope, out=None, stream=None):
 def kv4_write_args(cache, key, value, slots, positions=None, rope=None, q=None, q_out=None):
     """Fill a SpecKV4WriteArgs (no copies): key and value [N, heads, head_dim]
     with unit stride along head_dim, slots [N] int64 (-1: not written); with a
-    Rope the keys are turned to positions [N] int32 first, and queries q [N,
+    Rope the keys are turned to positions [N] int32 or int64 first, and queries q [N,
     q_heads, head_dim] into q_out."""
     torch = _torch()
     N, dev = slots.shape[0], cache.device
@@ -1354,7 +1360,7 @@ def kv4_write_args(cache, key, value, slots, positions=None, rope=None, q=None, 
         if rope.inv_freq.device != dev:
             raise ValueError("all tensors must be on the same GPU")
         a.rot_dim, a.interleaved, a.inv_freq, a.scale = rope.rot_dim, rope.interleaved, rope.ptr, rope.scale
-        a.positions = _want(positions, torch.int32, (N,), dev, "positions")
+        a.positions, a.wide_positions = _positions(positions, N, dev)
     if q is not None:
         if rope is None:
             raise ValueError("queries are turned as a Rope says: none is given")
@@ -1369,7 +1375,7 @@ def kv4_write_args(cache, key, value, slots, positions=None, rope=None, q=None, 
 def rope_kv_write(cache, q, key, value, positions, slots, rope, q_out=None, stream=None):
     """rope() of queries [N, q_heads, head_dim] and keys, and kv_write() of the
     keys and values [N, heads, head_dim] into a KVCache4, in one launch: the
-    queries and keys turned to positions [N] int32, the keys (not rounded in
+    queries and keys turned to positions [N] int32 or int64 (an expansion's out_positions), the keys (not rounded in
     between) and values quantised into the cache at slots [N] int64 (-1 is
     skipped).  q may be None.  Returns the turned queries (q_out, which may be
     q itself)."""

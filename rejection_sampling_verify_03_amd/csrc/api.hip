@@ -356,12 +356,13 @@ bool cut_shape_ok(int32_t B, int32_t R, int32_t V) {
 }
 
 // The sizes, settings and workspace that a sampling and a truncation share.
+// rowless: the logits have no rows (every entry of the row table is outside them).
 template <class Args>
-int cut_check(const Args* a) {
+int cut_check(const Args* a, bool rowless) {
   if (!a || !cut_shape_ok(a->B, a->R, a->V)) return SPEC_EINVAL;
   if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
   if (a->B == 0 || a->R == 0) return SPEC_OK;
-  if (!a->logits || !a->temperature || !a->workspace) return SPEC_EINVAL;
+  if ((!a->logits && !rowless) || !a->temperature || !a->workspace) return SPEC_EINVAL;
   if (a->row_stride < a->V) return SPEC_EINVAL;
   if (!aligned16(a->workspace)) return SPEC_EALIGN;
   if (a->workspace_bytes < cut_ws_bytes(a->B, a->R)) return SPEC_EWORKSPACE;
@@ -469,6 +470,7 @@ int rope_check(const spec_rope_args* a, RopeParams& P) {
   P.half = a->rot_dim / 2;
   P.inter = a->interleaved != 0;
   P.positions = a->positions;
+  P.wide = a->wide_positions != 0;
   P.inv_freq = a->inv_freq;
   P.scale = a->scale;
   P.src[0] = static_cast<const char*>(a->q);
@@ -514,6 +516,7 @@ int kv4_write_check(const spec_kv4_write_args* a, RopeParams& P) {
   P.inter = a->rot_dim == 0 || a->interleaved != 0;  // (nothing turned: no lane needs another's elements)
   P.write = 1;
   P.positions = a->positions;
+  P.wide = a->wide_positions != 0;
   P.inv_freq = a->inv_freq;
   P.scale = a->scale;
   P.src[0] = static_cast<const char*>(a->q);
@@ -1021,7 +1024,7 @@ int spec_attn4_launch(const spec_attn4_args* a, hipStream_t stream) {
 }
 
 int spec_sample_launch(const spec_sample_args* a, hipStream_t stream) {
-  int rc = cut_check(a);
+  const int rc = cut_check(a, a && a->row_index && a->rows == 0);
   if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
   if (!a->uniforms || !a->tokens) return SPEC_EINVAL;
   if (a->row_index ? a->rows < 0 : a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;
@@ -1038,7 +1041,7 @@ size_t spec_sample_workspace_bytes(int32_t B, int32_t R, int32_t V) {
 }
 
 int spec_truncate_launch(const spec_truncate_args* a, hipStream_t stream) {
-  int rc = cut_check(a);
+  const int rc = cut_check(a, false);
   if (rc != SPEC_OK || a->B == 0 || a->R == 0) return rc;
   if (!a->out) return SPEC_EINVAL;
   if (a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;

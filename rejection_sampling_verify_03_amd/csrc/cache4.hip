@@ -120,7 +120,9 @@ __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
   for (int i = tid; i < tokens * half; i += kWG) {
     const int t = i / half, f = i - t * half;
     double sn, cs;
-    sin_cos((double)P.positions[n0 + t] * P.inv_freq[f], sn, cs);
+    const double at = P.wide ? (double)static_cast<const int64_t*>(P.positions)[n0 + t]
+                             : (double)static_cast<const int32_t*>(P.positions)[n0 + t];
+    sin_cos(at * P.inv_freq[f], sn, cs);
     s_turn[t * half + (f % step) * rows + f / step] = double2{cs * P.scale, sn * P.scale};
   }
   __syncthreads();

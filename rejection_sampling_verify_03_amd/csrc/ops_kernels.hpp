@@ -132,7 +132,8 @@ struct RopeParams {
   int32_t inter, write; // pairs side by side; keys and values go to the cache
   int32_t tokens;       // of a workgroup, at most kRopeAngles / half
   int32_t shares;       // workgroups to a set of tokens
-  const int32_t* positions;
+  const void* positions;
+  int32_t wide;         // positions are 64 bits
   const double* inv_freq;
   double scale;
   const char* src[3];   // queries, keys, values

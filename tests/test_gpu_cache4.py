@@ -1,0 +1,386 @@
+"""Rotation, the 4-bit paged cache's write (with and without it) and read on
+the GPU against the 64-bit definition: layouts of pairs, parts of heads, types,
+odd sizes, far and negative positions, pages, scales and codes bit by bit,
+values at the ends of the range, strides, in place, captured and far apart.
+
+The rotated values are rounded once from 64 bits: half a step of the type, and
+an fp32 step of that for the rounding through 32 bits.  Codes and scales equal
+the definition's."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_oracle as do
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sv():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import rejection_sampling_verify_03_amd as m
+    return m
+
+
+def near(got, want, dtype):
+    got = got.cpu().double().numpy()
+    half = torch.finfo(dtype).eps / 2
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    fin = ~np.isnan(want)
+    tol = half * (1 + 2.0 ** -15) * np.abs(want) + 1e-12 + 2.0 ** -140
+    assert np.all((np.abs(got - want) <= tol)[fin]), np.max((np.abs(got - want) / tol)[fin])
+
+
+def table(rot, base=10000.0):
+    return base ** (-2.0 * np.arange(rot // 2) / rot)
+
+
+def rope_of(sv, f, scale=1.0, inter=False):
+    return sv.Rope(torch.from_numpy(np.asarray(f, np.float64)).cuda(), scale, inter)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dim,rot", [(16, 16), (64, 64), (128, 128), (256, 256), (80, 32), (96, 96), (104, 48), (256, 16),
+                                     (40, 16), (192, 176)])
+def test_rotation(sv, dim, rot, inter, dtype):
+    g = torch.Generator().manual_seed(dim + rot)
+    for N, hq, hk in ((1, 1, 1), (5, 7, 3), (33, 16, 1), (2, 0, 4), (3, 5, 0)):
+        q, k = (torch.randn(N, h, dim, generator=g).to(dtype) for h in (hq, hk))
+        pos = torch.randint(-5, 200000, (N,), generator=g).to(torch.int32 if N % 2 else torch.int64)
+        f = table(rot)
+        r = rope_of(sv, f, 1.25, inter)
+        a, b = sv.rope(q.cuda(), k.cuda() if hk else None, pos.cuda(), r)
+        torch.cuda.synchronize()
+        near(a, do.rotate(q.double().numpy(), pos.numpy(), f, 1.25, inter), dtype)
+        if hk:
+            near(b, do.rotate(k.double().numpy(), pos.numpy(), f, 1.25, inter), dtype)
+        else:
+            assert b is None
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_far_positions(sv, inter):
+    """Angles up to the largest that positions can make, and back again."""
+    f = table(64)
+    pos = torch.tensor([0, 1, 2 ** 20, 2 ** 24 + 1, 2 ** 31 - 1, -1, -2 ** 31, 123456789], dtype=torch.int32)
+    x = torch.randn(8, 3, 64, generator=torch.Generator().manual_seed(1))
+    a, _ = sv.rope(x.cuda(), None, pos.cuda(), rope_of(sv, f, 1.0, inter))
+    torch.cuda.synchronize()
+    # (the product in 64 bits is off by up to 2^-53 of the angle, the oracle's by as much)
+    got, want = a.cpu().double().numpy(), do.rotate(x.double().numpy(), pos.numpy(), f, 1.0, inter)
+    tol = 2.0 ** -24 * np.abs(want) + 4 * 2.0 ** -53 * np.abs(pos.numpy().astype(np.float64))[:, None, None] + 1e-12
+    assert np.all(np.abs(got - want) <= tol)
+    assert torch.equal(a[0].cpu(), x[0])
+    wide, _ = sv.rope(x.cuda(), None, pos.long().cuda(), rope_of(sv, f, 1.0, inter))
+    assert torch.equal(wide, a)
+    back, _ = sv.rope(a, None, torch.where(pos > -2 ** 31, -pos, pos).cuda(), rope_of(sv, f, 1.0, inter))
+    torch.cuda.synchronize()
+    assert float((back[pos > -2 ** 31].cpu() - x[pos > -2 ** 31]).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_in_place_and_strided(sv, inter, dtype):
+    """Queries and keys as slices of one projection, at odd offsets, rotated
+    where they stand; what lies between them stays."""
+    g = torch.Generator().manual_seed(3)
+    for dim, rot in ((64, 64), (128, 96), (80, 16)):
+        N, hq, hk = 70, 9, 2
+        buf = torch.randn(N, (hq + 2 * hk) * dim + 5, generator=g).to(dtype).cuda()
+        before = buf.clone()
+        q = buf[:, 3:3 + hq * dim].unflatten(1, (hq, dim))
+        k = buf[:, 3 + hq * dim:3 + (hq + hk) * dim].unflatten(1, (hk, dim))
+        pos = torch.arange(1000, 1000 + N, dtype=torch.int32)
+        f = table(rot)
+        a, b = sv.rope(q, k, pos.cuda(), rope_of(sv, f, 1.0, inter), out=(q, k))
+        torch.cuda.synchronize()
+        assert a is q and b is k
+        old = before.cpu().double().numpy()
+        near(q, do.rotate(old[:, 3:3 + hq * dim].reshape(N, hq, dim), pos.numpy(), f, 1.0, inter), dtype)
+        near(k, do.rotate(old[:, 3 + hq * dim:3 + (hq + hk) * dim].reshape(N, hk, dim), pos.numpy(), f, 1.0, inter), dtype)
+        q.copy_(before[:, 3:3 + hq * dim].unflatten(1, (hq, dim)))
+        k.copy_(before[:, 3 + hq * dim:3 + (hq + hk) * dim].unflatten(1, (hk, dim)))
+        assert torch.equal(buf, before)
+        # heads outside tokens
+        t = before[:, :hq * dim].reshape(N, hq, dim).transpose(0, 1).contiguous().transpose(0, 1)
+        o = torch.empty(hq, N, dim, dtype=dtype, device="cuda").transpose(0, 1)
+        a, _ = sv.rope(t, None, pos.cuda(), rope_of(sv, f, 1.0, inter), out=(o, None))
+        torch.cuda.synchronize()
+        near(a, do.rotate(t.cpu().double().numpy(), pos.numpy(), f, 1.0, inter), dtype)
+
+
+def test_rotation_refusals(sv):
+    q = torch.zeros(4, 2, 64, device="cuda")
+    pos = torch.zeros(4, dtype=torch.int32, device="cuda")
+    r = rope_of(sv, table(64))
+    for call, e in ((lambda: sv.rope(q, q.bfloat16(), pos, r), TypeError), (lambda: sv.rope(q.half(), None, pos, r), TypeError),
+                    (lambda: sv.rope(q, q[:3], pos, r), ValueError), (lambda: sv.rope(q, None, pos[:3], r), ValueError),
+                    (lambda: sv.rope(q, None, pos.float(), r), ValueError),
+                    (lambda: sv.rope(q.transpose(1, 2), None, pos, r), ValueError),
+                    (lambda: sv.rope(q[..., :32].contiguous(), None, pos, r), sv.SpecError),
+                    (lambda: sv.rope(q, None, pos, r, out=(q[:, :1], None)), ValueError)):
+        with pytest.raises(e):
+            call()
+    a, b = sv.rope(q[:0], q[:0], pos[:0], r)
+    assert a.shape == (0, 2, 64) and b.shape == (0, 2, 64)
+
+
+# --------------------------------------------------------------------- cache
+class Cache:
+    """A filled cache on both sides."""
+
+    def __init__(self, sv, blocks, bs, heads, dim, seed, order="heads"):
+        k, v, ks, vs = do.random_cache(blocks, bs, heads, dim, seed, order)
+        self.host = [t.numpy().copy() for t in (k, ks, v, vs)]
+        self.dev = sv.KVCache4(*(do.up(t) for t in (k, v, ks, vs)))
+
+    def same(self):
+        d = self.dev
+        return all(np.array_equal(t.cpu().numpy(), h) for t, h in zip((d.k, d.k_scale, d.v, d.v_scale), self.host))
+
+    def write(self, key, value, slots):
+        do.kv_write(self.host[0], self.host[1], key, slots)
+        do.kv_write(self.host[2], self.host[3], value, slots)
+
+
+def slots_of(N, total, g, skipped=0.2):
+    s = torch.randperm(total, generator=g)[:N]
+    if len(s) < N:
+        s = torch.cat([s, torch.full((N - len(s),), -1)])
+    return torch.where(torch.rand(N, generator=g) < skipped, -1, s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("order", ["heads", "tokens"])
+@pytest.mark.parametrize("bs,heads,dim", [(16, 1, 32), (16, 8, 64), (32, 3, 96), (64, 2, 128), (1024, 1, 256), (128, 5, 160)])
+def test_writes_and_reads(sv, bs, heads, dim, order, dtype):
+    g = torch.Generator().manual_seed(bs + dim)
+    blocks = max(3, 200 // bs)
+    c = Cache(sv, blocks, bs, heads, dim, 1, order)
+    for N in (1, 2, 77):
+        key, val = ((torch.randn(N, heads, dim, generator=g) * torch.exp(3 * torch.randn(N, heads, 1, generator=g))).to(dtype)
+                    for _ in range(2))
+        slots = slots_of(N, blocks * bs, g)
+        assert sv.kv_write(c.dev, key.cuda(), val.cuda(), slots.cuda()) is c.dev
+        torch.cuda.synchronize()
+        c.write(key.double().numpy(), val.double().numpy(), slots.tolist())
+        assert c.same()
+        k, v = sv.kv_read(c.dev, slots.cuda(), dtype=dtype)
+        torch.cuda.synchronize()
+        assert np.array_equal(k.cpu().double().numpy(), do.kv_values(c.host[0], c.host[1], slots.numpy()))
+        assert np.array_equal(v.cpu().double().numpy(), do.kv_values(c.host[2], c.host[3], slots.numpy()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("hq,heads,dim,rot", [(8, 1, 64, 64), (4, 4, 128, 64), (6, 2, 96, 80), (0, 3, 32, 16), (3, 1, 256, 256),
+                                              (64, 8, 64, 64), (2, 2, 160, 48)])
+def test_rotated_writes(sv, hq, heads, dim, rot, inter, dtype):
+    """Keys turned in 64 bits and rounded once, to codes."""
+    g = torch.Generator().manual_seed(dim + rot)
+    bs, blocks = 16, 9
+    c = Cache(sv, blocks, bs, heads, dim, 2)
+    f = table(rot)
+    r = rope_of(sv, f, 1.1, inter)
+    for N in (1, 6, 90):
+        q = torch.randn(N, hq, dim, generator=g).to(dtype) if hq else None
+        key, val = ((torch.randn(N, heads, dim, generator=g) * 5).to(dtype) for _ in range(2))
+        slots = slots_of(N, blocks * bs, g)
+        pos = torch.randint(0, 100000, (N,), generator=g).to(torch.int32)
+        out = sv.rope_kv_write(c.dev, None if q is None else q.cuda(), key.cuda(), val.cuda(), pos.cuda(), slots.cuda(), r)
+        torch.cuda.synchronize()
+        c.write(do.rotate(key.double().numpy(), pos.numpy(), f, 1.1, inter), val.double().numpy(), slots.tolist())
+        assert c.same()
+        if hq:
+            near(out, do.rotate(q.double().numpy(), pos.numpy(), f, 1.1, inter), dtype)
+            d = q.cuda()
+            assert sv.rope_kv_write(c.dev, d, key.cuda(), val.cuda(), pos.cuda(), slots.cuda(), r, q_out=d) is d
+            torch.cuda.synchronize()
+            assert torch.equal(d, out) and c.same()
+        else:
+            assert out is None
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_at_the_ends_of_the_range(sv, dtype):
+    """Zeros of both signs, the smallest and largest numbers, ties between two
+    codes, scales one step apart, and what has no code: NaN and infinities."""
+    c = Cache(sv, 4, 16, 1, 32, 3)
+    big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).tiny
+    rows = [torch.zeros(32), -torch.zeros(32), torch.full((32,), big), torch.full((32,), -big), torch.full((32,), tiny),
+            torch.full((32,), tiny / 64), torch.linspace(-6, 6, 32), torch.full((32,), 6.0), torch.full((32,), 6.03125),
+            torch.full((32,), 1.5 * 2.0 ** -115), torch.full((32,), 2.0 ** -118)]
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    rows.append(torch.cat([ties, -ties, ties * 0.5, ties * 0.25]))
+    for e in (-100, -1, 0, 1, 60, 120):
+        rows.append(torch.cat([ties, -ties, ties * 0.5, ties * 0.25]) * 2.0 ** e)
+    for bad in (math.nan, math.inf, -math.inf):
+        y = torch.ones(32)
+        y[17] = bad
+        rows.append(y)
+    x = torch.stack(rows).to(dtype)[:, None]
+    N = len(rows)
+    slots = torch.arange(N) + 5
+    sv.kv_write(c.dev, x.cuda(), x.flip(0).cuda().contiguous(), slots.cuda())
+    k, v = sv.kv_read(c.dev, slots.cuda(), dtype=F32)
+    torch.cuda.synchronize()
+    c.write(x.double().numpy(), x.flip(0).double().numpy(), slots.tolist())
+    assert c.same()
+    with np.errstate(over="ignore"):
+        want = do.kv_values(c.host[0], c.host[1], slots.numpy()).astype(np.float32)
+    assert np.array_equal(k.cpu().numpy(), want, equal_nan=True)
+    assert torch.equal(torch.isnan(v), torch.isnan(k).flip(0)) and int(torch.isnan(k).all(-1).sum()) == 3
+
+
+def test_every_code_and_scale_is_read(sv):
+    """All 16 codes under all 256 exponent bytes, in both types."""
+    k = torch.zeros(16, 16, 1, 16, dtype=torch.uint8)
+    k[:] = torch.arange(0, 256, 17, dtype=torch.uint8)  # each byte one code twice
+    ks = torch.arange(256, dtype=torch.uint8).view(16, 1, 1, 16)
+    c = sv.KVCache4(k.cuda(), k.flip(3).contiguous().cuda(), ks.cuda(), ks.cuda())
+    slots = torch.arange(256)
+    want = do.kv_values(k.numpy(), ks.numpy(), slots.numpy())
+    with np.errstate(over="ignore"):
+        for dtype in (F32, BF16):
+            got, _ = sv.kv_read(c, slots.cuda(), dtype=dtype)
+            torch.cuda.synchronize()
+            w = torch.from_numpy(want).to(dtype).float().numpy()
+            assert np.array_equal(got.float().cpu().numpy(), w, equal_nan=True)
+
+
+def test_equal_slots_and_slots_outside(sv):
+    """Of equal slots next to each other the last entry counts; entries outside
+    the cache, far ones among them, write nothing and read zeros."""
+    c = Cache(sv, 3, 16, 2, 64, 4)
+    g = torch.Generator().manual_seed(2)
+    slots = torch.tensor([5, 5, 5, -1, 7, 48, 2 ** 40, -2 ** 62, 9, 9, 47])
+    key, val = (torch.randn(11, 2, 64, generator=g) for _ in range(2))
+    sv.kv_write(c.dev, key.cuda(), val.cuda(), slots.cuda())
+    k, _ = sv.kv_read(c.dev, slots.cuda(), dtype=F32)
+    torch.cuda.synchronize()
+    c.write(key.double().numpy(), val.double().numpy(), slots.tolist())
+    assert c.same()
+    assert np.array_equal(k.cpu().double().numpy(), do.kv_values(c.host[0], c.host[1], slots.numpy()))
+    assert not bool(k[3].any()) and not bool(k[5:8].any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_strided_sources(sv, dtype):
+    c = Cache(sv, 6, 16, 3, 64, 5)
+    g = torch.Generator().manual_seed(1)
+    buf = torch.randn(40, 700, generator=g).to(dtype)
+    q, key, val = (buf[:, a:a + 192].unflatten(1, (3, 64)) for a in (1, 195, 400))
+    slots = slots_of(40, 96, g)
+    pos = torch.arange(40, dtype=torch.int32)
+    d = buf.cuda()
+    dq, dk, dv = (d[:, a:a + 192].unflatten(1, (3, 64)) for a in (1, 195, 400))
+    f = table(64)
+    out = sv.rope_kv_write(c.dev, dq, dk, dv, pos.cuda(), slots.cuda(), rope_of(sv, f))
+    torch.cuda.synchronize()
+    c.write(do.rotate(key.double().numpy(), pos.numpy(), f, 1.0, False), val.double().numpy(), slots.tolist())
+    assert c.same()
+    near(out, do.rotate(q.double().numpy(), pos.numpy(), f, 1.0, False), dtype)
+    assert torch.equal(d.cpu(), buf)
+
+
+def test_refusals(sv):
+    c = sv.make_kv4_cache(4, 16, 2, 64)
+    x, s = torch.zeros(3, 2, 64, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    pos, r = torch.zeros(3, dtype=torch.int32, device="cuda"), rope_of(sv, table(64))
+    for call, e in ((lambda: sv.kv_write(c, x[:, :1], x, s), ValueError), (lambda: sv.kv_write(c, x, x.bfloat16(), s), TypeError),
+                    (lambda: sv.kv_write(c, x.half(), x.half(), s), TypeError), (lambda: sv.kv_write(c, x, x, s.int()), ValueError),
+                    (lambda: sv.kv_write(c, x.cpu(), x, s), ValueError),
+                    (lambda: sv.rope_kv_write(c, x, x, x, pos.short(), s, r), ValueError),
+                    (lambda: sv.rope_kv_write(c, x, x, x, pos, s, None), ValueError),
+                    (lambda: sv.rope_kv_write(c, x.bfloat16(), x, x, pos, s, r), TypeError),
+                    (lambda: sv.rope_kv_write(c, x, x, x, pos, s, rope_of(sv, table(128))), sv.SpecError),
+                    (lambda: sv.rope_kv_write(sv.make_kv_cache(4, 16, 2, 64), x, x, x, pos, s, r), TypeError),
+                    (lambda: sv.kv_read(c, s, dtype=torch.float16), TypeError),
+                    (lambda: sv.kv_write(sv.KVCache4(c.k, c.k, c.k_scale, c.v_scale), x, x, s), sv.SpecError),
+                    (lambda: sv.KVCache4(c.k, c.v.contiguous(), c.k_scale, c.v_scale), ValueError),
+                    (lambda: sv.KVCache4(c.k, c.v, c.k_scale[:, :, :1], c.v_scale), ValueError)):
+        with pytest.raises(e):
+            call()
+    assert sv.kv_write(c, x[:0], x[:0], s[:0]) is c
+    k, v = sv.kv_read(c, s[:0])
+    assert k.shape == (0, 2, 64)
+
+
+def test_slots_far_past_32_bits(sv):
+    """A cache whose codes and scales pass 2^32 bytes: written and read at both ends."""
+    bs, heads, dim = 16, 1, 256
+    blocks = 2 ** 32 // (bs * dim // 2) + 3
+    k, v = (torch.empty(blocks, heads, bs, dim // 2, dtype=torch.uint8, device="cuda").transpose(1, 2) for _ in range(2))
+    scales = torch.empty(blocks, heads, dim // 32, bs, dtype=torch.uint8, device="cuda")
+    c = sv.KVCache4(k, v, scales, torch.empty_like(scales))
+    last = blocks * bs - 1
+    slots = torch.tensor([0, last, 2 ** 31 // (dim // 2) * 2 + 1, last - 17])
+    x = torch.randn(4, heads, dim, generator=torch.Generator().manual_seed(1))
+    sv.kv_write(c, x.cuda(), (x * 3).cuda(), slots.cuda())
+    a, b = sv.kv_read(c, slots.cuda(), dtype=F32)
+    torch.cuda.synchronize()
+    for got, y in ((a, x), (b, x * 3)):
+        kc, sc = np.zeros((4, 16, heads, dim // 2), np.uint8), np.zeros((4, heads, dim // 32, 16), np.uint8)
+        do.kv_write(kc, sc, y.double().numpy(), [0, 16, 32, 48])
+        assert np.array_equal(got.cpu().double().numpy(), do.kv_values(kc, sc, [0, 16, 32, 48]))
+
+
+def test_prompts_take_other_shares(sv):
+    """Many tokens, where a workgroup takes several, against few at a time."""
+    g = torch.Generator().manual_seed(6)
+    for heads, hq, dim, rot, inter, N in ((2, 6, 64, 64, False, 5000), (1, 3, 128, 32, True, 4500), (1, 1, 256, 256, False, 9001)):
+        f = table(rot)
+        r = rope_of(sv, f, 1.0, inter)
+        q, key, val = (torch.randn(N, h, dim, generator=g).to(BF16).cuda() for h in (hq, heads, heads))
+        pos = torch.arange(N, dtype=torch.int32).cuda()
+        slots = torch.randperm(N, generator=g).cuda()
+        one, two = (sv.make_kv4_cache(-(-N // 16), 16, heads, dim) for _ in range(2))
+        whole = sv.rope_kv_write(one, q, key, val, pos, slots, r)
+        parts = [sv.rope_kv_write(two, q[i:i + 501], key[i:i + 501], val[i:i + 501], pos[i:i + 501], slots[i:i + 501], r)
+                 for i in range(0, N, 501)]
+        a, _ = sv.rope(q, None, pos, r)
+        torch.cuda.synchronize()
+        assert torch.equal(whole, torch.cat(parts)) and torch.equal(whole, a)
+        for n in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(one, n), getattr(two, n))
+        near(whole[:40], do.rotate(q[:40].cpu().double().numpy(), np.arange(40), f, 1.0, inter), BF16)
+
+
+def test_replays_and_streams(sv):
+    N, hq, heads, dim = 12, 8, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = rope_of(sv, table(64))
+    q, key, val = (torch.randn(N, h, dim, generator=g, device="cuda").to(BF16) for h in (hq, heads, heads))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    slots = torch.arange(N, device="cuda")
+    one, two = (sv.make_kv4_cache(8, 16, heads, dim) for _ in range(2))
+
+    def go(c, **kw):
+        out = sv.rope_kv_write(c, q, key, val, pos, slots, r, **kw)
+        return (out,) + sv.kv_read(c, slots, **kw) + sv.rope(q, key, pos, r, **kw)
+    go(one)
+    go(two)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = go(one)
+    for i in range(4):
+        for t in (q, key, val):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        pos.add_(17)
+        slots.copy_(torch.randperm(8 * 16, generator=g, device="cuda")[:N])
+        graph.replay()
+        want = go(two)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        for n in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(one, n), getattr(two, n))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = go(two, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -760,8 +760,10 @@ int spec_truncate_launch(const spec_truncate_args* args, hipStream_t stream);
  *   (x cos a - y sin a, y cos a + x sin a) * scale,
  * pairs (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1), i < rot_dim / 2;
  * the elements of a head from rot_dim on stay as they are.  A negative position
- * turns back.  The angle is the fp64 product; its cosine and sine and the
- * products with them are taken in fp64 (|a| up to 2^31) and rounded once.
+ * turns back.  The angle is the fp64 product (|a| up to 2^31), its cosine and
+ * sine are taken in fp64; so are the products with them for fp32 tensors, rounded
+ * once.  For bf16 they are fp32 products of the rounded cosine and sine: 2^-23
+ * of |x| + |y| off at most, before the rounding to bf16.
  */
 typedef struct {
   int32_t N;                   /* tokens, >= 0 */
@@ -820,7 +822,7 @@ typedef struct {
  * [0, num_blocks * block_size) (the -1 of a slot mapping) are not written.  With
  * rot_dim > 0 the keys are first turned to positions[i] as by spec_rope_launch,
  * and so are queries, if there are any (q_heads > 0), for every entry, written
- * or not; what the keys become is not rounded in between.  32 elements get the
+ * or not; what the keys become (by fp64 products) is not rounded in between.  32 elements get the
  * smallest exponent e with |x| <= 6 * 2^e, at least -117, and are rounded to
  * nearest, ties to even; with a NaN or an infinity among them, all 32 are
  * stored as NaN.  (One of 1.75 * 2^127 or more rounds to 2^128, which bf16 and

@@ -441,10 +441,14 @@ bool turned_ok(const void* in, int64_t tok, int64_t head, const void* out, int64
 
 // How the tokens and heads of a rotation are shared out; false: too many.
 bool rope_split(RopeParams& P) {
-  const int64_t per = kThreads / (P.dim / 8), heads = (int64_t)P.heads[0] + (P.write ? 2 : 1) * (int64_t)P.heads[1];
+  const int64_t per = kThreads / ((P.dim + 15) / 16), heads = (int64_t)P.heads[0] + (P.write ? 2 : 1) * (int64_t)P.heads[1];
   const int64_t rounds = (heads + per - 1) / per;
-  P.tokens = 1;
-  P.shares = (int32_t)rounds;
+  P.by_heads = FastDiv::by((uint32_t)heads);
+  // many tokens: as many to a workgroup as its lanes work out angles for; few:
+  // one, its heads shared out
+  const bool many = (int64_t)P.N * rounds >= 16384;
+  P.tokens = !many ? 1 : P.half > 0 ? kRopeAngles / P.half : 8;
+  P.shares = many ? 1 : (int32_t)rounds;
   return fits_dispatch((((int64_t)P.N + P.tokens - 1) / P.tokens) * P.shares, kThreads);
 }
 
@@ -513,7 +517,7 @@ int kv4_write_check(const spec_kv4_write_args* a, RopeParams& P) {
   P.heads[1] = a->cache.heads;
   P.dim = a->cache.head_dim;
   P.half = a->rot_dim / 2;
-  P.inter = a->rot_dim == 0 || a->interleaved != 0;  // (nothing turned: no lane needs another's elements)
+  P.inter = a->interleaved != 0;
   P.write = 1;
   P.positions = a->positions;
   P.wide = a->wide_positions != 0;

@@ -18,8 +18,6 @@
 // instructions read.  A scale belongs to one token, so every token is written
 // by itself: no order among the writers, nothing read back.
 //
-// One lane takes 8 elements of one head of a token; four lanes hold the 32
-// elements of a scale.
 #include "cache_device.hpp"
 #include "unaligned.hpp"
 
@@ -66,12 +64,6 @@ __device__ __forceinline__ float to_odd(double y) {
   return __uint_as_float(u);
 }
 
-// The largest of the four lanes of a quad, in each of them.
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __int_as_float(dpp_i<0xb1, 0xf>(__float_as_int(x), 0)));
-  return fmaxf(x, __int_as_float(dpp_i<0x4e, 0xf>(__float_as_int(x), 0)));
-}
-
 // The smallest e with amax <= 6 * 2^e, at least kScaleMin; amax finite.
 __device__ __forceinline__ int exponent4(float amax) {
   const uint32_t u = __float_as_uint(amax);
@@ -104,116 +96,160 @@ __device__ __forceinline__ void store8(char* dst, const float x[8]) {
   }
 }
 
-// Grid: x sets of P.tokens tokens, y shares of a token's heads.  A round takes
-// as many heads as the workgroup holds.  In place, with pairs half a head
-// apart, two lanes write what both read: all of a round's reads are done
-// before its writes (heads are never shared between workgroups).
+// Two groups of 8 elements of a head, a and b, turned by 8 pairs' cosines and
+// sines: a[q] and b[q] are a pair, or with INTER the neighbours in a (pairs 0 to
+// 3) and in b (4 to 7).
+template <bool INTER, class T, class CosSin>
+__device__ __forceinline__ void turn16(T (&a)[8], T (&b)[8], CosSin cos_sin) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    T& x = !INTER ? a[q] : q < 4 ? a[2 * q] : b[2 * q - 8];
+    T& y = !INTER ? b[q] : q < 4 ? a[2 * q + 1] : b[2 * q - 7];
+    T c, s;
+    cos_sin(q, c, s);
+    const T u = x;
+    x = __builtin_fma(x, c, -(y * s));
+    y = __builtin_fma(u, s, y * c);
+  }
+}
+
+// A lane takes two groups of 8 elements of one head of a token: in the rotated
+// part groups half of it apart, whose elements are pairs of each other, or pairs
+// among themselves (so that every pair is one lane's, and in place nothing is
+// overwritten that another lane reads); behind it groups half of the rest apart.
+// Grid: x sets of P.tokens tokens, y shares of their heads.  The heads of a
+// set's tokens, end to end, go to the lanes in rounds.  (Two rounds' reads on
+// their way together: 166 us against 122 for 24000 tokens of 32 + 8 + 8 heads of
+// 128; the registers cost more waves than that gains.)
 template <int ES, bool WRITE, bool INTER>
 __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
-  // cosine and sine of pair 8 j + q (interleaved: 4 j + q) of a token at
-  // [token][q][j]: the lanes of a head read neighbouring places
+  // cosine and sine of a lane's pair q at [token][q][lane of the head], in both
+  // precisions: neighbouring lanes read neighbouring places
   __shared__ double2 s_turn[kRopeAngles];
+  __shared__ float2 s_turn32[kRopeAngles];
+  __shared__ __align__(16) float s_max[WRITE ? kWG * 2 : 1];
   const int tid = threadIdx.x;
-  const int half = P.half, step = INTER ? 4 : 8, rows = half / step;
+  const int half = P.half, rows = half >> 3;  // rows: lanes of a head whose elements are turned
   const int n0 = blockIdx.x * P.tokens;
   const int tokens = min(P.tokens, P.N - n0);
   for (int i = tid; i < tokens * half; i += kWG) {
     const int t = i / half, f = i - t * half;
-    double sn, cs;
     const double at = P.wide ? (double)static_cast<const int64_t*>(P.positions)[n0 + t]
                              : (double)static_cast<const int32_t*>(P.positions)[n0 + t];
+    double sn, cs;
     sin_cos(at * P.inv_freq[f], sn, cs);
-    s_turn[t * half + (f % step) * rows + f / step] = double2{cs * P.scale, sn * P.scale};
+    const int late = INTER && f >= half / 2 ? 4 : 0, g = late ? f - half / 2 : f;
+    const int place = t * half + (INTER ? (late + g % 4) * rows + g / 4 : g % 8 * rows + g / 8);
+    s_turn[place] = double2{cs * P.scale, sn * P.scale};
+    s_turn32[place] = float2{(float)(cs * P.scale), (float)(sn * P.scale)};
   }
   __syncthreads();
-  const int lanes = P.dim >> 3, per = kWG / lanes;
+  const int lanes = (P.dim + 15) >> 4, per = kWG / lanes;
   const int heads = P.heads[0] + (WRITE ? 2 : 1) * P.heads[1];
-  const int mine = tid / lanes, col = (tid - mine * lanes) * 8;
-  const int rounds = (heads + per - 1) / per;
-  for (int t = 0; t < tokens; ++t) {
-    const int n = n0 + t;
-    int64_t slot = -1;
-    if constexpr (WRITE) {
-      slot = P.slots[n];
-      // of equal slots next to each other the last counts
-      if (slot >= (int64_t)P.c.num_blocks << P.c.bs_shift || (n + 1 < P.N && P.slots[n + 1] == slot)) slot = -1;
-    }
-    for (int r = blockIdx.y; r < rounds; r += gridDim.y) {
-      int h = r * per + mine;
-      const bool on = mine < per && h < heads;
-      const int what = !on ? 0 : h < P.heads[0] ? 0 : h < P.heads[0] + P.heads[1] ? 1 : 2;  // queries, keys, values
-      h -= what == 0 ? 0 : what == 1 ? P.heads[0] : P.heads[0] + P.heads[1];
-      const bool turn = on && what < 2 && col < 2 * half;
-      RawGroup<ES, true> own = neg_inf_group<ES, true>(), other = own;
-      if (on) {
-        const char* src = P.src[what] + ((int64_t)n * P.tok[what] + (int64_t)h * P.hd[what]) * ES;
-        own = load_any<ES>(src, col);
-        if (!INTER && turn) other = load_any<ES>(src, col < half ? col + half : col - half);
-      }
-      if constexpr (!INTER) {
-        // (here, so that what was loaded has arrived)
-        opaque_group<ES, true>(own);
-        opaque_group<ES, true>(other);
-        __syncthreads();
-      }
-      if (!on) continue;
-      float x[8];
-      unpack_group<ES, true>(own, x);
-      if (turn) {
-        double y[8];
-        const double2* cs = s_turn + t * half;
-        if constexpr (INTER) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const double2 w = cs[q * rows + (col >> 3)];
-            const double a = x[2 * q], b = x[2 * q + 1];
-            y[2 * q] = __builtin_fma(a, w.x, -(b * w.y));
-            y[2 * q + 1] = __builtin_fma(a, w.y, b * w.x);
-          }
+  const int mine = tid / lanes, lane = tid - mine * lanes;
+  const bool turned = lane < rows;
+  const int behind = (P.dim - 2 * half) >> 3, front = (behind + 1) >> 1;  // groups that are not turned; of them first ones
+  const int col_a = turned ? 8 * lane : 2 * half + 8 * (lane - rows);
+  const int col_b = turned ? half + 8 * lane : col_a + 8 * front;
+  const bool two = turned || lane - rows + front < behind;  // (else the second group does not exist)
+  const int items = tokens * heads, rounds = (items + per - 1) / per;
+  for (int r = blockIdx.y; r < rounds; r += gridDim.y) {
+    const int item = r * per + mine;
+    const bool on = mine < per && item < items;
+    const int token = (int)P.by_heads.of((uint32_t)min(item, items - 1)), h = item - token * heads, n = n0 + token;
+    const int what = h < P.heads[0] ? 0 : h < P.heads[0] + P.heads[1] ? 1 : 2;  // queries, keys, values
+    const int head = h - (what == 1 ? P.heads[0] : what == 2 ? P.heads[0] + P.heads[1] : 0);
+    float a[8], b[8];
+    if (on) {
+      const char* src = P.src[what] + ((int64_t)n * P.tok[what] + (int64_t)head * P.hd[what]) * ES;
+      // (past the caches a line of which each load takes half comes twice: 38 us
+      // against 28 for the keys and values of 24000 tokens)
+      const RawGroup<ES, true> raw_a = load_cached<ES>(src, col_a), raw_b = load_cached<ES>(src, two ? col_b : col_a);
+      unpack_group<ES, true>(raw_a, a);
+      unpack_group<ES, true>(raw_b, b);
+      if (turned && what < 2) {
+        const int at = token * half + lane;
+        if (ES == 2 && (!WRITE || what == 0)) {
+          turn16<INTER>(a, b, [&](int q, float& c, float& s) {
+            const float2 v = s_turn32[at + q * rows];
+            c = v.x;
+            s = v.y;
+          });
         } else {
-          float z[8];
-          unpack_group<ES, true>(other, z);
-          const bool first = col < half;
-          const int j = (first ? col : col - half) >> 3;
+          double x[8], y[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const double2 w = cs[q * rows + j];
-            const double b = (double)z[q] * w.y;
-            y[q] = __builtin_fma((double)x[q], w.x, first ? -b : b);
+            x[q] = a[q];
+            y[q] = b[q];
           }
-        }
-        if (WRITE && what == 1) {
+          turn16<INTER>(x, y, [&](int q, double& c, double& s) {
+            const double2 v = s_turn[at + q * rows];
+            c = v.x;
+            s = v.y;
+          });
 #pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = to_odd(y[q]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = (float)y[q];
+          for (int q = 0; q < 8; ++q) {
+            a[q] = WRITE && what == 1 ? to_odd(x[q]) : (float)x[q];
+            b[q] = WRITE && what == 1 ? to_odd(y[q]) : (float)y[q];
+          }
         }
       }
       if (!WRITE || what == 0) {
-        store8<ES>(P.dst[what] + ((int64_t)n * P.dtok[what] + (int64_t)h * P.dhd[what] + col) * ES, x);
-        continue;
+        char* dst = P.dst[what] + ((int64_t)n * P.dtok[what] + (int64_t)head * P.dhd[what]) * ES;
+        store8<ES>(dst + col_a * ES, a);
+        if (two) store8<ES>(dst + col_b * ES, b);
       }
-      if constexpr (WRITE) {
-        // (the four lanes of a scale are together in all of this)
-        if (slot < 0) continue;
-        float amax = 0.f;
+    }
+    if constexpr (WRITE) {
+      const bool kept = on && what > 0;
+      float* top = s_max + mine * 2 * lanes;  // the largest of each group of 8 of the head
+      if (kept) {
+        float ma = 0.f, mb = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float a = fabsf(x[q]);
-          amax = fmaxf(amax, a <= FLT_MAX ? a : INFINITY);
+          const float x = fabsf(a[q]), y = fabsf(b[q]);
+          ma = fmaxf(ma, x <= FLT_MAX ? x : INFINITY);
+          mb = fmaxf(mb, y <= FLT_MAX ? y : INFINITY);
         }
-        amax = quad_max(amax);
-        const bool fine = amax <= FLT_MAX;
-        const int e = fine ? exponent4(amax) : 0;
+        top[col_a >> 3] = ma;
+        top[col_b >> 3] = mb;
+      }
+      // (a head's lanes are in one wave where they divide it)
+      if (64 % lanes == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      } else {
+        __syncthreads();
+      }
+      int64_t slot = -1;
+      if (kept) {
+        slot = P.slots[n];
+        // of equal slots next to each other the last counts
+        if (slot >= (int64_t)P.c.num_blocks << P.c.bs_shift || (n + 1 < P.N && P.slots[n + 1] == slot)) slot = -1;
+      }
+      if (slot >= 0) {
         const int64_t blk = slot >> P.c.bs_shift;
         const int in = (int)(slot & ((1 << P.c.bs_shift) - 1));
-        const uint32_t w = encode8(x, two_to(e));
-        *reinterpret_cast<uint32_t*>(P.c.codes[what - 1] + blk * P.c.block + (int64_t)in * P.c.token +
-                                     (int64_t)h * P.c.head + (col >> 1)) = fine ? w : 0u;
-        if ((tid & 3) == 0)
-          P.c.scales[what - 1][blk * P.c.sblock + (int64_t)h * P.c.shead + ((col >> 5) << P.c.bs_shift) + in] =
-              (uint8_t)(fine ? e + kScaleBias : 255);
+        uint8_t* codes = P.c.codes[what - 1] + blk * P.c.block + (int64_t)in * P.c.token + (int64_t)head * P.c.head;
+        uint8_t* scales = P.c.scales[what - 1] + blk * P.c.sblock + (int64_t)head * P.c.shead + in;
+        auto put = [&](const float (&x)[8], int col) {
+          const f32x4 m = *reinterpret_cast<const f32x4*>(&top[(col >> 5) * 4]);
+          const float amax = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+          const bool fine = amax <= FLT_MAX;
+          const int e = fine ? exponent4(amax) : 0;
+          const uint32_t w = encode8(x, two_to(e));
+          *reinterpret_cast<uint32_t*>(codes + (col >> 1)) = fine ? w : 0u;
+          if ((col & 31) == 0) scales[(col >> 5) << P.c.bs_shift] = (uint8_t)(fine ? e + kScaleBias : 255);
+        };
+        put(a, col_a);
+        put(b, col_b);
+      }
+      // (the next round writes there)
+      if (64 % lanes == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      } else {
+        __syncthreads();
       }
     }
   }

@@ -130,6 +130,7 @@ struct RopeParams {
   int32_t N, heads[2];  // tokens; query and key heads (values have the keys')
   int32_t dim, half;    // half: rotated pairs of a head
   int32_t inter, write; // pairs side by side; keys and values go to the cache
+  FastDiv by_heads;     // all heads of a token
   int32_t tokens;       // of a workgroup, at most kRopeAngles / half
   int32_t shares;       // workgroups to a set of tokens
   const void* positions;

@@ -23,4 +23,17 @@ __device__ __forceinline__ RawGroup<ES, true> load_any(const char* __restrict__ 
   return r;
 }
 
+// The same through the caches.
+template <int ES>
+__device__ __forceinline__ RawGroup<ES, true> load_cached(const char* row, int64_t e0) {
+  RawGroup<ES, true> r;
+  if constexpr (ES == 2) {
+    r.v = *reinterpret_cast<const u32x4_any*>(row + e0 * 2);
+  } else {
+    r.a = *reinterpret_cast<const f32x4_any*>(row + e0 * 4);
+    r.b = *reinterpret_cast<const f32x4_any*>(row + e0 * 4 + 16);
+  }
+  return r;
+}
+
 }  // namespace specv

@@ -3,9 +3,11 @@ the GPU against the 64-bit definition: layouts of pairs, parts of heads, types,
 odd sizes, far and negative positions, pages, scales and codes bit by bit,
 values at the ends of the range, strides, in place, captured and far apart.
 
-The rotated values are rounded once from 64 bits: half a step of the type, and
-an fp32 step of that for the rounding through 32 bits.  Codes and scales equal
-the definition's."""
+Rotated fp32 values are rounded once from 64 bits: half a step.  bf16 ones
+are rounded from fp32: half a step of the type and, before it, the cosine and
+sine rounded to 2^-24 each, one product and the sum: 2^-24 (2 |x c| + 3 |y s|),
+below 2^-22 (|x| + |y|) of the pair's inputs as they are scaled.  Codes and
+scales equal the definition's."""
 import math
 
 import numpy as np
@@ -25,12 +27,20 @@ def sv():
     return m
 
 
-def near(got, want, dtype):
+def near(got, x, pos, f, scale, inter):
+    """The rotation of x [N, heads, dim] against the definition."""
+    dtype = got.dtype
+    x, pos = x.cpu().double().numpy(), np.asarray(pos)
+    want = do.rotate(x, pos, f, scale, inter)
     got = got.cpu().double().numpy()
     half = torch.finfo(dtype).eps / 2
     assert np.array_equal(np.isnan(got), np.isnan(want))
     fin = ~np.isnan(want)
-    tol = half * (1 + 2.0 ** -15) * np.abs(want) + 1e-12 + 2.0 ** -140
+    rot, size = 2 * len(f), np.zeros_like(x)
+    i, j = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    size[..., i] = size[..., j] = scale * (np.abs(x[..., i]) + np.abs(x[..., j]))
+    early = 2.0 ** -22 * size if dtype == BF16 else 1e-12
+    tol = half * (np.abs(want) + early) + early + 2.0 ** -140
     assert np.all((np.abs(got - want) <= tol)[fin]), np.max((np.abs(got - want) / tol)[fin])
 
 
@@ -55,9 +65,9 @@ def test_rotation(sv, dim, rot, inter, dtype):
         r = rope_of(sv, f, 1.25, inter)
         a, b = sv.rope(q.cuda(), k.cuda() if hk else None, pos.cuda(), r)
         torch.cuda.synchronize()
-        near(a, do.rotate(q.double().numpy(), pos.numpy(), f, 1.25, inter), dtype)
+        near(a, q, pos, f, 1.25, inter)
         if hk:
-            near(b, do.rotate(k.double().numpy(), pos.numpy(), f, 1.25, inter), dtype)
+            near(b, k, pos, f, 1.25, inter)
         else:
             assert b is None
 
@@ -99,9 +109,8 @@ def test_rotation_in_place_and_strided(sv, inter, dtype):
         a, b = sv.rope(q, k, pos.cuda(), rope_of(sv, f, 1.0, inter), out=(q, k))
         torch.cuda.synchronize()
         assert a is q and b is k
-        old = before.cpu().double().numpy()
-        near(q, do.rotate(old[:, 3:3 + hq * dim].reshape(N, hq, dim), pos.numpy(), f, 1.0, inter), dtype)
-        near(k, do.rotate(old[:, 3 + hq * dim:3 + (hq + hk) * dim].reshape(N, hk, dim), pos.numpy(), f, 1.0, inter), dtype)
+        near(q, before[:, 3:3 + hq * dim].reshape(N, hq, dim), pos, f, 1.0, inter)
+        near(k, before[:, 3 + hq * dim:3 + (hq + hk) * dim].reshape(N, hk, dim), pos, f, 1.0, inter)
         q.copy_(before[:, 3:3 + hq * dim].unflatten(1, (hq, dim)))
         k.copy_(before[:, 3 + hq * dim:3 + (hq + hk) * dim].unflatten(1, (hk, dim)))
         assert torch.equal(buf, before)
@@ -110,7 +119,7 @@ def test_rotation_in_place_and_strided(sv, inter, dtype):
         o = torch.empty(hq, N, dim, dtype=dtype, device="cuda").transpose(0, 1)
         a, _ = sv.rope(t, None, pos.cuda(), rope_of(sv, f, 1.0, inter), out=(o, None))
         torch.cuda.synchronize()
-        near(a, do.rotate(t.cpu().double().numpy(), pos.numpy(), f, 1.0, inter), dtype)
+        near(a, t, pos, f, 1.0, inter)
 
 
 def test_rotation_refusals(sv):
@@ -196,7 +205,7 @@ def test_rotated_writes(sv, hq, heads, dim, rot, inter, dtype):
         c.write(do.rotate(key.double().numpy(), pos.numpy(), f, 1.1, inter), val.double().numpy(), slots.tolist())
         assert c.same()
         if hq:
-            near(out, do.rotate(q.double().numpy(), pos.numpy(), f, 1.1, inter), dtype)
+            near(out, q, pos, f, 1.1, inter)
             d = q.cuda()
             assert sv.rope_kv_write(c.dev, d, key.cuda(), val.cuda(), pos.cuda(), slots.cuda(), r, q_out=d) is d
             torch.cuda.synchronize()
@@ -283,7 +292,7 @@ def test_strided_sources(sv, dtype):
     torch.cuda.synchronize()
     c.write(do.rotate(key.double().numpy(), pos.numpy(), f, 1.0, False), val.double().numpy(), slots.tolist())
     assert c.same()
-    near(out, do.rotate(q.double().numpy(), pos.numpy(), f, 1.0, False), dtype)
+    near(out, q, pos, f, 1.0, False)
     assert torch.equal(d.cpu(), buf)
 
 
@@ -347,7 +356,7 @@ def test_prompts_take_other_shares(sv):
         assert torch.equal(whole, torch.cat(parts)) and torch.equal(whole, a)
         for n in ("k", "v", "k_scale", "v_scale"):
             assert torch.equal(getattr(one, n), getattr(two, n))
-        near(whole[:40], do.rotate(q[:40].cpu().double().numpy(), np.arange(40), f, 1.0, inter), BF16)
+        near(whole[:40], q[:40], np.arange(40), f, 1.0, inter)
 
 
 def test_replays_and_streams(sv):

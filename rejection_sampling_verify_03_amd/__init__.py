@@ -1050,21 +1050,23 @@ class KVCache4:
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "block_size", "heads", "head_dim", "device", "args")
 
     def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
         if k.dim() != 4 or k_scale.dim() != 4:
             raise ValueError("codes must be [num_blocks, block_size, heads, head_dim / 2], scales [num_blocks, heads, "
                              "head_dim / 32, block_size]")
-        torch = _torch()
-        if k.dtype not in (torch.uint8, torch.float4_e2m1fn_x2) or v.dtype != k.dtype or \
-                k_scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or v_scale.dtype != k_scale.dtype:
+        u8, code, scale = torch.uint8, k.dtype, k_scale.dtype
+        if code != u8 and code != torch.float4_e2m1fn_x2 or v.dtype != code or \
+                scale != u8 and scale != torch.float8_e8m0fnu or v_scale.dtype != scale:
             raise TypeError("codes must be uint8 or float4_e2m1fn_x2, scales uint8 or float8_e8m0fnu, alike for k and v")
-        _int32(*k.shape)
+        nb, bs, heads, half = shape = k.shape
+        _int32(nb, bs, heads, half)
         dev = _gpu_device(k)
         if v.device != dev or k_scale.device != dev or v_scale.device != dev:
             raise ValueError("all tensors must be on the same GPU")
-        nb, bs, heads, half = k.shape
-        st, sst = k.stride(), k_scale.stride()
-        if v.shape != k.shape or v.stride() != st or v_scale.shape != k_scale.shape or v_scale.stride() != sst or \
-                k_scale.shape != (nb, heads, half // 16, bs) or half % 16:
+        st, sst, groups = k.stride(), k_scale.stride(), half // 16
+        want = (nb, heads, groups, bs)
+        if v.shape != shape or v.stride() != st or v_scale.shape != want or v_scale.stride() != sst or \
+                k_scale.shape != want or half % 16:
             raise ValueError("k and v (and their scales) must agree in shape and strides")
         if st[3] != 1 or sst[3] != 1 or (half > 16 and sst[2] != bs):
             raise ValueError("codes must be contiguous along head_dim, the scales of a block and head too")
@@ -1072,7 +1074,7 @@ class KVCache4:
         self.num_blocks, self.block_size, self.heads, self.head_dim, self.device = nb, bs, heads, 2 * half, dev
         self.args = SpecKV4Cache(nb, bs, heads, 2 * half, k.data_ptr(), v.data_ptr(), st[0], st[1],
                                  st[2] if heads > 1 else half, k_scale.data_ptr(), v_scale.data_ptr(), sst[0],
-                                 sst[1] if heads > 1 else half // 16 * bs)
+                                 sst[1] if heads > 1 else groups * bs)
 
 
 def make_kv4_cache(num_blocks, block_size, heads, head_dim, device="cuda"):
@@ -1141,7 +1143,8 @@ def kv_read(cache, slots, dtype=None, stream=None, out=None):
     with _on(cache.device, stream) as s:
         if out is None:
             dt = torch.bfloat16 if dtype is None else dtype
-            key, value = torch.empty(shape, dtype=dt, device=dev), torch.empty(shape, dtype=dt, device=dev)
+            key = torch.empty(shape, dtype=dt, device=dev)
+            value = torch.empty_like(key)
         else:
             key, value = out
             dt = key.dtype if dtype is None else dtype
@@ -1229,12 +1232,12 @@ class Rope:
     GPU, the angle of each pair at position 1; scale, the factor of the turned
     elements; interleaved: pairs (2 i, 2 i + 1) in place of (i, i + rot_dim / 2).
     make_rope gives the usual tables."""
-    __slots__ = ("inv_freq", "scale", "interleaved", "rot_dim", "ptr")
+    __slots__ = ("inv_freq", "scale", "interleaved", "rot_dim", "ptr", "device")
 
     def __init__(self, inv_freq, scale=1.0, interleaved=False):
         if inv_freq.dtype != _torch().float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous float64 [rot_dim / 2]")
-        _gpu_device(inv_freq)
+        self.device = _gpu_device(inv_freq)
         self.inv_freq, self.scale, self.interleaved = inv_freq, float(scale), bool(interleaved)
         self.rot_dim, self.ptr = 2 * inv_freq.shape[0], inv_freq.data_ptr()
 
@@ -1278,13 +1281,20 @@ def make_rope(rot_dim, base=10000.0, scaling=None, factor=1.0, trained=None, int
 
 def _heads(t, N, dim, dtype, dev, name):
     """A tensor [N, heads, dim] with unit stride along dim: its heads, address and strides."""
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != dim or (t.stride(2) != 1 and dim > 1):
+    shape, (s0, s1, s2) = t.shape, t.stride() if t.dim() == 3 else (0, 0, 0)
+    if s2 != 1 or shape[0] != N or shape[2] != dim:
         raise ValueError("%s must be [N, heads, head_dim], contiguous along head_dim" % name)
     if t.dtype != dtype:
         raise TypeError("queries and keys must share a dtype")
     if t.device != dev:
         raise ValueError("all tensors must be on the same GPU")
-    return t.shape[1], t.data_ptr(), t.stride(0), t.stride(1)
+    return shape[1], t.data_ptr(), s0, s1
+
+
+def _like(t):
+    """A new contiguous tensor of this shape, type and device."""
+    torch = _torch()
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _positions(t, N, dev):
@@ -1300,17 +1310,19 @@ def rope_args(q, k, positions, rope, q_out, k_out):
     if q.dim() != 3:
         raise ValueError("q must be [N, heads, head_dim], contiguous along head_dim")
     dev = _gpu_device(q)
-    N, _, dim = q.shape
-    _int32(*q.shape)
-    dt = _kv_dtype(q.dtype)
-    if rope.inv_freq.device != dev:
+    N, _, dim = shape = q.shape
+    _int32(*shape)
+    dtype = q.dtype
+    dt = _kv_dtype(dtype)
+    if rope.device != dev:
         raise ValueError("all tensors must be on the same GPU")
-    hq, qp, q0, q1 = _heads(q, N, dim, q.dtype, dev, "q")
-    hqo, qop, qo0, qo1 = _heads(q_out, N, dim, q.dtype, dev, "q_out")
-    hk, kp, k0, k1, hko, kop, ko0, ko1 = (0, None, 0, 0) * 2
+    hq, qp, q0, q1 = _heads(q, N, dim, dtype, dev, "q")
+    hqo, qop, qo0, qo1 = _heads(q_out, N, dim, dtype, dev, "q_out")
+    hk = hko = k0 = k1 = ko0 = ko1 = 0
+    kp = kop = None
     if k is not None:
-        hk, kp, k0, k1 = _heads(k, N, dim, q.dtype, dev, "k")
-        hko, kop, ko0, ko1 = _heads(k_out, N, dim, q.dtype, dev, "k_out")
+        hk, kp, k0, k1 = _heads(k, N, dim, dtype, dev, "k")
+        hko, kop, ko0, ko1 = _heads(k_out, N, dim, dtype, dev, "k_out")
     if hqo != hq or hko != hk:
         raise ValueError("the outputs must have the inputs' shapes")
     at, wide = _positions(positions, N, dev)
@@ -1322,12 +1334,10 @@ def rope(q, k, positions, rope, out=None, stream=None):
     """Queries and keys [N, heads, head_dim] (bfloat16 or float32; k may be
     None) turned to positions [N] int32 or int64 as `rope`, a Rope, says.  Returns (q,
     k), new tensors or those of `out`, a pair which may be (q, k) themselves."""
-    torch = _torch()
-    dev = _gpu_device(q)
-    with _on(dev, stream) as s:
+    with _on(_gpu_device(q), stream) as s:
         if out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
+            q_out = _like(q)
+            k_out = None if k is None else _like(k)
         else:
             q_out, k_out = out
         rc = lib.spec_rope_launch(rope_args(q, k, positions, rope, q_out, k_out), s)
@@ -1339,37 +1349,42 @@ def rope(q, k, positions, rope, out=None, stream=None):
 def kv4_write_args(cache, key, value, slots, positions=None, rope=None, q=None, q_out=None):
     """Fill a SpecKV4WriteArgs (no copies): key and value [N, heads, head_dim]
     with unit stride along head_dim, slots [N] int64 (-1: not written); with a
-    Rope the keys are turned to positions [N] int32 or int64 first, and queries q [N,
-    q_heads, head_dim] into q_out."""
-    torch = _torch()
+    Rope the keys are turned to positions [N] int32 or int64 first, and queries
+    q [N, q_heads, head_dim] into q_out."""
     N, dev = slots.shape[0], cache.device
     if N > 0x7fffffff:
         _int32(N)
-    shape, dim = (N, cache.heads, cache.head_dim), cache.head_dim
+    dim = cache.head_dim
+    shape = (N, cache.heads, dim)
     k0, k1, k2 = key.stride() if key.dim() == 3 else (0, 0, 0)
     v0, v1, v2 = value.stride() if value.dim() == 3 else (0, 0, 0)
     if key.shape != shape or value.shape != shape or k2 != 1 or v2 != 1:
         raise ValueError("key and value must be [N, heads, head_dim], contiguous along head_dim")
-    if key.dtype != value.dtype:
+    dtype = key.dtype
+    if dtype != value.dtype:
         raise TypeError("key and value must share a dtype")
     if key.device != dev or value.device != dev:
         raise ValueError("all tensors must be on the same GPU")
-    a = SpecKV4WriteArgs(cache.args, N, _kv_dtype(key.dtype), key.data_ptr(), value.data_ptr(), k0, k1, v0, v1,
-                         _want(slots, torch.int64, (N,), dev, "slots"))
+    at = _want(slots, _torch().int64, (N,), dev, "slots")
+    rot, inter, freq, scale, pos, wide = 0, 0, None, 0.0, None, 0
+    hq = q0 = q1 = qo0 = qo1 = 0
+    qp = qop = None
     if rope is not None:
-        if rope.inv_freq.device != dev:
+        if rope.device != dev:
             raise ValueError("all tensors must be on the same GPU")
-        a.rot_dim, a.interleaved, a.inv_freq, a.scale = rope.rot_dim, rope.interleaved, rope.ptr, rope.scale
-        a.positions, a.wide_positions = _positions(positions, N, dev)
+        rot, inter, freq, scale = rope.rot_dim, rope.interleaved, rope.ptr, rope.scale
+        pos, wide = _positions(positions, N, dev)
     if q is not None:
         if rope is None:
             raise ValueError("queries are turned as a Rope says: none is given")
-        _int32(*q.shape)
-        a.q_heads, a.q, a.q_token_stride, a.q_head_stride = _heads(q, N, dim, key.dtype, dev, "q")
-        n, a.q_out, a.q_out_token_stride, a.q_out_head_stride = _heads(q_out, N, dim, key.dtype, dev, "q_out")
-        if n != a.q_heads:
+        hq, qp, q0, q1 = _heads(q, N, dim, dtype, dev, "q")
+        n, qop, qo0, qo1 = _heads(q_out, N, dim, dtype, dev, "q_out")
+        if n != hq:
             raise ValueError("the output must have the queries' shape")
-    return a
+        if hq > 0x7fffffff:
+            _int32(hq)
+    return SpecKV4WriteArgs(cache.args, N, _kv_dtype(dtype), key.data_ptr(), value.data_ptr(), k0, k1, v0, v1, at, rot,
+                            inter, freq, scale, pos, wide, hq, qp, q0, q1, qop, qo0, qo1)
 
 
 def rope_kv_write(cache, q, key, value, positions, slots, rope, q_out=None, stream=None):
@@ -1383,7 +1398,7 @@ def rope_kv_write(cache, q, key, value, positions, slots, rope, q_out=None, stre
         raise TypeError("the cache must be a KVCache4 (for a KVCache: rope(), then kv_write())")
     with _on(cache.device, stream) as s:
         if q is not None and q_out is None:
-            q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _like(q)
         rc = lib.spec_kv4_write_launch(kv4_write_args(cache, key, value, slots, positions, rope, q, q_out), s)
     if rc != SPEC_OK:
         raise SpecError(rc)
@@ -1391,8 +1406,14 @@ def rope_kv_write(cache, q, key, value, positions, slots, rope, q_out=None, stre
 
 
 # --------------------------------------- sampling from cut distributions
-def _per_request(t, dtype, B, dev, name):
-    return None if t is None else _want(t, dtype, (B,), dev, name)
+def _settings(temperature, top_k, top_p, min_p, B, dev):
+    """The addresses of each request's settings."""
+    torch = _torch()
+    f32, shape = torch.float32, (B,)
+    return (_want(temperature, f32, shape, dev, "temperature"),
+            None if top_k is None else _want(top_k, torch.int32, shape, dev, "top_k"),
+            None if top_p is None else _want(top_p, f32, shape, dev, "top_p"),
+            None if min_p is None else _want(min_p, f32, shape, dev, "min_p"))
 
 
 def sample_args(logits, uniforms, temperature, top_k, top_p, min_p, tokens, workspace, row_index=None):
@@ -1404,26 +1425,24 @@ def sample_args(logits, uniforms, temperature, top_k, top_p, min_p, tokens, work
     dev = _gpu_device(logits)
     if logits.dim() != (3 if row_index is None else 2) or uniforms.dim() != 2:
         raise ValueError("logits must be [B, R, V] ([rows, V] with a row table), uniforms [B, R]")
-    B, R = uniforms.shape
-    V = logits.shape[-1]
-    _int32(B, R, *logits.shape)
-    st = logits.stride()
+    B, R = both = uniforms.shape
+    shape, st = logits.shape, logits.stride()
+    V = shape[-1]
+    _int32(B, R, *shape)
     if st[-1] != 1 and V > 1:
         raise ValueError("logits must have contiguous rows")
     if row_index is None:
-        if logits.shape[:2] != uniforms.shape:
+        if shape[0] != B or shape[1] != R:
             raise ValueError("logits and uniforms must agree in requests and rows")
         req, row, rows, index = st[0] if B > 1 else 0, st[1] if R > 1 else V, 0, None
     else:
-        rows = logits.shape[0]
-        req, row, index = 0, st[0] if rows > 1 else V, _want(row_index, torch.int32, (B, R), dev, "row_index")
+        rows = shape[0]
+        req, row, index = 0, st[0] if rows > 1 else V, _want(row_index, torch.int32, both, dev, "row_index")
     ws = _want_workspace(workspace, dev)
     return SpecSampleArgs(
         B, R, V, _logit_dtype(logits), logits.data_ptr(), req, row, index, rows,
-        _want(temperature, torch.float32, (B,), dev, "temperature"), _per_request(top_k, torch.int32, B, dev, "top_k"),
-        _per_request(top_p, torch.float32, B, dev, "top_p"), _per_request(min_p, torch.float32, B, dev, "min_p"),
-        _want(uniforms, torch.float32, (B, R), dev, "uniforms"), _want(tokens, torch.int32, (B, R), dev, "tokens"),
-        ws[0], ws[1])
+        *_settings(temperature, top_k, top_p, min_p, B, dev), _want(uniforms, torch.float32, both, dev, "uniforms"),
+        _want(tokens, torch.int32, both, dev, "tokens"), ws[0], ws[1])
 
 
 def sample(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None, row_index=None, workspace=None,
@@ -1439,11 +1458,12 @@ def sample(logits, uniforms, temperature, top_k=None, top_p=None, min_p=None, ro
     dev = _gpu_device(logits)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(uniforms.shape, dtype=torch.int32, device=dev)
+            out = torch.empty_like(uniforms, dtype=torch.int32)
         if workspace is None:
             B, R = uniforms.shape if uniforms.dim() == 2 else (0, 0)
-            workspace = torch.empty(max(spec_sample_workspace_bytes(B, R, logits.shape[-1]), 16), dtype=torch.uint8,
-                                    device=dev)
+            n = spec_sample_workspace_bytes(B, R, logits.shape[-1])
+            if n:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         rc = lib.spec_sample_launch(sample_args(logits, uniforms, temperature, top_k, top_p, min_p, out, workspace,
                                                 row_index), s)
     if rc != SPEC_OK:
@@ -1468,9 +1488,7 @@ def truncate_args(logits, temperature, top_k, top_p, min_p, out, workspace):
     s0, s1, o0, o1 = s0 if B > 1 else 0, s1 if R > 1 else V, o0 if B > 1 else 0, o1 if R > 1 else V
     ws = _want_workspace(workspace, dev)
     return SpecTruncateArgs(
-        B, R, V, _logit_dtype(logits), logits.data_ptr(), s0, s1,
-        _want(temperature, torch.float32, (B,), dev, "temperature"), _per_request(top_k, torch.int32, B, dev, "top_k"),
-        _per_request(top_p, torch.float32, B, dev, "top_p"), _per_request(min_p, torch.float32, B, dev, "min_p"),
+        B, R, V, _logit_dtype(logits), logits.data_ptr(), s0, s1, *_settings(temperature, top_k, top_p, min_p, B, dev),
         out.data_ptr(), o0, o1, ws[0], ws[1])
 
 
@@ -1486,7 +1504,7 @@ def truncate_logits(logits, temperature, top_k=None, top_p=None, min_p=None, wor
         raise ValueError("logits must be [B, R, V]")
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            out = _like(logits)
         if workspace is None:
             workspace = torch.empty(max(spec_sample_workspace_bytes(*logits.shape), 16), dtype=torch.uint8, device=dev)
         rc = lib.spec_truncate_launch(truncate_args(logits, temperature, top_k, top_p, min_p, out, workspace), s)

@@ -350,9 +350,10 @@ size_t cut_ws_bytes(int32_t B, int32_t R) {
 
 bool cut_shape_ok(int32_t B, int32_t R, int32_t V) {
   if (B < 0 || R < 0 || V < 1 || V > SPEC_MAX_V) return false;
-  const int64_t rows = (int64_t)B * R, nseg = ((int64_t)V + kSeg - 1) / kSeg;
-  const int64_t C = (nseg + kCutChunkSegs - 1) / kCutChunkSegs;
-  return rows <= INT32_MAX && rows * C <= INT32_MAX && fits_dispatch(rows * C, kThreads) && fits_dispatch(rows, 1024);
+  const int64_t rows = (int64_t)B * R;
+  if (rows > INT32_MAX) return false;
+  const int64_t chunk = cut_chunk(rows, V), C = ((int64_t)V + chunk - 1) / chunk;
+  return rows * C <= INT32_MAX && fits_dispatch(rows * C, kThreads) && fits_dispatch(rows, 1024);
 }
 
 // The sizes, settings and workspace that a sampling and a truncation share.
@@ -375,7 +376,8 @@ CutParams cut_params(const Args* a) {
   P.B = a->B;
   P.R = a->R;
   P.V = a->V;
-  P.C = (int32_t)((((int64_t)a->V + kSeg - 1) / kSeg + kCutChunkSegs - 1) / kCutChunkSegs);
+  P.chunk = cut_chunk((int64_t)a->B * a->R, a->V);
+  P.C = (int32_t)(((int64_t)a->V + P.chunk - 1) / P.chunk);
   while (((int64_t)1 << P.ibits) < a->V) ++P.ibits;
   // V weights of at most 2^frac within 63 bits, eight within the 52 of a double
   int bits = P.ibits;

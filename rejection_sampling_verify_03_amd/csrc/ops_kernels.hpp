@@ -58,12 +58,14 @@ struct LogprobsParams {
 hipError_t launch_logprobs(const LogprobsParams& P, int dtype, hipStream_t stream);
 
 // ------------------------------------- sampling from cut distributions --
-constexpr int kCutChunkSegs = 8;         // segments per workgroup of the pass that writes cut rows
+// Logits to a workgroup of the pass that writes cut rows: many, but few where
+// they would not fill the card (18 rows of 32001 fp32 logits: 14 us with 32768).
+inline int32_t cut_chunk(int64_t rows, int32_t V) { return rows * (((int64_t)V + 16383) / 16384) >= 1024 ? 16384 : 2048; }
 constexpr uint64_t kCutAll = ~1ull;      // a row's last kept key: the row stays as it is
 constexpr uint64_t kCutBad = ~0ull;      // its settings cannot be used
 
 struct CutParams {
-  int32_t B, R, V, C;   // C: chunks of kCutChunkSegs segments per row
+  int32_t B, R, V, chunk, C;  // C: chunks of so many logits per row
   int32_t ibits, frac;       // bits of an index; weights are whole numbers of 2^-frac
   FastDiv by_C, by_R;
   const char* logits;

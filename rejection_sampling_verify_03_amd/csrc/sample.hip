@@ -70,15 +70,18 @@ __device__ __forceinline__ const char* row_of(const CutParams& P, int b, int r, 
   return P.logits + ((int64_t)b * P.req + (int64_t)r * P.row) * es;
 }
 
-// 2^(t + add) for t <= 0 (from -1100 on as 0 for every add below 48): by the
-// nearest whole exponent and the power series of 2^f, |f| <= 1/2, whose terms
-// left out are below 2^-47 of it.
-__device__ __forceinline__ double pow2(double t, int add) {
-  constexpr double L = 0.693147180559945309417;
+// 2^(t + frac) for t <= 0 as a whole number below 2^52, rounded to nearest: by
+// the nearest whole exponent and the power series of 2^f, |f| <= 1/2, whose terms
+// left out are below 2^-47 of it.  (Adding 1.5 * 2^52 rounds to a whole number,
+// which its low word then holds: conversions and fp64 scaling are slow here.)
+__device__ __forceinline__ double whole_pow2(double t, int frac) {
+  constexpr double kRound = 0x1.8p52, L = 0.693147180559945309417;
   constexpr double c2 = L * L / 2, c3 = c2 * L / 3, c4 = c3 * L / 4, c5 = c4 * L / 5, c6 = c5 * L / 6, c7 = c6 * L / 7,
                    c8 = c7 * L / 8, c9 = c8 * L / 9, c10 = c9 * L / 10, c11 = c10 * L / 11;
-  t = fmax(t, -1100.0);
-  const double n = __builtin_rint(t), f = t - n;
+  t = fmax(t, -56.0);  // (below that nothing is left of it: frac is at most 48)
+  const double r = t + kRound;
+  const int n = (int)(uint32_t)__double_as_longlong(r);
+  const double f = t - (r - kRound);
   double y = c11;
   y = __builtin_fma(y, f, c10);
   y = __builtin_fma(y, f, c9);
@@ -91,13 +94,14 @@ __device__ __forceinline__ double pow2(double t, int add) {
   y = __builtin_fma(y, f, c2);
   y = __builtin_fma(y, f, L);
   y = __builtin_fma(y, f, 1.0);
-  return ldexp(y, (int)n + add);
+  const uint64_t u = (uint64_t)__double_as_longlong(y) + ((uint64_t)(uint32_t)(n + frac) << 52);
+  return __longlong_as_double((long long)u) + 0x1p52;  // (rounds)
 }
 
+// The whole number that a value between 2^52 and 2^53 is above 2^52.
+__device__ __forceinline__ u64 above52(double y) { return (u64)__double_as_longlong(y) & ((1ull << 52) - 1); }
 // A value below 2^52 as a whole number, rounded to nearest.
-__device__ __forceinline__ u64 whole(double y) {
-  return (u64)__double_as_longlong(y + 0x1p52) & ((1ull << 52) - 1);
-}
+__device__ __forceinline__ u64 whole(double y) { return above52(y + 0x1p52); }
 
 // The place of a logit among all values of its type, larger for a larger one
 // (-0 as +0): 16 bits of a bf16, 32 of an fp32.
@@ -247,6 +251,7 @@ struct CutShared {
   u64 wave[2][16];
   float wave_f[16];
   uint32_t wave_u[16];
+  alignas(16) float tail[8];  // the row's last group, if that is not whole, filled up with -inf
   u64 before, through, special[3];
   int bin, count;
 };
@@ -260,8 +265,10 @@ __device__ __forceinline__ void slots8(const RawGroup<2, true>& g, uint32_t (&sl
     const u16x2 lo = (uint16_t)(B::kLo - 1), hi = (uint16_t)B::kHi, half = (uint16_t)B::kHalf;
     const uint32_t two = g.v[i];
     u16x2 mag = __builtin_bit_cast(u16x2, two & 0x7fff7fffu);
-    const u16x2 sign = __builtin_bit_cast(u16x2, two) >> (uint16_t)15;
-    mag = __builtin_elementwise_min(__builtin_elementwise_max(mag, lo), hi) - lo + sign * half;
+    uint32_t signs = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, two) >> (uint16_t)15);
+    asm volatile("" : "+v"(signs));  // (kept a factor: a choice between two values takes five instructions for two)
+    const u16x2 sign = __builtin_bit_cast(u16x2, signs);
+    mag = sign * half + (__builtin_elementwise_min(__builtin_elementwise_max(mag, lo), hi) - lo);
     const uint32_t both = __builtin_bit_cast(uint32_t, mag);
     slot[2 * i] = both & 0xffffu;
     slot[2 * i + 1] = both >> 16;
@@ -352,13 +359,35 @@ struct CutRow {
   __device__ __forceinline__ u64 bin_end(int bin) const { return rank_key(B::least(bin), 0) | index_mask(); }
 
   // The weight of a logit, a whole number.
-  __device__ __forceinline__ double weight_of(float x) const {
-    return __builtin_rint(pow2(((double)x - (double)m) * s, frac));
-  }
-  __device__ __forceinline__ u64 mass_of(float x) const { return whole(weight_of(x)); }
+  __device__ __forceinline__ double exponent(float x) const { return ((double)x - (double)m) * s; }
+  __device__ __forceinline__ double weight_of(float x) const { return whole_pow2(exponent(x), frac) - 0x1p52; }
+  __device__ __forceinline__ u64 mass_of(float x) const { return above52(whole_pow2(exponent(x), frac)); }
 
   // Whether logits of -2^7 and below (the last bin's) may have a weight.
   __device__ __forceinline__ bool low_weighs() const { return ((double)m + 128.0) * s < frac + 2; }
+
+  __device__ __forceinline__ void read_tail() const {
+    if (threadIdx.x < 8) {
+      const int e = (V & ~7) + threadIdx.x;
+      S.tail[threadIdx.x] = e < V ? load_one<ES>(lg, e) : -INFINITY;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ RawGroup<ES, true> tail() const {
+    RawGroup<ES, true> g;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(S.tail), b = *reinterpret_cast<const f32x4*>(S.tail + 4);
+    if constexpr (ES == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+        g.v[i] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xffff0000u);
+      }
+    } else {
+      g.a = a;
+      g.b = b;
+    }
+    return g;
+  }
 
   // f(raw, e) for the groups of 8 logits from index e on that hold some of
   // [first, last]; past the row's end -inf.
@@ -372,10 +401,10 @@ struct CutRow {
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) next[q] = load_any<ES>(lg, (int64_t)min(g0 + q * NT, full - 1) * 8);
       }
-      if (g1 > full) {  // the row's last group is not whole
+      if (g1 > full) {
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
-          if (g0 + q * NT == full) next[q] = load_end<ES>(lg, (int64_t)full * 8, V);
+          if (g0 + q * NT == full) next[q] = tail();
       }
     };
     int g0 = (first >> 3) + threadIdx.x;
@@ -526,18 +555,33 @@ struct CutRow {
     }
   }
 
+  // A sum of the group at e to its range, 2^shift >= 8 indices wide: the lanes of a
+  // range (wide enough, and lane order is index order) joined first, as they
+  // would all add in one place.  (The lanes at work are a prefix of the wave's.)
+  __device__ __forceinline__ void add_range(u64* ranges, int at, int shift, double sum) const {
+    const int lane = threadIdx.x & 63;
+    if (shift >= 7) {
+      sum += dpp_d0<0x111, 0xf>(sum);
+      sum += dpp_d0<0x112, 0xf>(sum);
+      sum += dpp_d0<0x114, 0xf>(sum);
+      sum += dpp_d0<0x118, 0xf>(sum);
+      const int last = 63 - __builtin_clzll(__ballot(true));
+      if ((lane & 15) != 15 && lane != last) return;
+    }
+    if (sum > 0.0) atomicAdd(&ranges[at], whole(sum));
+  }
+
   // The index in [lo, hi] at which the sum, with `offset` in front, reaches the
-  // border: sums over ranges of indices, then inside the range.  pass(lo, hi, f) calls f(e, sum) for the
-  // groups of [lo, hi] with their sum; one(x, e) is the part of a single logit.
+  // border: sums over ranges of indices, then inside the range.  pass(lo, hi, f)
+  // calls f(e, sum) for the groups of [lo, hi] with their sum (all lanes of a
+  // wave that have a group, or none); one(x, e) is the part of a single logit.
   template <class Pass, class One>
   __device__ __forceinline__ int search_index(int lo, int hi, Border border, u64 offset, Pass pass, One one) const {
     for (;;) {
       const int shift = max(bits_of((u64)(hi - lo)) - kRangeBits, 0);
       clear_ranges();
       if (shift >= 3) {  // (ranges of whole groups)
-        pass(lo, hi, [&](int e, double sum) {
-          if (sum > 0.0) atomicAdd(&S.ranges[(e - lo) >> shift], (u64)sum);
-        });
+        pass(lo, hi, [&](int e, double sum) { add_range(S.ranges, (e - lo) >> shift, shift, sum); });
       } else {
         each_group(lo, hi, [&](const RawGroup<ES, true>& raw, int e) {
           float x[8];
@@ -546,7 +590,7 @@ struct CutRow {
           for (int q = 0; q < 8; ++q)
             if (e + q >= lo && e + q <= hi) {
               const double y = one(x[q], e + q);
-              if (y > 0.0) atomicAdd(&S.ranges[(e + q - lo) >> shift], (u64)y);
+              if (y > 0.0) atomicAdd(&S.ranges[(e + q - lo) >> shift], whole(y));
             }
         });
       }
@@ -625,6 +669,15 @@ struct CutRow {
     return search_lds<false, MASS>(n, last, lo, hi, to, offset);
   }
 
+  // Whether a logit's key is at most `last`.
+  struct Upto {
+    float x;
+    int at;
+    __device__ __forceinline__ Upto(const CutRow& w, u64 last)
+        : x(last == kNone ? -INFINITY : w.key_logit(last)), at(last == kNone ? INT_MAX : (int)(last & w.index_mask())) {}
+    __device__ __forceinline__ bool operator()(float y, int e) const { return y > x || (y == x && e <= at); }
+  };
+
   // The c-th logit, by its index, among those in [lo, hi] equal to the value of a
   // bin: its key of rank.
   __device__ __forceinline__ u64 search_equal(int lo, int hi, int bin, u64 c) const {
@@ -651,6 +704,7 @@ template <int ES, int NT, bool SMALL, bool DRAW>
 __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
   using B = Bins<ES>;
   using Row = CutRow<ES, NT, SMALL>;
+  using Upto = typename Row::Upto;
   __shared__ CutShared<SMALL> S;
   const int i = blockIdx.x, tid = threadIdx.x;
   const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
@@ -667,6 +721,8 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
   };
   if (!cut.ok || !w.lg || (DRAW && !(u >= 0.0f && u < 1.0f))) return end(-1, kCutBad);
   if (!DRAW && (cut.greedy || cut.all)) return end(-1, kCutAll);
+
+  w.read_tail();
 
   if (DRAW && cut.greedy) {
     VI best{-INFINITY, INT_MAX};
@@ -805,21 +861,33 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
       if constexpr (ES == 4)
         for (int j = tid; j < B::kSlots; j += NT) masses[j] = 0;
       const bool low = counts[B::slot_of(B::kN - 1)] != 0 && w.low_weighs();
-      const bool some = ES == 4 || counts[B::slot_of(0)] != 0 || counts[B::slot_of(B::kMid)] != 0 || low;
+      const bool some = counts[B::slot_of(0)] != 0 || counts[B::slot_of(B::kMid)] != 0 || low;
       __syncthreads();
-      if (some)
+      const Upto stays(w, last);
+      if (ES == 4) {
         w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
           float x[8];
           unpack_group<ES, true>(raw, x);
-#pragma unroll 2
+#pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const int bin = B::of(x[q]);
-            if (!B::single(bin) && w.rank_key(x[q], e + q) <= last) {
-              const u64 y = w.mass_of(x[q]);
-              if (y) atomicAdd(ES == 4 ? &masses[B::slot_of(bin)] : &S.special[bin == 0 ? 0 : bin == B::kMid ? 1 : 2], y);
-            }
+            const u64 y = stays(x[q], e + q) ? w.mass_of(x[q]) : 0;
+            if (y) atomicAdd(&masses[B::slot(x[q])], y);  // (the slots of the middle bin are added up below)
           }
         });
+        __syncthreads();
+        if (tid == 0) masses[0] += masses[B::kHalf];
+      } else if (some) {
+        w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+          float x[8];
+          unpack_group<ES, true>(raw, x);
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            const int bin = B::of(x[q]);
+            if (!B::single(bin) && stays(x[q], e + q))
+              atomicAdd(&S.special[bin == 0 ? 0 : bin == B::kMid ? 1 : 2], w.mass_of(x[q]));
+          }
+        });
+      }
       auto mass = [&](int j) -> u64 {
         const int bin = j0 + j;
         if constexpr (ES == 4) return masses[B::slot_of(bin)];
@@ -878,7 +946,8 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
   if (held) return end((int)w.template search_lds<true, true>(n, last, 0, (u64)P.V - 1, above, 0), 0);
   if constexpr (!SMALL) {
     const float floor = last == kNone ? -INFINITY : w.key_logit(last);
-    auto one = [&](float x, int e) { return w.rank_key(x, e) <= last ? w.weight_of(x) : 0.0; };
+    Upto stays(w, last);
+    auto one = [&](float x, int e) { return stays(x, e) ? w.weight_of(x) : 0.0; };
     int token;
     if constexpr (ES == 2) {
       // the weight of each bin, 0 behind the last kept one's and for bins of
@@ -912,7 +981,7 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
       };
       auto pass = [&](int l, int h, auto f) {
         w.each_group(l, h, [&](const RawGroup<2, true>& raw, int e) {
-          if (!kept.reached(raw)) return;
+          if (!__ballot(kept.reached(raw))) return;
           uint32_t slot[8];
           slots8(raw, slot);
           double sum = sum_of(raw, slot, e);
@@ -932,13 +1001,13 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
         w.clear_ranges();
         const uint32_t end_slot = (uint32_t)B::slot_of(tie_bin);
         w.each_group(0, P.V - 1, [&](const RawGroup<2, true>& raw, int e) {
-          if (!kept.reached(raw)) return;
+          if (!__ballot(kept.reached(raw))) return;
           uint32_t slot[8], same = 0;
           slots8(raw, slot);
 #pragma unroll
           for (int q = 0; q < 8; ++q) same += slot[q] == end_slot;
           const double sum = sum_of(raw, slot, e);
-          if (sum > 0.0) atomicAdd(&S.ranges[e >> shift], (u64)sum);
+          w.add_range(S.ranges, e >> shift, shift, sum);
           if (same) atomicAdd(&equal[e >> shift], same);
         });
         constexpr int kMine = kRanges / NT;
@@ -952,7 +1021,7 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
             [](int) { return (u64)0; });
         // what is left lies in a range each: its logits one by one
         const int size = 1 << shift, l = c.bin << shift, l2 = d.bin << shift;
-        last = w.search_equal(l, min(P.V - 1, l + size - 1), tie_bin, stay);
+        stays = Upto(w, w.search_equal(l, min(P.V - 1, l + size - 1), tie_bin, stay));
         token = w.search_index(l2, min(P.V - 1, l2 + size - 1), Border{Border::kFixed, d.border, 0.0}, d.before,
                                [&](int a, int z, auto f) {
                                  w.each_group(a, z, [&](const RawGroup<2, true>& raw, int e) {
@@ -974,11 +1043,11 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
           0, P.V - 1, above, 0,
           [&](int l, int h, auto f) {
             w.each_group(l, h, [&](const RawGroup<4, true>& raw, int e) {
-              if (!kept.reached(raw)) return;
+              if (!__ballot(kept.reached(raw))) return;
               float x[8];
               unpack_group<4, true>(raw, x);
               double sum = 0.0;
-#pragma unroll 2
+#pragma unroll 4
               for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
               f(e, sum);
             });
@@ -999,9 +1068,9 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
   char* dst = P.out + ((int64_t)b * P.out_req + (int64_t)r * P.out_row) * ES;
   if (last == kCutAll && src == dst) return;
   const float fill = last == kCutBad ? __builtin_nanf("") : -INFINITY;
-  const int64_t e1 = min((int64_t)P.V, ((int64_t)chunk + 1) * kCutChunkSegs * kSeg);
-  for (int64_t e = (int64_t)chunk * kCutChunkSegs * kSeg + threadIdx.x * 8; e < e1; e += kWG * 8) {
-    RawGroup<ES, true> g = load_end<ES>(src, e, P.V);
+  const int64_t e0 = (int64_t)chunk * P.chunk, e1 = min((int64_t)P.V, e0 + P.chunk);
+  for (int64_t e = e0 + threadIdx.x * 8; e < e1; e += kWG * 8) {
+    const RawGroup<ES, true> g = load_end<ES>(src, e, P.V);
     bool some = false;
     float x[8];
     unpack_group<ES, true>(g, x);

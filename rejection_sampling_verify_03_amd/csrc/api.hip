@@ -563,9 +563,9 @@ bool attn_sizes_ok(const spec_attn_args* a) {
   return (int64_t)a->B * c.heads <= INT32_MAX;  // (times the blocks of rows, at most 2^26, within 64 bits)
 }
 
-AttnPlan attn_plan(const spec_attn_args* a) {
+AttnPlan attn_plan(const spec_attn_args* a, bool four) {
   return plan_attn(a->B, a->q_heads / a->cache.heads, a->cache.heads, a->cache.head_dim, a->max_q, a->max_ctx,
-                   a->window, a->cache.head_stride < a->cache.token_stride);
+                   a->window, a->cache.head_stride < a->cache.token_stride, four);
 }
 
 size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
@@ -576,7 +576,7 @@ size_t attn_ws_bytes(const spec_attn_args* a, const AttnPlan& p) {
 }
 
 // cache_rc: what the check of the cache says.
-int attn_check(const spec_attn_args* a, int cache_rc, AttnPlan& plan) {
+int attn_check(const spec_attn_args* a, int cache_rc, bool four, AttnPlan& plan) {
   if (!attn_sizes_ok(a)) return SPEC_EINVAL;
   if (a->dtype != SPEC_BF16) return SPEC_EDTYPE;
   if (cache_rc != SPEC_OK) return cache_rc;
@@ -587,7 +587,7 @@ int attn_check(const spec_attn_args* a, int cache_rc, AttnPlan& plan) {
   if (a->max_blocks > 0 && !a->block_table) return SPEC_EINVAL;
   if (a->q_token_stride < 0 || a->q_head_stride < 0) return SPEC_EINVAL;
   if (!aligned16(a->out)) return SPEC_EALIGN;
-  plan = attn_plan(a);
+  plan = attn_plan(a, four);
   const int64_t grid = (int64_t)a->B * a->cache.heads * plan.nrb;
   if (grid > INT32_MAX || !fits_dispatch((plan.groups + 7) / 8 * 8 * plan.items, kThreads) ||
       (plan.chunks > 0 && !fits_dispatch(grid * plan.rt, kThreads)))
@@ -1003,13 +1003,13 @@ int spec_kv_read_launch(const spec_kv_read_args* a, hipStream_t stream) {
 
 size_t spec_attn_workspace_bytes(const spec_attn_args* a) {
   if (!a || !attn_sizes_ok(a)) return 0;
-  return attn_ws_bytes(a, attn_plan(a));
+  return attn_ws_bytes(a, attn_plan(a, false));
 }
 
 int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
   if (!a) return SPEC_EINVAL;
   AttnPlan plan;
-  const int rc = attn_check(a, cache_check(a->cache), plan);
+  const int rc = attn_check(a, cache_check(a->cache), false, plan);
   if (rc != SPEC_OK || a->B == 0 || a->N == 0) return rc;
   return attn_launch(a, plan, cache_view(a->cache), false, stream);
 }
@@ -1017,14 +1017,14 @@ int spec_attn_launch(const spec_attn_args* a, hipStream_t stream) {
 size_t spec_attn4_workspace_bytes(const spec_attn4_args* a) {
   if (!a || a->cache.head_dim % 32) return 0;
   const spec_attn_args b = attn_of(a);
-  return spec_attn_workspace_bytes(&b);
+  return attn_sizes_ok(&b) ? attn_ws_bytes(&b, attn_plan(&b, true)) : 0;
 }
 
 int spec_attn4_launch(const spec_attn4_args* a, hipStream_t stream) {
   if (!a) return SPEC_EINVAL;
   const spec_attn_args b = attn_of(a);
   AttnPlan plan;
-  const int rc = attn_check(&b, cache4_check(a->cache), plan);
+  const int rc = attn_check(&b, cache4_check(a->cache), true, plan);
   if (rc != SPEC_OK || a->B == 0 || a->N == 0) return rc;
   return attn_launch(&b, plan, cache4_view(a->cache), true, stream);
 }

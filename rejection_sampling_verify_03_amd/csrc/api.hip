@@ -344,8 +344,9 @@ int kv_read_check(const spec_kv_read_args* a) {
 }
 
 // ------------------------------------------------ sampling, 4-bit cache, rotation
-size_t cut_ws_bytes(int32_t B, int32_t R) {
-  return align256((size_t)B * R * sizeof(uint64_t));
+size_t cut_ws_bytes(int32_t B, int32_t R, int32_t V) {
+  const size_t rows = (size_t)B * R;
+  return align256(rows * sizeof(uint64_t)) + rows * cut_split_row(cut_parts((int64_t)rows, V, 4));
 }
 
 bool cut_shape_ok(int32_t B, int32_t R, int32_t V) {
@@ -366,7 +367,7 @@ int cut_check(const Args* a, bool rowless) {
   if ((!a->logits && !rowless) || !a->temperature || !a->workspace) return SPEC_EINVAL;
   if (a->row_stride < a->V) return SPEC_EINVAL;
   if (!aligned16(a->workspace)) return SPEC_EALIGN;
-  if (a->workspace_bytes < cut_ws_bytes(a->B, a->R)) return SPEC_EWORKSPACE;
+  if (a->workspace_bytes < cut_ws_bytes(a->B, a->R, a->V)) return SPEC_EWORKSPACE;
   return SPEC_OK;
 }
 
@@ -393,6 +394,16 @@ CutParams cut_params(const Args* a) {
   P.top_p = a->top_p;
   P.min_p = a->min_p;
   P.last = static_cast<uint64_t*>(a->workspace);
+  const size_t rows = (size_t)a->B * a->R;
+  P.parts = cut_parts((int64_t)rows, a->V, a->dtype == SPEC_BF16 ? 2 : 4);
+  if (P.parts > 1) {  // (whole ranges of indices to a part)
+    const int64_t range = (int64_t)1 << (P.ibits > kCutRangeBits ? P.ibits - kCutRangeBits : 0);
+    const int64_t ranges = (a->V + range - 1) / range;
+    P.seg = (int32_t)((ranges + P.parts - 1) / P.parts * range);
+    P.split_row = (int64_t)cut_split_row(P.parts);
+    P.parts = (int32_t)(((int64_t)a->V + P.seg - 1) / P.seg);
+    P.split = static_cast<char*>(a->workspace) + align256(rows * sizeof(uint64_t));
+  }
   return P;
 }
 
@@ -1043,7 +1054,7 @@ int spec_sample_launch(const spec_sample_args* a, hipStream_t stream) {
 }
 
 size_t spec_sample_workspace_bytes(int32_t B, int32_t R, int32_t V) {
-  return cut_shape_ok(B, R, V) ? cut_ws_bytes(B, R) : 0;
+  return cut_shape_ok(B, R, V) ? cut_ws_bytes(B, R, V) : 0;
 }
 
 int spec_truncate_launch(const spec_truncate_args* a, hipStream_t stream) {

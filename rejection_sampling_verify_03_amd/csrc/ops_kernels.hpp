@@ -64,8 +64,38 @@ inline int32_t cut_chunk(int64_t rows, int32_t V) { return rows * (((int64_t)V +
 constexpr uint64_t kCutAll = ~1ull;      // a row's last kept key: the row stays as it is
 constexpr uint64_t kCutBad = ~0ull;      // its settings cannot be used
 
+constexpr int kCutRangeBits = 10, kCutRanges = 1 << kCutRangeBits, kCutCand = 2048, kCutParts = 8;
+// What the workgroups of a row leave for each other, where several share it.
+// Behind it stand their counts, and (fp32 logits) masses.
+struct alignas(16) SplitRow {
+  uint64_t last, before, amount;
+  float m;
+  int32_t kind, bin, one, count;
+  struct {
+    float m;
+    uint32_t flags;
+    int32_t at;
+  } part[kCutParts];
+  uint64_t ranges[kCutRanges], cand[kCutCand];
+  uint32_t equal[kCutRanges];
+};
+constexpr size_t kSplitPartBytes = 41520;  // of a part's counts and masses
+// Workgroups to a row: several where rows of 256 KB and more are so few that one
+// each would leave most of the card idle (up to 64 rows; three or four kernels in
+// place of one).  64 rows of 201088 bf16 logits, top p: 51 us against 66, eight
+// rows 39 against 65; of 100000 fp32 logits 81 against 126.  64 rows of 67000
+// bf16 logits the other way: 43 us against 40, by top k 33 against 22.
+inline int32_t cut_parts(int64_t rows, int32_t V, int32_t es) {
+  if (rows < 1 || rows > 64 || (int64_t)V * es < 262144) return 1;
+  return (int32_t)(256 / rows < kCutParts ? 256 / rows : kCutParts);
+}
+inline size_t cut_split_row(int32_t parts) { return parts > 1 ? sizeof(SplitRow) + parts * kSplitPartBytes : 0; }
+
 struct CutParams {
   int32_t B, R, V, chunk, C;  // C: chunks of so many logits per row
+  int32_t parts, seg;         // workgroups to a row, and the logits of each (parts > 1)
+  char* split;                // their rows' places
+  int64_t split_row;
   int32_t ibits, frac;       // bits of an index; weights are whole numbers of 2^-frac
   FastDiv by_C, by_R;
   const char* logits;

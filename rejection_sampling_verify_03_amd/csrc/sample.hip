@@ -35,9 +35,10 @@
 
 namespace specv {
 
-constexpr int kRangeBits = 10, kRanges = 1 << kRangeBits;  // of a search's histogram
-constexpr int kCand = 2048;                                // candidates held in LDS
+constexpr int kRangeBits = kCutRangeBits, kRanges = kCutRanges;  // of a search's histogram
+constexpr int kCand = kCutCand;                                 // candidates held in LDS
 typedef unsigned long long u64;
+typedef u64 u64x2 __attribute__((ext_vector_type(2)));
 constexpr u64 kNone = ~0ull;
 
 // What a request asks for.
@@ -234,13 +235,15 @@ struct Bins {
 };
 static_assert((Bins<4>::kSlots + 1) / 2 + Bins<4>::kSlots <= Bins<2>::kSlots,
               "counts and masses of fp32 in the place of bf16's weights");
+static_assert(Bins<2>::kSlots % 4 == 0 && Bins<4>::kSlots % 4 == 0, "taken four at a time");
+static_assert(Bins<2>::kSlots * 4 <= kSplitPartBytes && Bins<4>::kSlots * 12 <= kSplitPartBytes, "room for a part's");
 
 // SMALL: rows of up to kCand logits, all of them candidates.
 template <bool SMALL>
 struct CutShared {
   // by slot.  bf16: counts (u32), later weights (double); fp32: counts, and
   // behind them masses
-  u64 bins[SMALL ? 1 : Bins<2>::kSlots];
+  alignas(16) u64 bins[SMALL ? 1 : Bins<2>::kSlots];
   union {
     u64 ranges[kRanges];
     struct {  // a range's candidates
@@ -366,12 +369,11 @@ struct CutRow {
   // Whether logits of -2^7 and below (the last bin's) may have a weight.
   __device__ __forceinline__ bool low_weighs() const { return ((double)m + 128.0) * s < frac + 2; }
 
-  __device__ __forceinline__ void read_tail() const {
+  __device__ __forceinline__ void read_tail() const {  // (a barrier stands in front of its use)
     if (threadIdx.x < 8) {
       const int e = (V & ~7) + threadIdx.x;
       S.tail[threadIdx.x] = e < V ? load_one<ES>(lg, e) : -INFINITY;
     }
-    __syncthreads();
   }
   __device__ __forceinline__ RawGroup<ES, true> tail() const {
     RawGroup<ES, true> g;
@@ -435,15 +437,25 @@ struct CutRow {
   // and, beside each, other(i)) the one at which the sum reaches the border, with
   // the sum of the others up to and with it.  All threads call it; what at()
   // reads is complete, and free when it returns.
-  template <class At, class Other>
+  // (N: at most so many, whose values stay in registers; 0: any number, read again)
+  template <int N, class At, class Other>
   __device__ __forceinline__ Crossing find_crossing(const Border& border, u64 offset, int place0, int n, At at,
                                                     Other other) const {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     __syncthreads();
-    u64 v = 0, o = 0;
-    for (int i = 0; i < n; ++i) {
-      v += at(i);
-      o += other(i);
+    u64 v = 0, o = 0, mine[N > 0 ? N : 1];
+    if constexpr (N > 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        mine[i] = i < n ? at(i) : 0;
+        v += mine[i];
+        o += i < n ? other(i) : 0;
+      }
+    } else {
+      for (int i = 0; i < n; ++i) {
+        v += at(i);
+        o += other(i);
+      }
     }
     const u64 x = wave_scan_u64(v), y = wave_scan_u64(o);
     if (lane == 63) {
@@ -463,11 +475,23 @@ struct CutRow {
     u64 sum = base + x - v, through = obase + y - o;
     if (sum < to && to <= sum + v) {
       int i = 0;
-      for (;; ++i) {
-        const u64 one = at(i);
-        through += other(i);
-        if (to <= sum + one) break;
-        sum += one;
+      if constexpr (N > 0) {
+        bool past = false;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (past) continue;
+          i = k;
+          through += other(k);
+          past = to <= sum + mine[k];
+          sum += past ? 0 : mine[k];
+        }
+      } else {
+        for (;; ++i) {
+          const u64 one = at(i);
+          through += other(i);
+          if (to <= sum + one) break;
+          sum += one;
+        }
       }
       S.bin = place0 + i;
       S.before = sum;
@@ -482,7 +506,7 @@ struct CutRow {
   __device__ __forceinline__ Crossing find_range(const Border& border, u64 offset) const {
     constexpr int kMine = kRanges / NT;
     const int t = threadIdx.x * kMine;
-    return find_crossing(border, offset, t, kMine, [&](int i) { return S.ranges[t + i]; }, [](int) { return (u64)0; });
+    return find_crossing<kMine>(border, offset, t, kMine, [&](int i) { return S.ranges[t + i]; }, [](int) { return (u64)0; });
   }
 
   __device__ __forceinline__ void clear_ranges() const {
@@ -560,15 +584,16 @@ struct CutRow {
   // would all add in one place.  (The lanes at work are a prefix of the wave's.)
   __device__ __forceinline__ void add_range(u64* ranges, int at, int shift, double sum) const {
     const int lane = threadIdx.x & 63;
+    u64 y = whole(sum);  // (a group's 8 weights, below 2^52: 16 groups' would be past a double's bits)
     if (shift >= 7) {
-      sum += dpp_d0<0x111, 0xf>(sum);
-      sum += dpp_d0<0x112, 0xf>(sum);
-      sum += dpp_d0<0x114, 0xf>(sum);
-      sum += dpp_d0<0x118, 0xf>(sum);
+      y += dpp_u64<0x111, 0xf>(y);
+      y += dpp_u64<0x112, 0xf>(y);
+      y += dpp_u64<0x114, 0xf>(y);
+      y += dpp_u64<0x118, 0xf>(y);
       const int last = 63 - __builtin_clzll(__ballot(true));
       if ((lane & 15) != 15 && lane != last) return;
     }
-    if (sum > 0.0) atomicAdd(&ranges[at], whole(sum));
+    if (y) atomicAdd(&ranges[at], y);
   }
 
   // The index in [lo, hi] at which the sum, with `offset` in front, reaches the
@@ -607,12 +632,12 @@ struct CutRow {
   // The logits from `floor` up for which take(key) holds gathered into LDS, as
   // many as fit: how many there are.
   template <class Take>
-  __device__ __forceinline__ int gather(float floor, Take take) const {
+  __device__ __forceinline__ int gather(int first, int last, float floor, Take take) const {
     __syncthreads();
     if (threadIdx.x == 0) S.count = 0;
     __syncthreads();
     const Floor<ES> low(floor);
-    each_group(0, V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+    each_group(first, last, [&](const RawGroup<ES, true>& raw, int e) {
       if (!low.reached(raw)) return;
       float x[8];
       unpack_group<ES, true>(raw, x);
@@ -645,7 +670,7 @@ struct CutRow {
     const float floor = B::least(bin);
     u64 lo = bin > 0 ? bin_end(bin - 1) + 1 : 0, hi = min(last, bin_end(bin)), offset = 0;
     hi = min(hi, rank_key(-INFINITY, 0) | index_mask());
-    int n = gather(floor, [&](u64 key) { return key >= lo && key <= hi; });
+    int n = gather(0, V - 1, floor, [&](u64 key) { return key >= lo && key <= hi; });
     const Border to{Border::kFixed, border, 0.0};
     while (n > kCand) {  // their keys in finer ranges, over the row again
       const int shift = max(bits_of(hi - lo) - kRangeBits, 0);
@@ -664,7 +689,7 @@ struct CutRow {
       offset += c.before;
       lo += (u64)c.bin << shift;
       hi = min(hi, lo + (1ull << shift) - 1);
-      n = gather(floor, [&](u64 key) { return key >= lo && key <= hi; });
+      n = gather(0, V - 1, floor, [&](u64 key) { return key >= lo && key <= hi; });
     }
     return search_lds<false, MASS>(n, last, lo, hi, to, offset);
   }
@@ -699,60 +724,250 @@ struct CutRow {
   }
 };
 
-// ----------------------------------------------------------------- finish --
-template <int ES, int NT, bool SMALL, bool DRAW>
+// --------------------------------------------------------------------- cut --
+// What a kernel does of a row: all of it, or where few rows are shared out to
+// several workgroups each: the counts of its part; (fp32 logits and a top p) the
+// masses of its part; its part's candidates or sums of kept weights; or, one
+// workgroup to a row again, the rest.  What lies between the sweeps each
+// workgroup of a row does by itself, with the same whole numbers.
+enum CutPhase { kWhole, kCount, kMass, kSums, kRest };
+
+// What the last kernel finds to do: nothing; the candidates of a row cut by its
+// top k, or by its top p; the sums of ranges; these, without the logits of the
+// last kept one's bin, which are the candidates.
+enum SplitKind { kDone, kFromK, kFromP, kInRanges, kEdge };
+
+template <int ES, int NT, bool SMALL, bool DRAW, CutPhase PHASE>
 __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
   using B = Bins<ES>;
   using Row = CutRow<ES, NT, SMALL>;
   using Upto = typename Row::Upto;
   __shared__ CutShared<SMALL> S;
-  const int i = blockIdx.x, tid = threadIdx.x;
+  constexpr bool kParts = PHASE == kCount || PHASE == kMass || PHASE == kSums;  // several workgroups to a row
+  const int i = kParts ? blockIdx.y : blockIdx.x, part = kParts ? blockIdx.x : 0, tid = threadIdx.x;
+  const int a0 = kParts ? part * P.seg : 0, z0 = kParts ? min(P.V, a0 + P.seg) - 1 : P.V - 1;  // the logits to sweep
   const int b = (int)P.by_R.of((uint32_t)i), r = i - b * P.R;
   const Cut cut = cut_of(P, b);
   const float u = DRAW ? P.uniforms[i] : 0.f;
   Row w{S, row_of(P, b, r, ES), P.V, P.ibits, P.frac, 0.f, 0.0};
+  SplitRow* st = PHASE == kWhole ? nullptr : reinterpret_cast<SplitRow*>(P.split + (int64_t)i * P.split_row);
+  // parts' counts, and their masses
+  auto part_counts = [&](int g) { return reinterpret_cast<uint32_t*>(st + 1) + (int64_t)g * B::kSlots; };
+  auto part_masses = [&](int g) {
+    return reinterpret_cast<u64*>(reinterpret_cast<uint32_t*>(st + 1) + (int64_t)P.parts * B::kSlots) +
+           (int64_t)g * B::kSlots;
+  };
+  auto leave = [&](SplitKind kind, u64 last, int bin, u64 before, u64 amount, bool one) {
+    if (part != 0 || tid != 0) return;
+    st->kind = kind;
+    st->last = last;
+    st->bin = bin;
+    st->before = before;
+    st->amount = amount;
+    st->one = one;
+    st->m = w.m;
+  };
   auto end = [&](int token, u64 last) {  // of the row
-    if (tid == 0) {
+    if (PHASE == kCount || PHASE == kMass) return;
+    if (DRAW && PHASE == kSums) leave(kDone, 0, 0, 0, 0, false);
+    if (tid == 0 && part == 0) {
       if constexpr (DRAW)
         P.tokens[i] = token;
       else
         P.last[i] = last;
     }
   };
+  constexpr bool kTail = DRAW && PHASE == kRest;  // goes on from what the row's workgroups left
+  if (kTail && st->kind == kDone) return;
   if (!cut.ok || !w.lg || (DRAW && !(u >= 0.0f && u < 1.0f))) return end(-1, kCutBad);
   if (!DRAW && (cut.greedy || cut.all)) return end(-1, kCutAll);
+  if (PHASE == kMass && (cut.greedy || !(cut.p < 1.0f))) return;
 
-  w.read_tail();
+  if (!kTail) w.read_tail();
 
-  if (DRAW && cut.greedy) {
+  if (DRAW && !kTail && cut.greedy) {
     VI best{-INFINITY, INT_MAX};
-    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
-      float x[8];
-      unpack_group<ES, true>(raw, x);
+    if constexpr (PHASE != kSums) {
+      __syncthreads();
+      w.each_group(a0, z0, [&](const RawGroup<ES, true>& raw, int e) {
+        float x[8];
+        unpack_group<ES, true>(raw, x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) best = vi_pick(best, VI{x[q], e + q});
-    });
-    best = wave_argmax(vi_floor(best, 0));  // (a row with nothing above -inf: 0)
-    if ((tid & 63) == 0) {
-      S.wave_f[tid >> 6] = best.v;
-      S.wave_u[tid >> 6] = (uint32_t)best.i;
+        for (int q = 0; q < 8; ++q) best = vi_pick(best, VI{x[q], e + q});
+      });
+      best = wave_argmax(vi_floor(best, 0));  // (a row with nothing above -inf: 0)
+      if ((tid & 63) == 0) {
+        S.wave_f[tid >> 6] = best.v;
+        S.wave_u[tid >> 6] = (uint32_t)best.i;
+      }
+      __syncthreads();
+      if (tid != 0) return;
+      for (int k = 1; k < Row::kWavesNT; ++k) best = vi_pick(best, VI{S.wave_f[k], (int)S.wave_u[k]});
+      if constexpr (PHASE == kCount) {
+        st->part[part].m = best.v;
+        st->part[part].at = best.i;
+        return;
+      }
+    } else if (part == 0) {
+      for (int g = 0; g < P.parts; ++g) best = vi_pick(best, VI{st->part[g].m, st->part[g].at});
     }
-    __syncthreads();
-    if (tid != 0) return;
-    for (int k = 1; k < Row::kWavesNT; ++k) best = vi_pick(best, VI{S.wave_f[k], (int)S.wave_u[k]});
     return end(best.i, 0);
   }
 
-  // the counts of the bins, the largest logit, and whether there is a NaN
   const bool counted = !SMALL && (cut.k > 0 || cut.p < 1.0f);
   uint32_t* counts = w.counts();
   const int j0 = tid * Row::kPer, jn = max(0, min(Row::kPer, B::kN - j0));  // this thread's bins
+  w.s = 1.4426950408889634074 / (double)cut.T;
+  u64 last = kNone;  // the key of the last kept token
+  // the candidates in LDS, where they are all that can be kept, and the end of their keys
+  bool held = SMALL;
+  int n = SMALL ? P.V : 0;
+  u64 hi = w.rank_key(-INFINITY, 0) | w.index_mask();
+  // of the logits in the bin of the last kept token: how many stay, by their
+  // index, where the last one's index is still to be found (the bin, or -1)
+  int tie_bin = -1;
+  u64 ties = 0;
+
+  // The candidates gathered: of the row, or of its part for the last kernel.
+  auto gather = [&](float floor, auto take) __attribute__((always_inline)) {
+    const int n = w.gather(a0, z0, floor, take);
+    if constexpr (DRAW && PHASE == kSums) {
+      if (tid == 0) S.bin = n > 0 ? atomicAdd(&st->count, n) : 0;
+      __syncthreads();
+      const int at = S.bin;
+      for (int k = tid; k < n && at + k < kCand; k += NT) st->cand[at + k] = S.cand[k];
+    }
+    return n;
+  };
+  // The candidates up to bin `bin`, in front of which `before` stand, cut to the top k.
+  auto cut_k = [&](int bin, u64 before) __attribute__((always_inline)) {
+    held = true;
+    last = w.bin_end(bin);
+    hi = min(hi, last);
+    if (n > cut.k)
+      last = w.template search_lds<false, false>(n, kNone, bin > 0 ? w.bin_end(bin - 1) + 1 : 0, hi,
+                                                 Border{Border::kFixed, (u64)cut.k, 0.0}, before);
+  };
+  auto cut_p = [&]() __attribute__((always_inline)) {
+    last = min(last, w.template search_lds<false, true>(n, last, w.rank_key(w.m, 0), hi,
+                                                        Border{Border::kShare, 0, (double)cut.p}, 0));
+  };
+  // The logits of bin `bin` that are candidates cut to `amount` of their count
+  // (of one value) or their weights.
+  auto cut_bin = [&](int bin, u64 amount, bool one) __attribute__((always_inline)) {
+    const u64 from = bin > 0 ? w.bin_end(bin - 1) + 1 : 0;
+    const Border to{Border::kFixed, amount, 0.0};
+    hi = min(hi, w.bin_end(bin));
+    last = min(last, one ? w.template search_lds<false, false>(n, last, from, hi, to, 0)
+                         : w.template search_lds<false, true>(n, last, from, hi, to, 0));
+  };
+  // The key of the last place that min p leaves.
+  auto min_key = [&]() __attribute__((always_inline)) {
+    const double low = (double)w.m + (double)cut.T * log((double)cut.mn);
+    const float f = fmaxf(__double2float_ru(low), -FLT_MAX);
+    uint32_t q = place<ES>(f);
+    if (ES == 2 && value_at<2>(q) < f) ++q;  // (the bf16 values not below it)
+    return ((u64)((ES == 2 ? 0xffffu : 0xffffffffu) - q) << w.ibits) | w.index_mask();
+  };
+  const Border above{Border::kAbove, 0, (double)u};
+  auto draw_held = [&]() __attribute__((always_inline)) {
+    end((int)w.template search_lds<true, true>(n, last, 0, (u64)P.V - 1, above, 0), 0);
+  };
+  // Sums of weights by ranges of 2^shift indices, and beside them the counts of
+  // logits of the tie's bin: whole groups of 8, where the row is long enough.
+  const int shift = max(w.ibits - kRangeBits, 0);
+  uint32_t* equal = reinterpret_cast<uint32_t*>(S.cand);
+  // The token, from those of the whole row.
+  auto draw_ranges = [&]() __attribute__((always_inline)) {
+    if (shift < 3) {  // (few logits, one by one)
+      const Upto stays(w, last);
+      auto one = [&](float x, int e) { return stays(x, e) ? w.weight_of(x) : 0.0; };
+      return end(w.search_index(0, P.V - 1, above, 0, [](int, int, auto) {}, one), 0);
+    }
+    constexpr int kMine = kRanges / NT;
+    const int t = tid * kMine;
+    auto none = [](int) { return (u64)0; };
+    Crossing c{INT_MAX, 0, 0, 0};
+    u64 stay = 0, weight = 0;
+    if (tie_bin >= 0) {
+      c = w.template find_crossing<kMine>(Border{Border::kFixed, ties, 0.0}, 0, t, kMine,
+                                          [&](int j) { return (u64)equal[t + j]; }, none);
+      stay = ties - c.before;
+      weight = w.mass_of(B::value(tie_bin));
+    }
+    const Crossing d = w.template find_crossing<kMine>(
+        above, 0, t, kMine,
+        [&](int j) {
+          const int at = t + j;
+          const u64 same = tie_bin < 0 ? 0 : at < c.bin ? equal[at] : at == c.bin ? stay : 0;
+          return S.ranges[at] + weight * same;
+        },
+        none);
+    // inside the range a thread has few logits or one
+    const int l = d.bin << shift, size = 1 << shift, mine = max(1, size / NT), e0 = l + tid * mine;
+    const int n1 = max(0, min(mine, min(l + size, P.V) - e0));
+    Upto stays(w, last);
+    if (tie_bin >= 0) {
+      const float v = B::value(tie_bin);
+      stays.at = d.bin < c.bin ? INT_MAX : -1;
+      stays.x = v;
+      if (d.bin == c.bin) {
+        const Crossing f = w.template find_crossing<0>(
+            Border{Border::kFixed, stay, 0.0}, 0, e0, n1,
+            [&](int k) { return (u64)(load_one<ES>(w.lg, e0 + k) == v); }, none);
+        stays.at = f.bin;
+      }
+    }
+    const Crossing f = w.template find_crossing<0>(
+        Border{Border::kFixed, d.border, 0.0}, d.before, e0, n1,
+        [&](int k) {
+          const float x = load_one<ES>(w.lg, e0 + k);
+          return stays(x, e0 + k) ? w.mass_of(x) : 0;
+        },
+        none);
+    end(f.bin, 0);
+  };
+
+  if constexpr (kTail) {
+    const int kind = st->kind;
+    w.m = st->m;
+    last = st->last;
+    n = min(st->count, kCand);
+    if (kind != kInRanges) {
+      for (int k = tid; k < n; k += NT) S.cand[k] = st->cand[k];
+      __syncthreads();
+    }
+    if (kind == kFromK) {
+      cut_k(st->bin, st->before);
+      if (cut.p < 1.0f) cut_p();
+    } else if (kind == kFromP || kind == kEdge) {
+      cut_bin(st->bin, st->amount, st->one);
+    }
+    if (kind != kInRanges && cut.mn > 0.0f) last = min(last, min_key());
+    if (kind == kFromK || kind == kFromP) return draw_held();
+    for (int k = tid; k < kRanges; k += NT) S.ranges[k] = st->ranges[k];
+    if (kind == kEdge) {
+      __syncthreads();
+      for (int k = tid; k < n; k += NT) {
+        const u64 key = S.cand[k];
+        if (key <= last) atomicAdd(&S.ranges[(key & w.index_mask()) >> shift], w.mass_of(w.key_logit(key)));
+      }
+    } else if (st->bin >= 0) {
+      tie_bin = st->bin;
+      ties = st->amount;
+      for (int k = tid; k < kRanges; k += NT) equal[k] = st->equal[k];
+    }
+    return draw_ranges();
+  }
+
+  // the counts of the bins, the largest logit, and whether there is a NaN
   float m = -INFINITY;
   uint32_t big = 0, small = ~0u;
-  if (counted) {
+  bool nan = false, odd = false;
+  if (counted && (PHASE == kWhole || PHASE == kCount)) {
     for (int j = tid; j < B::kSlots; j += NT) counts[j] = 0;
     __syncthreads();
-    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int) {
+    w.each_group(a0, z0, [&](const RawGroup<ES, true>& raw, int) {
       if constexpr (ES == 2) {
         uint32_t slot[8];
         slots8(raw, slot);
@@ -780,20 +995,44 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
     if (tid == 0) {
       counts[0] += counts[B::kHalf];  // zeros and the like of either sign
       counts[B::kHalf] = 0;
-      const int last = B::slot_of(B::kN - 1);
-      counts[last] -= (8 - (P.V & 7)) & 7;  // (what the row's last group was filled up with)
+      if (z0 == P.V - 1) counts[B::slot_of(B::kN - 1)] -= (8 - (P.V & 7)) & 7;  // (what the last group was filled up with)
     }
     __syncthreads();
-    if constexpr (ES == 2) {  // the largest logit from the first bin, where that is one value
-      int first = B::kN;
-      for (int j = jn - 1; j >= 0; --j)
-        if (counts[B::slot_of(j0 + j)]) first = j0 + j;
-      first = (int)-w.block_max((float)-first);
-      if (B::single(first)) m = B::value(first);
-    }
   }
-  if (!(m > -INFINITY) && (ES == 2 || !counted)) {
-    w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+  if (PHASE != kWhole && PHASE != kCount) {
+    if (counted) {
+      // (all parts' on their way together)
+      for (int j = 4 * tid; j < B::kSlots; j += 4 * NT) {
+        u32x4 c[kCutParts], sum{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < kCutParts; ++g)
+          c[g] = *reinterpret_cast<const u32x4*>(part_counts(min(g, P.parts - 1)) + j);
+#pragma unroll
+        for (int g = 0; g < kCutParts; ++g) sum += g < P.parts ? c[g] : u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(counts + j) = sum;
+      }
+      __syncthreads();
+    }
+    uint32_t flags = 0;
+#pragma unroll
+    for (int g = 0; g < kCutParts; ++g) {
+      m = fmaxf(m, st->part[min(g, P.parts - 1)].m);
+      flags |= st->part[min(g, P.parts - 1)].flags;
+    }
+    nan = flags & 1u;
+    odd = flags & 2u;
+    big = flags & 4u ? ~0u : 0;
+  }
+  if (ES == 2 && counted && (PHASE == kWhole || PHASE == kCount)) {  // the largest logit from the first bin, where that is one value
+    int first = B::kN;
+    for (int j = jn - 1; j >= 0; --j)
+      if (counts[B::slot_of(j0 + j)]) first = j0 + j;
+    first = (int)-w.block_max((float)-first);
+    if (B::single(first)) m = B::value(first);
+  }
+  if ((PHASE == kWhole || PHASE == kCount) && (ES == 2 || !counted) && !(m > -INFINITY)) {
+    if (!counted) __syncthreads();
+    w.each_group(a0, z0, [&](const RawGroup<ES, true>& raw, int e) {
       float x[8];
       unpack_group<ES, true>(raw, x);
 #pragma unroll
@@ -807,39 +1046,41 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
     });
   }
   w.m = w.block_max(m);
-  const bool nan = __syncthreads_or(big > 0x7f800000u);
+  if (PHASE == kWhole || PHASE == kCount) {
+    nan = __syncthreads_or(big > 0x7f800000u);
+    if constexpr (!SMALL)  // logits whose bins are of several values, those of -2^7 and below apart
+      odd = __syncthreads_or(!counted && small < (B::kLo << B::kShift)) || (!counted && w.m >= 128.0f);
+  }
+  if constexpr (PHASE == kCount) {
+    const bool far = __syncthreads_or(big >= (B::kHi << B::kShift));
+    if (counted)
+      for (int j = tid; j < B::kSlots; j += NT) part_counts(part)[j] = counts[j];
+    if (tid == 0) {
+      st->part[part].m = w.m;
+      st->part[part].flags = (nan ? 1u : 0u) | (odd ? 2u : 0u) | (far ? 4u : 0u);
+      if (part == 0) st->count = 0;
+    }
+    return;
+  }
   if (nan || !(fabsf(w.m) <= FLT_MAX)) return end(-1, kCutAll);
-  w.s = 1.4426950408889634074 / (double)cut.T;
   auto count_of = [&](int j) { return (u64)counts[B::slot_of(j0 + j)]; };
 
-  u64 last = kNone;  // the key of the last kept token
-  // the candidates in LDS, where they are all that can be kept, and the range of their keys
-  bool held = SMALL;
-  int n = SMALL ? P.V : 0;
-  const u64 lo = w.rank_key(w.m, 0);
-  u64 hi = w.rank_key(-INFINITY, 0) | w.index_mask();
-  // of the logits in the bin of the last kept token: how many stay, by their
-  // index, where the last one's index is still to be found (the bin, or -1)
-  int tie_bin = -1;
-  u64 ties = 0;
   int k_bin = B::kN;
   u64 k_rest = 0;
   if (cut.k > 0) {
     const Border to{Border::kFixed, (u64)cut.k, 0.0};
     if constexpr (SMALL) {
-      last = w.template search_lds<false, false>(n, kNone, lo, hi, to, 0);
+      last = w.template search_lds<false, false>(n, kNone, w.rank_key(w.m, 0), hi, to, 0);
     } else {
-      const Crossing c = w.find_crossing(to, 0, j0, jn, count_of, count_of);
+      const Crossing c = w.template find_crossing<0>(to, 0, j0, jn, count_of, count_of);
       k_bin = c.bin;
       k_rest = (u64)cut.k - c.before;
       last = w.bin_end(k_bin);
       if (c.through <= kCand) {
-        n = w.gather(B::least(k_bin), [](u64) { return true; });
-        held = true;
-        hi = min(hi, last);
-        if (n > cut.k)
-          last = w.template search_lds<false, false>(n, kNone, k_bin > 0 ? w.bin_end(k_bin - 1) + 1 : 0, hi, to,
-                                                     c.before);
+        if (PHASE == kMass) return;
+        n = gather(B::least(k_bin), [](u64) { return true; });
+        if constexpr (DRAW && PHASE == kSums) return leave(kFromK, last, c.bin, c.before, 0, false);
+        cut_k(c.bin, c.before);
       } else if (c.through > (u64)cut.k) {
         if (B::single(k_bin)) {
           tie_bin = k_bin;
@@ -850,22 +1091,34 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
       }
     }
   }
+  int edge_bin = -1;
+  u64 edge = 0;
   if (cut.p < 1.0f) {
-    const Border share{Border::kShare, 0, (double)cut.p};
     if (held) {
-      last = min(last, w.template search_lds<false, true>(n, last, lo, hi, share, 0));
+      cut_p();
     } else if constexpr (!SMALL) {
       // the masses of bins with several values, logit by logit (those of -2^7 and below mostly have none)
       u64* masses = w.masses();
       if (tid < 3) S.special[tid] = 0;
-      if constexpr (ES == 4)
+      if (ES == 4 && PHASE != kSums && PHASE != kRest)
         for (int j = tid; j < B::kSlots; j += NT) masses[j] = 0;
       const bool low = counts[B::slot_of(B::kN - 1)] != 0 && w.low_weighs();
       const bool some = counts[B::slot_of(0)] != 0 || counts[B::slot_of(B::kMid)] != 0 || low;
       __syncthreads();
       const Upto stays(w, last);
-      if (ES == 4) {
-        w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+      if (ES == 4 && (PHASE == kSums || PHASE == kRest)) {
+        for (int j = 2 * tid; j < B::kSlots; j += 2 * NT) {
+          u64x2 y[kCutParts], sum{0, 0};
+#pragma unroll
+          for (int g = 0; g < kCutParts; ++g)
+            y[g] = *reinterpret_cast<const u64x2*>(part_masses(min(g, P.parts - 1)) + j);
+#pragma unroll
+          for (int g = 0; g < kCutParts; ++g) sum += g < P.parts ? y[g] : u64x2{0, 0};
+          masses[j] = sum.x;
+          masses[j + 1] = sum.y;
+        }
+      } else if (ES == 4) {
+        w.each_group(a0, z0, [&](const RawGroup<ES, true>& raw, int e) {
           float x[8];
           unpack_group<ES, true>(raw, x);
 #pragma unroll
@@ -888,6 +1141,11 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
           }
         });
       }
+      if constexpr (PHASE == kMass) {
+        __syncthreads();
+        for (int j = tid; j < B::kSlots; j += NT) part_masses(part)[j] = masses[j];
+        return;
+      }
       auto mass = [&](int j) -> u64 {
         const int bin = j0 + j;
         if constexpr (ES == 4) return masses[B::slot_of(bin)];
@@ -895,7 +1153,8 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
         const u64 c = bin < k_bin ? counts[B::slot_of(bin)] : bin == k_bin ? k_rest : 0;
         return c ? c * w.mass_of(B::value(bin)) : 0;
       };
-      const Crossing c = w.find_crossing(share, 0, j0, jn, mass, count_of);
+      const Crossing c = w.template find_crossing<Row::kPer <= 8 ? Row::kPer : 0>(Border{Border::kShare, 0, (double)cut.p},
+                                                                                  0, j0, jn, mass, count_of);
       const u64 rest = c.border - c.before;
       u64 one = 0, stay = 0;
       if (B::single(c.bin)) {  // (of equal logits as many as reach it)
@@ -903,12 +1162,11 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
         stay = (rest + one - 1) / one;
       }
       if (c.through <= kCand) {
-        n = w.gather(B::least(c.bin), [&](u64 key) { return key <= last; });
+        n = gather(B::least(c.bin), [&](u64 key) { return key <= last; });
+        if constexpr (DRAW && PHASE == kSums)
+          return leave(kFromP, last, c.bin, 0, one ? stay : rest, one != 0);
         held = true;
-        hi = min(hi, w.bin_end(c.bin));
-        const u64 from = c.bin > 0 ? w.bin_end(c.bin - 1) + 1 : 0;
-        last = min(last, one ? w.template search_lds<false, false>(n, last, from, hi, Border{Border::kFixed, stay, 0.0}, 0)
-                             : w.template search_lds<false, true>(n, last, from, hi, Border{Border::kFixed, rest, 0.0}, 0));
+        cut_bin(c.bin, one ? stay : rest, one != 0);
         tie_bin = -1;
       } else if (one) {
         if (c.bin < k_bin) {  // (in the k-th token's bin the rest of that is known)
@@ -919,6 +1177,9 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
           tie_bin = c.bin;
           ties = stay;
         }
+      } else if (ES == 4 && DRAW && PHASE == kSums && counts[B::slot_of(c.bin)] <= kCand) {
+        edge_bin = c.bin;  // (its border is found among its candidates, later)
+        edge = rest;
       } else {
         last = w.template search_bin<true>(c.bin, last, rest);
         tie_bin = -1;
@@ -926,135 +1187,110 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
     }
   }
   if (cut.mn > 0.0f) {
-    const double low = (double)w.m + (double)cut.T * log((double)cut.mn);
-    const float f = fmaxf(__double2float_ru(low), -FLT_MAX);
-    uint32_t q = place<ES>(f);
-    if (ES == 2 && value_at<2>(q) < f) ++q;  // (the bf16 values not below it)
-    const u64 at = ((u64)((ES == 2 ? 0xffffu : 0xffffffffu) - q) << w.ibits) | w.index_mask();
+    const u64 at = min_key();
     if (tie_bin >= 0 && at < w.rank_key(B::value(tie_bin), 0)) tie_bin = -1;
-    last = min(last, at);
+    if (edge_bin > 0 && at <= w.bin_end(edge_bin - 1)) edge_bin = -1;
+    if (edge_bin < 0) last = min(last, at);
   }
   // (a draw finds the last index together with its sums, where it goes by ranges of whole groups)
-  const int shift = max(w.ibits - kRangeBits, 0);
   if (!SMALL && tie_bin >= 0 && (!DRAW || shift < 3)) {
     last = w.search_equal(0, P.V - 1, tie_bin, ties);
     tie_bin = -1;
   }
   if constexpr (!DRAW) return end(0, min(last, (u64)kCutAll - 1));
 
-  const Border above{Border::kAbove, 0, (double)u};
-  if (held) return end((int)w.template search_lds<true, true>(n, last, 0, (u64)P.V - 1, above, 0), 0);
+  if constexpr (PHASE == kWhole)
+    if (held) return draw_held();
   if constexpr (!SMALL) {
-    const float floor = last == kNone ? -INFINITY : w.key_logit(last);
-    Upto stays(w, last);
-    auto one = [&](float x, int e) { return stays(x, e) ? w.weight_of(x) : 0.0; };
-    int token;
-    if constexpr (ES == 2) {
-      // the weight of each bin, 0 behind the last kept one's and for bins of
-      // several values; of the last kept one it stands up to the last index
-      const int end_bin = B::of(floor);
-      const int end_at = last == kNone || !B::single(end_bin) ? INT_MAX - 8 : (int)(last & w.index_mask());
-      double* weights = w.weights();
+    if (edge_bin >= 0) {
+      const u64 first = edge_bin > 0 ? w.bin_end(edge_bin - 1) + 1 : 0, end = min(last, w.bin_end(edge_bin));
+      gather(B::least(edge_bin), [&](u64 key) { return key >= first && key <= end; });
+      leave(kEdge, last, edge_bin, 0, edge, false);
       __syncthreads();
-      // whether some of a bin of several values may stay, with a weight
-      const bool low = end_bin == B::kN - 1 && w.low_weighs();
-      const bool odd = __syncthreads_or(
-          counted ? counts[B::slot_of(0)] != 0 || counts[0] != 0 || (low && counts[B::slot_of(B::kN - 1)] != 0)
-                  : w.m >= 128.0f || small < (B::kLo << B::kShift) || (low && big >= (B::kHi << B::kShift)));
-      for (int j = tid; j < B::kN; j += NT)
-        weights[B::slot_of(j)] = j <= end_bin && j != tie_bin && B::single(j) ? w.weight_of(B::value(j)) : 0.0;
-      if (tid == 0) weights[B::kHalf] = 0.0;
-      const double end_weight = B::single(end_bin) ? w.weight_of(floor) : 0.0;
-      const Floor<2> kept(floor);
-      auto sum_of = [&](const RawGroup<2, true>& raw, const uint32_t (&slot)[8], int e) {
-        double sum = 0.0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) sum += weights[slot[q]];
-        if (odd) {
-          float x[8];
-          unpack_group<2, true>(raw, x);
-#pragma unroll 1
-          for (int q = 0; q < 8; ++q)
-            if (!B::single(B::of(x[q]))) sum += one(x[q], e + q);
-        }
-        return sum;
-      };
-      auto pass = [&](int l, int h, auto f) {
-        w.each_group(l, h, [&](const RawGroup<2, true>& raw, int e) {
-          if (!__ballot(kept.reached(raw))) return;
-          uint32_t slot[8];
-          slots8(raw, slot);
-          double sum = sum_of(raw, slot, e);
-          if (e + 7 > end_at) {
-            float x[8];
-            unpack_group<2, true>(raw, x);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) sum -= x[q] == floor && e + q > end_at ? end_weight : 0.0;
-          }
-          f(e, sum);
-        });
-      };
-      if (tie_bin >= 0) {
-        // the sums without the last bin's logits, and those counted beside
-        uint32_t* equal = reinterpret_cast<uint32_t*>(S.cand);
+      last = edge_bin > 0 ? first - 1 : w.rank_key(INFINITY, 0);  // the sums: of what is in front of it
+    }
+    const float floor = last == kNone ? -INFINITY : w.key_logit(last);
+    const Upto stays(w, last);
+    auto one = [&](float x, int e) { return stays(x, e) ? w.weight_of(x) : 0.0; };
+    if (shift >= 3) {
+      const Floor<ES> kept(floor);
+      if constexpr (ES == 2) {
+        // the weight of each bin, 0 behind the last kept one's and for bins of
+        // several values
+        const int end_bin = B::of(floor);
+        double* weights = w.weights();
+        __syncthreads();
+        // whether some of a bin of several values may stay, with a weight
+        const bool low = end_bin == B::kN - 1 && w.low_weighs();
+        if (counted)
+          odd = counts[B::slot_of(0)] != 0 || counts[0] != 0 || (low && counts[B::slot_of(B::kN - 1)] != 0);
+        else
+          odd = __syncthreads_or(odd || (low && big >= (B::kHi << B::kShift)));
+        __syncthreads();
+        for (int j = tid; j < B::kN; j += NT)
+          weights[B::slot_of(j)] = j <= end_bin && j != tie_bin && B::single(j) ? w.weight_of(B::value(j)) : 0.0;
+        if (tid == 0) weights[B::kHalf] = 0.0;
         for (int j = tid; j < kRanges; j += NT) equal[j] = 0;
         w.clear_ranges();
-        const uint32_t end_slot = (uint32_t)B::slot_of(tie_bin);
-        w.each_group(0, P.V - 1, [&](const RawGroup<2, true>& raw, int e) {
-          if (!__ballot(kept.reached(raw))) return;
-          uint32_t slot[8], same = 0;
-          slots8(raw, slot);
+        auto sum_of = [&](const RawGroup<2, true>& raw, const uint32_t (&slot)[8], int e) __attribute__((always_inline)) {
+          double sum = 0.0;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) same += slot[q] == end_slot;
-          const double sum = sum_of(raw, slot, e);
-          w.add_range(S.ranges, e >> shift, shift, sum);
-          if (same) atomicAdd(&equal[e >> shift], same);
-        });
-        constexpr int kMine = kRanges / NT;
-        const int t = tid * kMine;
-        const Crossing c = w.find_crossing(Border{Border::kFixed, ties, 0.0}, 0, t, kMine,
-                                           [&](int j) { return (u64)equal[t + j]; }, [](int) { return (u64)0; });
-        const u64 stay = ties - c.before, weight = (u64)end_weight;
-        const Crossing d = w.find_crossing(
-            above, 0, t, kMine,
-            [&](int j) { return S.ranges[t + j] + weight * (t + j < c.bin ? equal[t + j] : t + j == c.bin ? stay : 0); },
-            [](int) { return (u64)0; });
-        // what is left lies in a range each: its logits one by one
-        const int size = 1 << shift, l = c.bin << shift, l2 = d.bin << shift;
-        stays = Upto(w, w.search_equal(l, min(P.V - 1, l + size - 1), tie_bin, stay));
-        token = w.search_index(l2, min(P.V - 1, l2 + size - 1), Border{Border::kFixed, d.border, 0.0}, d.before,
-                               [&](int a, int z, auto f) {
-                                 w.each_group(a, z, [&](const RawGroup<2, true>& raw, int e) {
-                                   float x[8];
-                                   unpack_group<2, true>(raw, x);
-                                   double sum = 0.0;
+          for (int q = 0; q < 8; ++q) sum += weights[slot[q]];
+          if (odd) {
+            float x[8];
+            unpack_group<2, true>(raw, x);
 #pragma unroll 1
-                                   for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
-                                   f(e, sum);
-                                 });
-                               },
-                               one);
+            for (int q = 0; q < 8; ++q)
+              if (!B::single(B::of(x[q]))) sum += one(x[q], e + q);
+          }
+          return sum;
+        };
+        auto sweep = [&](auto tie) __attribute__((always_inline)) {
+          const uint32_t end_slot = (uint32_t)B::slot_of(max(tie_bin, 0));
+          w.each_group(a0, z0, [&](const RawGroup<2, true>& raw, int e) {
+            if (!__ballot(kept.reached(raw))) return;
+            uint32_t slot[8], same = 0;
+            slots8(raw, slot);
+            if constexpr (tie) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) same += slot[q] == end_slot;
+            }
+            w.add_range(S.ranges, e >> shift, shift, sum_of(raw, slot, e));
+            if (tie && same) atomicAdd(&equal[e >> shift], same);
+          });
+        };
+        if (tie_bin >= 0)
+          sweep(std::true_type{});
+        else
+          sweep(std::false_type{});
       } else {
-        token = w.search_index(0, P.V - 1, above, 0, pass, one);
-      }
-    } else {
-      const Floor<4> kept(floor);
-      token = w.search_index(
-          0, P.V - 1, above, 0,
-          [&](int l, int h, auto f) {
-            w.each_group(l, h, [&](const RawGroup<4, true>& raw, int e) {
-              if (!__ballot(kept.reached(raw))) return;
-              float x[8];
-              unpack_group<4, true>(raw, x);
-              double sum = 0.0;
+        w.clear_ranges();
+        w.each_group(a0, z0, [&](const RawGroup<4, true>& raw, int e) {
+          if (!__ballot(kept.reached(raw))) return;
+          float x[8];
+          unpack_group<4, true>(raw, x);
+          double sum = 0.0;
 #pragma unroll 4
-              for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
-              f(e, sum);
-            });
-          },
-          one);
+          for (int q = 0; q < 8; ++q) sum += one(x[q], e + q);
+          w.add_range(S.ranges, e >> shift, shift, sum);
+        });
+      }
     }
-    end(token, 0);
+    if constexpr (PHASE == kSums) {
+      __syncthreads();
+      for (int k = (a0 >> shift) + tid; k <= z0 >> shift; k += NT) {
+        st->ranges[k] = S.ranges[k];
+        if (tie_bin >= 0) st->equal[k] = equal[k];
+      }
+      if (part == 0)
+        for (int k = (P.V - 1 >> shift) + 1 + tid; k < kRanges; k += NT) {
+          st->ranges[k] = 0;
+          st->equal[k] = 0;
+        }
+      if (edge_bin < 0) leave(kInRanges, last, tie_bin, 0, ties, false);
+      return;
+    }
+    draw_ranges();
   }
 }
 
@@ -1087,12 +1323,21 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
 
 template <int ES, bool DRAW>
 static hipError_t launch_rows(const CutParams& P, unsigned rows, hipStream_t stream) {
-  if (P.V <= kCand)
-    hipLaunchKernelGGL((cut_kernel<ES, 256, true, DRAW>), dim3(rows), dim3(256), 0, stream, P);
-  else if (rows <= 256)
-    hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW>), dim3(rows), dim3(1024), 0, stream, P);
-  else
-    hipLaunchKernelGGL((cut_kernel<ES, 512, false, DRAW>), dim3(rows), dim3(512), 0, stream, P);
+  if (P.parts > 1) {
+    const dim3 grid((unsigned)P.parts, rows);
+    hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW, kCount>), grid, dim3(1024), 0, stream, P);
+    if constexpr (ES == 4)
+      if (P.top_p) hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW, kMass>), grid, dim3(1024), 0, stream, P);
+    if constexpr (DRAW)
+      hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW, kSums>), grid, dim3(1024), 0, stream, P);
+    hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW, kRest>), dim3(rows), dim3(1024), 0, stream, P);
+  } else if (P.V <= kCand) {
+    hipLaunchKernelGGL((cut_kernel<ES, 256, true, DRAW, kWhole>), dim3(rows), dim3(256), 0, stream, P);
+  } else if (rows <= 256) {
+    hipLaunchKernelGGL((cut_kernel<ES, 1024, false, DRAW, kWhole>), dim3(rows), dim3(1024), 0, stream, P);
+  } else {
+    hipLaunchKernelGGL((cut_kernel<ES, 512, false, DRAW, kWhole>), dim3(rows), dim3(512), 0, stream, P);
+  }
   return hipGetLastError();
 }
 

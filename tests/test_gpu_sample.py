@@ -337,6 +337,88 @@ def test_a_long_vocabulary(sv):
         check(sv, y.cpu(), columns([s]), dev=y, seed=V)
 
 
+def shared_rows_of(dtype):
+    """The shortest odd vocabulary of which few rows are shared out to several workgroups each."""
+    return 262144 // dtype.itemsize + 5
+
+
+@pytest.mark.parametrize("kind", ["ties", "equal", "signs", "small", "mixed", "large", "deep", "masked", "lowest", "few"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_shared_by_workgroups(sv, dtype, kind):
+    """What the counted bins hold several values of, borders among equal logits
+    of many parts, masked parts: rows that several workgroups share."""
+    V, S = shared_rows_of(dtype), len(SETTINGS)
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(S, 1, V, generator=g)
+    if kind == "ties":
+        x = torch.randint(-2, 3, (S, 1, V), generator=g).float()
+    elif kind == "equal":
+        x[:] = torch.tensor([0.0, 1.5, -3.0, 1e-30, 200.0, -500.0]).repeat(S // 6).view(S, 1, 1)
+    elif kind == "signs":
+        x = torch.where(x < 0, 0.0, -0.0)
+    elif kind == "small":
+        x = x * 2.0 ** -21
+    elif kind == "mixed":
+        x = torch.where(torch.rand(S, 1, V, generator=g) < 0.5, x, x * 2.0 ** -21)
+    elif kind == "large":
+        x = x * 300
+    elif kind == "deep":
+        x = -300 - x.abs() * 20
+    elif kind == "masked":
+        x[:, :, : V - 3000] = -math.inf
+        x[1::3, :, 17] = math.nan
+        x[2::3, :, V - 1] = math.inf
+    elif kind == "lowest":
+        x[:, :, 10:] = torch.finfo(dtype).min
+    elif kind == "few":
+        x[:, :, 1:] = -math.inf
+    check(sv, x.to(dtype), columns(SETTINGS), seed=11)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [1, 63, 64, 65])
+def test_as_many_rows_as_are_shared(sv, rows, dtype):
+    """The same rows of the same settings, in a call of as many as are shared
+    out and of one more, at the ends of the parts and of the uniforms."""
+    V = shared_rows_of(dtype)
+    x = zipf(1, 1, V, dtype, 3).cuda()
+    sets = [t[torch.arange(rows) % len(SETTINGS)] for t in columns(SETTINGS)]
+    u = torch.linspace(0, 1, rows + 1)[:-1].view(rows, 1)
+    want = do.sample(x.cpu().expand(rows, 1, V), u.tolist(), *sets)
+    ws = torch.full((sv.spec_sample_workspace_bytes(rows, 1, V),), 255, dtype=torch.uint8, device="cuda")
+    got = sv.sample(x.expand(rows, 1, V), u.cuda(), *cuda(sets), workspace=ws)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_replays_of_rows_shared_by_workgroups(sv):
+    """Two graphs on one workspace, replayed in turn."""
+    sets = cuda(columns(SETTINGS))
+    B = len(SETTINGS)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    xs = [torch.randn(B, 1, shared_rows_of(t), generator=g, device="cuda").to(t) for t in (BF16, F32)]
+    u = torch.rand(B, 1, generator=g, device="cuda")
+    ws = torch.empty(max(sv.spec_sample_workspace_bytes(*x.shape) for x in xs), dtype=torch.uint8, device="cuda")
+
+    def go(i, **kw):
+        return sv.sample(xs[i], u, *sets, **kw), sv.truncate_logits(xs[i], *sets, **kw)
+    for i in range(2):
+        go(i, workspace=ws)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in xs], []
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            outs.append(go(i, workspace=ws))
+    for _ in range(4):
+        for i in range(2):
+            xs[i].copy_(torch.randn(xs[i].shape, generator=g, device="cuda") * 2)
+            u.copy_(torch.rand(u.shape, generator=g, device="cuda"))
+            sets[0].copy_(sets[0].roll(1))
+            graphs[i].replay()
+            want = go(i)
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
+
+
 def test_drafts_and_targets_cut_alike(sv):
     """A round of speculative decoding with cut distributions: the drafter's
     rows cut, drafts sampled from them, and the verification of those drafts

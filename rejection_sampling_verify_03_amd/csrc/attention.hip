@@ -1,5 +1,5 @@
-// attention.hip -- attention of each request's new tokens over its 8-bit paged
-// context, on gfx950.
+// attention.hip -- attention of each request's new tokens over its paged context
+// of 8 or 4 bits, on gfx950.
 //
 // For a row (new token i of request b, query head h of KV head kh) over the
 // positions j that it sees:  s_j = scale * q . k_j,
@@ -50,12 +50,23 @@
 // or two tiles to a block: the fixed costs of a block (69 us, of 5 for bytes).
 // RT is what 256 registers hold with few spilled: 5 row tiles at 64 dims (the 72
 // rows of nine tokens and a group of eight in one block, 2 registers spilled
-// with fine scales; 3 tiles: 175 us), 3 at 128 (7 spilled, 25 with fine scales;
+// with fine scales; 3 tiles: 175 us), 3 at 128 (8 spilled, 25 with fine scales;
 // with 4 the chunk takes 992 us against 382), 1 at 256 (19, 27): there the
 // verification batch is five units to a KV head, each of which reads the whole
 // context (726 us with heads of 256, 251 with 128).  A second tile on
 // its way in registers was no faster (133 against 133 us, long contexts 150
 // against 141).
+//
+// The 4-bit form (a scale for each 32 dims of a key) has half of the bytes and
+// the same instructions but for the widening: two e2m1 codes of one key and its
+// scale become two bf16 values in one instruction, keys as they lie, and of the
+// values two keys' results are put together by halves (in place of the bytes'
+// transposition).  No register is spilled in it.  The verification batch takes
+// 126 us (vector instructions in 58 % of the cycles, matrix instructions in
+// 20 %), single tokens over three contexts of up to 131072, 364 MB, 81 us, of
+// which the main kernel 75 (4.9 TB/s).  Two tiles on their way: 98 us (39
+// registers spilled to keep three workgroups to a CU); four workgroups to a CU
+// at 128 dims: 94 us (17 spilled).
 #include <limits.h>
 
 #include <type_traits>

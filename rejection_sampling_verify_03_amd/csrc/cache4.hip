@@ -5,18 +5,23 @@
 // Rotation: pair i of a head, (x, y), at position p becomes
 //   (x cos a - y sin a, y cos a + x sin a) * scale,  a = p * inv_freq[i],
 // pairs (i, i + rot / 2), or (2 i, 2 i + 1) interleaved.  The angle, its cosine
-// and sine and the products are taken in fp64 and rounded once: an angle of a
-// far position has no correct fraction in fp32, and the codes of the cache are
-// then those of the exact values (an fp32 product next to the border of two
-// codes picks the wrong one about once in a million).  The cosines and sines
-// are worked out once for all heads of a token; what is left is eight fp64
-// instructions for 16 bytes, below memory's rate.
+// and sine are taken in fp64: an angle of a far position has no correct fraction
+// in fp32.  They are worked out once for all heads of a token.  The products of
+// fp32 elements, and of keys that go into the cache, are fp64's too, rounded
+// once: the codes are then those of the exact values (an fp32 product next to
+// the border of two codes picks the wrong one about once in a million).  Those
+// that become bf16 elements are fp32's, whose error is 2^-15 of their rounding's.
 //
 // Cache: 32 consecutive elements of a token's head share the scale 2^e, e the
 // smallest exponent with |x| <= 6 * 2^e, and are held as e2m1 codes (0, 0.5, 1,
 // 1.5, 2, 3, 4, 6 and a sign), the microscaled format that the widening
 // instructions read.  A scale belongs to one token, so every token is written
 // by itself: no order among the writers, nothing read back.
+//
+// Bounds, measured (MI355X): memory.  8190 tokens of 32 + 8 heads of 128, half of
+// each rotated: 35 us, 4.8 TB/s read and written.  24000 tokens of 32 + 8 + 8 heads
+// of 128 rotated and written: 127 us, 4.2 TB/s; the cache's part read back as bf16
+// 24 us, 5.3 TB/s.  A decode step's 64 tokens take 4 us, what a launch takes.
 //
 #include "cache_device.hpp"
 #include "unaligned.hpp"

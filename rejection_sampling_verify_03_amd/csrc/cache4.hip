@@ -19,10 +19,13 @@
 // by itself: no order among the writers, nothing read back.
 //
 // Bounds, measured (MI355X): memory.  8190 tokens of 32 + 8 heads of 128, half of
-// each rotated: 35 us, 4.8 TB/s read and written.  24000 tokens of 32 + 8 + 8 heads
-// of 128 rotated and written: 127 us, 4.2 TB/s; the cache's part read back as bf16
-// 24 us, 5.3 TB/s.  A decode step's 64 tokens take 4 us, what a launch takes.
+// each rotated: 38 us with inputs past the caches (4.4 TB/s read and written), 30
+// with part of them within.  24000 tokens of 32 + 8 + 8 heads of 128 rotated and
+// written: 118 us, 4.4 TB/s; the cache's part read back as bf16 22 us, 5.7 TB/s.
+// A decode step's 64 tokens take 4 us, what a launch takes.
 //
+#include <type_traits>
+
 #include "cache_device.hpp"
 #include "unaligned.hpp"
 
@@ -88,53 +91,50 @@ __device__ __forceinline__ uint32_t encode8(const float x[8], float scale) {
 typedef uint32_t u32x4_any_out __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any_out __attribute__((ext_vector_type(4), aligned(4)));
 
+// (Written past the caches: 145 us against 152 for 24000 tokens of 32 + 8 + 8 heads
+// of 128 rotated, written and read back, 17 against 19 for 2000 fp32 tokens; bf16
+// heads of 64, whose pieces are half lines, the other way: 38 against 37.)
 template <int ES>
 __device__ __forceinline__ void store8(char* dst, const float x[8]) {
   if constexpr (ES == 2) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = round_bf16x2(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<u32x4_any_out*>(dst) = u32x4{w[0], w[1], w[2], w[3]};
+    __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_any_out*>(dst));
   } else {
-    *reinterpret_cast<f32x4_any_out*>(dst) = f32x4{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f32x4_any_out*>(dst + 16) = f32x4{x[4], x[5], x[6], x[7]};
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4_any_out*>(dst));
+    __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4_any_out*>(dst + 16));
   }
 }
 
-// Two groups of 8 elements of a head, a and b, turned by 8 pairs' cosines and
-// sines: a[q] and b[q] are a pair, or with INTER the neighbours in a (pairs 0 to
-// 3) and in b (4 to 7).
-template <bool INTER, class T, class CosSin>
-__device__ __forceinline__ void turn16(T (&a)[8], T (&b)[8], CosSin cos_sin) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    T& x = !INTER ? a[q] : q < 4 ? a[2 * q] : b[2 * q - 8];
-    T& y = !INTER ? b[q] : q < 4 ? a[2 * q + 1] : b[2 * q - 7];
-    T c, s;
-    cos_sin(q, c, s);
-    const T u = x;
-    x = __builtin_fma(x, c, -(y * s));
-    y = __builtin_fma(u, s, y * c);
-  }
+// A pair turned by its cosine and sine.
+template <class T>
+__device__ __forceinline__ void turn(T& x, T& y, T c, T s) {
+  const T u = x;
+  x = __builtin_fma(x, c, -(y * s));
+  y = __builtin_fma(u, s, y * c);
 }
 
-// A lane takes two groups of 8 elements of one head of a token: in the rotated
-// part groups half of it apart, whose elements are pairs of each other, or pairs
-// among themselves (so that every pair is one lane's, and in place nothing is
-// overwritten that another lane reads); behind it groups half of the rest apart.
+// A lane takes two groups of 8 elements of one head of a token, a and b.  Where
+// pairs lie apart: in the rotated part groups half of it apart, whose elements
+// are pairs of each other, behind it groups half of the rest apart.  Where they
+// lie side by side: groups half of the head apart.  Every pair is one lane's, and
+// in place nothing is overwritten that another lane reads; a load or store of a
+// head's lanes covers whole lines where it can.
 // Grid: x sets of P.tokens tokens, y shares of their heads.  The heads of a
 // set's tokens, end to end, go to the lanes in rounds.  (Two rounds' reads on
 // their way together: 166 us against 122 for 24000 tokens of 32 + 8 + 8 heads of
 // 128; the registers cost more waves than that gains.)
 template <int ES, bool WRITE, bool INTER>
 __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
-  // cosine and sine of a lane's pair q at [token][q][lane of the head], in both
+  // cosine and sine of a group's pair q at [token][q][group of the head], in both
   // precisions: neighbouring lanes read neighbouring places
   __shared__ double2 s_turn[kRopeAngles];
   __shared__ float2 s_turn32[kRopeAngles];
   __shared__ __align__(16) float s_max[WRITE ? kWG * 2 : 1];
   const int tid = threadIdx.x;
-  const int half = P.half, rows = half >> 3;  // rows: lanes of a head whose elements are turned
+  // turned: groups of a head whose elements are turned, with pairs apart those of a
+  const int half = P.half, turned = INTER ? half >> 2 : half >> 3;
   const int n0 = blockIdx.x * P.tokens;
   const int tokens = min(P.tokens, P.N - n0);
   for (int i = tid; i < tokens * half; i += kWG) {
@@ -143,8 +143,8 @@ __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
                              : (double)static_cast<const int32_t*>(P.positions)[n0 + t];
     double sn, cs;
     sin_cos(at * P.inv_freq[f], sn, cs);
-    const int late = INTER && f >= half / 2 ? 4 : 0, g = late ? f - half / 2 : f;
-    const int place = t * half + (INTER ? (late + g % 4) * rows + g / 4 : g % 8 * rows + g / 8);
+    constexpr int kPairs = INTER ? 4 : 8;  // of a group
+    const int place = t * half + f % kPairs * turned + f / kPairs;
     s_turn[place] = double2{cs * P.scale, sn * P.scale};
     s_turn32[place] = float2{(float)(cs * P.scale), (float)(sn * P.scale)};
   }
@@ -152,11 +152,12 @@ __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
   const int lanes = (P.dim + 15) >> 4, per = kWG / lanes;
   const int heads = P.heads[0] + (WRITE ? 2 : 1) * P.heads[1];
   const int mine = tid / lanes, lane = tid - mine * lanes;
-  const bool turned = lane < rows;
-  const int behind = (P.dim - 2 * half) >> 3, front = (behind + 1) >> 1;  // groups that are not turned; of them first ones
-  const int col_a = turned ? 8 * lane : 2 * half + 8 * (lane - rows);
-  const int col_b = turned ? half + 8 * lane : col_a + 8 * front;
-  const bool two = turned || lane - rows + front < behind;  // (else the second group does not exist)
+  const int groups = P.dim >> 3;
+  const int front = INTER ? lanes : (groups - 2 * turned + 1) >> 1;  // from a to b, where b is no partner
+  const bool turn_a = lane < turned, turn_b = INTER ? lane + front < turned : turn_a;
+  const int group_a = INTER || turn_a ? lane : lane + turned, group_b = !INTER && turn_a ? lane + turned : group_a + front;
+  const int col_a = 8 * group_a, col_b = 8 * group_b;
+  const bool two = group_b < groups;  // (else the second group does not exist)
   const int items = tokens * heads, rounds = (items + per - 1) / per;
   for (int r = blockIdx.y; r < rounds; r += gridDim.y) {
     const int item = r * per + mine;
@@ -172,14 +173,26 @@ __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
       const RawGroup<ES, true> raw_a = load_cached<ES>(src, col_a), raw_b = load_cached<ES>(src, two ? col_b : col_a);
       unpack_group<ES, true>(raw_a, a);
       unpack_group<ES, true>(raw_b, b);
-      if (turned && what < 2) {
+      if ((turn_a || turn_b) && what < 2) {
         const int at = token * half + lane;
+        auto turn16 = [&](auto& a, auto& b, auto* table) {
+          using T = std::remove_reference_t<decltype(a[0])>;
+          if constexpr (INTER) {
+            if (turn_a)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                turn<T>(a[2 * q], a[2 * q + 1], table[at + q * turned].x, table[at + q * turned].y);
+            if (turn_b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                turn<T>(b[2 * q], b[2 * q + 1], table[at + front + q * turned].x, table[at + front + q * turned].y);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) turn<T>(a[q], b[q], table[at + q * turned].x, table[at + q * turned].y);
+          }
+        };
         if (ES == 2 && (!WRITE || what == 0)) {
-          turn16<INTER>(a, b, [&](int q, float& c, float& s) {
-            const float2 v = s_turn32[at + q * rows];
-            c = v.x;
-            s = v.y;
-          });
+          turn16(a, b, s_turn32);
         } else {
           double x[8], y[8];
 #pragma unroll
@@ -187,11 +200,7 @@ __global__ __launch_bounds__(kWG) void rope_kernel(RopeParams P) {
             x[q] = a[q];
             y[q] = b[q];
           }
-          turn16<INTER>(x, y, [&](int q, double& c, double& s) {
-            const double2 v = s_turn[at + q * rows];
-            c = v.x;
-            s = v.y;
-          });
+          turn16(x, y, s_turn);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             a[q] = WRITE && what == 1 ? to_odd(x[q]) : (float)x[q];
@@ -277,7 +286,8 @@ hipError_t launch_rope(const RopeParams& P, int dtype, hipStream_t stream) {
 
 // One lane takes 8 elements of one (entry, head) row, keys and values, a cell;
 // a workgroup takes P.per entries, and a lane has the loads of kReadCells
-// cells on their way together.
+// cells on their way together.  Written past the caches (of 24000 tokens of 8
+// heads of 128: 5 us less).
 template <int ES>
 __global__ __launch_bounds__(kWG) void kv4_read_kernel(KvReadParams P) {
   const CacheView& c = P.c;
@@ -314,16 +324,17 @@ __global__ __launch_bounds__(kWG) void kv4_read_kernel(KvReadParams P) {
       for (int kv = 0; kv < 2; ++kv) {
         char* dst = P.dst[kv] + ((int64_t)i0 * cells + x) * 8 * ES;
         if constexpr (ES == 2) {
-          *reinterpret_cast<u32x4_any_out*>(dst) =
+          __builtin_nontemporal_store(
               u32x4{widen4<0>(w[kv][q], f[kv][q]), widen4<1>(w[kv][q], f[kv][q]), widen4<2>(w[kv][q], f[kv][q]),
-                    widen4<3>(w[kv][q], f[kv][q])};
+                    widen4<3>(w[kv][q], f[kv][q])},
+              reinterpret_cast<u32x4_any_out*>(dst));
         } else {
           const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][q], f[kv][q], 0),
                       b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][q], f[kv][q], 1),
                       d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][q], f[kv][q], 2),
                       e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][q], f[kv][q], 3);
-          *reinterpret_cast<f32x4_any_out*>(dst) = f32x4{a.x, a.y, b.x, b.y};
-          *reinterpret_cast<f32x4_any_out*>(dst + 16) = f32x4{d.x, d.y, e.x, e.y};
+          __builtin_nontemporal_store(f32x4{a.x, a.y, b.x, b.y}, reinterpret_cast<f32x4_any_out*>(dst));
+          __builtin_nontemporal_store(f32x4{d.x, d.y, e.x, e.y}, reinterpret_cast<f32x4_any_out*>(dst + 16));
         }
       }
     }

@@ -390,6 +390,56 @@ def test_as_many_rows_as_are_shared(sv, rows, dtype):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_shared_rows_by_a_table_and_in_place(sv, dtype):
+    """Rows at odd strides and offsets through a table, one several times and
+    some that do not exist; cut where they stand, on two streams at once."""
+    V, S = shared_rows_of(dtype), len(SETTINGS)
+    buf = zipf(1, 7, V + 3, dtype, 5)[0].cuda()
+    x = buf[:, 1:V + 1]
+    index = (torch.arange(S * 2).view(S, 2) % 7).to(torch.int32)
+    index[3, 0], index[4, 1], index[5] = -1, 7, 2
+    u = torch.rand(S, 2, generator=torch.Generator().manual_seed(6))
+    sets = columns(SETTINGS)
+    got = sv.sample(x, u.cuda(), *cuda(sets), row_index=index.cuda()).cpu().numpy()
+    want = do.sample(x.cpu()[index.clamp(0, 6).long()], u.tolist(), *sets)
+    want[3, 0] = want[4, 1] = -1
+    assert np.array_equal(got, want)
+    rows = [x[:1].expand(S, V).unsqueeze(1).clone(), x[1:2].expand(S, V).unsqueeze(1).clone()]
+    cut = [do.truncate(r.cpu(), *sets) for r in rows]
+    dev, streams = cuda(sets), [torch.cuda.Stream() for _ in rows]
+    torch.cuda.synchronize()
+    for r, st in zip(rows, streams):
+        assert sv.truncate_logits(r, *dev, out=r, stream=st) is r
+    torch.cuda.synchronize()
+    for r, w in zip(rows, cut):
+        assert np.array_equal(r.cpu().double().numpy(), w, equal_nan=True)
+
+
+@pytest.mark.parametrize("rows", [1, 65])
+def test_the_longest_vocabulary(sv, rows):
+    """A row of the largest size, alone (shared by workgroups) and read by 65
+    requests (a workgroup each): equal logits, of which the n-th token is the
+    one at u n, and few finite ones at its ends."""
+    V = sv.SPEC_MAX_V
+    x = torch.zeros(1, V, dtype=BF16, device="cuda")
+    index = torch.zeros(rows, 1, dtype=torch.int32, device="cuda")
+    k = torch.full((rows,), V // 4 + 1, dtype=torch.int32, device="cuda")
+    T, p = torch.ones(rows, device="cuda"), torch.full((rows,), 0.5, device="cuda")
+    u = torch.tensor([1023 / 1024, 0.0, 0.25, 0.5]).repeat(17)[:rows].view(rows, 1)
+    for kw, n in (({}, V), ({"top_k": k}, V // 4 + 1), ({"top_p": p}, V // 2)):
+        t = sv.sample(x, u.cuda(), T, row_index=index, **kw)[:, 0].cpu()
+        assert t.tolist() == [int(float(v) * n) for v in u[:, 0]]
+    x.fill_(-math.inf)
+    at = torch.tensor([0, 5, 1 << 30, V - 9, V - 2, V - 1])
+    few = torch.tensor([[[0.5, 1.0, 2.0, 1.0, 1.5, 1.0]]]).to(BF16)
+    x[0, at.cuda()] = few[0, 0].cuda()
+    for s in ((1.0, 0, 1.0, 0.0), (1.0, 3, 1.0, 0.0), (0.7, 0, 0.95, 0.0), (1.0, 0, 1.0, 0.3), (0.0, 0, 1.0, 0.0)):
+        sets = columns([s] * rows)
+        t = sv.sample(x, u.cuda(), *cuda(sets), row_index=index)[:, 0].cpu().numpy()
+        assert np.array_equal(t, at.numpy()[do.sample(few.expand(rows, 1, 6), u.tolist(), *sets)[:, 0]])
+
+
 def test_replays_of_rows_shared_by_workgroups(sv):
     """Two graphs on one workspace, replayed in turn."""
     sets = cuda(columns(SETTINGS))

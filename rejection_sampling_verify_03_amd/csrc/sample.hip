@@ -230,7 +230,7 @@ struct Bins {
     const uint32_t u = __float_as_uint(x);
     return (int)(min(max((u & 0x7fffffffu) >> kShift, kLo - 1), kHi) - (kLo - 1) + (u >> 31) * kHalf);
   }
-  static __device__ __forceinline__ int slot_of(int bin) { return bin <= kMid ? kMid - bin : kHalf + bin - kMid; }
+  static __host__ __device__ __forceinline__ constexpr int slot_of(int bin) { return bin <= kMid ? kMid - bin : kHalf + bin - kMid; }
   static __device__ __forceinline__ int of(float x) {
     const int s = slot(x);
     return s < kHalf ? kMid - s : kMid + s - kHalf;
@@ -293,6 +293,31 @@ __device__ __forceinline__ void slots8(const RawGroup<2, true>& g, uint32_t (&sl
     slot[2 * i] = both & 0xffffu;
     slot[2 * i + 1] = both >> 16;
   }
+}
+
+// Whether some of 8 bf16 logits falls into the last bin (as unsigned numbers
+// these are the largest).
+__device__ __forceinline__ bool lowest8(const RawGroup<2, true>& g) {
+  const uint32_t two[4] = {g.v.x, g.v.y, g.v.z, g.v.w};
+  u16x2 m = __builtin_bit_cast(u16x2, two[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, two[i]));
+  return max(m.x, m.y) >= (uint16_t)(0x8000u | Bins<2>::kHi);
+}
+
+// Whether some of 8 bf16 logits falls into a bin of several values, the last one
+// counted or not.
+__device__ __forceinline__ bool special8(const RawGroup<2, true>& g, bool last) {
+  using B = Bins<2>;
+  const uint32_t two[4] = {g.v.x, g.v.y, g.v.z, g.v.w};
+  const u16x2 cap = (uint16_t)(last ? 0xffffu : 0x8000u | (B::kHi - 1)), lo = (uint16_t)B::kLo;
+  u16x2 m{0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 a = __builtin_elementwise_min(__builtin_bit_cast(u16x2, two[i]), cap) & (uint16_t)0x7fff;
+    m = __builtin_elementwise_max(m, a - lo);
+  }
+  return max(m.x, m.y) >= (uint16_t)(B::kHi - B::kLo);
 }
 
 // A bound from below on logits, as the test of a group of 8 takes it: bf16
@@ -684,10 +709,11 @@ struct CutRow {
   // up to `last` reach the border.
   template <bool MASS>
   __device__ __forceinline__ u64 search_bin(int bin, u64 last, u64 border) const {
-    const float floor = B::least(bin);
+    const float floor = fmaxf(B::least(bin), -FLT_MAX);  // (-inf stays what it is, kept or not)
     u64 lo = bin > 0 ? bin_end(bin - 1) + 1 : 0, hi = min(last, bin_end(bin)), offset = 0;
-    hi = min(hi, rank_key(-INFINITY, 0) | index_mask());
+    hi = min(hi, rank_key(-FLT_MAX, 0) | index_mask());
     int n = gather(0, V - 1, floor, [&](u64 key) { return key >= lo && key <= hi; });
+    if (!MASS && border > (u64)n) return hi;
     const Border to{Border::kFixed, border, 0.0};
     while (n > kCand) {  // their keys in finer ranges, over the row again
       const int shift = max(bits_of(hi - lo) - kRangeBits, 0);
@@ -982,6 +1008,10 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
   uint32_t big = 0, small = ~0u;
   bool nan = false, odd = false;
   if (counted && (PHASE == kWhole || PHASE == kCount)) {
+    // (the last bin holds what the others do not: masked logits, of which a row may
+    // have mostly, would all add in one place)
+    constexpr int kLowest = B::kSlots - 1;
+    static_assert(B::slot_of(B::kN - 1) == kLowest, "the last bin's");
     for (int j = tid; j < B::kSlots; j += NT) counts[j] = 0;
     __syncthreads();
     w.each_group(a0, z0, [&](const RawGroup<ES, true>& raw, int) {
@@ -995,8 +1025,14 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
           mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2, two));
         }
         big = max(big, (uint32_t)max(mag.x, mag.y) << 16);
+        if (__ballot(lowest8(raw))) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) atomicAdd(&counts[slot[q]], 1u);
+          for (int q = 0; q < 8; ++q)
+            if (slot[q] != kLowest) atomicAdd(&counts[slot[q]], 1u);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) atomicAdd(&counts[slot[q]], 1u);
+        }
       } else {
         float x[8];
         unpack_group<ES, true>(raw, x);
@@ -1004,16 +1040,22 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
         for (int q = 0; q < 8; ++q) {
           m = fmaxf(m, x[q]);
           big = max(big, __float_as_uint(x[q]) & 0x7fffffffu);
-          atomicAdd(&counts[B::slot(x[q])], 1u);
+          const int slot = B::slot(x[q]);
+          if (slot != kLowest) atomicAdd(&counts[slot], 1u);
         }
       }
     });
     __syncthreads();
+    uint32_t sum = 0;
+    for (int j = tid; j < kLowest; j += NT) sum += j != 0 && j != B::kHalf ? counts[j] : 0;
+    sum = (uint32_t)wave_scan_u64(sum);
     if (tid == 0) {
-      counts[0] += counts[B::kHalf];  // zeros and the like of either sign
+      const uint32_t mid = counts[0] + counts[B::kHalf];  // zeros and the like of either sign
+      counts[0] = mid;
       counts[B::kHalf] = 0;
-      if (z0 == P.V - 1) counts[B::slot_of(B::kN - 1)] -= (8 - (P.V & 7)) & 7;  // (what the last group was filled up with)
+      atomicAdd(&counts[kLowest], (uint32_t)(z0 - a0 + 1) - mid);
     }
+    if ((tid & 63) == 63) atomicSub(&counts[kLowest], sum);
     __syncthreads();
   }
   if (PHASE != kWhole && PHASE != kCount) {
@@ -1148,6 +1190,8 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
         if (tid == 0) masses[0] += masses[B::kHalf];
       } else if (some) {
         w.each_group(0, P.V - 1, [&](const RawGroup<ES, true>& raw, int e) {
+          if constexpr (ES == 2)
+            if (!special8(raw, low)) return;
           float x[8];
           unpack_group<ES, true>(raw, x);
 #pragma unroll 1
@@ -1253,7 +1297,7 @@ __global__ __launch_bounds__(NT, 4) void cut_kernel(CutParams P) {
           double sum = 0.0;
 #pragma unroll
           for (int q = 0; q < 8; ++q) sum += weights[slot[q]];
-          if (odd) {
+          if (odd && special8(raw, low)) {
             float x[8];
             unpack_group<2, true>(raw, x);
 #pragma unroll 1

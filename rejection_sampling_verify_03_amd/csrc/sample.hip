@@ -33,14 +33,17 @@
 // from the joined ones; what lies between two sweeps every workgroup of a row
 // works out by itself.
 //
-// Bounds, measured (MI355X).  512 rows of 151936 bf16 logits, top p: 85 us, of
+// Bounds, measured (MI355X).  512 rows of 151936 bf16 logits, top p: 87 us, of
 // which the bytes need 23; 21 vector instructions a logit fill 60 % of the issue
 // slots (the place of a logit among the bins, 4.5 of them, in each of two
 // sweeps), and the atomic additions and lookups in LDS, which half collide, 32 %
 // of its cycles.  64 rows of 201088 with settings of their own: 53 us (the parts'
 // counts 14, their candidates or sums 24, the rest 15), of which the bytes need
-// 4: chains of dependent steps on a few waves.  288 such rows cut: 57 us, and 31
-// (5.6 TB/s) to write what is left of the logits.  Four rows of 1024 fp32 logits,
+// 4: chains of dependent steps on a few waves.  288 such rows cut: 60 us, and 31
+// (5.6 TB/s) to write what is left of the logits.  Rows that are masked for the
+// most part cost no more (288 rows of 151936 with a half, a hundredth or 15 of
+// the logits left, top k: 49, 46, 65 us; whole rows 46): the last bin's count is
+// what the others leave, where all would add in one place (274 us).  Four rows of 1024 fp32 logits,
 // top k: 11 us, a chain of steps again.
 //
 #include <limits.h>

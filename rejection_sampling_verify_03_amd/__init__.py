@@ -1168,27 +1168,28 @@ def kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, s
     out [N, q_heads, head_dim] bfloat16, lse [N, q_heads] float32."""
     torch = _torch()
     dev = cache.device
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.stride(2) != 1:
+    whole, (q0, q1, q2) = q.shape, q.stride() if q.dim() == 3 else (0, 0, 0)
+    if q2 != 1 or whole[2] != cache.head_dim:
         raise ValueError("q must be [N, q_heads, head_dim], contiguous along head_dim")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16, got %s" % q.dtype)
-    N, Hq, D = q.shape
+    N, Hq, D = whole
     B = ctx_len.shape[0]
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
-            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    table, (t0, t1) = block_table.shape, block_table.stride() if block_table.dim() == 2 else (0, 0)
+    if block_table.dtype != torch.int32 or len(table) != 2 or table[0] != B or (t1 != 1 and table[1] > 1):
         raise ValueError("block_table must be int32 [B, max_blocks] with unit column stride")
     if q.device != dev or block_table.device != dev:
         raise ValueError("all tensors must be on the same GPU")
-    max_blocks = block_table.shape[1]
+    max_blocks = table[1]
     if not 0 <= (B | N | Hq | max_q | max_ctx | window | max_blocks) <= 0x7fffffff:  # (some bit above the 31, or a sign)
         _int32(B, N, Hq, max_q, max_ctx, window, max_blocks)
     ws = _want_workspace(workspace, dev)
     return (SpecAttn4Args if type(cache) is KVCache4 else SpecAttnArgs)(
-        cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q.stride(0), q.stride(1),
+        cache.args, B, N, Hq, max_q, max_ctx, window, SPEC_BF16, scale, q.data_ptr(), q0, q1,
         _want(q_start, torch.int32, (B + 1,), dev, "q_start"), _want(ctx_len, torch.int32, (B,), dev, "ctx_len"),
-        block_table.data_ptr(), block_table.stride(0) if B > 1 else max_blocks, max_blocks,
+        block_table.data_ptr(), t0 if B > 1 else max_blocks, max_blocks,
         None if sinks is None else _want(sinks, torch.float32, (Hq,), dev, "sinks"),
-        _want(out, torch.bfloat16, (N, Hq, D), dev, "out"),
+        _want(out, torch.bfloat16, whole, dev, "out"),
         None if lse is None else _want(lse, torch.float32, (N, Hq), dev, "lse"), ws[0], ws[1])
 
 
@@ -1211,7 +1212,7 @@ def kv_attention(q, cache, block_table, q_start, ctx_len, max_q, max_ctx=None, s
     four = type(cache) is KVCache4
     with _on(cache.device, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            out = _like(q)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
         a = kv_attention_args(q, cache, block_table, q_start, ctx_len, max_q, max_ctx, scale, out, lse, window, sinks,
                               workspace)

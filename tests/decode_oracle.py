@@ -193,3 +193,8 @@ def attention(q, codes, k_scale, v_codes, v_scale, block_table, q_start, ctx_len
                 otol[q0 + i, h] = 2.0 ** -8 * (np.abs(out[q0 + i, h]) + mag) + 2 * ds * mag + 1e-30
                 ltol[q0 + i, h] = ds + 2 * U * abs(lse[q0 + i, h])
     return out, lse, otol, ltol
+
+
+# single tokens of a full card of contexts: a unit each, four heads to a workgroup
+MANY_SHORT = dict(name="full_card_of_4_bits", lens=[1] * 520, ctx=[1025 + i * 977 % 3001 for i in range(520)], G=1,
+                  heads=16, dim=32, bs=16, max_ctx=4096, order="tokens", window=0, holes=True)

@@ -367,6 +367,12 @@ def test_every_cut(sv, c):
     assert rows > 0
 
 
+def test_a_full_card(sv):
+    """A unit to a wave's head, four heads to a workgroup: more requests than
+    the 8-bit cache's batch of that cut has, as more workgroups are resident."""
+    test_every_cut(sv, do.MANY_SHORT)
+
+
 # ----------------------------------------------------------- a decode round
 def test_a_decode_round(sv):
     """Expansion, rotation and cache write at its positions and slots, attention

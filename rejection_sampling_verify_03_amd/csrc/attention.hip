@@ -253,14 +253,8 @@ __device__ __forceinline__ void store_row(Params P, int64_t row, int d, f32x4 o,
 // 32 dims of a key.
 enum CacheForm { kCoarse8, kFine8, kFour };
 
-// Workgroups to a CU that its registers are kept low enough for: in the 4-bit
-// form at 64 dims and one row tile 4 (125 registers in place of 129; 256 contexts
-// of 2048 tokens, four heads of 64: 31 us against 46 with 3).
 template <int DP, int RT, CacheForm FORM>
-constexpr int kAttnResident = FORM == kFour && RT == 1 && DP <= 64 ? 4 : 2;
-
-template <int DP, int RT, CacheForm FORM>
-__global__ __launch_bounds__(kWG, (kAttnResident<DP, RT, FORM>)) void attn_kernel(AttnParams) {
+__global__ __launch_bounds__(kWG, attn_resident(DP, RT, FORM == kFour)) void attn_kernel(AttnParams) {
   constexpr bool FINE = FORM != kCoarse8, FOUR = FORM == kFour;
   constexpr int C = DP / 32;   // steps of the sum over dims
   constexpr int DT = DP / 16;  // 16-dim tiles of the output
@@ -272,6 +266,9 @@ __global__ __launch_bounds__(kWG, (kAttnResident<DP, RT, FORM>)) void attn_kerne
                                                                                 : kWaves * 16 * DP * 4];
   __shared__ float s_ref[kWaves][RT * 16], s_sum[kWaves][RT * 16];
   __shared__ uint32_t s_nan[kWaves][DP];
+  static_assert((sizeof(s_mem) + sizeof(s_ref) + sizeof(s_sum) + sizeof(s_nan)) * attn_resident(DP, RT, FORM == kFour) <=
+                    160 * 1024,
+                "LDS of the workgroups that the plan counts on");
   Params P = params_again();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // consecutive workgroups go to the 8 XCDs in turn; those that share lines

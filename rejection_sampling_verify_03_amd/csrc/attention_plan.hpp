@@ -27,6 +27,16 @@ struct AttnPlan {
   int64_t items, groups;
 };
 
+// Workgroups that a CU holds at once: the plan counts on so many, and the kernels'
+// launch bounds keep their registers low enough for them.  8 bits at 64 dims and
+// one row tile: 4 would fit in part, 118 us against 107 for 256 contexts of 2048
+// tokens.  4 bits, one row tile: 4 at 64 dims, 31 us against 46 with 3 for 256
+// contexts of 2048 tokens with four heads; 3 at 128, 81 us against 87 with 2 for
+// three contexts of up to 131072, 46 against 52 for 64 of 4096.
+constexpr int attn_resident(int dim, int rt, bool four) {
+  return four && rt == 1 && dim <= 128 ? (dim <= 64 ? 4 : 3) : dim <= 64 && rt <= 2 ? 3 : 2;
+}
+
 // heads_in: the heads of a token stand together in the cache; four: it holds 4 bits.
 inline AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int32_t max_q, int32_t max_ctx, int32_t window,
                    bool heads_in, bool four = false) {
@@ -41,13 +51,7 @@ inline AttnPlan plan_attn(int32_t B, int32_t G, int32_t heads, int32_t dim, int3
   int64_t keys = max_ctx;
   if (window > 0 && (int64_t)window + p.rt * 16 < keys) keys = (int64_t)window + p.rt * 16;
   const int64_t units = (int64_t)B * p.nrb;
-  // workgroups that the card holds at once, by the kernels' registers (8 bits at
-  // 64 dims and one row tile: 4 to a CU would fit in part, 118 us against 107 for
-  // 256 contexts of 2048 tokens; 4 bits, one row tile: 4 fit at 64 dims, 31 us
-  // against 46 for 256 contexts of 2048 tokens with four heads, and 3 at 128, 81 us
-  // against 87 for three contexts of up to 131072, 46 against 52 for 64 of 4096)
-  const int per_cu = four && p.rt == 1 && dim <= 128 ? (dim <= 64 ? 4 : 3) : dim <= 64 && p.rt <= 2 ? 3 : 2;
-  const int slots = 256 * per_cu;
+  const int slots = 256 * attn_resident(dim, p.rt, four);  // workgroups that the card holds at once
   // heads that stand side by side in a token, to a wave each: a workgroup reads
   // them together
   const int hw = p.rt > 1 || !heads_in ? 1 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;

@@ -61,7 +61,8 @@
 // the same instructions but for the widening: two e2m1 codes of one key and its
 // scale become two bf16 values in one instruction, keys as they lie, and of the
 // values two keys' results are put together by halves (in place of the bytes'
-// transposition).  No register is spilled in it.  The verification batch takes
+// transposition).  With two row tiles at 64 dims two registers are spilled in
+// it, with five one, in the others none.  The verification batch takes
 // 126 us (vector instructions in 58 % of the cycles, matrix instructions in
 // 20 %), single tokens over three contexts of up to 131072, 364 MB, 81 us, of
 // which the main kernel 75 (4.9 TB/s).  Two tiles on their way: 98 us (39
@@ -80,6 +81,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 static_assert(kAttnWaves == kWaves, "waves of a workgroup");
 constexpr float kNoRef = -FLT_MAX;   // the reference of a row that has seen nothing
 constexpr float kRefSlack = 8.0f;   // how far (log2) a score may pass the reference
+constexpr float kFarScale = 0x1p120f;  // the smallest scale under which an e4m3 code is infinite in bf16
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -190,6 +192,11 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
 // Bit 7 of each byte that is an e4m3 NaN (0x7f or 0xff).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Bit 7 of each byte whose lower 7 bits are `from` (1..127) or more.
+__device__ __forceinline__ uint32_t bytes_from(uint32_t w, uint32_t from) {
+  return ((w & 0x7f7f7f7fu) + (128u - from) * 0x01010101u) & 0x80808080u;
 }
 
 // Whether some byte is 0.
@@ -603,8 +610,8 @@ __global__ __launch_bounds__(kWG, attn_resident(DP, RT, FORM == kFour)) void att
 
     // a tile that some row sees only in part: scores not seen become -inf;
     // nothing of the keys that no row sees may enter (0 * NaN, 0 * inf), and a
-    // NaN among the others is kept apart
-    bool nans = false;
+    // NaN among the others, or what bf16 has as infinite, is kept apart
+    bool apart = false;
     if (!whole) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -619,13 +626,16 @@ __global__ __launch_bounds__(kWG, attn_resident(DP, RT, FORM == kFour)) void att
 #pragma unroll
           for (int w = 0; w < WV; ++w) {
             t.v[4 * u + j][w] = any ? t.v[4 * u + j][w] : 0u;
-            if constexpr (!FOUR) nans |= nan_bytes(t.v[4 * u + j][w]) != 0;
+            if constexpr (!FOUR) apart |= nan_bytes(t.v[4 * u + j][w]) != 0;
           }
           if constexpr (FINE) fine |= any ? t.vfine[u] & (0xffu << (8 * j)) : (uint32_t)kScaleBias << (8 * j);
         }
-        if constexpr (FOUR) nans |= zero_byte(~fine);  // (a scale byte of 255)
+        if constexpr (FOUR) apart |= (bytes_from(fine, 125) & fine) != 0;  // (a scale byte of 253 or more)
         if constexpr (FINE) t.vfine[u] = fine;
-        if constexpr (!FINE) t.vsc[u] = __ballot(some) ? t.vsc[u] : 1.0f;
+        if constexpr (!FINE) {
+          t.vsc[u] = __ballot(some) ? t.vsc[u] : 1.0f;
+          apart |= t.vsc[u] >= kFarScale;
+        }
         __builtin_amdgcn_sched_barrier(0);  // (few conditions at a time: each is a pair of scalar registers)
       }
 #pragma unroll
@@ -638,7 +648,7 @@ __global__ __launch_bounds__(kWG, attn_resident(DP, RT, FORM == kFour)) void att
           for (int j = 0; j < 4; ++j) s[rt][u][j] = (see >> (16 * u + j)) & 1u ? s[rt][u][j] : -INFINITY;
         __builtin_amdgcn_sched_barrier(0);
       }
-      nans = __ballot(nans) != 0;
+      apart = __ballot(apart) != 0;
     }
 
     // the weights, against a reference that follows the scores
@@ -680,27 +690,40 @@ __global__ __launch_bounds__(kWG, attn_resident(DP, RT, FORM == kFour)) void att
       pb[rt] = pack8(w[0], w[1], w[2], w[3]);
     }
 
-    if (nans) {
-      // a row that sees a NaN value gets NaN in that dim: the keys with a NaN
-      // in each dim as a mask in LDS, against the keys that a row sees; then
-      // the NaNs leave the codes
+    if (apart) {
+      // a row that sees such a value gets NaN in that dim: the keys with one in
+      // each dim as a mask in LDS, against the keys that a row sees; then they
+      // leave the codes
       uint32_t* mask = s_nan[wave];
       for (int d = lane; d < DP; d += 64) mask[d] = 0;
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t bit = 1u << (16 * (j >> 2) + 4 * g + (j & 3));
-        if constexpr (FOUR) {  // all dims of the scale
-          if (((t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu) == 255u) {
-            for (int d = 0; d < DT; ++d) atomicOr(&mask[r * DT + d], bit);
-            t.vfine[j >> 2] ^= 0x80u << (8 * (j & 3));  // (of 2^0; the codes may be any)
+        if constexpr (FOUR) {
+          // a scale byte of 255: all its codes; 254: those of 2 and more; 253: of 4 and more
+          const uint32_t b = (t.vfine[j >> 2] >> (8 * (j & 3))) & 0xffu;
+          if (b >= 253u) {
+#pragma unroll
+            for (int w = 0; w < WV; ++w) {
+              const uint32_t c = t.v[j][w];
+              const uint32_t out =
+                  (b == 255u ? ~0u : b == 254u ? c >> 2 : (c >> 2) & (c >> 1)) & (DP == 64 ? 0x1111u : 0x11111111u);
+              for (uint32_t m = out; m; m &= m - 1) atomicOr(&mask[r * DT + 8 * w + (__builtin_ctz(m) >> 2)], bit);
+              t.v[j][w] = c & ~(out * 15u);
+            }
+            if (b == 255u) t.vfine[j >> 2] ^= 0x80u << (8 * (j & 3));  // (2^0; the codes are 0)
           }
         } else {
+          // (with a scale to 16 keys or more: a code of exponent e where e - 7 + byte - 127 >= 128)
+          uint32_t from = 127u;
+          if constexpr (!FINE)
+            if (t.vsc[j >> 2] >= kFarScale) from = (262u - (__float_as_uint(t.vsc[j >> 2]) >> 23)) * 8u;
 #pragma unroll
           for (int w = 0; w < WV; ++w) {
-            const uint32_t nb = nan_bytes(t.v[j][w]);
-            for (uint32_t m = nb; m; m &= m - 1) atomicOr(&mask[r * DT + 4 * w + (__builtin_ctz(m) >> 3)], bit);
-            t.v[j][w] &= ~((nb >> 7) * 0xffu);
+            const uint32_t out = bytes_from(t.v[j][w], from);
+            for (uint32_t m = out; m; m &= m - 1) atomicOr(&mask[r * DT + 4 * w + (__builtin_ctz(m) >> 3)], bit);
+            t.v[j][w] &= ~((out >> 7) * 0xffu);
           }
         }
       }

@@ -1,0 +1,52 @@
+"""Rotation at the ends of the range: keys that leave fp32's on their way into
+the 4-bit cache."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_oracle as do
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sv():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import rejection_sampling_verify_03_amd as m
+    return m
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_turned_keys_past_fp32_count_as_infinite(sv, inter, dtype):
+    """Pairs near the largest number turned by an eighth of a circle, so that one
+    of them grows by up to 2^(1/2): what fp32 holds has the definition's codes, a
+    group with an element that it does not hold is NaN."""
+    dim, N = 64, 40
+    big = torch.finfo(dtype).max
+    g = torch.Generator().manual_seed(3)
+    key = torch.randn(N, 1, dim, generator=g)
+    i, j = (slice(0, dim, 2), slice(1, dim, 2)) if inter else (slice(0, dim // 2), slice(dim // 2, dim))
+    for n in range(N):                                   # one pair of each token, from half of the range up
+        p = n % (dim // 2)
+        key[n, 0, i][p] = key[n, 0, j][p] = big * (0.5 + n / (2 * N - 2))
+        if n % 3 == 1:
+            key[n, 0, i][p] *= -1
+    key = key.to(dtype)
+    f = np.full(dim // 2, math.pi / 4)
+    pos = torch.ones(N, dtype=torch.int32)
+    want = do.rotate(key.double().numpy(), pos.numpy(), f, 1.0, inter)
+    past = np.abs(want) >= 2.0 ** 128 - 2.0 ** 103       # (what rounds to 2^128)
+    assert 5 < past.any((1, 2)).sum() < N - 5
+    want[past] = np.inf
+    cache = sv.make_kv4_cache(3, 16, 1, dim)
+    host = [torch.zeros_like(t, device="cpu").numpy() for t in (cache.k, cache.k_scale)]
+    slots = torch.arange(N)
+    sv.rope_kv_write(cache, None, key.cuda(), key.cuda(), pos.cuda(), slots.cuda(),
+                     sv.Rope(torch.from_numpy(f).cuda(), 1.0, inter))
+    torch.cuda.synchronize()
+    do.kv_write(host[0], host[1], want, slots.tolist())
+    assert np.array_equal(cache.k_scale.cpu().numpy(), host[1]) and np.array_equal(cache.k.cpu().numpy(), host[0])

@@ -822,11 +822,12 @@ typedef struct {
  * [0, num_blocks * block_size) (the -1 of a slot mapping) are not written.  With
  * rot_dim > 0 the keys are first turned to positions[i] as by spec_rope_launch,
  * and so are queries, if there are any (q_heads > 0), for every entry, written
- * or not; what the keys become (by fp64 products) is not rounded in between.  32 elements get the
- * smallest exponent e with |x| <= 6 * 2^e, at least -117, and are rounded to
- * nearest, ties to even; with a NaN or an infinity among them, all 32 are
- * stored as NaN.  (One of 1.75 * 2^127 or more rounds to 2^128, which bf16 and
- * fp32 read as infinite.)
+ * or not; what the keys become (by fp64 products) is not rounded in between,
+ * but counts as infinite where fp32 would round it to 2^128 or more.  32
+ * elements get the smallest exponent e with |x| <= 6 * 2^e, at least -117, and
+ * are rounded to nearest, ties to even; with a NaN or an infinity among them,
+ * all 32 are stored as NaN.  (One of 1.75 * 2^127 or more rounds to 2^128, which
+ * bf16 and fp32 read as infinite.)
  * Of equal slots next to each other the last entry counts; equal slots apart
  * from each other leave a mixture of their entries.
  */

@@ -63,12 +63,13 @@ __device__ __forceinline__ void sin_cos(double a, double& sn, double& cs) {
 }
 
 // y rounded to fp32 so that a later rounding to fewer bits gives what rounding
-// y itself would (inexact: to the neighbour whose last bit is 1).
+// y itself would (inexact: to the neighbour whose last bit is 1).  What rounds
+// to 2^128 becomes infinite.
 __device__ __forceinline__ float to_odd(double y) {
   const float f = (float)y;
   const double d = y - (double)f;
   uint32_t u = __float_as_uint(f);
-  if ((d > 0.0 || d < 0.0) && !(u & 1u)) u += (d > 0.0) == (y > 0.0) ? 1u : ~0u;
+  if (d != 0.0 && fabsf(f) <= FLT_MAX && !(u & 1u)) u += (d > 0.0) == (y > 0.0) ? 1u : ~0u;
   return __uint_as_float(u);
 }
 

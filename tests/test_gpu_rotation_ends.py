@@ -41,6 +41,14 @@ def test_turned_keys_past_fp32_count_as_infinite(sv, inter, dtype):
     want = do.rotate(key.double().numpy(), pos.numpy(), f, 1.0, inter)
     past = np.abs(want) >= 2.0 ** 128 - 2.0 ** 103       # (what rounds to 2^128)
     assert 5 < past.any((1, 2)).sum() < N - 5
+    # cosine, sine, product and sum are off by 2^-53 of |x| + |y| each, on either side:
+    # where a pair of these sizes cancels, what is left of it is below 2^-50 of them,
+    # its digits are not determined, and so is the scale of a group that holds nothing larger
+    size = np.empty_like(want)
+    x = np.abs(key.double().numpy())
+    size[..., i] = size[..., j] = x[..., i] + x[..., j]
+    sure = (np.abs(want).reshape(N, 2, 32).max(2) > 2.0 ** -20 * size.reshape(N, 2, 32).max(2))  # [N, group]
+    assert sure[past.reshape(N, 2, 32).any(2)].all() and sure.sum() >= N
     want[past] = np.inf
     cache = sv.make_kv4_cache(3, 16, 1, dim)
     host = [torch.zeros_like(t, device="cpu").numpy() for t in (cache.k, cache.k_scale)]
@@ -49,4 +57,8 @@ def test_turned_keys_past_fp32_count_as_infinite(sv, inter, dtype):
                      sv.Rope(torch.from_numpy(f).cuda(), 1.0, inter))
     torch.cuda.synchronize()
     do.kv_write(host[0], host[1], want, slots.tolist())
-    assert np.array_equal(cache.k_scale.cpu().numpy(), host[1]) and np.array_equal(cache.k.cpu().numpy(), host[0])
+    t = slots.numpy()
+    got_scale, scale = (a[t // 16, 0, :, t % 16] for a in (cache.k_scale.cpu().numpy(), host[1]))    # [N, group]
+    got, codes = (a[t // 16, t % 16, 0].reshape(N, 2, 16) for a in (cache.k.cpu().numpy(), host[0]))
+    assert np.array_equal(got_scale[sure], scale[sure]) and np.array_equal(got[sure], codes[sure])
+    assert ((scale == 255) == past.reshape(N, 2, 32).any(2)).all()

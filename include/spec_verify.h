@@ -764,6 +764,8 @@ int spec_truncate_launch(const spec_truncate_args* args, hipStream_t stream);
  * sine are taken in fp64; so are the products with them for fp32 tensors, rounded
  * once.  For bf16 they are fp32 products of the rounded cosine and sine: 2^-23
  * of |x| + |y| off at most, before the rounding to bf16.
+ * Outputs with two elements in one place, or with one in that of the other
+ * output or of the other input, are refused (SPEC_EINVAL).
  */
 typedef struct {
   int32_t N;                   /* tokens, >= 0 */
@@ -849,8 +851,9 @@ typedef struct {
   int32_t q_heads;             /* 0..1024 */
   const void* q;               /* device [N, q_heads, head_dim], unit stride in head_dim */
   int64_t q_token_stride, q_head_stride;
-  void* q_out;                 /* device out: q itself with its strides, or memory that does not overlap */
-  int64_t q_out_token_stride, q_out_head_stride;
+  void* q_out;                 /* device out: q itself with its strides, or memory that does not overlap q,
+                                  key or value */
+  int64_t q_out_token_stride, q_out_head_stride;  /* elements, >= 0; no two elements in one place */
 } spec_kv4_write_args;
 
 int spec_kv4_write_launch(const spec_kv4_write_args* args, hipStream_t stream);

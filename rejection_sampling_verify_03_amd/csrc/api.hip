@@ -10,6 +10,7 @@
 
 #include "spec_verify.h"
 #include "ops_kernels.hpp"
+#include "overlap.hpp"
 #include "verify_kernels.hpp"
 #include "verify_layout.hpp"
 
@@ -446,10 +447,19 @@ CacheView cache4_view(const spec_kv4_cache& c) {
   return v;
 }
 
-// One rotated tensor: its input and output.
-bool turned_ok(const void* in, int64_t tok, int64_t head, const void* out, int64_t out_tok, int64_t out_head) {
+MemRows heads_of(const void* base, int32_t N, int64_t tok, int32_t heads, int64_t head, int32_t dim, int64_t es) {
+  constexpr int64_t kMost = INT64_MAX / 4;  // (in bytes within 64 bits; no memory is so large)
+  return MemRows{(uintptr_t)base, N, (tok < kMost ? tok : kMost) * es, heads, (head < kMost ? head : kMost) * es, dim * es};
+}
+
+// One rotated tensor: its input and output.  Lanes write the output in no order,
+// and others read.
+bool turned_ok(const void* in, int64_t tok, int64_t head, const void* out, int64_t out_tok, int64_t out_head, int32_t N,
+               int32_t heads, int32_t dim, int64_t es) {
   if (!in || !out || tok < 0 || head < 0 || out_tok < 0 || out_head < 0) return false;
-  return in != out || (tok == out_tok && head == out_head);
+  const MemRows to = heads_of(out, N, out_tok, heads, out_head, dim, es);
+  if (rows_share(to)) return false;
+  return in == out ? tok == out_tok && head == out_head : !rows_meet(heads_of(in, N, tok, heads, head, dim, es), to);
 }
 
 // How the tokens and heads of a rotation are shared out; false: too many.
@@ -473,12 +483,24 @@ int rope_check(const spec_rope_args* a, RopeParams& P) {
   if (!(fabs(a->scale) <= DBL_MAX)) return SPEC_EINVAL;
   if (a->N == 0 || a->q_heads + a->k_heads == 0) return SPEC_OK;
   if (!a->inv_freq || !a->positions) return SPEC_EINVAL;
-  if (a->q_heads > 0 && !turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride,
-                                   a->q_out_head_stride))
+  const int64_t es = a->dtype == SPEC_BF16 ? 2 : 4;
+  const bool q = a->q_heads > 0, k = a->k_heads > 0;
+  if (q && !turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride, a->q_out_head_stride,
+                      a->N, a->q_heads, a->head_dim, es))
     return SPEC_EINVAL;
-  if (a->k_heads > 0 && !turned_ok(a->k, a->k_token_stride, a->k_head_stride, a->k_out, a->k_out_token_stride,
-                                   a->k_out_head_stride))
+  if (k && !turned_ok(a->k, a->k_token_stride, a->k_head_stride, a->k_out, a->k_out_token_stride, a->k_out_head_stride,
+                      a->N, a->k_heads, a->head_dim, es))
     return SPEC_EINVAL;
+  if (q && k) {
+    const MemRows qo = heads_of(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, a->head_dim, es),
+                  ko = heads_of(a->k_out, a->N, a->k_out_token_stride, a->k_heads, a->k_out_head_stride, a->head_dim, es);
+    if (rows_meet(qo, ko) ||
+        (a->k != a->k_out &&
+         rows_meet(heads_of(a->k, a->N, a->k_token_stride, a->k_heads, a->k_head_stride, a->head_dim, es), qo)) ||
+        (a->q != a->q_out &&
+         rows_meet(heads_of(a->q, a->N, a->q_token_stride, a->q_heads, a->q_head_stride, a->head_dim, es), ko)))
+      return SPEC_EINVAL;
+  }
   P = {};
   P.N = a->N;
   P.heads[0] = a->q_heads;
@@ -520,9 +542,17 @@ int kv4_write_check(const spec_kv4_write_args* a, RopeParams& P) {
   if (a->k_token_stride < 0 || a->k_head_stride < 0 || a->v_token_stride < 0 || a->v_head_stride < 0)
     return SPEC_EINVAL;
   if (a->rot_dim > 0 && (!a->inv_freq || !a->positions)) return SPEC_EINVAL;
-  if (a->q_heads > 0 && !turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride,
-                                   a->q_out_head_stride))
-    return SPEC_EINVAL;
+  if (a->q_heads > 0) {
+    const int64_t es = a->dtype == SPEC_BF16 ? 2 : 4;
+    const int32_t heads = a->cache.heads, dim = a->cache.head_dim;
+    if (!turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride, a->q_out_head_stride,
+                   a->N, a->q_heads, dim, es))
+      return SPEC_EINVAL;
+    const MemRows qo = heads_of(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, dim, es);
+    if (rows_meet(heads_of(a->key, a->N, a->k_token_stride, heads, a->k_head_stride, dim, es), qo) ||
+        rows_meet(heads_of(a->value, a->N, a->v_token_stride, heads, a->v_head_stride, dim, es), qo))
+      return SPEC_EINVAL;
+  }
   P = {};
   P.c = cache4_view(a->cache);
   P.N = a->N;

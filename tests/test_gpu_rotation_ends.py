@@ -1,5 +1,5 @@
-"""Rotation at the ends of the range: keys that leave fp32's on their way into
-the 4-bit cache."""
+"""Rotation at its ends: keys that leave fp32's range on their way into the 4-bit
+cache, and tensors in and out of place next to each other."""
 import math
 
 import numpy as np
@@ -62,3 +62,32 @@ def test_turned_keys_past_fp32_count_as_infinite(sv, inter, dtype):
     got, codes = (a[t // 16, t % 16, 0].reshape(N, 2, 16) for a in (cache.k.cpu().numpy(), host[0]))
     assert np.array_equal(got_scale[sure], scale[sure]) and np.array_equal(got[sure], codes[sure])
     assert ((scale == 255) == past.reshape(N, 2, 32).any(2)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_in_place_with_queries_and_keys_side_by_side(sv, dtype):
+    """Queries, keys and values of a head next to each other, tokens outside or
+    inside: rotated where they stand, equal to new outputs, the rest untouched; the
+    same tensor twice, or a shared head, as an output is refused."""
+    g = torch.Generator().manual_seed(5)
+    N, H, D = 19, 5, 64
+    r = sv.make_rope(D)
+    pos = torch.arange(N, dtype=torch.int32).cuda()
+    for shape, of in (((N, H, 3, D), lambda t, i: t[:, :, i]), ((3, H, N, D), lambda t, i: t[i].transpose(0, 1))):
+        buf = torch.randn(shape, generator=g).to(dtype).cuda()
+        before = buf.clone()
+        q, k, v = (of(buf, i) for i in range(3))
+        want = sv.rope(q, k, pos, r)
+        got = sv.rope(q, k, pos, r, out=(q, k))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(v, of(before, 2))
+        cache = sv.make_kv4_cache(2, 16, H, D)
+        q.copy_(of(before, 0))
+        out = sv.rope_kv_write(cache, q, k, v, pos, pos.long(), r, q_out=q)
+        torch.cuda.synchronize()
+        assert out is q and torch.equal(q, want[0])
+        for call in (lambda: sv.rope(q, k, pos, r, out=(want[0], want[0])), lambda: sv.rope(q, k, pos, r, out=(k, q)),
+                     lambda: sv.rope(q, k, pos, r, out=(q[:, :1].expand(N, H, D), want[1])),
+                     lambda: sv.rope_kv_write(cache, q, k, v, pos, pos.long(), r, q_out=v)):
+            with pytest.raises(sv.SpecError):
+                call()

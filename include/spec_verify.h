@@ -732,7 +732,7 @@ int spec_sample_launch(const spec_sample_args* args, hipStream_t stream);
  * with a NaN or +inf logit or without a finite one, stays as it is; a row
  * whose request's settings are data errors (above) becomes NaN, which a
  * verification reports.  out may be the logits themselves (in place, with
- * their strides), or memory that does not overlap them.
+ * their strides), or memory that does not overlap them (else SPEC_EINVAL).
  */
 typedef struct {
   int32_t B, R, V;          /* as above */

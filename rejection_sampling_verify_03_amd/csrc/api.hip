@@ -29,6 +29,13 @@ constexpr int64_t kThreads = 256;  // per workgroup of the statistics, cache and
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// [n, m, len] elements of es bytes by their strides.
+MemRows mem_rows(const void* base, int32_t n, int64_t outer, int32_t m, int64_t inner, int64_t len, int64_t es) {
+  constexpr int64_t kMost = INT64_MAX / 4;  // (in bytes within 64 bits; no memory is so large)
+  auto bytes = [&](int32_t rows, int64_t stride) { return rows > 1 ? (stride < kMost ? stride : kMost) * es : 0; };
+  return MemRows{(uintptr_t)base, n, bytes(n, outer), m, bytes(m, inner), len * es};
+}
+
 // Device address of `scratch` per device, looked up on the first call made
 // with that device current (a lookup, not an allocation).
 constexpr int kMaxDevices = 64;
@@ -447,19 +454,14 @@ CacheView cache4_view(const spec_kv4_cache& c) {
   return v;
 }
 
-MemRows heads_of(const void* base, int32_t N, int64_t tok, int32_t heads, int64_t head, int32_t dim, int64_t es) {
-  constexpr int64_t kMost = INT64_MAX / 4;  // (in bytes within 64 bits; no memory is so large)
-  return MemRows{(uintptr_t)base, N, (tok < kMost ? tok : kMost) * es, heads, (head < kMost ? head : kMost) * es, dim * es};
-}
-
 // One rotated tensor: its input and output.  Lanes write the output in no order,
 // and others read.
 bool turned_ok(const void* in, int64_t tok, int64_t head, const void* out, int64_t out_tok, int64_t out_head, int32_t N,
                int32_t heads, int32_t dim, int64_t es) {
   if (!in || !out || tok < 0 || head < 0 || out_tok < 0 || out_head < 0) return false;
-  const MemRows to = heads_of(out, N, out_tok, heads, out_head, dim, es);
+  const MemRows to = mem_rows(out, N, out_tok, heads, out_head, dim, es);
   if (rows_share(to)) return false;
-  return in == out ? tok == out_tok && head == out_head : !rows_meet(heads_of(in, N, tok, heads, head, dim, es), to);
+  return in == out ? tok == out_tok && head == out_head : !rows_meet(mem_rows(in, N, tok, heads, head, dim, es), to);
 }
 
 // How the tokens and heads of a rotation are shared out; false: too many.
@@ -492,13 +494,13 @@ int rope_check(const spec_rope_args* a, RopeParams& P) {
                       a->N, a->k_heads, a->head_dim, es))
     return SPEC_EINVAL;
   if (q && k) {
-    const MemRows qo = heads_of(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, a->head_dim, es),
-                  ko = heads_of(a->k_out, a->N, a->k_out_token_stride, a->k_heads, a->k_out_head_stride, a->head_dim, es);
+    const MemRows qo = mem_rows(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, a->head_dim, es),
+                  ko = mem_rows(a->k_out, a->N, a->k_out_token_stride, a->k_heads, a->k_out_head_stride, a->head_dim, es);
     if (rows_meet(qo, ko) ||
         (a->k != a->k_out &&
-         rows_meet(heads_of(a->k, a->N, a->k_token_stride, a->k_heads, a->k_head_stride, a->head_dim, es), qo)) ||
+         rows_meet(mem_rows(a->k, a->N, a->k_token_stride, a->k_heads, a->k_head_stride, a->head_dim, es), qo)) ||
         (a->q != a->q_out &&
-         rows_meet(heads_of(a->q, a->N, a->q_token_stride, a->q_heads, a->q_head_stride, a->head_dim, es), ko)))
+         rows_meet(mem_rows(a->q, a->N, a->q_token_stride, a->q_heads, a->q_head_stride, a->head_dim, es), ko)))
       return SPEC_EINVAL;
   }
   P = {};
@@ -548,9 +550,9 @@ int kv4_write_check(const spec_kv4_write_args* a, RopeParams& P) {
     if (!turned_ok(a->q, a->q_token_stride, a->q_head_stride, a->q_out, a->q_out_token_stride, a->q_out_head_stride,
                    a->N, a->q_heads, dim, es))
       return SPEC_EINVAL;
-    const MemRows qo = heads_of(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, dim, es);
-    if (rows_meet(heads_of(a->key, a->N, a->k_token_stride, heads, a->k_head_stride, dim, es), qo) ||
-        rows_meet(heads_of(a->value, a->N, a->v_token_stride, heads, a->v_head_stride, dim, es), qo))
+    const MemRows qo = mem_rows(a->q_out, a->N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, dim, es);
+    if (rows_meet(mem_rows(a->key, a->N, a->k_token_stride, heads, a->k_head_stride, dim, es), qo) ||
+        rows_meet(mem_rows(a->value, a->N, a->v_token_stride, heads, a->v_head_stride, dim, es), qo))
       return SPEC_EINVAL;
   }
   P = {};
@@ -1093,8 +1095,14 @@ int spec_truncate_launch(const spec_truncate_args* a, hipStream_t stream) {
   if (!a->out) return SPEC_EINVAL;
   if (a->req_stride != 0 && a->req_stride / a->R < a->row_stride) return SPEC_EINVAL;
   if (a->out_row_stride < a->V || (a->B > 1 && a->out_req_stride / a->R < a->out_row_stride)) return SPEC_EINVAL;
-  if (a->out == a->logits && (a->out_row_stride != a->row_stride || (a->B > 1 && a->out_req_stride != a->req_stride)))
-    return SPEC_EINVAL;
+  if (a->out == a->logits) {
+    if (a->out_row_stride != a->row_stride || (a->B > 1 && a->out_req_stride != a->req_stride)) return SPEC_EINVAL;
+  } else {  // (one workgroup's writes would change what another still reads)
+    const int64_t es = a->dtype == SPEC_BF16 ? 2 : 4;
+    if (rows_meet(mem_rows(a->logits, a->B, a->req_stride, a->R, a->row_stride, a->V, es),
+                  mem_rows(a->out, a->B, a->out_req_stride, a->R, a->out_row_stride, a->V, es)))
+      return SPEC_EINVAL;
+  }
   CutParams P = cut_params(a);
   P.out = static_cast<char*>(a->out);
   P.out_req = a->out_req_stride;

@@ -8,7 +8,7 @@ import subprocess
 
 import pytest
 
-from test_decode_abi import P, rope_args, write_args
+from test_decode_abi import P, rope_args, truncate_args, write_args
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "rejection_sampling_verify_03_amd", "csrc")
@@ -101,3 +101,9 @@ def test_rotations_into_one_place(sv, kw):
                                 dict(key=16 * P, q_out=16 * P), dict(value=16 * P, q_out=16 * P + 128)])
 def test_rotated_queries_of_a_write_into_one_place(sv, kw):
     assert sv.spec_kv4_write_launch(write_args(sv, **{**dict(q=8 * P, q_out=32 * P), **kw}), None) == sv.SPEC_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(out=P + 2), dict(out=P + 2000 * 2), dict(out=P - 5998, out_req_stride=3500),
+                                dict(req_stride=0, out=P - 6000 * 2 + 2, out_row_stride=1000, out_req_stride=3000)])
+def test_truncation_into_what_it_reads(sv, kw):
+    assert sv.spec_truncate_launch(truncate_args(sv, **kw), None) == sv.SPEC_EINVAL

@@ -762,8 +762,9 @@ int spec_truncate_launch(const spec_truncate_args* args, hipStream_t stream);
  * the elements of a head from rot_dim on stay as they are.  A negative position
  * turns back.  The angle is the fp64 product (|a| up to 2^31), its cosine and
  * sine are taken in fp64; so are the products with them for fp32 tensors, rounded
- * once.  For bf16 they are fp32 products of the rounded cosine and sine: 2^-23
- * of |x| + |y| off at most, before the rounding to bf16.
+ * once.  For bf16 they are fp32 products of the cosine and sine as rounded to
+ * fp32: off by 2^-22 |scale| (|x| + |y|) at most before the rounding to bf16, as
+ * long as the products are normal fp32 numbers.
  * Outputs with two elements in one place, or with one in that of the other
  * output or of the other input, are refused (SPEC_EINVAL).
  */

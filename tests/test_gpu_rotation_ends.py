@@ -91,3 +91,29 @@ def test_in_place_with_queries_and_keys_side_by_side(sv, dtype):
                      lambda: sv.rope_kv_write(cache, q, k, v, pos, pos.long(), r, q_out=v)):
             with pytest.raises(sv.SpecError):
                 call()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("scale", [1.0, 1.2079, 4.0, -0.5])
+def test_bf16_rotation_within_its_documented_error(sv, scale, inter):
+    """Off by 2^-22 |scale| (|x| + |y|) at most before the rounding to bf16: pairs
+    of any angle, and such that almost cancel, where that rounding is small."""
+    N, H, D = 300, 4, 64
+    g = torch.Generator().manual_seed(11)
+    pos = torch.randint(-1000, 100000, (N,), generator=g).to(torch.int32)
+    f = 10000.0 ** (-2.0 * np.arange(D // 2) / D)
+    i, j = (slice(0, D, 2), slice(1, D, 2)) if inter else (slice(0, D // 2), slice(D // 2, D))
+    x = torch.randn(N, H, D, generator=g)
+    a = pos.double()[:, None, None] * torch.from_numpy(f)
+    y = x[..., i].double() * a.cos() / a.sin()
+    near = torch.rand(N, H, D // 2, generator=g) < 0.5
+    x[..., j] = torch.where(near & (y.abs() < 100), y.float(), x[..., j])
+    x = x.to(BF16)
+    got, _ = sv.rope(x.cuda(), None, pos.cuda(), sv.Rope(torch.from_numpy(f).cuda(), scale, inter))
+    torch.cuda.synchronize()
+    want = do.rotate(x.double().numpy(), pos.numpy(), f, scale, inter)
+    size = np.empty_like(want)
+    x = np.abs(x.double().numpy())
+    size[..., i] = size[..., j] = 2.0 ** -22 * abs(scale) * (x[..., i] + x[..., j])
+    assert (np.abs(want) < 2.0 ** -8 * abs(scale) * x.max()).mean() > 0.2  # (many cancel)
+    assert np.all(np.abs(got.cpu().double().numpy() - want) <= size + 2.0 ** -8 * (np.abs(want) + size))

@@ -470,8 +470,10 @@ bool rope_split(RopeParams& P) {
   const int64_t rounds = (heads + per - 1) / per;
   P.by_heads = FastDiv::by((uint32_t)heads);
   // many tokens: as many to a workgroup as its lanes work out angles for; few:
-  // one, its heads shared out
-  const bool many = (int64_t)P.N * rounds >= 16384;
+  // one, its heads shared out.  Two rounds to a token, 72 heads of 64, few against
+  // many: 3200 tokens 13.0 us against 14.8, 6400 27.0 against 22.7, 12800 50.4 against
+  // 47.8; 40 heads of 128: 13.8 against 12.9, 25.8 against 23.2, 49.6 against 41.8.
+  const bool many = (int64_t)P.N * rounds >= 8192;
   P.tokens = !many ? 1 : P.half > 0 ? kRopeAngles / P.half : 8;
   P.shares = many ? 1 : (int32_t)rounds;
   return fits_dispatch((((int64_t)P.N + P.tokens - 1) / P.tokens) * P.shares, kThreads);

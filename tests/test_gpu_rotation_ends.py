@@ -117,3 +117,41 @@ def test_bf16_rotation_within_its_documented_error(sv, scale, inter):
     size[..., i] = size[..., j] = 2.0 ** -22 * abs(scale) * (x[..., i] + x[..., j])
     assert (np.abs(want) < 2.0 ** -8 * abs(scale) * x.max()).mean() > 0.2  # (many cancel)
     assert np.all(np.abs(got.cpu().double().numpy() - want) <= size + 2.0 ** -8 * (np.abs(want) + size))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("hq,heads,dim,rot,N", [(2, 1, 64, 64, 17003), (6, 2, 128, 32, 9001), (3, 2, 96, 80, 18001), (1, 1, 256, 256, 16385),
+                                                (0, 1, 32, 16, 20011), (33, 4, 64, 48, 8200)])
+def test_many_tokens(sv, hq, heads, dim, rot, N, inter, dtype):
+    """Several tokens to a workgroup: queries against the definition, keys and
+    values in the cache against writes of few tokens at a time, some entries
+    skipped, some slots given to two entries next to each other."""
+    g = torch.Generator().manual_seed(N)
+    f = 10000.0 ** (-2.0 * np.arange(rot // 2) / rot)
+    r = sv.Rope(torch.from_numpy(f).cuda(), 1.1, inter)
+    q = torch.randn(N, hq, dim, generator=g).to(dtype) if hq else None
+    key, val = ((torch.randn(N, heads, dim, generator=g) * 3).to(dtype) for _ in range(2))
+    pos = torch.randint(0, 100000, (N,), generator=g).long()
+    slots = torch.randperm(N, generator=g)
+    slots[torch.rand(N, generator=g) < 0.1] = -1
+    twice = torch.arange(0, N - 1, 10)
+    slots[twice] = slots[twice + 1]
+    dq, dk, dv, dp, ds = (None if t is None else t.cuda() for t in (q, key, val, pos, slots))
+    one, two = (sv.make_kv4_cache(-(-N // 16), 16, heads, dim) for _ in range(2))
+    out = sv.rope_kv_write(one, dq, dk, dv, dp, ds, r)
+    for i in range(0, N, 1000):  # (no pair of equal slots is parted)
+        sv.rope_kv_write(two, None, dk[i:i + 1000], dv[i:i + 1000], dp[i:i + 1000], ds[i:i + 1000], r)
+    turned = sv.rope(dk if q is None else dq, dk, dp, r)
+    torch.cuda.synchronize()
+    for n in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(one, n), getattr(two, n)), n
+    i, j = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    for x, got in ((q, out), (q, turned[0] if hq else None), (key, turned[1])):
+        if got is None:
+            continue
+        x, got = x.double().numpy(), got.cpu().double().numpy()
+        want, size = do.rotate(x, pos.numpy(), f, 1.1, inter), np.zeros_like(x)
+        size[..., i] = size[..., j] = 1.1 * (np.abs(x[..., i]) + np.abs(x[..., j]))
+        early = 2.0 ** -22 * size if dtype == BF16 else 1e-12
+        assert np.all(np.abs(got - want) <= torch.finfo(dtype).eps / 2 * (np.abs(want) + early) + early)

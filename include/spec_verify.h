@@ -628,6 +628,8 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  * and lse = sinks[h], or -inf without sinks.  A sink may be any number, the
  * largest and the infinite ones among them: one of +inf takes all the weight
  * (out 0, lse +inf), one of -inf none.
+ * The weights exp(s_j - z) are rounded to bf16 for the sum of values (half a
+ * step, 2^-8 of each weight at most); lse comes from the unrounded ones.
  * The scores are computed in fp32: one above its range makes its row NaN, one
  * below it counts as -inf.  The sums of values too, with weights of up to 2^8:
  * 2^8 * ctx_len * max |v| has to lie in its range, over all positions that

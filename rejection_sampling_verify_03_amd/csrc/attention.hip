@@ -63,11 +63,14 @@
 // values two keys' results are put together by halves (in place of the bytes'
 // transposition).  With two row tiles at 64 dims two registers are spilled in
 // it, with five one, in the others none.  The verification batch takes
-// 126 us (vector instructions in 58 % of the cycles, matrix instructions in
-// 20 %), single tokens over three contexts of up to 131072, 364 MB, 81 us, of
-// which the main kernel 75 (4.9 TB/s).  Two tiles on their way: 98 us (39
-// registers spilled to keep three workgroups to a CU); four workgroups to a CU
-// at 128 dims: 94 us (17 spilled).
+// 124 us (vector instructions in 58 % of the cycles, matrix instructions in
+// 21 %), single tokens over three contexts of up to 131072, 364 MB, 81 us, of
+// which the main kernel 75 (4.9 TB/s).  Single tokens over 64 contexts of 4096: 38
+// us with eight heads of 64, 45 with 128 (vector 55 % in both: 240 and 303 vector
+// instructions for a tile of 2 and 4 KB, the scores' part does not shrink with the
+// head).  Chunks of 1000 tokens: vector 61 %, matrix 30 %, as the 8-bit form.
+// Two tiles on their way: 98 us (39 registers spilled to keep three workgroups to
+// a CU); four workgroups to a CU at 128 dims: 94 us (17 spilled).
 #include <limits.h>
 
 #include <type_traits>

@@ -86,7 +86,10 @@ constexpr size_t kSplitPartBytes = 41520;  // of a part's counts and masses
 // each would leave most of the card idle (up to 64 rows; three or four kernels in
 // place of one).  64 rows of 201088 bf16 logits, top p: 51 us against 66, eight
 // rows 39 against 65; of 100000 fp32 logits 81 against 126.  64 rows of 67000
-// bf16 logits the other way: 43 us against 40, by top k 33 against 22.
+// bf16 logits the other way: 43 us against 40, by top k 33 against 22.  More rows
+// have two workgroups at most: 66 rows of 151936 top k 36 us against 33, top p 47
+// against 53, settings of their own 52 against 53; 128 rows 41 against 34, 54 against
+// 53, 57 against 53 (of 100000 fp32 logits, top p, 105 against 127).
 inline int32_t cut_parts(int64_t rows, int32_t V, int32_t es) {
   if (rows < 1 || rows > 64 || (int64_t)V * es < 262144) return 1;
   return (int32_t)(256 / rows < kCutParts ? 256 / rows : kCutParts);

@@ -38,13 +38,23 @@
 // slots (the place of a logit among the bins, 4.5 of them, in each of two
 // sweeps), and the atomic additions and lookups in LDS, which half collide, 32 %
 // of its cycles.  64 rows of 201088 with settings of their own: 53 us (the parts'
-// counts 14, their candidates or sums 24, the rest 15), of which the bytes need
-// 4: chains of dependent steps on a few waves.  288 such rows cut: 60 us, and 31
-// (5.6 TB/s) to write what is left of the logits.  Rows that are masked for the
-// most part cost no more (288 rows of 151936 with a half, a hundredth or 15 of
-// the logits left, top k: 49, 46, 65 us; whole rows 46): the last bin's count is
-// what the others leave, where all would add in one place (274 us).  Four rows of 1024 fp32 logits,
-// top k: 11 us, a chain of steps again.
+// counts 15, their candidates or sums 23, the rest 14), of which the bytes need
+// 4: chains of dependent steps on a few waves.  288 such rows cut: 64 to 71 us by
+// their settings, and 31 (5.6 TB/s) to write what is left of the logits.  Four rows
+// of 1024 fp32 logits, top k: 11 us, a chain of steps again.
+//
+// Additions in one place of LDS follow one another.  Logits masked with -128 or
+// less are spared it: the last bin's count is what the others leave (288 rows of
+// 151936 with a hundredth of the logits left, top k: 47 us at -inf or -10000, whole
+// rows 46; added one by one 274).  Rows most of whose logits share a value above
+// -128 are not: 99 % at -100 or -50, top k 274 us, top p 291 (89 for whole rows); at 0,
+// where they have weight, 274 and 1566, uncut 204 (57); fp32 logits 282 and 350 (93 and
+// 340 for whole rows), at 0 282 and 2043.
+//
+// Registers: of the 128 that four waves to a SIMD have, 28 more would be needed in
+// the whole draw of bf16 rows with 1024 threads, 24 in its cut, 25 in the shared
+// cut's last kernel, 8 with 512 threads, 6 at most with fp32 logits: so many are
+// spilled.
 //
 #include <limits.h>
 
@@ -1389,7 +1399,9 @@ __global__ __launch_bounds__(kWG) void truncate_kernel(CutParams P) {
 
 // 1024 threads to a row up to 256 rows, a row to a CU, and 512 beyond, two rows to
 // a CU: 256 rows of 151936 bf16 logits 53 us against 58 with 512, of 40000 fp32
-// ones 64 against 68; 512 rows of 151936 79 us against 103 with 1024.
+// ones 64 against 68; with 1024 beyond, 288 rows of 151936 drawn with settings of
+// their own 91 us against 74, uncut 67 against 56, cut 116 against 102 (by top k 97
+// against 82), 261 rows cut 89 against 80, 504 rows 141 against 121.
 template <int ES, bool DRAW>
 static hipError_t launch_rows(const CutParams& P, unsigned rows, hipStream_t stream) {
   if (P.parts > 1) {

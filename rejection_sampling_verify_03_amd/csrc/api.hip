@@ -470,10 +470,17 @@ bool rope_split(RopeParams& P) {
   const int64_t rounds = (heads + per - 1) / per;
   P.by_heads = FastDiv::by((uint32_t)heads);
   // many tokens: as many to a workgroup as its lanes work out angles for; few:
-  // one, its heads shared out.  Two rounds to a token, 72 heads of 64, few against
-  // many: 3200 tokens 13.0 us against 14.8, 6400 27.0 against 22.7, 12800 50.4 against
-  // 47.8; 40 heads of 128: 13.8 against 12.9, 25.8 against 23.2, 49.6 against 41.8.
-  const bool many = (int64_t)P.N * rounds >= 8192;
+  // one, its heads shared out.  Few against many, us, on both sides of the border
+  // (72 = 64 + 8 heads, 40 = 32 + 8):
+  //   bf16, 4000, 8000, 16000 tokens  72 heads of 64    19.5 17.1   33.9 28.7   63.7 58.6
+  //                                   40 heads of 128   18.4 16.5   32.9 30.8   62.3 52.4
+  //                                   32 heads of 96    13.6 13.9   20.2 22.8   37.2 40.5
+  //   fp32                            72 heads of 64    29.2 27.6   55.2 52.4   111 115
+  //                                   40 heads of 128   32.0 31.9   61.5 61.5   119 132
+  // A small rotated part makes few workgroups of many tokens (72 heads of 192 of which
+  // 32 dims are rotated, bf16: 40.5 62.5 for 4000 tokens, 76.9 79.1 for 8000), and large
+  // fp32 batches lose as well: no border on the tokens alone suits all.
+  const bool many = (int64_t)P.N * rounds >= 16384;
   P.tokens = !many ? 1 : P.half > 0 ? kRopeAngles / P.half : 8;
   P.shares = many ? 1 : (int32_t)rounds;
   return fits_dispatch((((int64_t)P.N + P.tokens - 1) / P.tokens) * P.shares, kThreads);

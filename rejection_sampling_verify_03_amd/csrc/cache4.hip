@@ -21,7 +21,7 @@
 // by itself: no order among the writers, nothing read back.
 //
 // Bounds, measured (MI355X): memory.  8190 tokens of 32 + 8 heads of 128, half of
-// each rotated: 37 us with inputs past the caches (4.5 TB/s read and written), 27
+// each rotated: 38 us with inputs past the caches (4.4 TB/s read and written), 30
 // with part of them within.  24000 tokens of 32 + 8 + 8 heads of 128 rotated and
 // written: 119 us, 4.4 TB/s; the cache's part read back as bf16 22 us, 5.7 TB/s.
 // A decode step's 64 tokens take 4 us, what a launch takes.

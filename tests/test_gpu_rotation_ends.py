@@ -121,8 +121,8 @@ def test_bf16_rotation_within_its_documented_error(sv, scale, inter):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("hq,heads,dim,rot,N", [(2, 1, 64, 64, 17003), (6, 2, 128, 32, 9001), (3, 2, 96, 80, 18001), (1, 1, 256, 256, 16385),
-                                                (0, 1, 32, 16, 20011), (33, 4, 64, 48, 8200)])
+@pytest.mark.parametrize("hq,heads,dim,rot,N", [(2, 1, 64, 64, 17003), (6, 2, 128, 32, 16390), (3, 2, 96, 80, 18001), (1, 1, 256, 256, 16385),
+                                                (0, 1, 32, 16, 20011), (33, 4, 64, 48, 16400)])
 def test_many_tokens(sv, hq, heads, dim, rot, N, inter, dtype):
     """Several tokens to a workgroup: queries against the definition, keys and
     values in the cache against writes of few tokens at a time, some entries

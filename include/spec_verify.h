@@ -633,7 +633,9 @@ int spec_kv_read_launch(const spec_kv_read_args* args, hipStream_t stream);
  * The scores are computed in fp32: one above its range makes its row NaN, one
  * below it counts as -inf.  The sums of values too, with weights of up to 2^8:
  * 2^8 * ctx_len * max |v| has to lie in its range, over all positions that
- * the token sees (else its output is unspecified; others' are not concerned).
+ * the token sees, and so has 2^8 times the scale of each of them where a scale
+ * covers fewer than 16 tokens (else the token's output is unspecified; others' are
+ * not concerned).
  * Codes of positions that a token does not see never reach its output, NaN
  * and those that bf16 reads as infinite among them.  A request whose ctx_len is negative or above max_ctx or
  * max_blocks * block_size, or whose n_b is above max_q, is a data error: NaN
